@@ -441,6 +441,154 @@ gemm_status_t gemm_bf16_grouped_noalloc(const gemm_problem_t *problems, int num_
                                         gemm_out_t d_type, float alpha, float beta,
                                         gemm_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * Expert layers: routing, 8-bit integer products, weighted sums. Element
+ * types are gemm_out_t codes. The calls follow the rules above: device
+ * pointers owned by the caller, no allocation, asynchronous on `stream`,
+ * errors returned before anything is enqueued. Unless a rule below says
+ * otherwise, pointers need only the alignment of their elements and leading
+ * dimensions only the length of a row.
+ * ------------------------------------------------------------------- */
+
+typedef enum { GEMM_ROUTE_SOFTMAX = 0, GEMM_ROUTE_SIGMOID = 1 } gemm_score_t;
+
+/*
+ * How tokens choose experts (NULL: softmax scores, no groups, scale 1).
+ *   score         scores s of a token from its logits l: softmax over the E
+ *                 experts, or the sigmoid of each.
+ *   groups        0 or 1: none. Otherwise the experts form this many groups
+ *                 of E / groups neighbours (at most 32 groups; it divides E);
+ *   group_top     a group's score is the sum of its group_top (1 or 2; 0
+ *                 means 1) best s + bias;
+ *   groups_kept   only the experts of the groups_kept best groups stay.
+ *   renormalize   nonzero: a token's chosen scores are divided by their sum
+ *                 (a sum of 0 leaves weights of 0).
+ *   scale         factor on the weights; 0 means 1.
+ */
+typedef struct {
+    int score;
+    int groups;
+    int group_top;
+    int groups_kept;
+    int renormalize;
+    float scale;
+} gemm_route_t;
+
+#define GEMM_ROUTE_MAX_EXPERTS 1024
+#define GEMM_ROUTE_MAX_K 32
+
+/*
+ * gemm_route: for each of T tokens, the k experts with the largest s + bias
+ * (of the kept groups), best first, and their weights scale * s (/ the sum
+ * of the chosen s). The bias (E fp32 values, or NULL) steers the choice and
+ * is no part of the weights. Equal values go to the lower index; without a
+ * bias the choice goes by the logits, whose order is that of the scores.
+ *   logits: T x E of l_type, row stride ldl. weights: T x k fp32; ids: T x k
+ *   int32. 1 <= k <= min(E, GEMM_ROUTE_MAX_K), E <= GEMM_ROUTE_MAX_EXPERTS,
+ *   k at most the experts of the kept groups.
+ * A logit (or bias) of -inf or NaN is never chosen. Where fewer than k
+ * experts are left (a padded token has none), the remaining ids are -1 and
+ * their weights 0. A NaN logit, or under softmax one of +inf, makes all
+ * weights of its token NaN; the ids stay valid.
+ */
+gemm_status_t gemm_route(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl,
+                         const float *bias, int k, const gemm_route_t *route,
+                         float *weights, int32_t *ids, gemm_stream_t stream);
+
+/*
+ * gemm_route_backward: the gradient of the logits from that of the weights,
+ * for the ids that gemm_route chose (the choice itself, and with it the bias,
+ * has none). dweights: T x k fp32; dlogits: T x E of l_type, row stride lddl,
+ * written whole. Ids outside 0..E-1 carry nothing; the others of a token are
+ * distinct. k and route as in the forward call (groups play no part).
+ */
+gemm_status_t gemm_route_backward(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl,
+                                  int k, const gemm_route_t *route, const int32_t *ids,
+                                  const float *dweights, void *dlogits, int64_t lddl, gemm_stream_t stream);
+
+/*
+ * gemm_route_plan: the order of the T * k (token, choice) pairs by expert,
+ * for gemm_int8_grouped and the sums below. Pairs of one expert keep their
+ * order (a stable counting sort: the result does not depend on timing).
+ *   offsets  E + 1 int32: rows offsets[e] .. offsets[e+1]-1 are expert e's;
+ *   slots    T x k int32: the row of each pair, -1 where its id is outside
+ *            0..E-1;
+ *   tokens   T * k int32: the token of each row, -1 past offsets[E].
+ * T * k < 2^31. workspace: gemm_route_plan_workspace_size(T, E, k) bytes,
+ * 4-byte aligned (may be NULL where that is 0); it needs no initialisation.
+ */
+size_t gemm_route_plan_workspace_size(int64_t T, int64_t E, int k);
+
+gemm_status_t gemm_route_plan(int64_t T, int64_t E, int k, const int32_t *ids, int32_t *offsets,
+                              int32_t *slots, int32_t *tokens, void *workspace, size_t workspace_bytes,
+                              gemm_stream_t stream);
+
+typedef enum { GEMM_QUANT_PLAIN = 0, GEMM_QUANT_GATED = 1 } gemm_quant_t;
+
+/*
+ * gemm_quantize_int8: rows to 8-bit integers, one scale a row:
+ *   scales[m] = max_k |x[m,k]| / 127,  Q[m,k] = round(x[m,k] / scales[m])
+ * (ties to even; a row of zeros has scale 0). x[m,:] is row index[m] of X
+ * (row m without an index), X having x_rows rows of x_type with stride ldx.
+ * GEMM_QUANT_GATED: X rows are 2K wide, x = silu(X[:, :K]) * X[:, K:].
+ * An index outside 0..x_rows-1 gives a row of zeros. A row that holds a
+ * NaN or an infinity gets scale NaN and zeros, so that its products are NaN.
+ * Q: M x K int8, row stride ldq (columns K..ldq-1 are not written).
+ */
+gemm_status_t gemm_quantize_int8(int64_t M, int64_t K, const void *X, gemm_out_t x_type, int64_t x_rows,
+                                 int64_t ldx, const int32_t *index, gemm_quant_t mode,
+                                 int8_t *Q, int64_t ldq, float *scales, gemm_stream_t stream);
+
+/*
+ * gemm_int8: D[m,n] = scale_a[m] * scale_b[n] * sum_k A[m,k] * B[n,k], the
+ * product of 8-bit integers with a scale for each row (token) of A and each
+ * row (channel) of B. A is M x K, B is N x K (both K-major), D is M x N of
+ * d_type. sm_103a has no integer tcgen05 kind: the integers are widened to
+ * fp16 on chip, where they and their products are exact, and summed in fp32,
+ * exactly while partial sums stay below 2^24 in magnitude (any K <= 1040,
+ * and far longer rows of quantised data), and to fp32 rounding beyond.
+ * A and B 16-byte aligned, lda and ldb multiples of 16; K == 0 writes zeros.
+ */
+gemm_status_t gemm_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a,
+                        const int8_t *B, int64_t ldb, const float *scale_b,
+                        void *D, int64_t ldd, gemm_out_t d_type, gemm_stream_t stream);
+
+/*
+ * gemm_int8_grouped: the same over rows sorted by expert: rows offsets[e] ..
+ * offsets[e+1]-1 of A (device memory, E + 1 int32, as gemm_route_plan writes
+ * them, read by the kernel: no sizes pass through the host) multiply expert
+ * e's matrix B + e * stride_b (N x K; stride_b in elements, a multiple of 16)
+ * with its channel scales scale_b[e * N + n]. M is the room of A and D in
+ * rows; rows from offsets[E] on are not written. Offsets that fall, or leave
+ * 0..M, are clamped into it. 1 <= E <= GEMM_ROUTE_MAX_EXPERTS.
+ */
+gemm_status_t gemm_int8_grouped(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t *offsets,
+                                const int8_t *A, int64_t lda, const float *scale_a,
+                                const int8_t *B, int64_t ldb, int64_t stride_b, const float *scale_b,
+                                void *D, int64_t ldd, gemm_out_t d_type, gemm_stream_t stream);
+
+/*
+ * gemm_route_combine: D[t,:] = sum_j weights[t,j] * Y[slots[t,j],:], summed
+ * in fp32 in the order of j. Y has y_rows rows of N values of y_type (stride
+ * ldy), D is T x N of d_type. Slots outside 0..y_rows-1 add nothing, whatever
+ * their weight. 1 <= k <= GEMM_ROUTE_MAX_K.
+ */
+gemm_status_t gemm_route_combine(int64_t T, int64_t N, int k, const void *Y, gemm_out_t y_type, int64_t y_rows,
+                                 int64_t ldy, const int32_t *slots, const float *weights,
+                                 void *D, gemm_out_t d_type, int64_t ldd, gemm_stream_t stream);
+
+/*
+ * gemm_route_combine_backward: dY[slots[t,j],:] = weights[t,j] * dD[t,:] and
+ * dweights[t,j] = sum_n dD[t,n] * Y[slots[t,j],n] (0 where the slot is
+ * outside 0..y_rows-1). dY: y_rows rows of y_type, stride lddy; rows that no
+ * slot names are left as they are. The slots are distinct, as
+ * gemm_route_plan makes them. dD is T x N of d_type.
+ */
+gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const void *dD, gemm_out_t d_type,
+                                          int64_t lddd, const void *Y, gemm_out_t y_type, int64_t y_rows,
+                                          int64_t ldy, const int32_t *slots, const float *weights,
+                                          void *dY, int64_t lddy, float *dweights, gemm_stream_t stream);
+
 /* Synchronises `stream`, reads the device status word of this library,
  * clears it, and returns GEMM_OK or GEMM_ERR_TIMEOUT (GEMM_ERR_CUDA if the
  * read fails). `detail` (may be NULL) receives the raw word: bits 0-7 the

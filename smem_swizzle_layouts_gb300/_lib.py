@@ -26,6 +26,9 @@ K_MAJOR, MN_MAJOR = 0, 1
 OUT_F32, OUT_BF16, OUT_F16 = 0, 1, 2
 FP8_E4M3, FP8_E5M2 = 0, 1
 FP4_NVFP4, FP4_MXFP4 = 0, 1
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+QUANT_PLAIN, QUANT_GATED = 0, 1
+ROUTE_MAX_EXPERTS, ROUTE_MAX_K = 1024, 32
 SWIZZLE_AUTO, SWIZZLE_32B, SWIZZLE_64B, SWIZZLE_128B, SWIZZLE_NONE, SWIZZLE_128B_ATOM32 = 0, 1, 2, 3, 4, 5
 
 _i64, _vp, _f, _int, _u32, _u64 = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_int,
@@ -43,6 +46,11 @@ class GemmOptions(ctypes.Structure):
 class GemmProblem(ctypes.Structure):
     _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("A", _vp), ("B", _vp), ("C", _vp),
                 ("D", _vp), ("lda", _i64), ("ldb", _i64), ("ldc", _i64), ("ldd", _i64)]
+
+
+class GemmRoute(ctypes.Structure):
+    _fields_ = [("score", _int), ("groups", _int), ("group_top", _int), ("groups_kept", _int), ("renormalize", _int),
+                ("scale", _f)]
 
 
 _single = [_i64, _i64, _i64, _vp, _int, _i64, _vp, _int, _i64, _vp, _i64, _vp, _i64, _int, _f, _f, _vp]
@@ -85,7 +93,22 @@ _lib.gemm_debug_inject_timeout.argtypes = [_int]
 _lib.gemm_debug_inject_timeout.restype = None
 _lib.gemm_debug_inject_timeout_at.argtypes = [_int, _int]
 _lib.gemm_debug_inject_timeout_at.restype = None
-for _name in ("gemm_bf16", "gemm_f16", "gemm_ex", "gemm_fp8", "gemm_fp8_ex", "gemm_mxfp8", "gemm_fp4", "gemm_bf16_grouped",
+_route = ctypes.POINTER(GemmRoute)
+_lib.gemm_route.argtypes = [_i64, _i64, _vp, _int, _i64, _vp, _int, _route, _vp, _vp, _vp]
+_lib.gemm_route_backward.argtypes = [_i64, _i64, _vp, _int, _i64, _int, _route, _vp, _vp, _vp, _i64, _vp]
+_lib.gemm_route_plan_workspace_size.argtypes = [_i64, _i64, _int]
+_lib.gemm_route_plan_workspace_size.restype = ctypes.c_size_t
+_lib.gemm_route_plan.argtypes = [_i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.gemm_quantize_int8.argtypes = [_i64, _i64, _vp, _int, _i64, _i64, _vp, _int, _vp, _i64, _vp, _vp]
+_lib.gemm_int8.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _int, _vp]
+_lib.gemm_int8_grouped.argtypes = [_i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _int,
+                                   _vp]
+_lib.gemm_route_combine.argtypes = [_i64, _i64, _int, _vp, _int, _i64, _i64, _vp, _vp, _vp, _int, _i64, _vp]
+_lib.gemm_route_combine_backward.argtypes = [_i64, _i64, _int, _vp, _int, _i64, _vp, _int, _i64, _i64, _vp, _vp, _vp,
+                                             _i64, _vp, _vp]
+for _name in ("gemm_route", "gemm_route_backward", "gemm_route_plan", "gemm_quantize_int8", "gemm_int8",
+              "gemm_int8_grouped", "gemm_route_combine", "gemm_route_combine_backward",
+              "gemm_bf16", "gemm_f16", "gemm_ex", "gemm_fp8", "gemm_fp8_ex", "gemm_mxfp8", "gemm_fp4", "gemm_bf16_grouped",
               "gemm_f16_grouped",
               "gemm_bf16_grouped_noalloc",
               "gemm_last_device_status", "gemm_debug_descriptors", "gemm_debug_stage_image"):
@@ -96,6 +119,8 @@ EXPORTED = ("gemm_bf16", "gemm_f16", "gemm_ex", "gemm_fp8", "gemm_fp8_ex", "gemm
             "gemm_streamk_workspace_size",
             "gemm_grouped_workspace_size",
             "gemm_bf16_grouped", "gemm_grouped_ex",
+            "gemm_route", "gemm_route_backward", "gemm_route_plan", "gemm_route_plan_workspace_size",
+            "gemm_quantize_int8", "gemm_int8", "gemm_int8_grouped", "gemm_route_combine", "gemm_route_combine_backward",
             "gemm_f16_grouped", "gemm_bf16_grouped_noalloc", "gemm_last_device_status", "gemm_status_string", "gemm_launch_count",
             "gemm_debug_descriptors", "gemm_debug_stage_image", "gemm_debug_plan", "gemm_debug_streamk_units",
             "gemm_debug_inject_timeout", "gemm_debug_inject_timeout_at")
@@ -311,6 +336,71 @@ def gemm_bf16_grouped_noalloc(problems, a_major, b_major, d_type, alpha, beta, s
     arr = _problem_array(problems)
     _check(_lib.gemm_bf16_grouped_noalloc(arr, len(problems), a_major, b_major, d_type, alpha, beta,
                                           _stream(stream)), "gemm_bf16_grouped_noalloc")
+
+
+def _route_rule(route):
+    if route is None:
+        return None
+    if isinstance(route, GemmRoute):
+        return ctypes.pointer(route)
+    unknown = set(route) - {name for name, _ in GemmRoute._fields_}
+    if unknown:  # ctypes would take them as plain attributes
+        raise TypeError(f"GemmRoute has no field {sorted(unknown)}")
+    return ctypes.pointer(GemmRoute(**route))
+
+
+def gemm_route(T, E, logits, l_type, ldl, bias, k, route, weights, ids, stream=None):
+    """The k experts of each token and their weights. ``route``: a GemmRoute, a dict of its fields, or None."""
+    _check(_lib.gemm_route(T, E, _addr(logits), l_type, ldl, _addr(bias), k, _route_rule(route), _addr(weights),
+                           _addr(ids), _stream(stream)), "gemm_route")
+
+
+def gemm_route_backward(T, E, logits, l_type, ldl, k, route, ids, dweights, dlogits, lddl, stream=None):
+    """The gradient of the logits from that of the weights."""
+    _check(_lib.gemm_route_backward(T, E, _addr(logits), l_type, ldl, k, _route_rule(route), _addr(ids),
+                                    _addr(dweights), _addr(dlogits), lddl, _stream(stream)), "gemm_route_backward")
+
+
+def gemm_route_plan_workspace_size(T: int, E: int, k: int) -> int:
+    return int(_lib.gemm_route_plan_workspace_size(T, E, k))
+
+
+def gemm_route_plan(T, E, k, ids, offsets, slots, tokens, workspace, workspace_bytes, stream=None):
+    """The order of the (token, choice) pairs by expert."""
+    _check(_lib.gemm_route_plan(T, E, k, _addr(ids), _addr(offsets), _addr(slots), _addr(tokens), _addr(workspace),
+                                workspace_bytes, _stream(stream)), "gemm_route_plan")
+
+
+def gemm_quantize_int8(M, K, X, x_type, x_rows, ldx, index, mode, Q, ldq, scales, stream=None):
+    """Rows (of X, or those that ``index`` names) to int8 with one scale each; QUANT_GATED applies the SwiGLU gate."""
+    _check(_lib.gemm_quantize_int8(M, K, _addr(X), x_type, x_rows, ldx, _addr(index), mode, _addr(Q), ldq,
+                                   _addr(scales), _stream(stream)), "gemm_quantize_int8")
+
+
+def gemm_int8(M, N, K, A, lda, scale_a, B, ldb, scale_b, D, ldd, d_type, stream=None):
+    """The product of int8 matrices with a scale for each row of A and of B."""
+    _check(_lib.gemm_int8(M, N, K, _addr(A), lda, _addr(scale_a), _addr(B), ldb, _addr(scale_b), _addr(D), ldd,
+                          d_type, _stream(stream)), "gemm_int8")
+
+
+def gemm_int8_grouped(M, N, K, E, offsets, A, lda, scale_a, B, ldb, stride_b, scale_b, D, ldd, d_type, stream=None):
+    """The experts' int8 products over rows sorted by expert; ``offsets`` is read on the GPU."""
+    _check(_lib.gemm_int8_grouped(M, N, K, E, _addr(offsets), _addr(A), lda, _addr(scale_a), _addr(B), ldb, stride_b,
+                                  _addr(scale_b), _addr(D), ldd, d_type, _stream(stream)), "gemm_int8_grouped")
+
+
+def gemm_route_combine(T, N, k, Y, y_type, y_rows, ldy, slots, weights, D, d_type, ldd, stream=None):
+    """The weighted sum of each token's rows of Y."""
+    _check(_lib.gemm_route_combine(T, N, k, _addr(Y), y_type, y_rows, ldy, _addr(slots), _addr(weights), _addr(D),
+                                   d_type, ldd, _stream(stream)), "gemm_route_combine")
+
+
+def gemm_route_combine_backward(T, N, k, dD, d_type, lddd, Y, y_type, y_rows, ldy, slots, weights, dY, lddy, dweights,
+                                stream=None):
+    """The gradients of the weighted sum: of the rows, and of the weights."""
+    _check(_lib.gemm_route_combine_backward(T, N, k, _addr(dD), d_type, lddd, _addr(Y), y_type, y_rows, ldy,
+                                            _addr(slots), _addr(weights), _addr(dY), lddy, _addr(dweights),
+                                            _stream(stream)), "gemm_route_combine_backward")
 
 
 def gemm_last_device_status(stream=None) -> tuple[int, int]:

@@ -1,0 +1,1085 @@
+// Expert-layer operators around the products: routing and its gradient, the
+// order of the rows by expert, the quantisation of rows to 8 bits, and the
+// weighted sum of the experts' rows with its gradient. Contracts are in
+// include/gemm_gb300.h.
+//
+// All of them read their inputs once and are bound by memory or, for a few
+// tokens, by launch latency; sums and softmax statistics are fp32 and results
+// are rounded once, on the store.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/gemm_gb300.h"
+#include "host.h"
+
+using namespace g300;
+
+namespace {
+
+// ---------------------------------------------------------------- element access
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x)
+{
+    return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x)
+{
+    return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x)
+{
+    return __float2half_rn(x);
+}
+
+// Eight neighbouring elements: 16-byte accesses when WIDE (the pointer is
+// 16-byte aligned), else single elements, of which `n` exist.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void load8(const T *p, int n, float (&v)[8])
+{
+    if constexpr (WIDE) {
+        union {
+            uint4 w[sizeof(T) / 2];
+            T e[8];
+        } u;
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            u.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = to_float(u.e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = i < n ? to_float(p[i]) : 0.0f;
+    }
+}
+
+template <typename T, bool WIDE>
+__device__ __forceinline__ void store8(T *p, int n, const float (&v)[8])
+{
+    if constexpr (WIDE) {
+        union {
+            uint4 w[sizeof(T) / 2];
+            T e[8];
+        } u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            u.e[i] = from_float<T>(v[i]);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            reinterpret_cast<uint4 *>(p)[i] = u.w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                p[i] = from_float<T>(v[i]);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
+
+// ---------------------------------------------------------------- routing
+
+struct RouteParams {
+    long long T;
+    int E, k;
+    long long ldl;
+    const float *bias;
+    float *weights;
+    int *ids;
+    int sigmoid, groups, per, group_top, groups_kept, renorm;
+    float scale;
+    unsigned int per_inv;  // ceil(2^32 / per): e / per = umulhi(e, per_inv) for per >= 2
+};
+
+// Order-preserving code of a choice value; 0 for what is never chosen (-inf
+// and NaN). +0 and -0 get one code.
+__device__ __forceinline__ uint32_t choice_key(float v)
+{
+    if (!(v > -INFINITY))
+        return 0u;
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+constexpr int kRouteWarps = 4;
+
+// One warp per token; lane l holds experts l, l + 32, ... (NPL of them). The
+// k best are taken one at a time: a warp-wide integer maximum of the lanes'
+// best codes, then the lowest expert index among those equal to it.
+template <typename L, int NPL>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *__restrict__ logits, const RouteParams p)
+{
+    extern __shared__ float group_smem[];  // per warp: groups x (per | 1) choice values
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp;
+    if (t >= p.T)
+        return;
+    const L *row = logits + t * p.ldl;
+    float l[NPL];
+    float top = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane + 32 * i;
+        l[i] = e < p.E ? to_float(row[e]) : -INFINITY;
+        bad |= l[i] != l[i] || (!p.sigmoid && l[i] == INFINITY);
+        top = fmaxf(top, l[i]);
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    // the softmax over all experts: needed for the weights when they are not
+    // renormalised (renormalised ones are a softmax over the chosen), and for
+    // the choice when a bias is added to the scores or groups are summed
+    float total = 0.0f;
+    if (!p.sigmoid) {
+        top = warp_max(top);
+        if (top == -INFINITY)
+            top = 0.0f;
+        if (!p.renorm || p.bias || p.groups > 1) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                total += l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
+            total = warp_sum(total);
+            if (total == 0.0f)
+                total = 1.0f;
+        }
+    }
+    // what the choice goes by
+    uint32_t key[NPL];
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            key[i] = 0u;
+            if (l[i] > -INFINITY) {
+                const float s = p.sigmoid ? sigmoid(l[i]) : __fdiv_rn(expf(l[i] - top), total);
+                key[i] = choice_key(__fadd_rn(s, p.bias[e]));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            key[i] = choice_key(l[i]);
+    }
+    if (p.groups > 1) {
+        const int stride = p.per | 1;  // odd: the lanes reading one value of each group meet distinct banks
+        float *gs = group_smem + warp * p.groups * stride;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            if (e < p.E) {
+                float v = -INFINITY;
+                if (key[i] != 0u) {
+                    const float s = p.sigmoid ? sigmoid(l[i]) : __fdiv_rn(expf(l[i] - top), total);
+                    v = p.bias ? __fadd_rn(s, p.bias[e]) : s;
+                }
+                const int g = p.per == 1 ? e : static_cast<int>(__umulhi(static_cast<unsigned>(e), p.per_inv));
+                gs[g * stride + e - g * p.per] = v;
+            }
+        }
+        __syncwarp();
+        uint32_t gkey = 0u;
+        if (lane < p.groups) {
+            float a = -INFINITY, b = -INFINITY;
+            for (int i = 0; i < p.per; ++i) {
+                const float v = gs[lane * stride + i];
+                b = fmaxf(b, fminf(a, v));
+                a = fmaxf(a, v);
+            }
+            if (a > -INFINITY)
+                gkey = choice_key(p.group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
+        }
+        int rank = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const uint32_t o = __shfl_sync(0xffffffffu, gkey, g);
+            rank += o > gkey || (o == gkey && g < lane);
+        }
+        const uint32_t kept = __ballot_sync(0xffffffffu, lane < p.groups && gkey != 0u && rank < p.groups_kept);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            if (e < p.E) {
+                const int g = p.per == 1 ? e : static_cast<int>(__umulhi(static_cast<unsigned>(e), p.per_inv));
+                if (!((kept >> g) & 1u))
+                    key[i] = 0u;
+            }
+        }
+    }
+    // the k best; lane j keeps the j-th
+    int my_id = -1;
+    float my_l = -INFINITY;
+    uint32_t best = 0u;
+    int best_e = INT_MAX;
+    float best_l = 0.0f;
+    auto rescan = [&]() {
+        best = 0u;
+        best_e = INT_MAX;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                best_e = lane + 32 * i;
+                best_l = l[i];
+            }
+    };
+    rescan();
+    for (int j = 0; j < p.k; ++j) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        if (m == 0u)
+            break;
+        const int e = static_cast<int>(
+            __reduce_min_sync(0xffffffffu, static_cast<unsigned>(best == m ? best_e : INT_MAX)));
+        const float v = __shfl_sync(0xffffffffu, best_l, e & 31);
+        if (lane == j) {
+            my_id = e;
+            my_l = v;
+        }
+        if (lane == (e & 31)) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if (lane + 32 * i == e)
+                    key[i] = 0u;
+            rescan();
+        }
+    }
+    // weights of the chosen, one lane each
+    float s = 0.0f;
+    if (p.sigmoid) {
+        if (my_id >= 0)
+            s = sigmoid(my_l);
+    } else if (p.renorm) {
+        const float m = warp_max(my_l);  // relative to the largest chosen logit: its term is 1, the sum never 0
+        if (my_id >= 0)
+            s = expf(my_l - m);
+    } else if (my_id >= 0) {
+        s = __fdiv_rn(expf(my_l - top), total);
+    }
+    if (p.renorm) {
+        const float sum = warp_sum(s);
+        s = __fdiv_rn(s, sum == 0.0f ? 1.0f : sum);
+    }
+    if (lane < p.k) {
+        p.weights[t * p.k + lane] = bad ? NAN : s * p.scale;
+        p.ids[t * p.k + lane] = my_id;
+    }
+}
+
+struct RouteGradParams {
+    long long T;
+    int E, k;
+    long long ldl, lddl;
+    const int *ids;
+    const float *dweights;
+    int sigmoid, renorm;
+    float scale;
+};
+
+// One warp per token. The chosen experts' values are computed one lane each
+// and put into a shared-memory row of zeros, which is then written whole;
+// only the softmax over all experts reads the other logits.
+template <typename L>
+__global__ void __launch_bounds__(32 * kRouteWarps)
+    route_backward_kernel(const L *__restrict__ logits, L *__restrict__ dlogits, const RouteGradParams p)
+{
+    extern __shared__ float grad_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp;
+    if (t >= p.T)
+        return;
+    float *ds = grad_smem + warp * p.E;
+    const L *row = logits + t * p.ldl;
+    L *out = dlogits + t * p.lddl;
+    for (int e = lane; e < p.E; e += 32)
+        ds[e] = 0.0f;
+    int id = -1;
+    float g = 0.0f, x = -INFINITY;
+    if (lane < p.k) {
+        id = p.ids[t * p.k + lane];
+        if (id < 0 || id >= p.E)
+            id = -1;
+        if (id >= 0) {
+            g = p.dweights[t * p.k + lane] * p.scale;
+            x = to_float(row[id]);
+        }
+    }
+    __syncwarp();
+    if (p.sigmoid || p.renorm) {
+        // share of the chosen score in the sum, and d score / d logit over the score
+        float s = 0.0f, rest = 1.0f;
+        if (p.sigmoid) {
+            if (id >= 0) {
+                s = sigmoid(x);
+                rest = sigmoid(-x);  // 1 - s without its cancellation
+            }
+        } else {
+            const float m = warp_max(x);
+            if (id >= 0)
+                s = expf(x - m);
+        }
+        float d = g * s * rest;
+        if (p.renorm) {
+            float sum = warp_sum(s);
+            if (sum == 0.0f)
+                sum = 1.0f;
+            const float w = __fdiv_rn(s, sum);
+            d = w * (g - warp_sum(g * w)) * rest;
+        }
+        if (id >= 0)
+            ds[id] = d;
+        __syncwarp();
+        for (int e = lane; e < p.E; e += 32)
+            out[e] = from_float<L>(ds[e]);
+        return;
+    }
+    // softmax over all experts: dl_e = s_e (ds_e - sum ds s)
+    float top = -INFINITY;
+    for (int e = lane; e < p.E; e += 32)
+        top = fmaxf(top, to_float(row[e]));
+    top = warp_max(top);
+    if (top == -INFINITY)
+        top = 0.0f;
+    float total = 0.0f;
+    for (int e = lane; e < p.E; e += 32)
+        total += expf(to_float(row[e]) - top);
+    total = warp_sum(total);
+    if (total == 0.0f)
+        total = 1.0f;
+    const float s = id >= 0 ? __fdiv_rn(expf(x - top), total) : 0.0f;
+    const float dot = warp_sum(g * s);
+    if (id >= 0)
+        ds[id] = g;
+    __syncwarp();
+    for (int e = lane; e < p.E; e += 32)
+        out[e] = from_float<L>(__fdiv_rn(expf(to_float(row[e]) - top), total) * (ds[e] - dot));
+}
+
+// ---------------------------------------------------------------- order by expert
+//
+// A stable counting sort. The pairs are cut into one contiguous part per
+// block, a part into one run per warp. plan_count_kernel leaves each part's
+// count of every expert; plan_scatter_kernel adds the counts of the parts and
+// warps before it and hands out the rows in order, 32 pairs at a time. One
+// part needs no count kernel.
+
+constexpr int kPlanWarps = 8;
+constexpr int kPlanPart = 1024;      // pairs per block before more blocks are taken
+constexpr int kPlanMaxBlocks = 128;  // every block reads the counts of all: more cost more than they give
+
+__host__ __device__ inline int plan_blocks(long long pairs)
+{
+    const long long b = (pairs + kPlanPart - 1) / kPlanPart;
+    return static_cast<int>(b < 1 ? 1 : b > kPlanMaxBlocks ? kPlanMaxBlocks : b);
+}
+
+__global__ void __launch_bounds__(32 * kPlanWarps)
+    plan_count_kernel(const int *__restrict__ ids, long long pairs, long long part, int E, int *__restrict__ counts)
+{
+    extern __shared__ int plan_smem[];
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+        plan_smem[e] = 0;
+    __syncthreads();
+    const long long lo = blockIdx.x * part, hi = min(lo + part, pairs);
+    for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x) {
+        const int e = ids[i];
+        if (e >= 0 && e < E)
+            atomicAdd(&plan_smem[e], 1);  // a count: the order of the additions does not show
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+        counts[static_cast<long long>(blockIdx.x) * E + e] = plan_smem[e];
+}
+
+// Shared memory: kPlanWarps x E counts, then E totals.
+__global__ void __launch_bounds__(32 * kPlanWarps)
+    plan_scatter_kernel(const int *__restrict__ ids, long long pairs, long long part, int E, int k,
+                        const int *__restrict__ counts, int *__restrict__ offsets, int *__restrict__ slots,
+                        int *__restrict__ tokens)
+{
+    extern __shared__ int plan_smem[];
+    int *hist = plan_smem;                  // [warp][E]
+    int *start = plan_smem + kPlanWarps * E;  // first row of each expert
+    __shared__ int warp_total[kPlanWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long lo = blockIdx.x * part, hi = min(lo + part, pairs);
+    const long long run = (((hi > lo ? hi - lo : 0) + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+    const long long wlo = min(lo + warp * run, hi), whi = min(wlo + run, hi);
+    for (int i = tid; i < kPlanWarps * E; i += blockDim.x)
+        hist[i] = 0;
+    __syncthreads();
+    for (long long i = wlo + lane; i < whi; i += 32) {
+        const int e = ids[i];
+        if (e >= 0 && e < E)
+            atomicAdd(&hist[warp * E + e], 1);
+    }
+    __syncthreads();
+    // totals of every expert, and of the parts before this one
+    int before[(GEMM_ROUTE_MAX_EXPERTS + 32 * kPlanWarps - 1) / (32 * kPlanWarps)];
+    int r = 0;
+    for (int e = tid; e < E; e += blockDim.x, ++r) {
+        int total = 0, prior = 0;
+        if (gridDim.x == 1) {
+            for (int w = 0; w < kPlanWarps; ++w)
+                total += hist[w * E + e];
+        } else {
+            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+                const int c = __ldg(counts + static_cast<long long>(b) * E + e);
+                total += c;
+                prior += b < static_cast<int>(blockIdx.x) ? c : 0;
+            }
+        }
+        start[e] = total;
+        before[r] = prior;
+    }
+    __syncthreads();
+    // exclusive scan of the totals: each warp takes a run of experts, one lane
+    // a part of it
+    const int per = (E + 32 * kPlanWarps - 1) / (32 * kPlanWarps);
+    const int e0 = min(tid * per, E), e1 = min(e0 + per, E);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e)
+        sum += start[e];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += v;
+    }
+    if (lane == 31)
+        warp_total[warp] = incl;
+    __syncthreads();
+    int base = incl - sum, kept = 0;
+    for (int w = 0; w < kPlanWarps; ++w) {
+        if (w < warp)
+            base += warp_total[w];
+        kept += warp_total[w];
+    }
+    for (int e = e0; e < e1; ++e) {
+        const int n = start[e];
+        start[e] = base;
+        base += n;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int e = tid; e < E; e += blockDim.x)
+            offsets[e] = start[e];
+        if (tid == 0)
+            offsets[E] = kept;
+    }
+    // first row of each warp's pairs of each expert
+    r = 0;
+    for (int e = tid; e < E; e += blockDim.x, ++r) {
+        int at = start[e] + before[r];
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int n = hist[w * E + e];
+            hist[w * E + e] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    int *mine = hist + warp * E;
+    for (long long i0 = wlo; i0 < whi; i0 += 32) {
+        const long long i = i0 + lane;
+        int e = i < whi ? ids[i] : -1;
+        if (e < 0 || e >= E)
+            e = -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        int slot = -1;
+        if (e >= 0)
+            slot = mine[e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0 && (same >> lane) == 1u)  // the last of its expert moves the count on
+            mine[e] = slot + 1;
+        __syncwarp();
+        if (i < whi) {
+            slots[i] = slot;
+            if (slot >= 0)
+                tokens[slot] = static_cast<int>(i / k);
+        }
+    }
+    // rows that no pair has
+    for (long long i = kept + static_cast<long long>(blockIdx.x) * blockDim.x + tid; i < pairs;
+         i += static_cast<long long>(gridDim.x) * blockDim.x)
+        tokens[i] = -1;
+}
+
+// ---------------------------------------------------------------- quantisation
+
+struct QuantParams {
+    long long M;
+    int K;
+    const int *index;
+    long long x_rows, ldx, ldq;
+    float *scales;
+};
+
+constexpr int kQuantMaxThreads = 512;
+
+template <typename X, bool GATED, bool WIDE>
+__device__ __forceinline__ void quant_load8(const X *row, int c, int K, float (&v)[8])
+{
+    const int n = K - c;
+    if (n <= 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = 0.0f;
+        return;
+    }
+    load8<X, WIDE>(row + c, n, v);
+    if constexpr (GATED) {
+        float u[8];
+        load8<X, WIDE>(row + K + c, n, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)  // silu(gate) * up
+            v[i] = __fmul_rn(__fdiv_rn(v[i], 1.0f + expf(-v[i])), u[i]);
+    }
+}
+
+__device__ __forceinline__ void quant_store8(int8_t *q, int n, bool wide, const float (&v)[8], float scale)
+{
+    int b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        b[i] = max(-127, min(127, __float2int_rn(__fdiv_rn(v[i], scale))));
+    if (wide) {
+        const uint32_t lo = (b[0] & 0xFF) | (b[1] & 0xFF) << 8 | (b[2] & 0xFF) << 16 | static_cast<uint32_t>(b[3]) << 24;
+        const uint32_t hi = (b[4] & 0xFF) | (b[5] & 0xFF) << 8 | (b[6] & 0xFF) << 16 | static_cast<uint32_t>(b[7]) << 24;
+        *reinterpret_cast<uint2 *>(q) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                q[i] = static_cast<int8_t>(b[i]);
+    }
+}
+
+// One block per row, CH chunks of 8 elements a thread kept in registers
+// between the maximum and the rounding (CH 0: rows too long for that are read
+// twice, the second time from L2). WIDE: 16-byte loads and 8-byte stores.
+template <typename X, bool GATED, bool WIDE, int CH>
+__global__ void __launch_bounds__(kQuantMaxThreads)
+    quantize_kernel(const X *__restrict__ x, int8_t *__restrict__ q, const QuantParams p)
+{
+    const long long m = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float warp_top[kQuantMaxThreads / 32];
+    __shared__ int any_bad;
+    if (tid == 0)
+        any_bad = 0;
+    const long long r = p.index ? p.index[m] : m;
+    const bool live = r >= 0 && r < p.x_rows;
+    const int K = live ? p.K : 0;
+    const X *row = x + (live ? r : 0) * p.ldx;
+    float v[CH ? CH : 1][8];
+    float top = 0.0f;
+    bool bad = false;
+    const int step = 8 * blockDim.x;
+    __syncthreads();
+    if constexpr (CH > 0) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            quant_load8<X, GATED, WIDE>(row, 8 * tid + c * step, K, v[c]);
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                top = fmaxf(top, fabsf(v[c][i]));
+                bad |= !(fabsf(v[c][i]) < INFINITY);
+            }
+    } else {
+        for (int c = 8 * tid; c < K; c += step) {
+            quant_load8<X, GATED, WIDE>(row, c, K, v[0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                top = fmaxf(top, fabsf(v[0][i]));
+                bad |= !(fabsf(v[0][i]) < INFINITY);
+            }
+        }
+    }
+    top = warp_max(top);
+    if (lane == 0)
+        warp_top[warp] = top;
+    if (bad)
+        any_bad = 1;
+    __syncthreads();
+    bad = any_bad != 0;
+    top = 0.0f;
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w)
+        top = fmaxf(top, warp_top[w]);
+    const float scale = __fdiv_rn(top, 127.0f);
+    // a scale that is 0 (also: rounded to 0) divides by 1 and leaves zeros
+    const float by = bad || scale == 0.0f ? 1.0f : scale;
+    if (tid == 0)
+        p.scales[m] = bad ? NAN : scale;
+    int8_t *out = q + m * p.ldq;
+    if constexpr (CH > 0) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int at = 8 * tid + c * step;
+            if (at < p.K) {
+                if (bad) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[c][i] = 0.0f;
+                }
+                quant_store8(out + at, p.K - at, WIDE, v[c], by);
+            }
+        }
+    } else {
+        for (int at = 8 * tid; at < p.K; at += step) {
+            quant_load8<X, GATED, WIDE>(row, at, K, v[0]);
+            if (bad) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[0][i] = 0.0f;
+            }
+            quant_store8(out + at, p.K - at, WIDE, v[0], by);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- weighted sums
+
+struct CombineParams {
+    long long T;
+    int N, k;
+    long long y_rows, ldy, ldd;
+    const int *slots;
+    const float *weights;
+};
+
+constexpr int kCombineThreads = 128;
+
+// One block per token and 1024 columns; each thread sums 8 columns over the k
+// rows, two of which are in flight at a time.
+template <typename Y, typename D, bool WIDE>
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_kernel(const Y *__restrict__ y, D *__restrict__ d, const CombineParams p, int col_blocks)
+{
+    const long long t = blockIdx.x / col_blocks;
+    const int c = static_cast<int>(blockIdx.x % col_blocks) * (8 * kCombineThreads) + 8 * threadIdx.x;
+    if (c >= p.N)
+        return;
+    const int *slots = p.slots + t * p.k;
+    const float *weights = p.weights + t * p.k;
+    float acc[8] = {};
+#pragma unroll 4
+    for (int j = 0; j < p.k; ++j) {
+        const int r = __ldg(slots + j);
+        if (r >= 0 && r < p.y_rows) {
+            const float w = __ldg(weights + j);
+            float v[8];
+            load8<Y, WIDE>(y + r * p.ldy + c, p.N - c, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc[i] = fmaf(w, v[i], acc[i]);
+        }
+    }
+    store8<D, WIDE>(d + t * p.ldd + c, p.N - c, acc);
+}
+
+struct CombineGradParams {
+    long long T;
+    int N, k;
+    long long y_rows, ldy, lddy, lddd;
+    const int *slots;
+    const float *weights;
+    float *dweights;
+};
+
+constexpr int kCombineGradWarps = 8;
+
+// One warp per (token, choice) pair: it walks the N columns once, writing the
+// row of dY and summing the dot product; a token's warps share dD's row in L1.
+template <typename Y, typename D, bool WIDE>
+__global__ void __launch_bounds__(32 * kCombineGradWarps)
+    combine_backward_kernel(const D *__restrict__ dd, const Y *__restrict__ y, Y *__restrict__ dy,
+                            const CombineGradParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const long long pair = static_cast<long long>(blockIdx.x) * kCombineGradWarps + (threadIdx.x >> 5);
+    if (pair >= p.T * p.k)
+        return;
+    const long long t = pair / p.k;
+    const int r = p.slots[pair];
+    float dot = 0.0f;
+    if (r >= 0 && r < p.y_rows) {
+        const float w = p.weights[pair];
+        const D *g = dd + t * p.lddd;
+        const Y *yr = y + r * p.ldy;
+        Y *o = dy + r * p.lddy;
+#pragma unroll 4
+        for (int c = 8 * lane; c < p.N; c += 256) {
+            float a[8], b[8];
+            load8<D, WIDE>(g + c, p.N - c, a);
+            load8<Y, WIDE>(yr + c, p.N - c, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dot = fmaf(a[i], b[i], dot);
+                b[i] = w * a[i];
+            }
+            store8<Y, WIDE>(o + c, p.N - c, b);
+        }
+    }
+    dot = warp_sum(dot);
+    if (lane == 0)
+        p.dweights[pair] = dot;
+}
+
+// ---------------------------------------------------------------- host
+
+// Calls fn with a value of the element type `type` names.
+template <typename F>
+gemm_status_t with_type(int type, F fn)
+{
+    switch (type) {
+    case GEMM_OUT_F32: return fn(float());
+    case GEMM_OUT_BF16: return fn(__nv_bfloat16());
+    case GEMM_OUT_F16: return fn(__half());
+    }
+    return GEMM_ERR_INVALID_ARG;
+}
+
+// The rule of a call with its defaults filled in; false if it makes no sense for E experts and k choices.
+bool route_rule(const gemm_route_t *route, int64_t E, int k, gemm_route_t *r)
+{
+    gemm_route_t d = {};
+    *r = route ? *route : d;
+    if (r->score != GEMM_ROUTE_SOFTMAX && r->score != GEMM_ROUTE_SIGMOID)
+        return false;
+    if (r->groups < 0 || r->group_top < 0 || r->group_top > 2 || r->groups_kept < 0 || !std::isfinite(r->scale))
+        return false;
+    if (r->scale == 0.0f)
+        r->scale = 1.0f;
+    if (r->groups == 0)
+        r->groups = 1;
+    if (r->group_top == 0)
+        r->group_top = 1;
+    if (E < 1 || E > GEMM_ROUTE_MAX_EXPERTS || k < 1 || k > GEMM_ROUTE_MAX_K || k > E)
+        return false;
+    if (r->groups > 1) {
+        if (r->groups > 32 || E % r->groups != 0 || r->groups_kept < 1 || r->groups_kept > r->groups)
+            return false;
+        const int64_t per = E / r->groups;
+        if (r->group_top > per || k > per * r->groups_kept)
+            return false;
+    }
+    return true;
+}
+
+template <typename L, int NPL>
+gemm_status_t launch_route(const void *logits, const RouteParams &p, cudaStream_t st)
+{
+    const long long blocks = (p.T + kRouteWarps - 1) / kRouteWarps;
+    const size_t smem = p.groups > 1 ? sizeof(float) * kRouteWarps * p.groups * (p.per | 1) : 0;
+    route_kernel<L, NPL><<<static_cast<unsigned>(blocks), 32 * kRouteWarps, smem, st>>>(static_cast<const L *>(logits), p);
+    return host_launched();
+}
+
+template <typename X, bool GATED>
+gemm_status_t launch_quantize(const void *x, int8_t *q, const QuantParams &p, cudaStream_t st)
+{
+    const bool wide = aligned_to(x, 16) && aligned_to(q, 8) && p.ldx * static_cast<int64_t>(sizeof(X)) % 16 == 0 &&
+                      p.ldq % 8 == 0 && p.K % 8 == 0;
+    const int chunks = (p.K + 7) / 8;
+    const int ch = chunks <= kQuantMaxThreads / 2 ? 1 : chunks <= 2 * kQuantMaxThreads ? 2 : chunks <= 4 * kQuantMaxThreads ? 4 : 0;
+    int threads = kQuantMaxThreads;
+    if (ch > 0)
+        threads = std::max(32, ((chunks + ch - 1) / ch + 31) / 32 * 32);
+    const X *xp = static_cast<const X *>(x);
+    const unsigned grid = static_cast<unsigned>(p.M);
+#define G300_QUANT(W, C) quantize_kernel<X, GATED, W, C><<<grid, threads, 0, st>>>(xp, q, p)
+    if (wide) {
+        if (ch == 1)
+            G300_QUANT(true, 1);
+        else if (ch == 2)
+            G300_QUANT(true, 2);
+        else if (ch == 4)
+            G300_QUANT(true, 4);
+        else
+            G300_QUANT(true, 0);
+    } else {
+        G300_QUANT(false, 0);
+    }
+#undef G300_QUANT
+    return host_launched();
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- C ABI
+
+extern "C" {
+
+gemm_status_t gemm_route(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl, const float *bias,
+                         int k, const gemm_route_t *route, float *weights, int32_t *ids, gemm_stream_t stream)
+{
+    gemm_route_t r;
+    if (!valid_size(T) || !valid_type(l_type) || !route_rule(route, E, k, &r))
+        return GEMM_ERR_INVALID_ARG;
+    if (T == 0)
+        return GEMM_OK;
+    const int es = type_bytes(l_type);
+    if (!logits || !weights || !ids || ldl < E || !valid_stride(ldl, es))
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned_to(logits, es) || !aligned_to(weights, 4) || !aligned_to(ids, 4) || !aligned_to(bias, 4))
+        return GEMM_ERR_ALIGNMENT;
+    RouteParams p = {};
+    p.T = T;
+    p.E = static_cast<int>(E);
+    p.k = k;
+    p.ldl = ldl;
+    p.bias = bias;
+    p.weights = weights;
+    p.ids = ids;
+    p.sigmoid = r.score == GEMM_ROUTE_SIGMOID;
+    p.groups = r.groups;
+    p.per = static_cast<int>(E) / r.groups;
+    p.group_top = r.group_top;
+    p.groups_kept = r.groups_kept;
+    p.renorm = r.renormalize != 0;
+    p.scale = r.scale;
+    p.per_inv = p.per > 1 ? static_cast<unsigned int>(((uint64_t(1) << 32) + p.per - 1) / p.per) : 0u;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return with_type(l_type, [&](auto tag) {
+        using L = decltype(tag);
+        return E <= 32    ? launch_route<L, 1>(logits, p, st)
+               : E <= 64  ? launch_route<L, 2>(logits, p, st)
+               : E <= 128 ? launch_route<L, 4>(logits, p, st)
+               : E <= 256 ? launch_route<L, 8>(logits, p, st)
+               : E <= 512 ? launch_route<L, 16>(logits, p, st)
+                          : launch_route<L, 32>(logits, p, st);
+    });
+}
+
+gemm_status_t gemm_route_backward(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl, int k,
+                                  const gemm_route_t *route, const int32_t *ids, const float *dweights, void *dlogits,
+                                  int64_t lddl, gemm_stream_t stream)
+{
+    gemm_route_t r;
+    if (!valid_size(T) || !valid_type(l_type) || !route_rule(route, E, k, &r))
+        return GEMM_ERR_INVALID_ARG;
+    if (T == 0)
+        return GEMM_OK;
+    const int es = type_bytes(l_type);
+    if (!logits || !ids || !dweights || !dlogits || ldl < E || lddl < E || !valid_stride(ldl, es) ||
+        !valid_stride(lddl, es))
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !aligned_to(ids, 4) || !aligned_to(dweights, 4))
+        return GEMM_ERR_ALIGNMENT;
+    RouteGradParams p = {};
+    p.T = T;
+    p.E = static_cast<int>(E);
+    p.k = k;
+    p.ldl = ldl;
+    p.lddl = lddl;
+    p.ids = ids;
+    p.dweights = dweights;
+    p.sigmoid = r.score == GEMM_ROUTE_SIGMOID;
+    p.renorm = r.renormalize != 0;
+    p.scale = r.scale;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return with_type(l_type, [&](auto tag) {
+        using L = decltype(tag);
+        const unsigned blocks = static_cast<unsigned>((T + kRouteWarps - 1) / kRouteWarps);
+        route_backward_kernel<L><<<blocks, 32 * kRouteWarps, sizeof(float) * kRouteWarps * E, st>>>(
+            static_cast<const L *>(logits), static_cast<L *>(dlogits), p);
+        return host_launched();
+    });
+}
+
+size_t gemm_route_plan_workspace_size(int64_t T, int64_t E, int k)
+{
+    if (T <= 0 || E < 1 || E > GEMM_ROUTE_MAX_EXPERTS || k < 1 || k > GEMM_ROUTE_MAX_K || T > kSizeLimit)
+        return 0;
+    const int blocks = plan_blocks(T * k);
+    return blocks > 1 ? static_cast<size_t>(blocks) * static_cast<size_t>(E) * sizeof(int32_t) : 0;
+}
+
+gemm_status_t gemm_route_plan(int64_t T, int64_t E, int k, const int32_t *ids, int32_t *offsets, int32_t *slots,
+                              int32_t *tokens, void *workspace, size_t workspace_bytes, gemm_stream_t stream)
+{
+    if (!valid_size(T) || E < 1 || E > GEMM_ROUTE_MAX_EXPERTS || k < 1 || k > GEMM_ROUTE_MAX_K || T * k > kSizeLimit)
+        return GEMM_ERR_INVALID_ARG;
+    if (!offsets || (T > 0 && (!ids || !slots || !tokens)))
+        return GEMM_ERR_INVALID_ARG;
+    const size_t need = gemm_route_plan_workspace_size(T, E, k);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned_to(ids, 4) || !aligned_to(offsets, 4) || !aligned_to(slots, 4) || !aligned_to(tokens, 4) ||
+        (need > 0 && !aligned_to(workspace, 4)))
+        return GEMM_ERR_ALIGNMENT;
+    const int64_t pairs = T * k;
+    const int blocks = plan_blocks(pairs);
+    const long long part = (pairs + blocks - 1) / blocks;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    int *counts = static_cast<int *>(workspace);
+    int launched = 0;
+    if (blocks > 1) {
+        plan_count_kernel<<<blocks, 32 * kPlanWarps, E * sizeof(int), st>>>(ids, pairs, part, static_cast<int>(E), counts);
+        if (cudaPeekAtLastError() == cudaSuccess)
+            ++launched;
+    }
+    plan_scatter_kernel<<<blocks, 32 * kPlanWarps, (kPlanWarps + 1) * E * sizeof(int), st>>>(
+        ids, pairs, part, static_cast<int>(E), k, counts, offsets, slots, tokens);
+    return host_launched(launched + 1);
+}
+
+gemm_status_t gemm_quantize_int8(int64_t M, int64_t K, const void *X, gemm_out_t x_type, int64_t x_rows, int64_t ldx,
+                                 const int32_t *index, gemm_quant_t mode, int8_t *Q, int64_t ldq, float *scales,
+                                 gemm_stream_t stream)
+{
+    if (!valid_size(M) || !valid_size(K) || !valid_size(x_rows) || !valid_type(x_type) ||
+        (mode != GEMM_QUANT_PLAIN && mode != GEMM_QUANT_GATED))
+        return GEMM_ERR_INVALID_ARG;
+    if (M == 0)
+        return GEMM_OK;
+    const bool gated = mode == GEMM_QUANT_GATED;
+    const int es = type_bytes(x_type);
+    if (!scales || (!index && x_rows < M))
+        return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!Q || (x_rows > 0 && !X) || ldx < (gated ? 2 * K : K) || ldq < K || !valid_stride(ldx, es) ||
+                  !valid_stride(ldq, 1)))
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned_to(X, es) || !aligned_to(index, 4) || !aligned_to(scales, 4))
+        return GEMM_ERR_ALIGNMENT;
+    QuantParams p = {};
+    p.M = M;
+    p.K = static_cast<int>(K);
+    p.index = index;
+    p.x_rows = x_rows;
+    p.ldx = ldx;
+    p.ldq = ldq;
+    p.scales = scales;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return with_type(x_type, [&](auto tag) {
+        using X_ = decltype(tag);
+        return gated ? launch_quantize<X_, true>(X, Q, p, st) : launch_quantize<X_, false>(X, Q, p, st);
+    });
+}
+
+gemm_status_t gemm_route_combine(int64_t T, int64_t N, int k, const void *Y, gemm_out_t y_type, int64_t y_rows,
+                                 int64_t ldy, const int32_t *slots, const float *weights, void *D, gemm_out_t d_type,
+                                 int64_t ldd, gemm_stream_t stream)
+{
+    if (!valid_size(T) || !valid_size(N) || !valid_size(y_rows) || k < 1 || k > GEMM_ROUTE_MAX_K ||
+        !valid_type(y_type) || !valid_type(d_type))
+        return GEMM_ERR_INVALID_ARG;
+    if (T == 0 || N == 0)
+        return GEMM_OK;
+    const int ey = type_bytes(y_type), ed = type_bytes(d_type);
+    if ((y_rows > 0 && !Y) || !slots || !weights || !D || ldy < N || ldd < N || !valid_stride(ldy, ey) ||
+        !valid_stride(ldd, ed))
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned_to(Y, ey) || !aligned_to(D, ed) || !aligned_to(slots, 4) || !aligned_to(weights, 4))
+        return GEMM_ERR_ALIGNMENT;
+    const int64_t col_blocks = (N + 8 * kCombineThreads - 1) / (8 * kCombineThreads);
+    if (col_blocks * T > kSizeLimit)
+        return GEMM_ERR_UNSUPPORTED;
+    CombineParams p = {};
+    p.T = T;
+    p.N = static_cast<int>(N);
+    p.k = k;
+    p.y_rows = y_rows;
+    p.ldy = ldy;
+    p.ldd = ldd;
+    p.slots = slots;
+    p.weights = weights;
+    const bool wide = N % 8 == 0 && aligned_to(Y, 16) && aligned_to(D, 16) && ldy * ey % 16 == 0 && ldd * ed % 16 == 0;
+    const unsigned grid = static_cast<unsigned>(col_blocks * T);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return with_type(y_type, [&](auto ytag) {
+        using Y_ = decltype(ytag);
+        return with_type(d_type, [&](auto dtag) {
+            using D_ = decltype(dtag);
+            const Y_ *yp = static_cast<const Y_ *>(Y);
+            D_ *dp = static_cast<D_ *>(D);
+            if (wide)
+                combine_kernel<Y_, D_, true><<<grid, kCombineThreads, 0, st>>>(yp, dp, p, static_cast<int>(col_blocks));
+            else
+                combine_kernel<Y_, D_, false><<<grid, kCombineThreads, 0, st>>>(yp, dp, p, static_cast<int>(col_blocks));
+            return host_launched();
+        });
+    });
+}
+
+gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const void *dD, gemm_out_t d_type, int64_t lddd,
+                                          const void *Y, gemm_out_t y_type, int64_t y_rows, int64_t ldy,
+                                          const int32_t *slots, const float *weights, void *dY, int64_t lddy,
+                                          float *dweights, gemm_stream_t stream)
+{
+    if (!valid_size(T) || !valid_size(N) || !valid_size(y_rows) || k < 1 || k > GEMM_ROUTE_MAX_K ||
+        !valid_type(y_type) || !valid_type(d_type) || T * k > kSizeLimit)
+        return GEMM_ERR_INVALID_ARG;
+    if (T == 0)
+        return GEMM_OK;
+    const int ey = type_bytes(y_type), ed = type_bytes(d_type);
+    if (!slots || !weights || !dweights || (N > 0 && !dD) || (N > 0 && y_rows > 0 && (!Y || !dY)) || lddd < N ||
+        ldy < N || lddy < N || !valid_stride(lddd, ed) || !valid_stride(ldy, ey) || !valid_stride(lddy, ey))
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned_to(dD, ed) || !aligned_to(Y, ey) || !aligned_to(dY, ey) || !aligned_to(slots, 4) ||
+        !aligned_to(weights, 4) || !aligned_to(dweights, 4))
+        return GEMM_ERR_ALIGNMENT;
+    CombineGradParams p = {};
+    p.T = T;
+    p.N = static_cast<int>(N);
+    p.k = k;
+    p.y_rows = y_rows;
+    p.ldy = ldy;
+    p.lddy = lddy;
+    p.lddd = lddd;
+    p.slots = slots;
+    p.weights = weights;
+    p.dweights = dweights;
+    const bool wide = N % 8 == 0 && aligned_to(dD, 16) && aligned_to(Y, 16) && aligned_to(dY, 16) &&
+                      lddd * ed % 16 == 0 && ldy * ey % 16 == 0 && lddy * ey % 16 == 0;
+    const unsigned grid = static_cast<unsigned>((T * k + kCombineGradWarps - 1) / kCombineGradWarps);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return with_type(y_type, [&](auto ytag) {
+        using Y_ = decltype(ytag);
+        return with_type(d_type, [&](auto dtag) {
+            using D_ = decltype(dtag);
+            const D_ *gp = static_cast<const D_ *>(dD);
+            const Y_ *yp = static_cast<const Y_ *>(Y);
+            Y_ *op = static_cast<Y_ *>(dY);
+            if (wide)
+                combine_backward_kernel<Y_, D_, true><<<grid, 32 * kCombineGradWarps, 0, st>>>(gp, yp, op, p);
+            else
+                combine_backward_kernel<Y_, D_, false><<<grid, 32 * kCombineGradWarps, 0, st>>>(gp, yp, op, p);
+            return host_launched();
+        });
+    });
+}
+
+}  // extern "C"

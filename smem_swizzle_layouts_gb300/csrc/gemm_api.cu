@@ -13,6 +13,7 @@
 
 #include "../../include/gemm_gb300.h"
 #include "gemm_kernel.cuh"
+#include "host.h"
 #include "launch.cuh"
 #include "variants.h"
 
@@ -1001,6 +1002,41 @@ gemm_status_t run_grouped_noalloc(int in_bf16, const gemm_problem_t *probs, int 
 }
 
 }  // namespace
+
+// ---------------------------------------------------------------- services of the other units
+
+namespace g300 {
+
+gemm_status_t host_device(int *dev, unsigned int **status, int *sms) { return device_state(dev, status, sms); }
+
+gemm_status_t host_encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *ptr,
+                                const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+                                CUtensorMapSwizzle swz)
+{
+    cuuint64_t d[3], st[2];
+    cuuint32_t b[3], estr[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i > 0)
+            st[i - 1] = strides[i - 1];
+    }
+    const CUresult r = g_encode(map, dt, static_cast<cuuint32_t>(rank), const_cast<void *>(ptr), d, st, b, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+}
+
+int host_take_injection(int *timeout_ms)
+{
+    const int ms = g_inject_timeout_ms.exchange(0);
+    *timeout_ms = ms;
+    return ms > 0 ? g_inject_role.load() : 0;
+}
+
+void host_count_launches(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
+
+}  // namespace g300
 
 // ---------------------------------------------------------------- C ABI
 
