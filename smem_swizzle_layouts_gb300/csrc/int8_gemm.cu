@@ -13,11 +13,25 @@
 // are the MMA's M and the rows of A (tokens) its N, so that a tile of few
 // tokens still uses whole 128-row MMAs and reads every weight once.
 //
+// Widened channels go to Tensor Memory, from where the MMA takes its first
+// operand, widened tokens to shared memory. With both in shared memory a
+// 128 x 256 tile moves 288 bytes of shared memory per MMA cycle (raw writes and
+// reads, fp16 writes, MMA reads) where an SM moves 128, which held the product
+// at 0.44 of the tensor rate; with the channels in Tensor Memory and CTA pairs
+// (each CTA widens its 128 channels and half of the tokens of a 256-channel
+// tile) it is 135 bytes.
+//
 // Warp roles of a CTA:
-//   warp 0      TMA producer: raw int8 stages of 128 elements of K;
-//   warp 1      TMEM allocator and MMA issuer;
-//   warps 2-5   epilogue: accumulator (lane = channel, column = token) to D;
-//   warps 6-13  converters: raw stages to fp16 stages of 64 elements of K.
+//   warp 0       TMA producer: raw int8 stages of 128 elements of K;
+//   warp 1       TMEM allocator and MMA issuer (pairs: of the even CTA);
+//   warps 2-5    epilogue: accumulator (lane = channel, column = token) to D,
+//                double-buffered against the next tile's MMAs;
+//   warps 6-21   converters in two groups of 8 warps that take alternate
+//                stages; a group reads and widens a stage into registers
+//                before it waits for room to write it.
+// For few tokens and few tiles a cluster of CTAs shares one tile's K
+// (KS > 1): the others leave their fp32 sums in the first CTA's shared memory,
+// which adds them in the order of their ranks.
 // Every wait is bounded, as in gemm_kernel.cuh.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -35,17 +49,18 @@
 
 namespace g300 {
 
-constexpr int kI8Channels = 128;  // rows of B per tile (MMA M)
-constexpr int kI8RawK = 128;      // elements of K per raw stage: one 128-byte swizzled row
-constexpr int kI8ConvK = 64;      // elements of K per fp16 stage: one 128-byte swizzled row
-constexpr int kI8ConvWarps = 8;
-constexpr int kI8FirstConvWarp = 6;
-constexpr int kI8Threads = 32 * (kI8FirstConvWarp + kI8ConvWarps);
+constexpr int kI8Channels = 128;  // rows of B per CTA (MMA M per CTA)
+constexpr int kI8K = 128;         // elements of K per stage: one 128-byte swizzled int8 row, two fp16 ones
+constexpr int kI8GroupWarps = 8;  // converter warps per group
+constexpr int kI8FirstConvWarp = 2 + kEpiWarps;
+constexpr int kI8Threads = 32 * (kI8FirstConvWarp + 2 * kI8GroupWarps);
+constexpr int kI8MaxSmem = 232448;
 
 enum : uint32_t {
     kRoleConvert = 6,
     kWaitRawFull = 11 << 8,
     kWaitConvEmpty = 12 << 8,
+    kWaitSplit = 13 << 8,
 };
 
 struct I8Params {
@@ -62,25 +77,39 @@ struct I8Params {
     unsigned int *status;
 };
 
-// BT: tokens per tile (MMA N).
-template <int BT>
+// CG: CTAs sharing a tile of CG x 128 channels as a pair. BT: tokens per tile
+// (MMA N). KS: most CTAs sharing one tile's K (1: none do).
+template <int CG, int BT, int KS>
 struct I8Cfg {
-    static constexpr int RAW_STAGES = BT >= 256 ? 2 : BT >= 128 ? 3 : 5;
-    static constexpr int CONV_STAGES = 2;
-    static constexpr int RAW_W = kI8Channels * kI8RawK;
-    static constexpr int RAW_BYTES = RAW_W + BT * kI8RawK;
-    static constexpr int CONV_W = kI8Channels * kI8ConvK * 2;
-    static constexpr int CONV_BYTES = CONV_W + BT * kI8ConvK * 2;
+    static constexpr int TOK = BT / CG;  // tokens widened by each CTA
+    static constexpr int CH = CG * kI8Channels;
+    static constexpr int ACC_STRIDE = BT < 32 ? 32 : BT;  // whole 32-column epilogue reads
+    static constexpr int A_COL0 = 2 * ACC_STRIDE;         // widened channels: 64 columns a stage
+    static constexpr int A_COLS = kI8K / 2;
+    static constexpr int CONV_FIT = (512 - A_COL0) / A_COLS;
+    static constexpr int CONV_MOST = TOK >= 128 || (KS > 1 && BT >= 64) ? 2 : 4;  // what shared memory has room for
+    static constexpr int CONV_STAGES = CONV_FIT < CONV_MOST ? CONV_FIT : CONV_MOST;
+    static constexpr int RAW_W = kI8Channels * kI8K;
+    static constexpr int RAW_BYTES = RAW_W + TOK * kI8K;
+    static constexpr int CONV_BYTES = 2 * TOK * kI8K;  // two tiles of 64 elements of K
+    static constexpr int PART_BYTES = (KS - 1) * BT * kI8Channels * 4;
+    static constexpr int FIXED = CONV_STAGES * CONV_BYTES + PART_BYTES + 1024 /* alignment */ + 512 /* barriers */ +
+                                 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1);
+    static constexpr int RAW_FIT = (kI8MaxSmem - FIXED) / RAW_BYTES;
+    static constexpr int RAW_STAGES = RAW_FIT < 8 ? RAW_FIT : 8;
     static constexpr int CONV_OFF = RAW_STAGES * RAW_BYTES;
-    static constexpr int BAR_OFF = CONV_OFF + CONV_STAGES * CONV_BYTES;
-    static constexpr int NUM_BARS = 2 * RAW_STAGES + 2 * CONV_STAGES + 4 + 2;
+    static constexpr int PART_OFF = CONV_OFF + CONV_STAGES * CONV_BYTES;
+    static constexpr int BAR_OFF = PART_OFF + PART_BYTES;
+    static constexpr int NUM_BARS = 2 * RAW_STAGES + 2 * CONV_STAGES + 4 + 3;
     static constexpr int MISC_OFF = BAR_OFF + 8 * NUM_BARS;
-    static constexpr int SMEM_BASE = MISC_OFF + 16 + 1024;  // 1024: room to align the base
-    static constexpr int ACC_STRIDE = BT < 32 ? 32 : BT;    // whole 32-column epilogue reads
-    static constexpr int TMEM_COLS = 2 * ACC_STRIDE;
-    static_assert(RAW_BYTES % 1024 == 0 && CONV_BYTES % 1024 == 0, "swizzle atoms start on 1024-byte boundaries");
-    static_assert(BT % 16 == 0 && BT <= 256, "MMA N with M = 128: a multiple of 16");
-    static_assert(SMEM_BASE + 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1) <= 232448, "shared memory per CTA");
+    static constexpr int TABLE_OFF = MISC_OFF + 16;
+    static constexpr int CLUSTER = CG * KS;  // largest cluster
+    static constexpr int UNITS = (TOK * 8 + 32 * kI8GroupWarps - 1) / (32 * kI8GroupWarps);  // token units per thread
+    static_assert(CG == 1 || KS == 1, "pairs do not share K");
+    static_assert(8 * NUM_BARS + 16 <= 512, "barriers");
+    static_assert(RAW_BYTES % 1024 == 0 && CONV_BYTES % 1024 == 0 && TOK * kI8K % 1024 == 0,
+                  "swizzle atoms start on 1024-byte boundaries");
+    static_assert(BT % (16 * CG) == 0 && BT <= 256 && CONV_STAGES >= 2 && RAW_STAGES >= 3, "tile");
 };
 
 // ---------------------------------------------------------------- tiles
@@ -107,7 +136,7 @@ struct I8Sched {
     const int *tile_start;  // shared memory: experts + 1 first tiles
 };
 
-template <int BT>
+template <int BT, int CH>
 __device__ __forceinline__ I8Tile i8_tile(const I8Sched &s, int t)
 {
     I8Tile ti;
@@ -137,7 +166,7 @@ __device__ __forceinline__ I8Tile i8_tile(const I8Sched &s, int t)
     const int in_group = min(tiles_m - first, kI8GroupM);
     const int r = local - g * per_group;
     ti.m0 += (first + r % in_group) * BT;
-    ti.n0 = (r / in_group) * kI8Channels;
+    ti.n0 = (r / in_group) * CH;
     return ti;
 }
 
@@ -164,18 +193,51 @@ __device__ __forceinline__ void widen4(uint32_t q, uint32_t &lo, uint32_t &hi)
     hi = *reinterpret_cast<uint32_t *>(&y);
 }
 
-// One 16-byte unit of a raw row (unit c of row r of a 128-byte-swizzled int8
-// tile) to the two units it fills in row r of an fp16 tile.
-__device__ __forceinline__ void convert_unit(uint32_t raw, uint32_t conv, int r, int c_raw, int u)
+// Sixteen int8 to sixteen fp16, in order.
+__device__ __forceinline__ void widen16(const uint4 &q, uint32_t *h)
 {
-    const uint32_t key = static_cast<uint32_t>(r) & 7u;
-    uint32_t q[4], h[8];
-    ld_shared_v4(raw + r * 128 + ((static_cast<uint32_t>(c_raw) ^ key) << 4), q[0], q[1], q[2], q[3]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        widen4(q[i], h[2 * i], h[2 * i + 1]);
-    st_shared_v4(conv + r * 128 + ((static_cast<uint32_t>(u) ^ key) << 4), h[0], h[1], h[2], h[3]);
-    st_shared_v4(conv + r * 128 + ((static_cast<uint32_t>(u + 1) ^ key) << 4), h[4], h[5], h[6], h[7]);
+    widen4(q.x, h[0], h[1]);
+    widen4(q.y, h[2], h[3]);
+    widen4(q.z, h[4], h[5]);
+    widen4(q.w, h[6], h[7]);
+}
+
+// 32 lanes x 32 consecutive 32-bit columns of TMEM from registers.
+__device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+                 "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
+                 "%31, %32};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+                 "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+                 "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+                 : "memory");
+}
+
+// kind::f16 MMA with the first operand in TMEM (row = lane, two fp16 of K per
+// 32-bit column; a pair's CTAs each hold their own 128 rows).
+template <int CG>
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate)
+{
+    if constexpr (CG == 1)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                     : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 template <typename D>
@@ -196,19 +258,36 @@ __device__ __forceinline__ void store_scaled<__half>(__half *p, float v)
     *p = __float2half_rn(v);
 }
 
+// Scaled sums of one 32-token block, lane = channel n: D[m][n] for the block's
+// tokens that exist.
+template <typename D>
+__device__ __forceinline__ void store_block(D *out, long long ldd, const float (&v)[32], float sa, float sn, int rows, bool live)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float sm = __shfl_sync(0xffffffffu, sa, i);
+        if (live && i < rows)
+            store_scaled<D>(out + i * ldd, v[i] * sm * sn);
+    }
+}
+
 // ---------------------------------------------------------------- kernel
 
-template <int BT, typename D>
+template <int CG, int BT, int KS>
 __global__ void __launch_bounds__(kI8Threads, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ I8Params p)
+                     const __grid_constant__ I8Params p, const int ks)
 {
-    using C = I8Cfg<BT>;
+    using C = I8Cfg<CG, BT, KS>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw_addr);
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+    // a pair's CTAs, or the CTAs sharing a tile's K
+    const int cluster = CG == 2 ? 2 : KS > 1 ? ks : 1;
+    const int rank = C::CLUSTER > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int cluster_id = static_cast<int>(blockIdx.x) / cluster, clusters = static_cast<int>(gridDim.x) / cluster;
 
     const uint32_t bar_raw_full = base + C::BAR_OFF;
     const uint32_t bar_raw_empty = bar_raw_full + 8 * C::RAW_STAGES;
@@ -218,34 +297,36 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const uint32_t bar_acc_empty = bar_acc_full + 16;
     const uint32_t bar_drain = bar_acc_empty + 16;
     const uint32_t bar_inject = bar_drain + 8;
+    const uint32_t bar_part = bar_inject + 8;  // the other CTAs' sums have arrived (KS > 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + C::MISC_OFF + 4);
-    int *off = reinterpret_cast<int *>(smem + C::MISC_OFF + 16);
+    int *off = reinterpret_cast<int *>(smem + C::TABLE_OFF);
     int *tile_start = off + p.experts + 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::RAW_STAGES; ++s) {
             mbar_init(bar_raw_full + 8 * s, 1);
-            mbar_init(bar_raw_empty + 8 * s, kI8ConvWarps);
+            mbar_init(bar_raw_empty + 8 * s, kI8GroupWarps);
         }
         for (int s = 0; s < C::CONV_STAGES; ++s) {
-            mbar_init(bar_conv_full + 8 * s, kI8ConvWarps);
+            mbar_init(bar_conv_full + 8 * s, kI8GroupWarps * CG);
             mbar_init(bar_conv_empty + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_acc_full + 8 * b, 1);
-            mbar_init(bar_acc_empty + 8 * b, kEpiWarps);
+            mbar_init(bar_acc_empty + 8 * b, kEpiWarps * CG);
         }
         mbar_init(bar_drain, 1);
         mbar_init(bar_inject, 1);
+        mbar_init(bar_part, cluster > 1 ? kEpiWarps * (cluster - 1) : 1);
         *abort_flag = 0u;
         fence_mbar_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB);
     }
     if (warp == 1) {
-        tmem_alloc<1>(smem_u32(tmem_slot), C::TMEM_COLS);
-        tmem_relinquish<1>();
+        tmem_alloc<CG>(smem_u32(tmem_slot), 512);
+        tmem_relinquish<CG>();
     }
     if (warp == 2 && p.experts) {
         // clamped offsets and the first tile of each expert: a running
@@ -283,6 +364,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
     tc_fence_before_sync();
     __syncthreads();
+    if constexpr (C::CLUSTER > 1)
+        cluster_sync_all();  // the other CTAs' barriers exist before anything signals them
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
 
@@ -299,10 +382,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     sched.off = off;
     sched.tile_start = tile_start;
     sched.num_tiles = p.experts ? tile_start[p.experts] : i8_tiles(p.M, BT) * p.tiles_n;
-    const int raw_blocks = i8_tiles(p.K, kI8RawK);
-    // K past the end is zeros in the raw tiles; a last block of at most 64
-    // elements still fills both fp16 stages
-    const int conv_blocks = raw_blocks * (kI8RawK / kI8ConvK);
+    // this CTA's K blocks of a tile (zeros past the end of K)
+    const int all_blocks = i8_tiles(p.K, kI8K);
+    int kb0 = 0, kb1 = all_blocks;
+    if constexpr (KS > 1) {
+        kb0 = static_cast<int>(static_cast<long long>(all_blocks) * rank / cluster);
+        kb1 = static_cast<int>(static_cast<long long>(all_blocks) * (rank + 1) / cluster);
+    }
+    const int n_off = CG == 2 ? rank * kI8Channels : 0;  // this CTA's channels within the tile
 
     ProducerTail tail{0, 0, 0u};
     if (warp == 0) {
@@ -313,16 +400,17 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 int stage = 0, issued = 0;
                 uint32_t phase = 0;
                 bool ok = true;
-                for (int t = blockIdx.x; ok && t < sched.num_tiles; t += gridDim.x) {
-                    const I8Tile ti = i8_tile<BT>(sched, t);
-                    for (int kb = 0; kb < raw_blocks; ++kb) {
+                for (int t = cluster_id; ok && t < sched.num_tiles; t += clusters) {
+                    const I8Tile ti = i8_tile<BT, C::CH>(sched, t);
+                    const int m0 = ti.m0 + (CG == 2 ? rank * C::TOK : 0);
+                    for (int kb = kb0; kb < kb1; ++kb) {
                         ok = w.wait(bar_raw_empty + 8 * stage, phase ^ 1u, kRoleProducer | kWaitEmpty);
                         if (!ok)
                             break;
                         const uint32_t dst = base + stage * C::RAW_BYTES, bar = bar_raw_full + 8 * stage;
                         mbar_arrive_expect_tx(bar, C::RAW_BYTES);
-                        tma_load_3d(dst, &tmB, bar, kb * kI8RawK, ti.n0, ti.expert);
-                        tma_load_2d(dst + C::RAW_W, &tmA, bar, kb * kI8RawK, ti.m0);
+                        tma_load_3d(dst, &tmB, bar, kb * kI8K, ti.n0 + n_off, ti.expert);
+                        tma_load_2d(dst + C::RAW_W, &tmA, bar, kb * kI8K, m0);
                         ++issued;
                         if (++stage == C::RAW_STAGES) {
                             stage = 0;
@@ -334,32 +422,36 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && (CG == 1 || rank == 0)) {
             if (p.inject == kRoleMma)
                 w.wait(bar_inject, 0u, kRoleMma | kWaitInjected);
-            const uint32_t idesc = make_idesc_f16(kI8Channels, BT, 0, 0, 0);
-            const OperandPacking pk = operand_packing(0, 3, kI8Channels, kI8ConvK);
-            const uint64_t a_desc = make_smem_desc(base + C::CONV_OFF, pk.lbo, pk.sbo, pk.swz);
-            const uint64_t b_desc = make_smem_desc(base + C::CONV_OFF + C::CONV_W, pk.lbo, pk.sbo, pk.swz);
+            const uint32_t idesc = make_idesc_f16(CG * kI8Channels, BT, 0, 0, 0);
+            const OperandPacking pk = operand_packing(0, 3, C::TOK, kI8K / 2);
+            const uint64_t b_desc = make_smem_desc(base + C::CONV_OFF, pk.lbo, pk.sbo, pk.swz);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = p.inject != kRoleMma;
-            for (int t = blockIdx.x; ok && t < sched.num_tiles; t += gridDim.x) {
-                ok = w.wait(bar_acc_empty + 8 * acc, acc_phase ^ 1u, kRoleMma | kWaitAccEmpty);
+            for (int t = cluster_id; ok && t < sched.num_tiles; t += clusters) {
+                ok = w.wait(bar_acc_empty + 8 * acc, acc_phase ^ 1u, kRoleMma | kWaitAccEmpty, CG == 2);
                 if (!ok)
                     break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc * C::ACC_STRIDE);
-                for (int kb = 0; kb < conv_blocks; ++kb) {
-                    ok = w.wait(bar_conv_full + 8 * stage, phase, kRoleMma | kWaitFull);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = w.wait(bar_conv_full + 8 * stage, phase, kRoleMma | kWaitFull, CG == 2);
                     if (!ok)
                         break;
                     tc_fence_after_sync();
-                    const uint64_t step = static_cast<uint64_t>((stage * C::CONV_BYTES) >> 4);
+                    const uint32_t a = tmem_base + static_cast<uint32_t>(C::A_COL0 + stage * C::A_COLS);
+                    const uint64_t b = b_desc + static_cast<uint64_t>((stage * C::CONV_BYTES) >> 4);
 #pragma unroll
-                    for (int j = 0; j < kI8ConvK / 16; ++j)
-                        mma_f16<1>(d, a_desc + step + 2 * j, b_desc + step + 2 * j, idesc, (kb | j) != 0);
-                    mma_commit<1>(bar_conv_empty + 8 * stage);
+                    for (int j = 0; j < kI8K / 16; ++j)
+                        mma_f16_ta<CG>(d, a + 8 * j, b + (j >> 2) * ((C::TOK * kI8K) >> 4) + 2 * (j & 3), idesc,
+                                       ((kb - kb0) | j) != 0);
+                    if constexpr (CG == 2)
+                        mma_commit_pair_multicast(bar_conv_empty + 8 * stage);
+                    else
+                        mma_commit<1>(bar_conv_empty + 8 * stage);
                     if (++stage == C::CONV_STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -367,63 +459,107 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 }
                 if (!ok)
                     break;
-                mma_commit<1>(bar_acc_full + 8 * acc);
+                if constexpr (CG == 2)
+                    mma_commit_pair_multicast(bar_acc_full + 8 * acc);
+                else
+                    mma_commit<1>(bar_acc_full + 8 * acc);
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
             // every MMA this thread issued has completed before TMEM is freed
-            mma_commit<1>(bar_drain);
+            mma_commit<CG>(bar_drain);
             w.drain(bar_drain, 0u, 100000000ull);
         }
     } else if (warp >= kI8FirstConvWarp) {
-        const int ct = static_cast<int>(threadIdx.x) - 32 * kI8FirstConvWarp;
-        constexpr int kThreads = 32 * kI8ConvWarps;
+        const int cw = warp - kI8FirstConvWarp;
+        const int group = cw / kI8GroupWarps;
+        const int ct = (cw % kI8GroupWarps) * 32 + lane;  // thread within the group
+        const int q = warp & 3;                           // TMEM lane quarter this warp may write
+        const int half = (cw >> 2) & 1;                   // the 64 elements of K of its channels
+        const uint32_t key = static_cast<uint32_t>(lane) & 7u;
+        const uint8_t *raw = smem;
+        const uint32_t conv_full = CG == 2 ? mapa_shared(bar_conv_full, 0) : bar_conv_full;
         int rs = 0, cs = 0;
         uint32_t rphase = 0, cphase = 0;
+        int turn = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < sched.num_tiles; t += gridDim.x) {
-            for (int kb = 0; ok && kb < raw_blocks; ++kb) {
-                ok = w.wait(bar_raw_full + 8 * rs, rphase, kRoleConvert | kWaitRawFull);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
-                const uint32_t rw = base + rs * C::RAW_BYTES, rx = rw + C::RAW_W;
-#pragma unroll 1
-                for (int h = 0; h < kI8RawK / kI8ConvK; ++h) {
-                    ok = w.wait(bar_conv_empty + 8 * cs, cphase ^ 1u, kRoleConvert | kWaitConvEmpty);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok)
+        for (int t = cluster_id; ok && t < sched.num_tiles; t += clusters) {
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (turn == group) {
+                    ok = w.wait(bar_raw_full + 8 * rs, rphase, kRoleConvert | kWaitRawFull);
+                    if (!(ok = __all_sync(0xffffffffu, ok)))
                         break;
-                    const uint32_t cw = base + C::CONV_OFF + cs * C::CONV_BYTES, cx = cw + C::CONV_W;
-                    // neighbouring threads take neighbouring rows of one unit column: no bank conflicts
+                    const uint8_t *rw = raw + rs * C::RAW_BYTES, *rx = rw + C::RAW_W;
+                    // one channel's 64 elements, and every 256th 16-byte unit of the
+                    // tokens: neighbouring threads on neighbouring rows, whose
+                    // swizzled units lie in distinct banks
+                    uint32_t hw[32], hx[C::UNITS][8];
+                    {
+                        const uint8_t *row = rw + (32 * q + lane) * kI8K;
+                        uint4 u[4];
 #pragma unroll
-                    for (int i = ct; i < kI8Channels * 4; i += kThreads) {
-                        const int c = i / kI8Channels;
-                        convert_unit(rw, cw, i % kI8Channels, 4 * h + c, 2 * c);
-                    }
+                        for (int i = 0; i < 4; ++i)
+                            u[i] = *reinterpret_cast<const uint4 *>(row + (((4 * half + i) ^ key) << 4));
+                        uint4 x[C::UNITS];
 #pragma unroll
-                    for (int i = ct; i < BT * 4; i += kThreads) {
-                        const int c = i / BT;
-                        convert_unit(rx, cx, i % BT, 4 * h + c, 2 * c);
+                        for (int i = 0; i < C::UNITS; ++i) {
+                            const int unit = i * 32 * kI8GroupWarps + ct;
+                            const int r = unit % C::TOK, c = unit / C::TOK;
+                            if (unit < 8 * C::TOK)
+                                x[i] = *reinterpret_cast<const uint4 *>(rx + r * kI8K + ((c ^ (r & 7)) << 4));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            widen16(u[i], hw + 8 * i);
+#pragma unroll
+                        for (int i = 0; i < C::UNITS; ++i)
+                            widen16(x[i], hx[i]);
                     }
-                    fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(bar_conv_full + 8 * cs);
-                    if (++cs == C::CONV_STAGES) {
-                        cs = 0;
-                        cphase ^= 1u;
+                        mbar_arrive(bar_raw_empty + 8 * rs);
+                    ok = w.wait(bar_conv_empty + 8 * cs, cphase ^ 1u, kRoleConvert | kWaitConvEmpty, CG == 2);
+                    if (!(ok = __all_sync(0xffffffffu, ok)))
+                        break;
+                    tc_fence_after_sync();
+                    tmem_st_words(tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                      static_cast<uint32_t>(C::A_COL0 + cs * C::A_COLS + 32 * half),
+                                  hw);
+                    uint8_t *cx = smem + C::CONV_OFF + cs * C::CONV_BYTES;
+#pragma unroll
+                    for (int i = 0; i < C::UNITS; ++i) {
+                        const int unit = i * 32 * kI8GroupWarps + ct;
+                        const int r = unit % C::TOK, c = unit / C::TOK;
+                        if (unit < 8 * C::TOK) {
+                            uint8_t *row = cx + (c >> 2) * (C::TOK * kI8K) + r * kI8K;
+                            const int u0 = 2 * (c & 3);
+                            *reinterpret_cast<uint4 *>(row + ((u0 ^ (r & 7)) << 4)) =
+                                make_uint4(hx[i][0], hx[i][1], hx[i][2], hx[i][3]);
+                            *reinterpret_cast<uint4 *>(row + (((u0 + 1) ^ (r & 7)) << 4)) =
+                                make_uint4(hx[i][4], hx[i][5], hx[i][6], hx[i][7]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2)
+                            mbar_arrive_cluster(conv_full + 8 * cs);
+                        else
+                            mbar_arrive(conv_full + 8 * cs);
                     }
                 }
-                if (!ok)
-                    break;
-                if (lane == 0)
-                    mbar_arrive(bar_raw_empty + 8 * rs);
+                turn ^= 1;
                 if (++rs == C::RAW_STAGES) {
                     rs = 0;
                     rphase ^= 1u;
+                }
+                if (++cs == C::CONV_STAGES) {
+                    cs = 0;
+                    cphase ^= 1u;
                 }
             }
         }
@@ -431,34 +567,76 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const int q = warp & 3;  // TMEM lane quarter of this warp
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int t = blockIdx.x; t < sched.num_tiles; t += gridDim.x) {
-            const I8Tile ti = i8_tile<BT>(sched, t);
-            const int n = ti.n0 + 32 * q + lane;
+        const uint32_t acc_empty = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
+        for (int t = cluster_id; t < sched.num_tiles; t += clusters) {
+            const I8Tile ti = i8_tile<BT, C::CH>(sched, t);
+            const int n = ti.n0 + n_off + 32 * q + lane;
             const bool live = n < p.N;
             const float sn = live ? p.sb[static_cast<long long>(ti.expert) * p.N + n] : 0.0f;
-            bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull);
+            bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull, CG == 2);
             if (!__all_sync(0xffffffffu, ok))
                 break;
             tc_fence_after_sync();
             const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc * C::ACC_STRIDE);
             const int rows = min(ti.m1 - ti.m0, BT);
-            for (int c = 0; c < rows; c += 32) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(src + c, r);
-                const float my_sa = c + lane < rows ? p.sa[ti.m0 + c + lane] : 0.0f;
-                tmem_ld_wait();
-                D *out = static_cast<D *>(p.d) + static_cast<long long>(ti.m0 + c) * p.ldd + n;
+            if (KS > 1 && rank > 0) {
+                // this CTA's sums to the first CTA, [rank - 1][token][channel]
+                const uint32_t part = mapa_shared(base + C::PART_OFF, 0) +
+                                      4u * static_cast<uint32_t>(((rank - 1) * BT) * kI8Channels + 32 * q + lane);
+                for (int c = 0; c < rows; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(src + c, r);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float sm = __shfl_sync(0xffffffffu, my_sa, i);
-                    if (live && c + i < rows)
-                        store_scaled<D>(out + i * p.ldd, __uint_as_float(r[i]) * sm * sn);
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < rows)
+                            st_cluster_f32(part + 4u * static_cast<uint32_t>((c + i) * kI8Channels), __uint_as_float(r[i]));
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(mapa_shared(bar_part, 0));
+            } else {
+                if (KS > 1 && cluster > 1) {
+                    ok = w.wait(bar_part, 0u, kRoleEpilogue | kWaitSplit, true);
+                    if (!__all_sync(0xffffffffu, ok))
+                        break;
+                }
+                for (int c = 0; c < rows; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(src + c, r);
+                    const int left = rows - c;
+                    const float sa = lane < left ? p.sa[ti.m0 + c + lane] : 0.0f;
+                    tmem_ld_wait();
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __uint_as_float(r[i]);
+                    if constexpr (KS > 1) {
+                        const float *part = reinterpret_cast<const float *>(smem + C::PART_OFF) + c * kI8Channels + 32 * q + lane;
+                        for (int k = 1; k < cluster; ++k, part += BT * kI8Channels) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < left)
+                                    v[i] += part[i * kI8Channels];
+                        }
+                    }
+                    const long long at = static_cast<long long>(ti.m0 + c) * p.ldd + n;
+                    if (p.out_type == GEMM_OUT_F32)
+                        store_block(static_cast<float *>(p.d) + at, p.ldd, v, sa, sn, left, live);
+                    else if (p.out_type == GEMM_OUT_BF16)
+                        store_block(static_cast<__nv_bfloat16 *>(p.d) + at, p.ldd, v, sa, sn, left, live);
+                    else
+                        store_block(static_cast<__half *>(p.d) + at, p.ldd, v, sa, sn, left, live);
                 }
             }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_acc_empty + 8 * acc);
+            if (lane == 0) {
+                if constexpr (CG == 2)
+                    mbar_arrive_cluster(acc_empty + 8 * acc);
+                else
+                    mbar_arrive(acc_empty + 8 * acc);
+            }
             if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;
@@ -471,9 +649,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         drain_producer_tail<C::RAW_STAGES>(tail, bar_raw_full, w);
     tc_fence_before_sync();
     __syncthreads();
+    if constexpr (C::CLUSTER > 1)
+        cluster_sync_all();  // no CTA exits while another may still write into it
     if (warp == 1) {
         tc_fence_after_sync();
-        tmem_dealloc<1>(tmem_base, C::TMEM_COLS);
+        tmem_dealloc<CG>(tmem_base, 512);
     }
 }
 
@@ -493,48 +673,82 @@ __global__ void int8_zero_kernel(const I8Params p)
             store_scaled<D>(static_cast<D *>(p.d) + (i + first) * p.ldd + n, 0.0f);
 }
 
-template <int BT, typename D>
+template <int CG, int BT, int KS>
 std::atomic<uint64_t> i8_attribute_set[2] = {{0}, {0}};
 
-template <int BT, typename D>
-gemm_status_t launch_int8(const CUtensorMap &a, const CUtensorMap &b, const I8Params &p, int sms, cudaStream_t st)
+// Launches tiles of CG x 128 channels and BT tokens, `ks` CTAs sharing a
+// tile's K (1 unless the kernel is built for it and every tile has a cluster
+// of its own).
+template <int CG, int BT, int KS>
+gemm_status_t launch_int8(const CUtensorMap &a, const CUtensorMap &b, const I8Params &p, int ks, int sms, cudaStream_t st)
 {
-    using C = I8Cfg<BT>;
-    auto kern = int8_gemm_kernel<BT, D>;
-    const int most = C::SMEM_BASE + 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1);
-    if (ensure_smem_attribute(kern, most, i8_attribute_set<BT, D>) != cudaSuccess)
+    using C = I8Cfg<CG, BT, KS>;
+    auto kern = int8_gemm_kernel<CG, BT, KS>;
+    constexpr int kBase = C::TABLE_OFF + 1024;
+    if (ensure_smem_attribute(kern, kBase + 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1), i8_attribute_set<CG, BT, KS>) != cudaSuccess)
         return GEMM_ERR_CUDA;
-    const int smem = C::SMEM_BASE + (p.experts ? 2 * 4 * (p.experts + 1) : 0);
     // tiles of the launch, or for experts the most there can be
     const int64_t tiles_m = (static_cast<int64_t>(p.M) + BT - 1) / BT + (p.experts ? std::min(p.experts, p.M) : 0);
-    const int grid = static_cast<int>(std::min<int64_t>(tiles_m * p.tiles_n, sms));
-    kern<<<grid, kI8Threads, smem, st>>>(a, b, p);
+    const int64_t tiles = tiles_m * p.tiles_n;
+    const int cluster = CG * ks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(KS > 1 ? tiles * cluster : std::min<int64_t>(tiles, sms / cluster) * cluster), 1, 1);
+    cfg.blockDim = dim3(kI8Threads, 1, 1);
+    cfg.dynamicSmemBytes = kBase + (p.experts ? 2 * 4 * (p.experts + 1) : 0);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    if (C::CLUSTER > 1) {
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&cfg, kern, a, b, p, ks) != cudaSuccess)
+        return GEMM_ERR_CUDA;
     return host_launched();
 }
 
-template <typename D>
-gemm_status_t run_int8_typed(const CUtensorMap &a, const CUtensorMap &b, const I8Params &p, int bt, int sms,
-                             cudaStream_t st)
+// How a product is cut: CTAs per tile of channels, tokens per tile, CTAs
+// sharing a tile's K.
+struct I8Plan {
+    int cg, bt, ks;
+};
+
+I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms)
 {
-    switch (bt) {
-    case 16: return launch_int8<16, D>(a, b, p, sms, st);
-    case 32: return launch_int8<32, D>(a, b, p, sms, st);
-    case 64: return launch_int8<64, D>(a, b, p, sms, st);
-    case 128: return launch_int8<128, D>(a, b, p, sms, st);
-    default: return launch_int8<256, D>(a, b, p, sms, st);
+    const int64_t rows = E ? (M + E - 1) / E : M;  // of one matrix, on average
+    I8Plan pl = {1, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1};
+    if (pl.bt == 128 && N > kI8Channels) {
+        // pairs; 192 tokens where that takes fewer token-rounds of the pairs
+        pl.cg = 2;
+        const int64_t tn = (N + 255) / 256, pairs = sms / 2;
+        auto rounds = [&](int bt) { return ((E ? E * ((rows + bt - 1) / bt) : (M + bt - 1) / bt) * tn + pairs - 1) / pairs * bt; };
+        if (rows > 128 && rounds(192) <= rounds(128) + rounds(128) / 8)
+            pl.bt = 192;
     }
+    if (E == 0 && pl.cg == 1 && pl.bt <= 64) {
+        const int64_t tiles = (M + pl.bt - 1) / pl.bt * ((N + kI8Channels - 1) / kI8Channels);
+        const int most = pl.bt == 16 ? 8 : 4;
+        const int64_t blocks = (K + kI8K - 1) / kI8K;
+        while (pl.ks < most && tiles * pl.ks * 2 <= sms && blocks >= 4 * pl.ks)
+            pl.ks *= 2;
+    }
+    return pl;
 }
 
-// Tokens per tile: the smallest that takes the rows of one expert (on
-// average), 256 only where such tiles fill the SMs.
-int int8_tile_tokens(int64_t M, int64_t N, int64_t E, int sms)
+gemm_status_t launch_int8_plan(const CUtensorMap &a, const CUtensorMap &b, const I8Params &p, const I8Plan &pl, int sms,
+                               cudaStream_t st)
 {
-    const int64_t rows = E ? (M + E - 1) / E : M;
-    int bt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
-    const int64_t tiles_n = (N + kI8Channels - 1) / kI8Channels;
-    while (bt > 128 && (M + bt - 1) / bt * tiles_n < sms)
-        bt /= 2;
-    return bt;
+    if (pl.cg == 2)
+        return pl.bt == 192 ? launch_int8<2, 192, 1>(a, b, p, 1, sms, st) : launch_int8<2, 128, 1>(a, b, p, 1, sms, st);
+    switch (pl.bt) {
+    case 16: return pl.ks > 1 ? launch_int8<1, 16, 8>(a, b, p, pl.ks, sms, st) : launch_int8<1, 16, 1>(a, b, p, 1, sms, st);
+    case 32: return pl.ks > 1 ? launch_int8<1, 32, 4>(a, b, p, pl.ks, sms, st) : launch_int8<1, 32, 1>(a, b, p, 1, sms, st);
+    case 64: return pl.ks > 1 ? launch_int8<1, 64, 4>(a, b, p, pl.ks, sms, st) : launch_int8<1, 64, 1>(a, b, p, 1, sms, st);
+    default: return launch_int8<1, 128, 1>(a, b, p, 1, sms, st);
+    }
 }
 
 gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t *offsets, const int8_t *A, int64_t lda,
@@ -558,9 +772,6 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
         if (!aligned_to(A, 16) || !aligned_to(B, 16) || lda % 16 != 0 || ldb % 16 != 0 || (E > 1 && stride_b % 16 != 0))
             return GEMM_ERR_ALIGNMENT;
     }
-    const int64_t tiles_n = (N + kI8Channels - 1) / kI8Channels;
-    if (tiles_n * ((M + 15) / 16 + (E ? std::min(E, M) : 0)) > kSizeLimit)
-        return GEMM_ERR_UNSUPPORTED;
     int dev = 0, sms = 0;
     unsigned int *status = nullptr;
     gemm_status_t s = host_device(&dev, &status, &sms);
@@ -572,7 +783,6 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     p.K = static_cast<int>(K);
     p.experts = static_cast<int>(E);
     p.offsets = offsets;
-    p.tiles_n = static_cast<int>(tiles_n);
     p.sa = sa;
     p.sb = sb;
     p.d = D;
@@ -592,12 +802,16 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     int ms = 0;
     p.inject = host_take_injection(&ms);
     p.timeout_ns = static_cast<unsigned long long>(ms > 0 ? ms : 2000) * 1000000ull;
-    const int bt = int8_tile_tokens(M, N, E, sms);
+    const I8Plan pl = int8_plan(M, N, K, E, sms);
+    const int64_t tiles_n = (N + pl.cg * kI8Channels - 1) / (pl.cg * kI8Channels);
+    if (tiles_n * ((M + pl.bt - 1) / pl.bt + (E ? std::min(E, M) : 0)) > kSizeLimit)
+        return GEMM_ERR_UNSUPPORTED;
+    p.tiles_n = static_cast<int>(tiles_n);
     CUtensorMap a, b;
     {
         const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(M)};
         const uint64_t strides[1] = {static_cast<uint64_t>(lda)};
-        const uint32_t box[2] = {kI8RawK, static_cast<uint32_t>(bt)};
+        const uint32_t box[2] = {kI8K, static_cast<uint32_t>(pl.bt / pl.cg)};
         if ((s = host_encode_tiled(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) !=
             GEMM_OK)
             return s;
@@ -605,16 +819,12 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     {
         const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E ? E : 1)};
         const uint64_t strides[2] = {static_cast<uint64_t>(ldb), static_cast<uint64_t>(E > 1 ? stride_b : ldb)};
-        const uint32_t box[3] = {kI8RawK, kI8Channels, 1};
+        const uint32_t box[3] = {kI8K, kI8Channels, 1};
         if ((s = host_encode_tiled(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, B, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) !=
             GEMM_OK)
             return s;
     }
-    if (d_type == GEMM_OUT_F32)
-        return run_int8_typed<float>(a, b, p, bt, sms, st);
-    if (d_type == GEMM_OUT_BF16)
-        return run_int8_typed<__nv_bfloat16>(a, b, p, bt, sms, st);
-    return run_int8_typed<__half>(a, b, p, bt, sms, st);
+    return launch_int8_plan(a, b, p, pl, sms, st);
 }
 
 }  // namespace g300
