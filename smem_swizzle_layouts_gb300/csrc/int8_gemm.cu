@@ -24,11 +24,13 @@
 // Warp roles of a CTA:
 //   warp 0       TMA producer: raw int8 stages of 128 elements of K;
 //   warp 1       TMEM allocator and MMA issuer (pairs: of the even CTA);
-//   warps 2-5    epilogue: accumulator (lane = channel, column = token) to D,
+//                (warps 2 and 3 only complete the warpgroup)
+//   warps 4-7    epilogue: accumulator (lane = channel, column = token) to D,
 //                double-buffered against the next tile's MMAs;
-//   warps 6-21   converters in two groups of 8 warps that take alternate
+//   warps 8-23   converters in two groups of 8 warps that take alternate
 //                stages; a group reads and widens a stage into registers
-//                before it waits for room to write it.
+//                before it waits for room to write it. They take the registers
+//                the other warps have no use for (setmaxnreg).
 // For few tokens and few tiles a cluster of CTAs shares one tile's K
 // (KS > 1): the others leave their fp32 sums in the first CTA's shared memory,
 // which adds them in the order of their ranks.
@@ -52,9 +54,15 @@ namespace g300 {
 constexpr int kI8Channels = 128;  // rows of B per CTA (MMA M per CTA)
 constexpr int kI8K = 128;         // elements of K per stage: one 128-byte swizzled int8 row, two fp16 ones
 constexpr int kI8GroupWarps = 8;  // converter warps per group
-constexpr int kI8FirstConvWarp = 2 + kEpiWarps;
+constexpr int kI8FirstEpiWarp = 4;
+constexpr int kI8FirstConvWarp = kI8FirstEpiWarp + kEpiWarps;
 constexpr int kI8Threads = 32 * (kI8FirstConvWarp + 2 * kI8GroupWarps);
 constexpr int kI8MaxSmem = 232448;
+// Registers a thread: at launch, and after the warpgroups have shared them out
+// (one of producer and MMA issuer, one of epilogue, four of converters).
+constexpr int kI8LaunchRegs = 80, kI8IssueRegs = 40, kI8EpiRegs = 56, kI8ConvRegs = 96;
+static_assert(kI8IssueRegs + kI8EpiRegs + 4 * kI8ConvRegs <= 6 * kI8LaunchRegs && kI8Threads == 768,
+              "the shares add up to no more than the block was launched with");
 
 enum : uint32_t {
     kRoleConvert = 6,
@@ -235,6 +243,70 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
                      : "memory");
 }
 
+// Registers a thread of this warpgroup, given up or taken (every warp of the
+// warpgroup executes it).
+template <int N>
+__device__ __forceinline__ void reg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Waiter::wait for the many warps of this kernel: a probe that does not find
+// the phase complete sleeps in the hardware until it is, or for 20 us, so that
+// waiting warps leave the issue slots to the converters.
+__device__ __forceinline__ bool probe_asleep(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "r"(20000u)
+                 : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool probe_asleep_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "r"(20000u)
+                 : "memory");
+    return ok != 0;
+}
+
+struct I8Waiter {
+    Waiter w;
+
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t code, bool cluster = false) const
+    {
+        if (cluster ? probe_asleep_cluster(bar, parity) : probe_asleep(bar, parity))
+            return true;
+        const uint64_t t0 = globaltimer_ns();
+        while (!(cluster ? probe_asleep_cluster(bar, parity) : probe_asleep(bar, parity))) {
+            if (*w.abort_flag)
+                return false;
+            if (globaltimer_ns() - t0 > w.timeout_ns) {
+                w.fail(code);
+                return false;
+            }
+        }
+        return true;
+    }
+};
+
+// Keeps a value in a register from here on: what computes it is not moved past.
+__device__ __forceinline__ void pin(uint32_t &v) { asm volatile("" : "+r"(v)); }
+
 // Arrive on the even CTA's barrier for a stage this warp has written into its
 // own CTA's shared memory and TMEM. The proxy fence and tcgen05.wait::st before
 // it have completed those writes where the pair's MMA will read them, and the
@@ -339,7 +411,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         tmem_alloc<CG>(smem_u32(tmem_slot), 512);
         tmem_relinquish<CG>();
     }
-    if (warp == 2 && p.experts) {
+    if (warp == kI8FirstEpiWarp && p.experts) {
         // clamped offsets and the first tile of each expert: a running
         // maximum and a running sum, 32 experts at a time
         int low = 0, tiles = 0;
@@ -380,11 +452,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
 
-    Waiter w;
-    w.timeout_ns = p.timeout_ns;
-    w.abort_flag = abort_flag;
-    w.status = p.status;
-    w.all_cluster_scope = false;
+    I8Waiter w;
+    w.w.timeout_ns = p.timeout_ns;
+    w.w.abort_flag = abort_flag;
+    w.w.status = p.status;
+    w.w.all_cluster_scope = false;
 
     I8Sched sched;
     sched.experts = p.experts;
@@ -403,8 +475,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int n_off = CG == 2 ? rank * kI8Channels : 0;  // this CTA's channels within the tile
 
     ProducerTail tail{0, 0, 0u};
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < kI8FirstEpiWarp) {
+        reg_dec<kI8IssueRegs>();
+        if (warp == 0 && lane == 0) {
             if (p.inject == kRoleProducer) {
                 w.wait(bar_inject, 0u, kRoleProducer | kWaitInjected);
             } else {
@@ -432,8 +505,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 tail = ProducerTail{issued < C::RAW_STAGES ? issued : C::RAW_STAGES, stage, phase};
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0 && (CG == 1 || rank == 0)) {
+        if (warp == 1 && lane == 0 && (CG == 1 || rank == 0)) {
             if (p.inject == kRoleMma)
                 w.wait(bar_inject, 0u, kRoleMma | kWaitInjected);
             const uint32_t idesc = make_idesc_f16(CG * kI8Channels, BT, 0, 0, 0);
@@ -481,16 +553,42 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             }
             // every MMA this thread issued has completed before TMEM is freed
             mma_commit<CG>(bar_drain);
-            w.drain(bar_drain, 0u, 100000000ull);
+            w.w.drain(bar_drain, 0u, 100000000ull);
         }
     } else if (warp >= kI8FirstConvWarp) {
+        reg_inc<kI8ConvRegs>();
         const int cw = warp - kI8FirstConvWarp;
         const int group = cw / kI8GroupWarps;
         const int ct = (cw % kI8GroupWarps) * 32 + lane;  // thread within the group
         const int q = warp & 3;                           // TMEM lane quarter this warp may write
         const int half = (cw >> 2) & 1;                   // the 64 elements of K of its channels
-        const uint32_t key = static_cast<uint32_t>(lane) & 7u;
-        const uint8_t *raw = smem;
+        // This thread's share of a stage: one channel's 64 elements, and every
+        // 256th 16-byte unit of the tokens. Neighbouring threads take
+        // neighbouring rows, whose swizzled units lie in distinct banks. The
+        // offsets are computed once.
+        uint32_t w_at[4], x_at[C::UNITS], y_at[C::UNITS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w_at[i] = static_cast<uint32_t>((32 * q + lane) * kI8K + (((4 * half + i) ^ (lane & 7)) << 4));
+#pragma unroll
+        for (int i = 0; i < C::UNITS; ++i) {
+            const int unit = i * 32 * kI8GroupWarps + ct;
+            const int r = unit % C::TOK, c = unit / C::TOK;
+            x_at[i] = static_cast<uint32_t>(C::RAW_W + r * kI8K + ((c ^ (r & 7)) << 4));
+            // the unit's two fp16 units: the second at the first's offset ^ 16
+            y_at[i] = static_cast<uint32_t>((c >> 2) * (C::TOK * kI8K) + r * kI8K + (((2 * (c & 3)) ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            pin(w_at[i]);
+#pragma unroll
+        for (int i = 0; i < C::UNITS; ++i) {
+            pin(x_at[i]);
+            pin(y_at[i]);
+        }
+        constexpr bool kWholeUnits = 8 * C::TOK % (32 * kI8GroupWarps) == 0;
+        const bool has_unit = kWholeUnits || ct < 8 * C::TOK;  // fewer units than threads
+        static_assert(kWholeUnits || C::UNITS == 1, "every thread has the same number of units, or one at most");
         const uint32_t conv_full = CG == 2 ? mapa_shared(bar_conv_full, 0) : bar_conv_full;
         int rs = 0, cs = 0;
         uint32_t rphase = 0, cphase = 0;
@@ -502,31 +600,30 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                     ok = w.wait(bar_raw_full + 8 * rs, rphase, kRoleConvert | kWaitRawFull);
                     if (!(ok = __all_sync(0xffffffffu, ok)))
                         break;
-                    const uint8_t *rw = raw + rs * C::RAW_BYTES, *rx = rw + C::RAW_W;
-                    // one channel's 64 elements, and every 256th 16-byte unit of the
-                    // tokens: neighbouring threads on neighbouring rows, whose
-                    // swizzled units lie in distinct banks
+                    const uint8_t *raw = smem + rs * C::RAW_BYTES;
                     uint32_t hw[32], hx[C::UNITS][8];
                     {
-                        const uint8_t *row = rw + (32 * q + lane) * kI8K;
-                        uint4 u[4];
+                        uint4 u[4], x[C::UNITS];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            u[i] = *reinterpret_cast<const uint4 *>(row + (((4 * half + i) ^ key) << 4));
-                        uint4 x[C::UNITS];
+                            u[i] = *reinterpret_cast<const uint4 *>(raw + w_at[i]);
 #pragma unroll
-                        for (int i = 0; i < C::UNITS; ++i) {
-                            const int unit = i * 32 * kI8GroupWarps + ct;
-                            const int r = unit % C::TOK, c = unit / C::TOK;
-                            if (unit < 8 * C::TOK)
-                                x[i] = *reinterpret_cast<const uint4 *>(rx + r * kI8K + ((c ^ (r & 7)) << 4));
-                        }
+                        for (int i = 0; i < C::UNITS; ++i)
+                            if (has_unit)
+                                x[i] = *reinterpret_cast<const uint4 *>(raw + x_at[i]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             widen16(u[i], hw + 8 * i);
 #pragma unroll
                         for (int i = 0; i < C::UNITS; ++i)
                             widen16(x[i], hx[i]);
+                        // all of it before the wait for room: only the writes follow it
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            pin(hw[i]);
+#pragma unroll
+                        for (int i = 0; i < C::UNITS * 8; ++i)
+                            pin(hx[i / 8][i % 8]);
                     }
                     __syncwarp();
                     if (lane == 0)
@@ -540,18 +637,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                                   hw);
                     uint8_t *cx = smem + C::CONV_OFF + cs * C::CONV_BYTES;
 #pragma unroll
-                    for (int i = 0; i < C::UNITS; ++i) {
-                        const int unit = i * 32 * kI8GroupWarps + ct;
-                        const int r = unit % C::TOK, c = unit / C::TOK;
-                        if (unit < 8 * C::TOK) {
-                            uint8_t *row = cx + (c >> 2) * (C::TOK * kI8K) + r * kI8K;
-                            const int u0 = 2 * (c & 3);
-                            *reinterpret_cast<uint4 *>(row + ((u0 ^ (r & 7)) << 4)) =
-                                make_uint4(hx[i][0], hx[i][1], hx[i][2], hx[i][3]);
-                            *reinterpret_cast<uint4 *>(row + (((u0 + 1) ^ (r & 7)) << 4)) =
-                                make_uint4(hx[i][4], hx[i][5], hx[i][6], hx[i][7]);
+                    for (int i = 0; i < C::UNITS; ++i)
+                        if (has_unit) {
+                            *reinterpret_cast<uint4 *>(cx + y_at[i]) = make_uint4(hx[i][0], hx[i][1], hx[i][2], hx[i][3]);
+                            *reinterpret_cast<uint4 *>(cx + (y_at[i] ^ 16u)) = make_uint4(hx[i][4], hx[i][5], hx[i][6], hx[i][7]);
                         }
-                    }
                     fence_proxy_async_smem();
                     tmem_st_wait();
                     tc_fence_before_sync();
@@ -575,6 +665,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             }
         }
     } else {
+        reg_dec<kI8EpiRegs>();
         const int q = warp & 3;  // TMEM lane quarter of this warp
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -657,7 +748,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     __syncwarp();
     __syncthreads();  // every role has returned: the abort flag is final
     if (*abort_flag && warp == 0 && lane == 0)
-        drain_producer_tail<C::RAW_STAGES>(tail, bar_raw_full, w);
+        drain_producer_tail<C::RAW_STAGES>(tail, bar_raw_full, w.w);
     tc_fence_before_sync();
     __syncthreads();
     if constexpr (C::CLUSTER > 1)
