@@ -187,21 +187,24 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, uint3
                  : "memory");
 }
 
-// Four int8 to four fp16: with its sign bit flipped a byte is q + 128; as the
-// low byte of 0x64xx it is the fp16 number 1024 + q + 128, from which 1152 is
-// taken off exactly.
+// Four int8 to four fp16, in the order 0, 2, 1, 3 (both operands take the same
+// order of K, so the sum does not see it): with its sign bit flipped a byte is
+// q + 128; as the low byte of 0x64xx it is the fp16 number 1024 + q + 128, from
+// which 1152 is taken off exactly. One three-input logic operation masks a
+// pair of bytes, flips their signs and sets the exponents.
 __device__ __forceinline__ void widen4(uint32_t q, uint32_t &lo, uint32_t &hi)
 {
-    const uint32_t u = q ^ 0x80808080u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
     const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t a, b;  // (q & 0x00ff00ff) ^ 0x64806480
+    asm("lop3.b32 %0, %1, 0x00ff00ff, 0x64806480, 0x6a;" : "=r"(a) : "r"(q));
+    asm("lop3.b32 %0, %1, 0x00ff00ff, 0x64806480, 0x6a;" : "=r"(b) : "r"(q >> 8));
     __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
     __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
     lo = *reinterpret_cast<uint32_t *>(&x);
     hi = *reinterpret_cast<uint32_t *>(&y);
 }
 
-// Sixteen int8 to sixteen fp16, in order.
+// Sixteen int8 to sixteen fp16.
 __device__ __forceinline__ void widen16(const uint4 &q, uint32_t *h)
 {
     widen4(q.x, h[0], h[1]);
@@ -590,79 +593,80 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const bool has_unit = kWholeUnits || ct < 8 * C::TOK;  // fewer units than threads
         static_assert(kWholeUnits || C::UNITS == 1, "every thread has the same number of units, or one at most");
         const uint32_t conv_full = CG == 2 ? mapa_shared(bar_conv_full, 0) : bar_conv_full;
-        int rs = 0, cs = 0;
-        uint32_t rphase = 0, cphase = 0;
-        int turn = 0;
+        // the group's next stage, raw and widened: every second one
+        int rs = group % C::RAW_STAGES, cs = group % C::CONV_STAGES;
+        uint32_t rphase = 0, cphase = 1;
+        int skip = group;  // blocks of the tile before the group's next one
         bool ok = true;
         for (int t = cluster_id; ok && t < sched.num_tiles; t += clusters) {
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (turn == group) {
-                    ok = w.wait(bar_raw_full + 8 * rs, rphase, kRoleConvert | kWaitRawFull);
-                    if (!(ok = __all_sync(0xffffffffu, ok)))
-                        break;
-                    const uint8_t *raw = smem + rs * C::RAW_BYTES;
-                    uint32_t hw[32], hx[C::UNITS][8];
-                    {
-                        uint4 u[4], x[C::UNITS];
+            int kb = kb0 + skip;
+            for (; kb < kb1; kb += 2) {
+                ok = w.wait(bar_raw_full + 8 * rs, rphase, kRoleConvert | kWaitRawFull);
+                if (!(ok = __all_sync(0xffffffffu, ok)))
+                    break;
+                const uint32_t raw = base + static_cast<uint32_t>(rs * C::RAW_BYTES);
+                uint32_t hw[32], hx[C::UNITS][8];
+                {
+                    uint4 u[4], x[C::UNITS];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            u[i] = *reinterpret_cast<const uint4 *>(raw + w_at[i]);
-#pragma unroll
-                        for (int i = 0; i < C::UNITS; ++i)
-                            if (has_unit)
-                                x[i] = *reinterpret_cast<const uint4 *>(raw + x_at[i]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            widen16(u[i], hw + 8 * i);
-#pragma unroll
-                        for (int i = 0; i < C::UNITS; ++i)
-                            widen16(x[i], hx[i]);
-                        // all of it before the wait for room: only the writes follow it
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            pin(hw[i]);
-#pragma unroll
-                        for (int i = 0; i < C::UNITS * 8; ++i)
-                            pin(hx[i / 8][i % 8]);
-                    }
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar_raw_empty + 8 * rs);
-                    ok = w.wait(bar_conv_empty + 8 * cs, cphase ^ 1u, kRoleConvert | kWaitConvEmpty, CG == 2);
-                    if (!(ok = __all_sync(0xffffffffu, ok)))
-                        break;
-                    tc_fence_after_sync();
-                    tmem_st_words(tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                                      static_cast<uint32_t>(C::A_COL0 + cs * C::A_COLS + 32 * half),
-                                  hw);
-                    uint8_t *cx = smem + C::CONV_OFF + cs * C::CONV_BYTES;
+                    for (int i = 0; i < 4; ++i)
+                        ld_shared_v4(raw + w_at[i], u[i].x, u[i].y, u[i].z, u[i].w);
 #pragma unroll
                     for (int i = 0; i < C::UNITS; ++i)
-                        if (has_unit) {
-                            *reinterpret_cast<uint4 *>(cx + y_at[i]) = make_uint4(hx[i][0], hx[i][1], hx[i][2], hx[i][3]);
-                            *reinterpret_cast<uint4 *>(cx + (y_at[i] ^ 16u)) = make_uint4(hx[i][4], hx[i][5], hx[i][6], hx[i][7]);
-                        }
-                    fence_proxy_async_smem();
-                    tmem_st_wait();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 2)
-                            mbar_arrive_peer(conv_full + 8 * cs);
-                        else
-                            mbar_arrive(conv_full + 8 * cs);
-                    }
+                        if (has_unit)
+                            ld_shared_v4(raw + x_at[i], x[i].x, x[i].y, x[i].z, x[i].w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        widen16(u[i], hw + 8 * i);
+#pragma unroll
+                    for (int i = 0; i < C::UNITS; ++i)
+                        widen16(x[i], hx[i]);
+                    // all of it before the wait for room: only the writes follow it
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        pin(hw[i]);
+#pragma unroll
+                    for (int i = 0; i < C::UNITS * 8; ++i)
+                        pin(hx[i / 8][i % 8]);
                 }
-                turn ^= 1;
-                if (++rs == C::RAW_STAGES) {
-                    rs = 0;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_raw_empty + 8 * rs);
+                ok = w.wait(bar_conv_empty + 8 * cs, cphase, kRoleConvert | kWaitConvEmpty, CG == 2);
+                if (!(ok = __all_sync(0xffffffffu, ok)))
+                    break;
+                tc_fence_after_sync();
+                tmem_st_words(tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                  static_cast<uint32_t>(C::A_COL0 + cs * C::A_COLS + 32 * half),
+                              hw);
+                const uint32_t conv = base + static_cast<uint32_t>(C::CONV_OFF + cs * C::CONV_BYTES);
+#pragma unroll
+                for (int i = 0; i < C::UNITS; ++i)
+                    if (has_unit) {
+                        const uint32_t at = conv + y_at[i];
+                        st_shared_v4(at, hx[i][0], hx[i][1], hx[i][2], hx[i][3]);
+                        st_shared_v4(at ^ 16u, hx[i][4], hx[i][5], hx[i][6], hx[i][7]);
+                    }
+                fence_proxy_async_smem();
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_peer(conv_full + 8 * cs);
+                    else
+                        mbar_arrive(conv_full + 8 * cs);
+                }
+                if ((rs += 2) >= C::RAW_STAGES) {
+                    rs -= C::RAW_STAGES;
                     rphase ^= 1u;
                 }
-                if (++cs == C::CONV_STAGES) {
-                    cs = 0;
+                if ((cs += 2) >= C::CONV_STAGES) {
+                    cs -= C::CONV_STAGES;
                     cphase ^= 1u;
                 }
             }
+            skip = kb - kb1;  // 0 or 1 of the next tile's blocks is the other group's
         }
     } else {
         reg_dec<kI8EpiRegs>();
