@@ -9,31 +9,38 @@
 // sm_103a's tcgen05 has no integer kind, so the integers are widened on chip:
 // TMA brings int8 tiles to shared memory, converter warps turn them into fp16
 // (exact: |q| <= 128 has 8 significant bits of fp16's 11) and kind::f16 MMAs
-// multiply and sum them in fp32 (exact below 2^24). The rows of B (channels)
-// are the MMA's M and the rows of A (tokens) its N, so that a tile of few
-// tokens still uses whole 128-row MMAs and reads every weight once.
+// multiply and sum them in fp32 (exact below 2^24). The widened rows of the
+// MMA's M side go to Tensor Memory, from where the MMA takes its first operand,
+// those of its N side to shared memory: with both in shared memory a 128 x 256
+// tile moves 288 bytes of it per MMA cycle (raw writes and reads, fp16 writes,
+// MMA reads) where an SM moves 128, which held 8192^3 at 0.48 of the tensor rate.
 //
-// Widened channels go to Tensor Memory, from where the MMA takes its first
-// operand, widened tokens to shared memory. With both in shared memory a
-// 128 x 256 tile moves 288 bytes of shared memory per MMA cycle (raw writes and
-// reads, fp16 writes, MMA reads) where an SM moves 128, which held the product
-// at 0.44 of the tensor rate; with the channels in Tensor Memory and CTA pairs
-// (each CTA widens its 128 channels and half of the tokens of a 256-channel
-// tile) it is 135 bytes.
+// Two shapes of tile:
+//   narrow  128 channels (rows of B) on the M side, 16 to 128 tokens (rows of
+//           A) on the N side, single CTAs: few tokens still use whole 128-row
+//           MMAs and every weight is read once. Such MMAs are short and the
+//           issuing thread, about 1000 cycles for the eight of a stage, is
+//           the limit; so two threads issue alternate stages, each into an
+//           accumulator of its own, and the epilogue adds the two. For few
+//           tiles a cluster of CTAs shares one tile's K (KS > 1): the others
+//           leave their fp32 sums in the first CTA's shared memory, which adds
+//           them in the order of their ranks.
+//   wide    256 tokens on the M side, 256 channels on the N side, CTA pairs
+//           (cta_group::2; each CTA widens its 128 tokens and half of the
+//           channels): a stage's eight MMAs take 1024 cycles and keep the
+//           tensor pipe fed. The accumulator's 256 columns and the widened
+//           stages fill TMEM, so a tile's epilogue does not overlap the next
+//           tile's MMAs; eight warps empty it.
 //
 // Warp roles of a CTA:
 //   warp 0       TMA producer: raw int8 stages of 128 elements of K;
 //   warp 1       TMEM allocator and MMA issuer (pairs: of the even CTA);
-//                (warps 2 and 3 only complete the warpgroup)
-//   warps 4-7    epilogue: accumulator (lane = channel, column = token) to D,
-//                double-buffered against the next tile's MMAs;
-//   warps 8-23   converters in two groups of 8 warps that take alternate
+//   warp 2       narrow: second MMA issuer; warp 3 completes the warpgroup;
+//   warps 4-     epilogue (four warps, wide eight);
+//   the last 16  converters in two groups of 8 warps that take alternate
 //                stages; a group reads and widens a stage into registers
-//                before it waits for room to write it. They take the registers
-//                the other warps have no use for (setmaxnreg).
-// For few tokens and few tiles a cluster of CTAs shares one tile's K
-// (KS > 1): the others leave their fp32 sums in the first CTA's shared memory,
-// which adds them in the order of their ranks.
+//                before it waits for room to write it. The warpgroups share
+//                the registers out by need (setmaxnreg).
 // Every wait is bounded, as in gemm_kernel.cuh.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -51,18 +58,12 @@
 
 namespace g300 {
 
-constexpr int kI8Channels = 128;  // rows of B per CTA (MMA M per CTA)
+constexpr int kI8Rows = 128;      // rows of the MMA's M side per CTA
 constexpr int kI8K = 128;         // elements of K per stage: one 128-byte swizzled int8 row, two fp16 ones
 constexpr int kI8GroupWarps = 8;  // converter warps per group
+constexpr int kI8GroupThreads = 32 * kI8GroupWarps;
 constexpr int kI8FirstEpiWarp = 4;
-constexpr int kI8FirstConvWarp = kI8FirstEpiWarp + kEpiWarps;
-constexpr int kI8Threads = 32 * (kI8FirstConvWarp + 2 * kI8GroupWarps);
 constexpr int kI8MaxSmem = 232448;
-// Registers a thread: at launch, and after the warpgroups have shared them out
-// (one of producer and MMA issuer, one of epilogue, four of converters).
-constexpr int kI8LaunchRegs = 80, kI8IssueRegs = 40, kI8EpiRegs = 56, kI8ConvRegs = 96;
-static_assert(kI8IssueRegs + kI8EpiRegs + 4 * kI8ConvRegs <= 6 * kI8LaunchRegs && kI8Threads == 768,
-              "the shares add up to no more than the block was launched with");
 
 enum : uint32_t {
     kRoleConvert = 6,
@@ -80,44 +81,67 @@ struct I8Params {
     void *d;
     long long ldd;
     int out_type;
+    int vec;     // rows of D start on multiples of four elements
     int inject;  // test hook: the role that waits on a barrier nothing arrives at
     unsigned long long timeout_ns;
     unsigned int *status;
 };
 
-// CG: CTAs sharing a tile of CG x 128 channels as a pair. BT: tokens per tile
-// (MMA N). KS: most CTAs sharing one tile's K (1: none do).
-template <int CG, int BT, int KS>
+// NS: rows of the N side of one MMA (narrow: tokens; wide: 256 channels).
+// KS: most CTAs sharing one tile's K (1: none do).
+template <int NS, int KS, bool WIDE>
 struct I8Cfg {
-    static constexpr int TOK = BT / CG;  // tokens widened by each CTA
-    static constexpr int CH = CG * kI8Channels;
-    static constexpr int ACC_STRIDE = BT < 32 ? 32 : BT;  // whole 32-column epilogue reads
-    static constexpr int A_COL0 = 2 * ACC_STRIDE;         // widened channels: 64 columns a stage
+    static constexpr int CG = WIDE ? 2 : 1;
+    static constexpr int TOKENS = WIDE ? 256 : NS, CHANNELS = WIDE ? NS : 128;  // of a tile
+    static constexpr int SIDE = NS / CG;                                        // N-side rows widened by each CTA
+    static constexpr int ISSUERS = WIDE ? 1 : 2;
+    static constexpr int EPI_WARPS = WIDE ? 8 : 4;
+    static constexpr int FIRST_CONV_WARP = kI8FirstEpiWarp + EPI_WARPS;
+    static constexpr int THREADS = 32 * (FIRST_CONV_WARP + 2 * kI8GroupWarps);
+    // TMEM: accumulators (buffers x issuers), then the widened M side, 64 columns a stage
+    static constexpr int ACC_STRIDE = NS < 32 ? 32 : NS;  // whole 32-column epilogue reads
+    static constexpr int ACC_BUFS = WIDE || NS == 128 ? 1 : 2;
+    static constexpr int A_COL0 = ACC_BUFS * ISSUERS * ACC_STRIDE;
     static constexpr int A_COLS = kI8K / 2;
     static constexpr int CONV_FIT = (512 - A_COL0) / A_COLS;
-    static constexpr int CONV_MOST = TOK >= 128 || (KS > 1 && BT >= 64) ? 2 : 4;  // what shared memory has room for
+    static constexpr int CONV_MOST = WIDE || (KS > 1 && NS >= 64) ? 2 : NS == 128 ? 3 : 4;  // shared memory has room for
     static constexpr int CONV_STAGES = CONV_FIT < CONV_MOST ? CONV_FIT : CONV_MOST;
-    static constexpr int RAW_W = kI8Channels * kI8K;
-    static constexpr int RAW_BYTES = RAW_W + TOK * kI8K;
-    static constexpr int CONV_BYTES = 2 * TOK * kI8K;  // two tiles of 64 elements of K
-    static constexpr int PART_BYTES = (KS - 1) * BT * kI8Channels * 4;
-    static constexpr int FIXED = CONV_STAGES * CONV_BYTES + PART_BYTES + 1024 /* alignment */ + 512 /* barriers */ +
-                                 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1);
+    static constexpr int RAW_M = kI8Rows * kI8K;
+    static constexpr int RAW_BYTES = RAW_M + SIDE * kI8K;
+    static constexpr int CONV_BYTES = 2 * SIDE * kI8K;  // two tiles of 64 elements of K
+    static constexpr int PART_BYTES = (KS - 1) * NS * kI8Rows * 4;
+    static constexpr int EPI_BYTES = WIDE ? EPI_WARPS * 4096 : 0;  // 32 x 32 fp32 a warp
+    static constexpr int FIXED = CONV_STAGES * CONV_BYTES + PART_BYTES + EPI_BYTES + 1024 /* alignment */ +
+                                 512 /* barriers */ + 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1);
     static constexpr int RAW_FIT = (kI8MaxSmem - FIXED) / RAW_BYTES;
     static constexpr int RAW_STAGES = RAW_FIT < 8 ? RAW_FIT : 8;
     static constexpr int CONV_OFF = RAW_STAGES * RAW_BYTES;
     static constexpr int PART_OFF = CONV_OFF + CONV_STAGES * CONV_BYTES;
-    static constexpr int BAR_OFF = PART_OFF + PART_BYTES;
+    static constexpr int EPI_OFF = PART_OFF + PART_BYTES;
+    static constexpr int BAR_OFF = EPI_OFF + EPI_BYTES;
     static constexpr int NUM_BARS = 2 * RAW_STAGES + 2 * CONV_STAGES + 4 + 3;
     static constexpr int MISC_OFF = BAR_OFF + 8 * NUM_BARS;
     static constexpr int TABLE_OFF = MISC_OFF + 16;
     static constexpr int CLUSTER = CG * KS;  // largest cluster
-    static constexpr int UNITS = (TOK * 8 + 32 * kI8GroupWarps - 1) / (32 * kI8GroupWarps);  // token units per thread
-    static_assert(CG == 1 || KS == 1, "pairs do not share K");
+    // 16-byte units of the N side of a stage per converter thread, and how many
+    // unit columns apart a thread's units lie
+    static constexpr int UNITS = SIDE * 8 < kI8GroupThreads ? 1 : SIDE * 8 / kI8GroupThreads;
+    static constexpr int UNIT_STEP = kI8GroupThreads / SIDE;
+    // Registers a thread: at launch, and after the warpgroups have shared them
+    // out (producer and issuers; epilogue; converters)
+    static constexpr int LAUNCH_REGS = WIDE ? 72 : 80;
+    static constexpr int ISSUE_REGS = WIDE ? 40 : 48;
+    static constexpr int EPI_REGS = WIDE ? 56 : NS == 128 ? 80 : 112;
+    static constexpr int CONV_REGS = WIDE || NS == 128 ? 88 : 80;
+    static constexpr int REG_TOTAL = 128 * (ISSUE_REGS + EPI_WARPS / 4 * EPI_REGS + 4 * CONV_REGS);
+    static_assert(REG_TOTAL <= THREADS * LAUNCH_REGS && THREADS * LAUNCH_REGS <= 65536,
+                  "the shares add up to no more than the block is launched with");
+    static_assert(!WIDE || (NS == 256 && KS == 1), "wide tiles: 256 channels, no shared K");
+    static_assert((SIDE & (SIDE - 1)) == 0 && SIDE >= 16 && SIDE <= 128, "unit arithmetic");
     static_assert(8 * NUM_BARS + 16 <= 512, "barriers");
-    static_assert(RAW_BYTES % 1024 == 0 && CONV_BYTES % 1024 == 0 && TOK * kI8K % 1024 == 0,
+    static_assert(RAW_BYTES % 1024 == 0 && CONV_BYTES % 1024 == 0 && SIDE * kI8K % 1024 == 0,
                   "swizzle atoms start on 1024-byte boundaries");
-    static_assert(BT % (16 * CG) == 0 && BT <= 256 && CONV_STAGES >= 2 && RAW_STAGES >= 3, "tile");
+    static_assert(CONV_STAGES >= 2 && RAW_STAGES >= 3, "stages");
 };
 
 // ---------------------------------------------------------------- tiles
@@ -134,9 +158,9 @@ struct I8Tile {
     int n0;
 };
 
-// Raster of one expert's (or the one matrix's) tiles: groups of 16 token
+// Raster of one expert's (or the one matrix's) tiles: groups of 8 token
 // tiles, so that tiles running together share panels of both operands.
-constexpr int kI8GroupM = 16;
+constexpr int kI8GroupM = 8;
 
 struct I8Sched {
     int experts, M, tiles_n, num_tiles;
@@ -246,18 +270,15 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
                      : "memory");
 }
 
-// Registers a thread of this warpgroup, given up or taken (every warp of the
-// warpgroup executes it).
-template <int N>
-__device__ __forceinline__ void reg_dec()
+// Changes the registers a thread of this warpgroup from FROM to TO (every warp
+// of the warpgroup executes it).
+template <int FROM, int TO>
+__device__ __forceinline__ void set_regs()
 {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-template <int N>
-__device__ __forceinline__ void reg_inc()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    if constexpr (TO < FROM)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TO));
+    else if constexpr (TO > FROM)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TO));
 }
 
 // Waiter::wait for the many warps of this kernel: a probe that does not find
@@ -344,27 +365,99 @@ __device__ __forceinline__ void store_scaled<__half>(__half *p, float v)
     *p = __float2half_rn(v);
 }
 
-// Scaled sums of one 32-token block, lane = channel n: D[m][n] for the block's
-// tokens that exist.
+// 32 columns of this lane's sums, from one accumulator or the sum of two.
+__device__ __forceinline__ void load_sums(uint32_t src0, uint32_t src1, bool both, float (&v)[32])
+{
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(src0, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = __uint_as_float(r[i]);
+    if (both) {
+        tmem_ld_32x32b_x32(src1, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] += __uint_as_float(r[i]);
+    }
+}
+
+// Scaled sums of one 32-token block, lane = channel: `out` is the channel's
+// column of D at the block's first token, `rows` of which exist. Eight tokens
+// at a time: their scales are fetched from the lanes that hold them before the
+// first of them is stored.
 template <typename D>
 __device__ __forceinline__ void store_block(D *out, long long ldd, const float (&v)[32], float sa, float sn, int rows, bool live)
 {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float sm = __shfl_sync(0xffffffffu, sa, i);
-        if (live && i < rows)
-            store_scaled<D>(out + i * ldd, v[i] * sm * sn);
+    for (int i = 0; i < 32; i += 8) {
+        if (i >= rows)
+            break;
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = v[i + j] * __shfl_sync(0xffffffffu, sa, i + j) * sn;
+        if (live) {
+            if (i + 8 <= rows) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    store_scaled<D>(out + (i + j) * ldd, x[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (i + j < rows)
+                        store_scaled<D>(out + (i + j) * ldd, x[j]);
+            }
+        }
+    }
+}
+
+// Four neighbouring channels of a row of D, of which `n` exist.
+__device__ __forceinline__ void store4(void *d, int type, long long at, const float4 &v, int n, bool vec)
+{
+    if (type == GEMM_OUT_F32) {
+        float *o = static_cast<float *>(d) + at;
+        if (vec && n >= 4) {
+            *reinterpret_cast<float4 *>(o) = v;
+        } else {
+            if (n > 0) o[0] = v.x;
+            if (n > 1) o[1] = v.y;
+            if (n > 2) o[2] = v.z;
+            if (n > 3) o[3] = v.w;
+        }
+        return;
+    }
+    uint32_t lo, hi;
+    if (type == GEMM_OUT_BF16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        lo = *reinterpret_cast<const uint32_t *>(&a);
+        hi = *reinterpret_cast<const uint32_t *>(&b);
+    } else {
+        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+        lo = *reinterpret_cast<const uint32_t *>(&a);
+        hi = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    unsigned short *o = static_cast<unsigned short *>(d) + at;
+    if (vec && n >= 4) {
+        *reinterpret_cast<uint2 *>(o) = make_uint2(lo, hi);
+    } else {
+        if (n > 0) o[0] = static_cast<unsigned short>(lo);
+        if (n > 1) o[1] = static_cast<unsigned short>(lo >> 16);
+        if (n > 2) o[2] = static_cast<unsigned short>(hi);
+        if (n > 3) o[3] = static_cast<unsigned short>(hi >> 16);
     }
 }
 
 // ---------------------------------------------------------------- kernel
 
-template <int CG, int BT, int KS>
-__global__ void __launch_bounds__(kI8Threads, 1)
+template <int NS, int KS, bool WIDE>
+__global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ I8Params p, const int ks)
 {
-    using C = I8Cfg<CG, BT, KS>;
+    using C = I8Cfg<NS, KS, WIDE>;
+    constexpr int CG = C::CG;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -399,12 +492,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             mbar_init(bar_conv_empty + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(bar_acc_full + 8 * b, 1);
-            mbar_init(bar_acc_empty + 8 * b, kEpiWarps * CG);
+            mbar_init(bar_acc_full + 8 * b, C::ISSUERS);
+            mbar_init(bar_acc_empty + 8 * b, C::EPI_WARPS * CG);
         }
-        mbar_init(bar_drain, 1);
+        mbar_init(bar_drain, C::ISSUERS);
         mbar_init(bar_inject, 1);
-        mbar_init(bar_part, cluster > 1 ? kEpiWarps * (cluster - 1) : 1);
+        mbar_init(bar_part, cluster > 1 ? C::EPI_WARPS * (cluster - 1) : 1);
         *abort_flag = 0u;
         fence_mbar_init();
         prefetch_tensormap(&tmA);
@@ -432,7 +525,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             if (lane == 0)
                 prev = e0 == 0 ? v : low;
             // tiles of expert e - 1, which lies between prev and v
-            int n = e <= p.experts ? i8_tiles(v - prev, BT) * p.tiles_n : 0;
+            int n = e <= p.experts ? i8_tiles(v - prev, C::TOKENS) * p.tiles_n : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, n, o);
@@ -467,7 +560,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     sched.tiles_n = p.tiles_n;
     sched.off = off;
     sched.tile_start = tile_start;
-    sched.num_tiles = p.experts ? tile_start[p.experts] : i8_tiles(p.M, BT) * p.tiles_n;
+    sched.num_tiles = p.experts ? tile_start[p.experts] : i8_tiles(p.M, C::TOKENS) * p.tiles_n;
     // this CTA's K blocks of a tile (zeros past the end of K)
     const int all_blocks = i8_tiles(p.K, kI8K);
     int kb0 = 0, kb1 = all_blocks;
@@ -475,11 +568,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         kb0 = static_cast<int>(static_cast<long long>(all_blocks) * rank / cluster);
         kb1 = static_cast<int>(static_cast<long long>(all_blocks) * (rank + 1) / cluster);
     }
-    const int n_off = CG == 2 ? rank * kI8Channels : 0;  // this CTA's channels within the tile
 
     ProducerTail tail{0, 0, 0u};
     if (warp < kI8FirstEpiWarp) {
-        reg_dec<kI8IssueRegs>();
+        set_regs<C::LAUNCH_REGS, C::ISSUE_REGS>();
         if (warp == 0 && lane == 0) {
             if (p.inject == kRoleProducer) {
                 w.wait(bar_inject, 0u, kRoleProducer | kWaitInjected);
@@ -488,16 +580,16 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 uint32_t phase = 0;
                 bool ok = true;
                 for (int t = cluster_id; ok && t < sched.num_tiles; t += clusters) {
-                    const I8Tile ti = i8_tile<BT, C::CH>(sched, t);
-                    const int m0 = ti.m0 + (CG == 2 ? rank * C::TOK : 0);
+                    const I8Tile ti = i8_tile<C::TOKENS, C::CHANNELS>(sched, t);
+                    const int m0 = ti.m0 + (WIDE ? rank * kI8Rows : 0), n0 = ti.n0 + (WIDE ? rank * C::SIDE : 0);
                     for (int kb = kb0; kb < kb1; ++kb) {
                         ok = w.wait(bar_raw_empty + 8 * stage, phase ^ 1u, kRoleProducer | kWaitEmpty);
                         if (!ok)
                             break;
                         const uint32_t dst = base + stage * C::RAW_BYTES, bar = bar_raw_full + 8 * stage;
                         mbar_arrive_expect_tx(bar, C::RAW_BYTES);
-                        tma_load_3d(dst, &tmB, bar, kb * kI8K, ti.n0 + n_off, ti.expert);
-                        tma_load_2d(dst + C::RAW_W, &tmA, bar, kb * kI8K, m0);
+                        tma_load_3d(WIDE ? dst + C::RAW_M : dst, &tmB, bar, kb * kI8K, n0, ti.expert);
+                        tma_load_2d(WIDE ? dst : dst + C::RAW_M, &tmA, bar, kb * kI8K, m0);
                         ++issued;
                         if (++stage == C::RAW_STAGES) {
                             stage = 0;
@@ -508,13 +600,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 tail = ProducerTail{issued < C::RAW_STAGES ? issued : C::RAW_STAGES, stage, phase};
             }
         }
-        if (warp == 1 && lane == 0 && (CG == 1 || rank == 0)) {
+        const int issuer = warp - 1;  // takes every ISSUERS-th stage
+        if (issuer >= 0 && issuer < C::ISSUERS && lane == 0 && (CG == 1 || rank == 0)) {
             if (p.inject == kRoleMma)
                 w.wait(bar_inject, 0u, kRoleMma | kWaitInjected);
-            const uint32_t idesc = make_idesc_f16(CG * kI8Channels, BT, 0, 0, 0);
-            const OperandPacking pk = operand_packing(0, 3, C::TOK, kI8K / 2);
+            const uint32_t idesc = make_idesc_f16(CG * kI8Rows, NS, 0, 0, 0);
+            const OperandPacking pk = operand_packing(0, 3, C::SIDE, kI8K / 2);
             const uint64_t b_desc = make_smem_desc(base + C::CONV_OFF, pk.lbo, pk.sbo, pk.swz);
-            int stage = 0, acc = 0;
+            int stage = issuer, acc = 0, skip = issuer;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = p.inject != kRoleMma;
             for (int t = cluster_id; ok && t < sched.num_tiles; t += clusters) {
@@ -522,8 +615,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 if (!ok)
                     break;
                 tc_fence_after_sync();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * C::ACC_STRIDE);
-                for (int kb = kb0; kb < kb1; ++kb) {
+                const uint32_t d = tmem_base + static_cast<uint32_t>((acc * C::ISSUERS + issuer) * C::ACC_STRIDE);
+                int kb = kb0 + skip;
+                uint32_t accumulate = 0;
+                for (; kb < kb1; kb += C::ISSUERS) {
                     ok = w.wait(bar_conv_full + 8 * stage, phase, kRoleMma | kWaitFull, CG == 2);
                     if (!ok)
                         break;
@@ -531,25 +626,27 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                     const uint32_t a = tmem_base + static_cast<uint32_t>(C::A_COL0 + stage * C::A_COLS);
                     const uint64_t b = b_desc + static_cast<uint64_t>((stage * C::CONV_BYTES) >> 4);
 #pragma unroll
-                    for (int j = 0; j < kI8K / 16; ++j)
-                        mma_f16_ta<CG>(d, a + 8 * j, b + (j >> 2) * ((C::TOK * kI8K) >> 4) + 2 * (j & 3), idesc,
-                                       ((kb - kb0) | j) != 0);
+                    for (int j = 0; j < kI8K / 16; ++j) {
+                        mma_f16_ta<CG>(d, a + 8 * j, b + (j >> 2) * ((C::SIDE * kI8K) >> 4) + 2 * (j & 3), idesc, accumulate);
+                        accumulate = 1;
+                    }
                     if constexpr (CG == 2)
                         mma_commit_pair_multicast(bar_conv_empty + 8 * stage);
                     else
                         mma_commit<1>(bar_conv_empty + 8 * stage);
-                    if (++stage == C::CONV_STAGES) {
-                        stage = 0;
+                    if ((stage += C::ISSUERS) >= C::CONV_STAGES) {
+                        stage -= C::CONV_STAGES;
                         phase ^= 1u;
                     }
                 }
                 if (!ok)
                     break;
+                skip = kb - kb1;
                 if constexpr (CG == 2)
                     mma_commit_pair_multicast(bar_acc_full + 8 * acc);
                 else
                     mma_commit<1>(bar_acc_full + 8 * acc);
-                if (++acc == 2) {
+                if (++acc == C::ACC_BUFS) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
@@ -558,40 +655,27 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             mma_commit<CG>(bar_drain);
             w.w.drain(bar_drain, 0u, 100000000ull);
         }
-    } else if (warp >= kI8FirstConvWarp) {
-        reg_inc<kI8ConvRegs>();
-        const int cw = warp - kI8FirstConvWarp;
+    } else if (warp >= C::FIRST_CONV_WARP) {
+        set_regs<C::LAUNCH_REGS, C::CONV_REGS>();
+        const int cw = warp - C::FIRST_CONV_WARP;
         const int group = cw / kI8GroupWarps;
         const int ct = (cw % kI8GroupWarps) * 32 + lane;  // thread within the group
         const int q = warp & 3;                           // TMEM lane quarter this warp may write
-        const int half = (cw >> 2) & 1;                   // the 64 elements of K of its channels
-        // This thread's share of a stage: one channel's 64 elements, and every
-        // 256th 16-byte unit of the tokens. Neighbouring threads take
-        // neighbouring rows, whose swizzled units lie in distinct banks. The
-        // offsets are computed once.
-        uint32_t w_at[4], x_at[C::UNITS], y_at[C::UNITS];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w_at[i] = static_cast<uint32_t>((32 * q + lane) * kI8K + (((4 * half + i) ^ (lane & 7)) << 4));
-#pragma unroll
-        for (int i = 0; i < C::UNITS; ++i) {
-            const int unit = i * 32 * kI8GroupWarps + ct;
-            const int r = unit % C::TOK, c = unit / C::TOK;
-            x_at[i] = static_cast<uint32_t>(C::RAW_W + r * kI8K + ((c ^ (r & 7)) << 4));
-            // the unit's two fp16 units: the second at the first's offset ^ 16
-            y_at[i] = static_cast<uint32_t>((c >> 2) * (C::TOK * kI8K) + r * kI8K + (((2 * (c & 3)) ^ (r & 7)) << 4));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            pin(w_at[i]);
-#pragma unroll
-        for (int i = 0; i < C::UNITS; ++i) {
-            pin(x_at[i]);
-            pin(y_at[i]);
-        }
-        constexpr bool kWholeUnits = 8 * C::TOK % (32 * kI8GroupWarps) == 0;
-        const bool has_unit = kWholeUnits || ct < 8 * C::TOK;  // fewer units than threads
-        static_assert(kWholeUnits || C::UNITS == 1, "every thread has the same number of units, or one at most");
+        const int half = (cw >> 2) & 1;                   // the 64 elements of K of its M-side row
+        // This thread's share of a stage: 64 elements of one M-side row, and
+        // every 256th 16-byte unit of the N side. Neighbouring threads take
+        // neighbouring rows, whose swizzled units lie in distinct banks. A
+        // unit's column enters its address by XOR, so that one offset serves
+        // all of a thread's units.
+        uint32_t w_at = static_cast<uint32_t>((32 * q + lane) * kI8K + (((4 * half) ^ (lane & 7)) << 4));
+        const int r = ct % C::SIDE, c0 = ct / C::SIDE;
+        uint32_t x_at = static_cast<uint32_t>(C::RAW_M + r * kI8K + ((c0 ^ (r & 7)) << 4));
+        // a raw unit fills two fp16 units: the second at the first's offset ^ 16
+        uint32_t y_at = static_cast<uint32_t>((c0 >> 2) * (C::SIDE * kI8K) + r * kI8K + (((2 * (c0 & 3)) ^ (r & 7)) << 4));
+        pin(w_at);
+        pin(x_at);
+        pin(y_at);
+        const bool has_unit = C::SIDE * 8 >= kI8GroupThreads || ct < C::SIDE * 8;  // fewer units than threads
         const uint32_t conv_full = CG == 2 ? mapa_shared(bar_conv_full, 0) : bar_conv_full;
         // the group's next stage, raw and widened: every second one
         int rs = group % C::RAW_STAGES, cs = group % C::CONV_STAGES;
@@ -610,11 +694,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                     uint4 u[4], x[C::UNITS];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        ld_shared_v4(raw + w_at[i], u[i].x, u[i].y, u[i].z, u[i].w);
+                        ld_shared_v4((raw + w_at) ^ static_cast<uint32_t>(i << 4), u[i].x, u[i].y, u[i].z, u[i].w);
 #pragma unroll
                     for (int i = 0; i < C::UNITS; ++i)
                         if (has_unit)
-                            ld_shared_v4(raw + x_at[i], x[i].x, x[i].y, x[i].z, x[i].w);
+                            ld_shared_v4((raw + x_at) ^ static_cast<uint32_t>((i * C::UNIT_STEP) << 4), x[i].x, x[i].y, x[i].z, x[i].w);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         widen16(u[i], hw + 8 * i);
@@ -643,7 +727,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 #pragma unroll
                 for (int i = 0; i < C::UNITS; ++i)
                     if (has_unit) {
-                        const uint32_t at = conv + y_at[i];
+                        const int c = i * C::UNIT_STEP;  // unit columns from the thread's first
+                        const uint32_t at = ((conv + y_at) ^ static_cast<uint32_t>((2 * (c & 3)) << 4)) +
+                                            static_cast<uint32_t>((c >> 2) * (C::SIDE * kI8K));
                         st_shared_v4(at, hx[i][0], hx[i][1], hx[i][2], hx[i][3]);
                         st_shared_v4(at ^ 16u, hx[i][4], hx[i][5], hx[i][6], hx[i][7]);
                     }
@@ -669,81 +755,131 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             skip = kb - kb1;  // 0 or 1 of the next tile's blocks is the other group's
         }
     } else {
-        reg_dec<kI8EpiRegs>();
+        set_regs<C::LAUNCH_REGS, C::EPI_REGS>();
         const int q = warp & 3;  // TMEM lane quarter of this warp
+        const int blocks = kb1 - kb0;
         int acc = 0;
         uint32_t acc_phase = 0;
-        const uint32_t acc_empty = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
+        int first = 0;  // narrow: the issuer of the tile's first block
         for (int t = cluster_id; t < sched.num_tiles; t += clusters) {
-            const I8Tile ti = i8_tile<BT, C::CH>(sched, t);
-            const int n = ti.n0 + n_off + 32 * q + lane;
-            const bool live = n < p.N;
-            const float sn = live ? p.sb[static_cast<long long>(ti.expert) * p.N + n] : 0.0f;
-            bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull, CG == 2);
-            if (!__all_sync(0xffffffffu, ok))
-                break;
-            tc_fence_after_sync();
-            const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc * C::ACC_STRIDE);
-            const int rows = min(ti.m1 - ti.m0, BT);
-            if (KS > 1 && rank > 0) {
-                // this CTA's sums to the first CTA, [rank - 1][token][channel]
-                const uint32_t part = mapa_shared(base + C::PART_OFF, 0) +
-                                      4u * static_cast<uint32_t>(((rank - 1) * BT) * kI8Channels + 32 * q + lane);
-                for (int c = 0; c < rows; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(src + c, r);
+            const I8Tile ti = i8_tile<C::TOKENS, C::CHANNELS>(sched, t);
+            const float *sb = p.sb + static_cast<long long>(ti.expert) * p.N;
+            if constexpr (WIDE) {
+                // lane = token, column = channel; this warp's 32 tokens x 128 channels
+                const int row0 = ti.m0 + rank * kI8Rows + 32 * q, n0 = ti.n0 + 128 * ((warp - kI8FirstEpiWarp) >> 2);
+                const float sa = row0 + lane < ti.m1 ? p.sa[row0 + lane] : 0.0f;
+                bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull, true);
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                tc_fence_after_sync();
+                const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(n0 - ti.n0);
+                const uint32_t stage = base + static_cast<uint32_t>(C::EPI_OFF + (warp - kI8FirstEpiWarp) * 4096);
+                const int lr = lane >> 3, lc = lane & 7;  // this lane's row (of four) and four channels of a chunk's store
+                const int rows = ti.m1 - row0;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(src + 32 * c, v);
+                    const int n = n0 + 32 * c + 4 * lc;
+                    float4 sn;
+                    sn.x = n < p.N ? sb[n] : 0.0f;
+                    sn.y = n + 1 < p.N ? sb[n + 1] : 0.0f;
+                    sn.z = n + 2 < p.N ? sb[n + 2] : 0.0f;
+                    sn.w = n + 3 < p.N ? sb[n + 3] : 0.0f;
                     tmem_ld_wait();
+                    if (c == 3) {  // the accumulator has been read: the next tile's MMAs may start
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_peer(mapa_shared(bar_acc_empty + 8 * acc, 0));
+                    }
+                    // through a swizzled 32 x 32 tile, so that rows of D are written in whole 64- or 128-byte pieces
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c + i < rows)
-                            st_cluster_f32(part + 4u * static_cast<uint32_t>((c + i) * kI8Channels), __uint_as_float(r[i]));
+                    for (int u = 0; u < 8; ++u)
+                        st_shared_v4(stage + lane * 128 + ((u ^ (lane & 7)) << 4),
+                                     __float_as_uint(__uint_as_float(v[4 * u]) * sa), __float_as_uint(__uint_as_float(v[4 * u + 1]) * sa),
+                                     __float_as_uint(__uint_as_float(v[4 * u + 2]) * sa), __float_as_uint(__uint_as_float(v[4 * u + 3]) * sa));
+                    __syncwarp();
+                    const long long at = static_cast<long long>(row0 + lr) * p.ldd + n;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 4 * i + lr;
+                        uint32_t x[4];
+                        ld_shared_v4(stage + row * 128 + ((lc ^ (row & 7)) << 4), x[0], x[1], x[2], x[3]);
+                        if (row < rows)
+                            store4(p.d, p.out_type, at + 4 * i * p.ldd,
+                                   make_float4(__uint_as_float(x[0]) * sn.x, __uint_as_float(x[1]) * sn.y,
+                                               __uint_as_float(x[2]) * sn.z, __uint_as_float(x[3]) * sn.w),
+                                   p.N - n, p.vec != 0);
+                    }
+                    __syncwarp();
                 }
+            } else {
+                // lane = channel, column = token
+                const int n = ti.n0 + 32 * q + lane;
+                const bool live = n < p.N;
+                const float sn = live ? sb[n] : 0.0f;
+                bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull);
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                tc_fence_after_sync();
+                // the issuers' sums; a single block leaves one of them unwritten
+                const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                       static_cast<uint32_t>(acc * C::ISSUERS * C::ACC_STRIDE);
+                const uint32_t src0 = lanes + static_cast<uint32_t>(blocks > 1 ? 0 : first * C::ACC_STRIDE);
+                const uint32_t src1 = lanes + static_cast<uint32_t>(C::ACC_STRIDE);
+                first = (first + blocks) & 1;
+                const int rows = min(ti.m1 - ti.m0, NS);
+                if (KS > 1 && rank > 0) {
+                    // this CTA's sums to the first CTA, [rank - 1][token][channel]
+                    const uint32_t part = mapa_shared(base + C::PART_OFF, 0) +
+                                          4u * static_cast<uint32_t>(((rank - 1) * NS) * kI8Rows + 32 * q + lane);
+                    for (int c = 0; c < rows; c += 32) {
+                        float v[32];
+                        load_sums(src0 + c, src1 + c, blocks > 1, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < rows)
+                                st_cluster_f32(part + 4u * static_cast<uint32_t>((c + i) * kI8Rows), v[i]);
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(mapa_shared(bar_part, 0));
+                } else {
+                    if (KS > 1 && cluster > 1) {
+                        ok = w.wait(bar_part, 0u, kRoleEpilogue | kWaitSplit, true);
+                        if (!__all_sync(0xffffffffu, ok))
+                            break;
+                    }
+                    for (int c = 0; c < rows; c += 32) {
+                        const int left = rows - c;
+                        const float sa = lane < left ? p.sa[ti.m0 + c + lane] : 0.0f;
+                        float v[32];
+                        load_sums(src0 + c, src1 + c, blocks > 1, v);
+                        if constexpr (KS > 1) {
+                            const float *part = reinterpret_cast<const float *>(smem + C::PART_OFF) + c * kI8Rows + 32 * q + lane;
+                            for (int k = 1; k < cluster; ++k, part += NS * kI8Rows) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i < left)
+                                        v[i] += part[i * kI8Rows];
+                            }
+                        }
+                        const long long at = static_cast<long long>(ti.m0 + c) * p.ldd + n;
+                        if (p.out_type == GEMM_OUT_F32)
+                            store_block(static_cast<float *>(p.d) + at, p.ldd, v, sa, sn, left, live);
+                        else if (p.out_type == GEMM_OUT_BF16)
+                            store_block(static_cast<__nv_bfloat16 *>(p.d) + at, p.ldd, v, sa, sn, left, live);
+                        else
+                            store_block(static_cast<__half *>(p.d) + at, p.ldd, v, sa, sn, left, live);
+                    }
+                }
+                tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(mapa_shared(bar_part, 0));
-            } else {
-                if (KS > 1 && cluster > 1) {
-                    ok = w.wait(bar_part, 0u, kRoleEpilogue | kWaitSplit, true);
-                    if (!__all_sync(0xffffffffu, ok))
-                        break;
-                }
-                for (int c = 0; c < rows; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(src + c, r);
-                    const int left = rows - c;
-                    const float sa = lane < left ? p.sa[ti.m0 + c + lane] : 0.0f;
-                    tmem_ld_wait();
-                    float v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = __uint_as_float(r[i]);
-                    if constexpr (KS > 1) {
-                        const float *part = reinterpret_cast<const float *>(smem + C::PART_OFF) + c * kI8Channels + 32 * q + lane;
-                        for (int k = 1; k < cluster; ++k, part += BT * kI8Channels) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < left)
-                                    v[i] += part[i * kI8Channels];
-                        }
-                    }
-                    const long long at = static_cast<long long>(ti.m0 + c) * p.ldd + n;
-                    if (p.out_type == GEMM_OUT_F32)
-                        store_block(static_cast<float *>(p.d) + at, p.ldd, v, sa, sn, left, live);
-                    else if (p.out_type == GEMM_OUT_BF16)
-                        store_block(static_cast<__nv_bfloat16 *>(p.d) + at, p.ldd, v, sa, sn, left, live);
-                    else
-                        store_block(static_cast<__half *>(p.d) + at, p.ldd, v, sa, sn, left, live);
-                }
+                    mbar_arrive(bar_acc_empty + 8 * acc);
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 2)
-                    mbar_arrive_cluster(acc_empty + 8 * acc);
-                else
-                    mbar_arrive(acc_empty + 8 * acc);
-            }
-            if (++acc == 2) {
+            if (++acc == C::ACC_BUFS) {
                 acc = 0;
                 acc_phase ^= 1u;
             }
@@ -779,27 +915,35 @@ __global__ void int8_zero_kernel(const I8Params p)
             store_scaled<D>(static_cast<D *>(p.d) + (i + first) * p.ldd + n, 0.0f);
 }
 
-template <int CG, int BT, int KS>
+template <int NS, int KS, bool WIDE>
 std::atomic<uint64_t> i8_attribute_set[2] = {{0}, {0}};
 
-// Launches tiles of CG x 128 channels and BT tokens, `ks` CTAs sharing a
-// tile's K (1 unless the kernel is built for it and every tile has a cluster
-// of its own).
-template <int CG, int BT, int KS>
+// Launches tiles of 128 channels x NS tokens, `ks` CTAs sharing a tile's K (1
+// unless the kernel is built for it and every tile has a cluster of its own),
+// or wide tiles.
+template <int NS, int KS, bool WIDE>
 gemm_status_t launch_int8(const CUtensorMap &a, const CUtensorMap &b, const I8Params &p, int ks, int sms, cudaStream_t st)
 {
-    using C = I8Cfg<CG, BT, KS>;
-    auto kern = int8_gemm_kernel<CG, BT, KS>;
+    using C = I8Cfg<NS, KS, WIDE>;
+    auto kern = int8_gemm_kernel<NS, KS, WIDE>;
     constexpr int kBase = C::TABLE_OFF + 1024;
-    if (ensure_smem_attribute(kern, kBase + 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1), i8_attribute_set<CG, BT, KS>) != cudaSuccess)
+    if (ensure_smem_attribute(kern, kBase + 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1), i8_attribute_set<NS, KS, WIDE>) != cudaSuccess)
         return GEMM_ERR_CUDA;
+    // the register shares were added up for this many registers at launch
+    static const bool regs_ok = [&] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs * C::THREADS >= C::REG_TOTAL &&
+               at.numRegs <= C::LAUNCH_REGS;
+    }();
+    if (!regs_ok)
+        return GEMM_ERR_UNSUPPORTED;
     // tiles of the launch, or for experts the most there can be
-    const int64_t tiles_m = (static_cast<int64_t>(p.M) + BT - 1) / BT + (p.experts ? std::min(p.experts, p.M) : 0);
+    const int64_t tiles_m = (static_cast<int64_t>(p.M) + C::TOKENS - 1) / C::TOKENS + (p.experts ? std::min(p.experts, p.M) : 0);
     const int64_t tiles = tiles_m * p.tiles_n;
-    const int cluster = CG * ks;
+    const int cluster = C::CG * ks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(KS > 1 ? tiles * cluster : std::min<int64_t>(tiles, sms / cluster) * cluster), 1, 1);
-    cfg.blockDim = dim3(kI8Threads, 1, 1);
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
     cfg.dynamicSmemBytes = kBase + (p.experts ? 2 * 4 * (p.experts + 1) : 0);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -816,27 +960,26 @@ gemm_status_t launch_int8(const CUtensorMap &a, const CUtensorMap &b, const I8Pa
     return host_launched();
 }
 
-// How a product is cut: CTAs per tile of channels, tokens per tile, CTAs
-// sharing a tile's K.
+// How a product is cut: wide tiles, or narrow ones of `ns` tokens with `ks`
+// CTAs sharing a tile's K.
 struct I8Plan {
-    int cg, bt, ks;
+    bool wide;
+    int ns, ks;
+    int tokens() const { return wide ? 256 : ns; }
+    int channels() const { return wide ? 256 : 128; }
 };
 
 I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms)
 {
     const int64_t rows = E ? (M + E - 1) / E : M;  // of one matrix, on average
-    I8Plan pl = {1, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1};
-    if (pl.bt == 128 && N > kI8Channels) {
-        // pairs; 192 tokens where that takes fewer token-rounds of the pairs
-        pl.cg = 2;
-        const int64_t tn = (N + 255) / 256, pairs = sms / 2;
-        auto rounds = [&](int bt) { return ((E ? E * ((rows + bt - 1) / bt) : (M + bt - 1) / bt) * tn + pairs - 1) / pairs * bt; };
-        if (rows > 128 && rounds(192) <= rounds(128) + rounds(128) / 8)
-            pl.bt = 192;
+    I8Plan pl = {false, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1};
+    if (rows > 128 && N > 128) {
+        pl.wide = true;
+        return pl;
     }
-    if (E == 0 && pl.cg == 1 && pl.bt <= 64) {
-        const int64_t tiles = (M + pl.bt - 1) / pl.bt * ((N + kI8Channels - 1) / kI8Channels);
-        const int most = pl.bt == 16 ? 8 : 4;
+    if (E == 0 && pl.ns <= 64) {
+        const int64_t tiles = (M + pl.ns - 1) / pl.ns * ((N + 127) / 128);
+        const int most = pl.ns == 16 ? 8 : 4;
         const int64_t blocks = (K + kI8K - 1) / kI8K;
         while (pl.ks < most && tiles * pl.ks * 2 <= sms && blocks >= 4 * pl.ks)
             pl.ks *= 2;
@@ -847,13 +990,13 @@ I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms)
 gemm_status_t launch_int8_plan(const CUtensorMap &a, const CUtensorMap &b, const I8Params &p, const I8Plan &pl, int sms,
                                cudaStream_t st)
 {
-    if (pl.cg == 2)
-        return pl.bt == 192 ? launch_int8<2, 192, 1>(a, b, p, 1, sms, st) : launch_int8<2, 128, 1>(a, b, p, 1, sms, st);
-    switch (pl.bt) {
-    case 16: return pl.ks > 1 ? launch_int8<1, 16, 8>(a, b, p, pl.ks, sms, st) : launch_int8<1, 16, 1>(a, b, p, 1, sms, st);
-    case 32: return pl.ks > 1 ? launch_int8<1, 32, 4>(a, b, p, pl.ks, sms, st) : launch_int8<1, 32, 1>(a, b, p, 1, sms, st);
-    case 64: return pl.ks > 1 ? launch_int8<1, 64, 4>(a, b, p, pl.ks, sms, st) : launch_int8<1, 64, 1>(a, b, p, 1, sms, st);
-    default: return launch_int8<1, 128, 1>(a, b, p, 1, sms, st);
+    if (pl.wide)
+        return launch_int8<256, 1, true>(a, b, p, 1, sms, st);
+    switch (pl.ns) {
+    case 16: return pl.ks > 1 ? launch_int8<16, 8, false>(a, b, p, pl.ks, sms, st) : launch_int8<16, 1, false>(a, b, p, 1, sms, st);
+    case 32: return pl.ks > 1 ? launch_int8<32, 4, false>(a, b, p, pl.ks, sms, st) : launch_int8<32, 1, false>(a, b, p, 1, sms, st);
+    case 64: return pl.ks > 1 ? launch_int8<64, 4, false>(a, b, p, pl.ks, sms, st) : launch_int8<64, 1, false>(a, b, p, 1, sms, st);
+    default: return launch_int8<128, 1, false>(a, b, p, 1, sms, st);
     }
 }
 
@@ -894,6 +1037,7 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     p.d = D;
     p.ldd = ldd;
     p.out_type = d_type;
+    p.vec = aligned_to(D, 4 * od) && ldd % 4 == 0;
     p.status = status;
     if (K == 0) {
         const int grid = static_cast<int>(std::min<int64_t>(M, 8 * sms));
@@ -909,15 +1053,15 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     p.inject = host_take_injection(&ms);
     p.timeout_ns = static_cast<unsigned long long>(ms > 0 ? ms : 2000) * 1000000ull;
     const I8Plan pl = int8_plan(M, N, K, E, sms);
-    const int64_t tiles_n = (N + pl.cg * kI8Channels - 1) / (pl.cg * kI8Channels);
-    if (tiles_n * ((M + pl.bt - 1) / pl.bt + (E ? std::min(E, M) : 0)) > kSizeLimit)
+    const int64_t tiles_n = (N + pl.channels() - 1) / pl.channels();
+    if (tiles_n * ((M + pl.tokens() - 1) / pl.tokens() + (E ? std::min(E, M) : 0)) > kSizeLimit)
         return GEMM_ERR_UNSUPPORTED;
     p.tiles_n = static_cast<int>(tiles_n);
     CUtensorMap a, b;
     {
         const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(M)};
         const uint64_t strides[1] = {static_cast<uint64_t>(lda)};
-        const uint32_t box[2] = {kI8K, static_cast<uint32_t>(pl.bt / pl.cg)};
+        const uint32_t box[2] = {kI8K, static_cast<uint32_t>(pl.wide ? kI8Rows : pl.ns)};
         if ((s = host_encode_tiled(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) !=
             GEMM_OK)
             return s;
@@ -925,7 +1069,7 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     {
         const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E ? E : 1)};
         const uint64_t strides[2] = {static_cast<uint64_t>(ldb), static_cast<uint64_t>(E > 1 ? stride_b : ldb)};
-        const uint32_t box[3] = {kI8K, kI8Channels, 1};
+        const uint32_t box[3] = {kI8K, 128, 1};
         if ((s = host_encode_tiled(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, B, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) !=
             GEMM_OK)
             return s;
