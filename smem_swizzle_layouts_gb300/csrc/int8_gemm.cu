@@ -104,17 +104,21 @@ struct I8Cfg {
     static constexpr int A_COL0 = ACC_BUFS * ISSUERS * ACC_STRIDE;
     static constexpr int A_COLS = kI8K / 2;
     static constexpr int CONV_FIT = (512 - A_COL0) / A_COLS;
-    static constexpr int CONV_MOST = WIDE || (KS > 1 && NS >= 64) ? 2 : NS == 128 ? 3 : 4;  // shared memory has room for
+    static constexpr int CONV_MOST = WIDE || NS == 128 ? 2 : 4;  // shared memory has room for
+    // Both rings have an even number of stages: the two converter groups (and
+    // the two issuers) take alternate blocks, so each stage always belongs to
+    // the same one. With an odd number a group that runs ahead would wait for
+    // the phase after next of a barrier, whose parity is that of the last one.
     static constexpr int CONV_STAGES = CONV_FIT < CONV_MOST ? CONV_FIT : CONV_MOST;
     static constexpr int RAW_M = kI8Rows * kI8K;
     static constexpr int RAW_BYTES = RAW_M + SIDE * kI8K;
     static constexpr int CONV_BYTES = 2 * SIDE * kI8K;  // two tiles of 64 elements of K
     static constexpr int PART_BYTES = (KS - 1) * NS * kI8Rows * 4;
-    static constexpr int EPI_BYTES = WIDE ? EPI_WARPS * 4096 : 0;  // 32 x 32 fp32 a warp
+    static constexpr int EPI_BYTES = WIDE ? EPI_WARPS * 2048 : 0;  // 16 x 32 fp32 a warp
     static constexpr int FIXED = CONV_STAGES * CONV_BYTES + PART_BYTES + EPI_BYTES + 1024 /* alignment */ +
                                  512 /* barriers */ + 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1);
     static constexpr int RAW_FIT = (kI8MaxSmem - FIXED) / RAW_BYTES;
-    static constexpr int RAW_STAGES = RAW_FIT < 8 ? RAW_FIT : 8;
+    static constexpr int RAW_STAGES = RAW_FIT < 8 ? RAW_FIT & ~1 : 8;
     static constexpr int CONV_OFF = RAW_STAGES * RAW_BYTES;
     static constexpr int PART_OFF = CONV_OFF + CONV_STAGES * CONV_BYTES;
     static constexpr int EPI_OFF = PART_OFF + PART_BYTES;
@@ -141,7 +145,7 @@ struct I8Cfg {
     static_assert(8 * NUM_BARS + 16 <= 512, "barriers");
     static_assert(RAW_BYTES % 1024 == 0 && CONV_BYTES % 1024 == 0 && SIDE * kI8K % 1024 == 0,
                   "swizzle atoms start on 1024-byte boundaries");
-    static_assert(CONV_STAGES >= 2 && RAW_STAGES >= 3, "stages");
+    static_assert(CONV_STAGES % 2 == 0 && RAW_STAGES % 2 == 0 && CONV_STAGES >= 2 && RAW_STAGES >= 4, "stages");
 };
 
 // ---------------------------------------------------------------- tiles
@@ -413,40 +417,47 @@ __device__ __forceinline__ void store_block(D *out, long long ldd, const float (
     }
 }
 
-// Four neighbouring channels of a row of D, of which `n` exist.
-__device__ __forceinline__ void store4(void *d, int type, long long at, const float4 &v, int n, bool vec)
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr)
 {
-    if (type == GEMM_OUT_F32) {
-        float *o = static_cast<float *>(d) + at;
-        if (vec && n >= 4) {
-            *reinterpret_cast<float4 *>(o) = v;
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store1(void *d, int type, long long at, float v)
+{
+    if (type == GEMM_OUT_F32)
+        static_cast<float *>(d)[at] = v;
+    else if (type == GEMM_OUT_BF16)
+        static_cast<__nv_bfloat16 *>(d)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half *>(d)[at] = __float2half_rn(v);
+}
+
+// Four neighbouring channels of a row of D (its address a multiple of four
+// elements), of which `n` exist.
+__device__ __forceinline__ void store4(void *d, int type, long long at, const float4 &v, int n)
+{
+    if (n >= 4) {
+        if (type == GEMM_OUT_F32) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(d) + at) = v;
+        } else if (type == GEMM_OUT_BF16) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(d) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
         } else {
-            if (n > 0) o[0] = v.x;
-            if (n > 1) o[1] = v.y;
-            if (n > 2) o[2] = v.z;
-            if (n > 3) o[3] = v.w;
+            const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+            *reinterpret_cast<uint2 *>(static_cast<__half *>(d) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
         }
         return;
     }
-    uint32_t lo, hi;
-    if (type == GEMM_OUT_BF16) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-        lo = *reinterpret_cast<const uint32_t *>(&a);
-        hi = *reinterpret_cast<const uint32_t *>(&b);
-    } else {
-        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-        lo = *reinterpret_cast<const uint32_t *>(&a);
-        hi = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    unsigned short *o = static_cast<unsigned short *>(d) + at;
-    if (vec && n >= 4) {
-        *reinterpret_cast<uint2 *>(o) = make_uint2(lo, hi);
-    } else {
-        if (n > 0) o[0] = static_cast<unsigned short>(lo);
-        if (n > 1) o[1] = static_cast<unsigned short>(lo >> 16);
-        if (n > 2) o[2] = static_cast<unsigned short>(hi);
-        if (n > 3) o[3] = static_cast<unsigned short>(hi >> 16);
-    }
+    if (n > 0)
+        store1(d, type, at, v.x);
+    if (n > 1)
+        store1(d, type, at + 1, v.y);
+    if (n > 2)
+        store1(d, type, at + 2, v.z);
 }
 
 // ---------------------------------------------------------------- kernel
@@ -773,7 +784,7 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
                     break;
                 tc_fence_after_sync();
                 const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(n0 - ti.n0);
-                const uint32_t stage = base + static_cast<uint32_t>(C::EPI_OFF + (warp - kI8FirstEpiWarp) * 4096);
+                const uint32_t stage = base + static_cast<uint32_t>(C::EPI_OFF + (warp - kI8FirstEpiWarp) * 2048);
                 const int lr = lane >> 3, lc = lane & 7;  // this lane's row (of four) and four channels of a chunk's store
                 const int rows = ti.m1 - row0;
 #pragma unroll 1
@@ -793,26 +804,47 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
                         if (lane == 0)
                             mbar_arrive_peer(mapa_shared(bar_acc_empty + 8 * acc, 0));
                     }
-                    // through a swizzled 32 x 32 tile, so that rows of D are written in whole 64- or 128-byte pieces
+                    // through a swizzled tile, 16 tokens at a time, so that rows of D are
+                    // written in whole 64- or 128-byte pieces
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        if ((lane >> 4) == half) {
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        st_shared_v4(stage + lane * 128 + ((u ^ (lane & 7)) << 4),
-                                     __float_as_uint(__uint_as_float(v[4 * u]) * sa), __float_as_uint(__uint_as_float(v[4 * u + 1]) * sa),
-                                     __float_as_uint(__uint_as_float(v[4 * u + 2]) * sa), __float_as_uint(__uint_as_float(v[4 * u + 3]) * sa));
-                    __syncwarp();
-                    const long long at = static_cast<long long>(row0 + lr) * p.ldd + n;
+                            for (int u = 0; u < 8; ++u)
+                                st_shared_v4(stage + (lane & 15) * 128 + ((u ^ (lane & 7)) << 4),
+                                             __float_as_uint(__uint_as_float(v[4 * u]) * sa),
+                                             __float_as_uint(__uint_as_float(v[4 * u + 1]) * sa),
+                                             __float_as_uint(__uint_as_float(v[4 * u + 2]) * sa),
+                                             __float_as_uint(__uint_as_float(v[4 * u + 3]) * sa));
+                        }
+                        __syncwarp();
+                        if (p.vec) {
+                            // four rows at a time, four channels a lane
+                            const long long at = static_cast<long long>(row0 + 16 * half + lr) * p.ldd + n;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = 4 * i + lr;
-                        uint32_t x[4];
-                        ld_shared_v4(stage + row * 128 + ((lc ^ (row & 7)) << 4), x[0], x[1], x[2], x[3]);
-                        if (row < rows)
-                            store4(p.d, p.out_type, at + 4 * i * p.ldd,
-                                   make_float4(__uint_as_float(x[0]) * sn.x, __uint_as_float(x[1]) * sn.y,
-                                               __uint_as_float(x[2]) * sn.z, __uint_as_float(x[3]) * sn.w),
-                                   p.N - n, p.vec != 0);
+                            for (int i = 0; i < 4; ++i) {
+                                const int row = 4 * i + lr;
+                                uint32_t x[4];
+                                ld_shared_v4(stage + row * 128 + ((lc ^ (row & 7)) << 4), x[0], x[1], x[2], x[3]);
+                                if (16 * half + row < rows)
+                                    store4(p.d, p.out_type, at + 4 * i * p.ldd,
+                                           make_float4(__uint_as_float(x[0]) * sn.x, __uint_as_float(x[1]) * sn.y,
+                                                       __uint_as_float(x[2]) * sn.z, __uint_as_float(x[3]) * sn.w),
+                                           p.N - n);
+                            }
+                        } else {
+                            // rows of D start anywhere: a row at a time, a channel a lane
+                            const int n1 = n0 + 32 * c + lane;
+                            const float s1 = n1 < p.N ? sb[n1] : 0.0f;
+                            const long long at = static_cast<long long>(row0 + 16 * half) * p.ldd + n1;
+                            for (int row = 0; row < 16 && 16 * half + row < rows; ++row) {
+                                const float x = ld_shared_f32(stage + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + 4 * (lane & 3));
+                                if (n1 < p.N)
+                                    store1(p.d, p.out_type, at + row * p.ldd, x * s1);
+                            }
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             } else {
                 // lane = channel, column = token
@@ -979,7 +1011,7 @@ I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms)
     }
     if (E == 0 && pl.ns <= 64) {
         const int64_t tiles = (M + pl.ns - 1) / pl.ns * ((N + 127) / 128);
-        const int most = pl.ns == 16 ? 8 : 4;
+        const int most = pl.ns == 16 ? 8 : pl.ns == 32 ? 4 : 2;
         const int64_t blocks = (K + kI8K - 1) / kI8K;
         while (pl.ks < most && tiles * pl.ks * 2 <= sms && blocks >= 4 * pl.ks)
             pl.ks *= 2;
@@ -995,7 +1027,7 @@ gemm_status_t launch_int8_plan(const CUtensorMap &a, const CUtensorMap &b, const
     switch (pl.ns) {
     case 16: return pl.ks > 1 ? launch_int8<16, 8, false>(a, b, p, pl.ks, sms, st) : launch_int8<16, 1, false>(a, b, p, 1, sms, st);
     case 32: return pl.ks > 1 ? launch_int8<32, 4, false>(a, b, p, pl.ks, sms, st) : launch_int8<32, 1, false>(a, b, p, 1, sms, st);
-    case 64: return pl.ks > 1 ? launch_int8<64, 4, false>(a, b, p, pl.ks, sms, st) : launch_int8<64, 1, false>(a, b, p, 1, sms, st);
+    case 64: return pl.ks > 1 ? launch_int8<64, 2, false>(a, b, p, pl.ks, sms, st) : launch_int8<64, 1, false>(a, b, p, 1, sms, st);
     default: return launch_int8<128, 1, false>(a, b, p, 1, sms, st);
     }
 }

@@ -83,6 +83,42 @@ def test_product_large_tiles(g):
         assert torch.equal(D, y)
 
 
+@pytest.mark.parametrize("M", [1, 8, 16, 32, 64, 128, 200, 600])
+@pytest.mark.parametrize("N,K", [(1000, 4096), (20000, 2048), (40960, 1152)])
+def test_long_rows_many_times(g, M, N, K):
+    """Many stages and tiles a CTA on every tile shape, launched over and over: every result the same, and right."""
+    rng = np.random.default_rng(M + N)
+    _, ad = int8_matrix(rng, M, K, K, -30, 30)
+    _, bd = int8_matrix(rng, N, K, K, -30, 30)
+    sa, sb = torch.rand(M, device=DEV), torch.rand(N, device=DEV)
+    y = (ad.double() @ bd.double().t()).float() * sa[:, None] * sb
+    outs = [torch.empty(M, N, device=DEV) for _ in range(12)]
+    for D in outs:
+        g.gemm_int8(M, N, K, ad, K, sa, bd, K, sb, D, N, 0)
+    ok(g)
+    assert all(torch.equal(D, y) for D in outs)
+
+
+@pytest.mark.parametrize("M,E", [(96, 64), (1500, 64), (4000, 64), (9000, 33)])
+def test_experts_many_times(g, M, E):
+    rng = np.random.default_rng(M)
+    N, K = 512, 2048
+    _, ad = int8_matrix(rng, M, K, K, -30, 30)
+    _, bd = int8_matrix(rng, E * N, K, K, -30, 30)
+    sa, sb = torch.rand(M, device=DEV), torch.rand(E, N, device=DEV)
+    cut = np.concatenate([[0], np.sort(rng.integers(0, M + 1, E - 1)), [M]])
+    y = torch.empty(M, N, device=DEV)
+    for e in range(E):
+        lo, hi = int(cut[e]), int(cut[e + 1])
+        y[lo:hi] = (ad[lo:hi].double() @ bd[e * N:(e + 1) * N].double().t()).float() * sa[lo:hi, None] * sb[e]
+    off = torch.from_numpy(cut.astype(np.int32)).to(DEV)
+    outs = [torch.empty(M, N, device=DEV) for _ in range(12)]
+    for D in outs:
+        g.gemm_int8_grouped(M, N, K, E, off, ad, K, sa, bd, K, N * K, sb, D, N, 0)
+    ok(g)
+    assert all(torch.equal(D, y) for D in outs)
+
+
 def test_sums_past_two_to_the_24(g):
     M, N, K = 40, 160, 16384
     rng = np.random.default_rng(4)
