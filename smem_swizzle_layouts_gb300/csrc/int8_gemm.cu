@@ -28,16 +28,18 @@
 //   wide    256 tokens on the M side, 256 channels on the N side, CTA pairs
 //           (cta_group::2; each CTA widens its 128 tokens and half of the
 //           channels): a stage's eight MMAs take 1024 cycles and keep the
-//           tensor pipe fed. The accumulator's 256 columns and the widened
-//           stages fill TMEM, so a tile's epilogue does not overlap the next
-//           tile's MMAs; eight warps empty it.
+//           tensor pipe fed. One accumulator of 256 columns fits beside the
+//           widened stages, so what counts is how soon it is empty again: the
+//           sixteen converter warps widen the first blocks of the next tile,
+//           take the accumulator into registers at one go, and store it while
+//           the MMAs run on those blocks.
 //
 // Warp roles of a CTA:
 //   warp 0       TMA producer: raw int8 stages of 128 elements of K;
 //   warp 1       TMEM allocator and MMA issuer (pairs: of the even CTA);
 //   warp 2       narrow: second MMA issuer; warp 3 completes the warpgroup;
-//   warps 4-     epilogue (four warps, wide eight);
-//   the last 16  converters in two groups of 8 warps that take alternate
+//   warps 4-7    narrow: epilogue;
+//   the last 16  converters (wide: and epilogue) in two groups of 8 warps that take alternate
 //                stages; a group reads and widens a stage into registers
 //                before it waits for room to write it. The warpgroups share
 //                the registers out by need (setmaxnreg).
@@ -95,7 +97,7 @@ struct I8Cfg {
     static constexpr int TOKENS = WIDE ? 256 : NS, CHANNELS = WIDE ? NS : 128;  // of a tile
     static constexpr int SIDE = NS / CG;                                        // N-side rows widened by each CTA
     static constexpr int ISSUERS = WIDE ? 1 : 2;
-    static constexpr int EPI_WARPS = WIDE ? 8 : 4;
+    static constexpr int EPI_WARPS = WIDE ? 0 : 4;  // of their own
     static constexpr int FIRST_CONV_WARP = kI8FirstEpiWarp + EPI_WARPS;
     static constexpr int THREADS = 32 * (FIRST_CONV_WARP + 2 * kI8GroupWarps);
     // TMEM: accumulators (buffers x issuers), then the widened M side, 64 columns a stage
@@ -114,7 +116,7 @@ struct I8Cfg {
     static constexpr int RAW_BYTES = RAW_M + SIDE * kI8K;
     static constexpr int CONV_BYTES = 2 * SIDE * kI8K;  // two tiles of 64 elements of K
     static constexpr int PART_BYTES = (KS - 1) * NS * kI8Rows * 4;
-    static constexpr int EPI_BYTES = WIDE ? EPI_WARPS * 2048 : 0;  // 16 x 32 fp32 a warp
+    static constexpr int EPI_BYTES = WIDE ? 2 * kI8GroupWarps * 1024 : 0;  // 8 x 32 fp32 a warp
     static constexpr int FIXED = CONV_STAGES * CONV_BYTES + PART_BYTES + EPI_BYTES + 1024 /* alignment */ +
                                  512 /* barriers */ + 2 * 4 * (GEMM_ROUTE_MAX_EXPERTS + 1);
     static constexpr int RAW_FIT = (kI8MaxSmem - FIXED) / RAW_BYTES;
@@ -133,10 +135,10 @@ struct I8Cfg {
     static constexpr int UNIT_STEP = kI8GroupThreads / SIDE;
     // Registers a thread: at launch, and after the warpgroups have shared them
     // out (producer and issuers; epilogue; converters)
-    static constexpr int LAUNCH_REGS = WIDE ? 72 : 80;
-    static constexpr int ISSUE_REGS = WIDE ? 40 : 48;
-    static constexpr int EPI_REGS = WIDE ? 56 : NS == 128 ? 80 : 112;
-    static constexpr int CONV_REGS = WIDE || NS == 128 ? 88 : 80;
+    static constexpr int LAUNCH_REGS = WIDE ? 96 : 80;
+    static constexpr int ISSUE_REGS = WIDE ? 32 : 48;
+    static constexpr int EPI_REGS = NS == 128 ? 80 : 112;
+    static constexpr int CONV_REGS = WIDE ? 112 : NS == 128 ? 88 : 80;
     static constexpr int REG_TOTAL = 128 * (ISSUE_REGS + EPI_WARPS / 4 * EPI_REGS + 4 * CONV_REGS);
     static_assert(REG_TOTAL <= THREADS * LAUNCH_REGS && THREADS * LAUNCH_REGS <= 65536,
                   "the shares add up to no more than the block is launched with");
@@ -460,6 +462,91 @@ __device__ __forceinline__ void store4(void *d, int type, long long at, const fl
         store1(d, type, at + 2, v.z);
 }
 
+// One warp's part of a wide tile: lane = token (quarter q of this CTA's 128),
+// 64 channels from the warp's column block. The sums are taken into registers
+// and the accumulator released before anything is stored.
+__device__ __forceinline__ void wide_epilogue(const I8Params &p, const I8Tile &ti, uint32_t tmem_base, uint32_t bar_acc_empty,
+                                              uint32_t stage, int rank, int q, int block, int lane)
+{
+    const int row0 = ti.m0 + rank * kI8Rows + 32 * q, n0 = ti.n0 + 64 * block;
+    const int rows = ti.m1 - row0;
+    const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(64 * block);
+    uint32_t v[2][32];
+    tmem_ld_32x32b_x32(src, v[0]);
+    tmem_ld_32x32b_x32(src + 32, v[1]);
+    const float sa = lane < rows ? p.sa[row0 + lane] : 0.0f;
+    tmem_ld_wait();
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive_peer(mapa_shared(bar_acc_empty, 0));
+    if (rows <= 0)
+        return;
+    const float *sb = p.sb + static_cast<long long>(ti.expert) * p.N;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        // through a swizzled tile of 8 tokens x 32 channels, so that rows of D
+        // are written in whole 64- or 128-byte pieces
+        const int lr = lane >> 3, lc = lane & 7;  // row (of four) and four channels of this lane's stores
+        const int nc = n0 + 32 * c, n = nc + (p.vec ? 4 * lc : lane);
+        float4 sn;
+        sn.x = n < p.N ? sb[n] : 0.0f;
+        sn.y = p.vec && n + 1 < p.N ? sb[n + 1] : 0.0f;
+        sn.z = p.vec && n + 2 < p.N ? sb[n + 2] : 0.0f;
+        sn.w = p.vec && n + 3 < p.N ? sb[n + 3] : 0.0f;
+#pragma unroll 1
+        for (int eight = 0; eight < 4; ++eight) {
+            if ((lane >> 3) == eight) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    st_shared_v4(stage + (lane & 7) * 128 + ((u ^ (lane & 7)) << 4),
+                                 __float_as_uint(__uint_as_float(v[c][4 * u]) * sa),
+                                 __float_as_uint(__uint_as_float(v[c][4 * u + 1]) * sa),
+                                 __float_as_uint(__uint_as_float(v[c][4 * u + 2]) * sa),
+                                 __float_as_uint(__uint_as_float(v[c][4 * u + 3]) * sa));
+            }
+            __syncwarp();
+            const long long at = static_cast<long long>(row0 + 8 * eight) * p.ldd + n;
+            if (p.vec) {
+                // four rows at a time, four channels a lane
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = 4 * i + lr;
+                    uint32_t x[4];
+                    ld_shared_v4(stage + row * 128 + ((lc ^ row) << 4), x[0], x[1], x[2], x[3]);
+                    if (8 * eight + row < rows)
+                        store4(p.d, p.out_type, at + row * p.ldd,
+                               make_float4(__uint_as_float(x[0]) * sn.x, __uint_as_float(x[1]) * sn.y,
+                                           __uint_as_float(x[2]) * sn.z, __uint_as_float(x[3]) * sn.w),
+                               p.N - n);
+                }
+            } else {
+                // rows of D start anywhere: a row at a time, a channel a lane
+#pragma unroll
+                for (int row = 0; row < 8; ++row) {
+                    const float x = ld_shared_f32(stage + row * 128 + (((lane >> 2) ^ row) << 4) + 4 * (lane & 3));
+                    if (8 * eight + row < rows && n < p.N)
+                        store1(p.d, p.out_type, at + row * p.ldd, x * sn.x);
+                }
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// Waits for a wide tile's sums and stores this warp's part; false if the wait gave up.
+__device__ __forceinline__ bool store_wide_tile(const I8Params &p, const I8Waiter &w, const I8Tile &ti, uint32_t bar_acc_full,
+                                                uint32_t acc_phase, uint32_t bar_acc_empty, uint32_t tmem_base, uint32_t stage,
+                                                int rank, int q, int block, int lane)
+{
+    const bool ok = w.wait(bar_acc_full, acc_phase, kRoleEpilogue | kWaitAccFull, true);
+    if (!__all_sync(0xffffffffu, ok))
+        return false;
+    tc_fence_after_sync();
+    wide_epilogue(p, ti, tmem_base, bar_acc_empty, stage, rank, q, block, lane);
+    return true;
+}
+
 // ---------------------------------------------------------------- kernel
 
 template <int NS, int KS, bool WIDE>
@@ -504,11 +591,11 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_acc_full + 8 * b, C::ISSUERS);
-            mbar_init(bar_acc_empty + 8 * b, C::EPI_WARPS * CG);
+            mbar_init(bar_acc_empty + 8 * b, WIDE ? 2 * kI8GroupWarps * CG : C::EPI_WARPS);
         }
         mbar_init(bar_drain, C::ISSUERS);
         mbar_init(bar_inject, 1);
-        mbar_init(bar_part, cluster > 1 ? C::EPI_WARPS * (cluster - 1) : 1);
+        mbar_init(bar_part, KS > 1 && cluster > 1 ? C::EPI_WARPS * (cluster - 1) : 1);
         *abort_flag = 0u;
         fence_mbar_init();
         prefetch_tensormap(&tmA);
@@ -693,6 +780,10 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
         uint32_t rphase = 0, cphase = 1;
         int skip = group;  // blocks of the tile before the group's next one
         bool ok = true;
+        // wide: the tile whose sums are still to be stored, and the parity of its accumulator
+        int done = -1;
+        uint32_t acc_phase = 0;
+        const uint32_t epi_stage = base + static_cast<uint32_t>(C::EPI_OFF + (WIDE ? cw * 1024 : 0));
         for (int t = cluster_id; ok && t < sched.num_tiles; t += clusters) {
             int kb = kb0 + skip;
             for (; kb < kb1; kb += 2) {
@@ -762,10 +853,27 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
                     cs -= C::CONV_STAGES;
                     cphase ^= 1u;
                 }
+                if (WIDE && done >= 0) {
+                    ok = store_wide_tile(p, w, i8_tile<C::TOKENS, C::CHANNELS>(sched, done), bar_acc_full, acc_phase, bar_acc_empty, tmem_base,
+                                             epi_stage, rank, q, cw >> 2, lane);
+                    done = -1;
+                    acc_phase ^= 1u;
+                    if (!ok)
+                        break;
+                }
             }
             skip = kb - kb1;  // 0 or 1 of the next tile's blocks is the other group's
+            if (WIDE && ok && done >= 0) {  // a tile without a block of this group
+                ok = store_wide_tile(p, w, i8_tile<C::TOKENS, C::CHANNELS>(sched, done), bar_acc_full, acc_phase, bar_acc_empty, tmem_base,
+                                     epi_stage, rank, q, cw >> 2, lane);
+                acc_phase ^= 1u;
+            }
+            done = t;
         }
-    } else {
+        if (WIDE && ok && done >= 0)
+            store_wide_tile(p, w, i8_tile<C::TOKENS, C::CHANNELS>(sched, done), bar_acc_full, acc_phase, bar_acc_empty, tmem_base,
+                            epi_stage, rank, q, cw >> 2, lane);
+    } else if (!WIDE) {
         set_regs<C::LAUNCH_REGS, C::EPI_REGS>();
         const int q = warp & 3;  // TMEM lane quarter of this warp
         const int blocks = kb1 - kb0;
@@ -775,78 +883,7 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
         for (int t = cluster_id; t < sched.num_tiles; t += clusters) {
             const I8Tile ti = i8_tile<C::TOKENS, C::CHANNELS>(sched, t);
             const float *sb = p.sb + static_cast<long long>(ti.expert) * p.N;
-            if constexpr (WIDE) {
-                // lane = token, column = channel; this warp's 32 tokens x 128 channels
-                const int row0 = ti.m0 + rank * kI8Rows + 32 * q, n0 = ti.n0 + 128 * ((warp - kI8FirstEpiWarp) >> 2);
-                const float sa = row0 + lane < ti.m1 ? p.sa[row0 + lane] : 0.0f;
-                bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull, true);
-                if (!__all_sync(0xffffffffu, ok))
-                    break;
-                tc_fence_after_sync();
-                const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(n0 - ti.n0);
-                const uint32_t stage = base + static_cast<uint32_t>(C::EPI_OFF + (warp - kI8FirstEpiWarp) * 2048);
-                const int lr = lane >> 3, lc = lane & 7;  // this lane's row (of four) and four channels of a chunk's store
-                const int rows = ti.m1 - row0;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(src + 32 * c, v);
-                    const int n = n0 + 32 * c + 4 * lc;
-                    float4 sn;
-                    sn.x = n < p.N ? sb[n] : 0.0f;
-                    sn.y = n + 1 < p.N ? sb[n + 1] : 0.0f;
-                    sn.z = n + 2 < p.N ? sb[n + 2] : 0.0f;
-                    sn.w = n + 3 < p.N ? sb[n + 3] : 0.0f;
-                    tmem_ld_wait();
-                    if (c == 3) {  // the accumulator has been read: the next tile's MMAs may start
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_peer(mapa_shared(bar_acc_empty + 8 * acc, 0));
-                    }
-                    // through a swizzled tile, 16 tokens at a time, so that rows of D are
-                    // written in whole 64- or 128-byte pieces
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        if ((lane >> 4) == half) {
-#pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                st_shared_v4(stage + (lane & 15) * 128 + ((u ^ (lane & 7)) << 4),
-                                             __float_as_uint(__uint_as_float(v[4 * u]) * sa),
-                                             __float_as_uint(__uint_as_float(v[4 * u + 1]) * sa),
-                                             __float_as_uint(__uint_as_float(v[4 * u + 2]) * sa),
-                                             __float_as_uint(__uint_as_float(v[4 * u + 3]) * sa));
-                        }
-                        __syncwarp();
-                        if (p.vec) {
-                            // four rows at a time, four channels a lane
-                            const long long at = static_cast<long long>(row0 + 16 * half + lr) * p.ldd + n;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int row = 4 * i + lr;
-                                uint32_t x[4];
-                                ld_shared_v4(stage + row * 128 + ((lc ^ (row & 7)) << 4), x[0], x[1], x[2], x[3]);
-                                if (16 * half + row < rows)
-                                    store4(p.d, p.out_type, at + 4 * i * p.ldd,
-                                           make_float4(__uint_as_float(x[0]) * sn.x, __uint_as_float(x[1]) * sn.y,
-                                                       __uint_as_float(x[2]) * sn.z, __uint_as_float(x[3]) * sn.w),
-                                           p.N - n);
-                            }
-                        } else {
-                            // rows of D start anywhere: a row at a time, a channel a lane
-                            const int n1 = n0 + 32 * c + lane;
-                            const float s1 = n1 < p.N ? sb[n1] : 0.0f;
-                            const long long at = static_cast<long long>(row0 + 16 * half) * p.ldd + n1;
-                            for (int row = 0; row < 16 && 16 * half + row < rows; ++row) {
-                                const float x = ld_shared_f32(stage + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + 4 * (lane & 3));
-                                if (n1 < p.N)
-                                    store1(p.d, p.out_type, at + row * p.ldd, x * s1);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                }
-            } else {
+            {
                 // lane = channel, column = token
                 const int n = ti.n0 + 32 * q + lane;
                 const bool live = n < p.N;
