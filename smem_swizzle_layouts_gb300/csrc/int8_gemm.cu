@@ -83,7 +83,7 @@ struct I8Params {
     void *d;
     long long ldd;
     int out_type;
-    int vec;     // rows of D start on multiples of four elements
+    int vec;     // rows of D start on multiples of 32 bytes
     int inject;  // test hook: the role that waits on a barrier nothing arrives at
     unsigned long long timeout_ns;
     unsigned int *status;
@@ -436,70 +436,117 @@ __device__ __forceinline__ void store1(void *d, int type, long long at, float v)
         static_cast<__half *>(d)[at] = __float2half_rn(v);
 }
 
-// Four neighbouring channels of a row of D (its address a multiple of four
-// elements), of which `n` exist.
-__device__ __forceinline__ void store4(void *d, int type, long long at, const float4 &v, int n)
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v)
 {
-    if (n >= 4) {
-        if (type == GEMM_OUT_F32) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(d) + at) = v;
-        } else if (type == GEMM_OUT_BF16) {
-            const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(d) + at) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-        } else {
-            const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-            *reinterpret_cast<uint2 *>(static_cast<__half *>(d) + at) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-        }
-        return;
-    }
-    if (n > 0)
-        store1(d, type, at, v.x);
-    if (n > 1)
-        store1(d, type, at + 1, v.y);
-    if (n > 2)
-        store1(d, type, at + 2, v.z);
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// One warp's part of a wide tile: lane = token (quarter q of this CTA's 128),
-// 64 channels from the warp's column block. The sums are taken into registers
-// and the accumulator released before anything is stored.
-__device__ __forceinline__ void wide_epilogue(const I8Params &p, const I8Tile &ti, uint32_t tmem_base, uint32_t bar_acc_empty,
-                                              uint32_t stage, int rank, int q, int block, int lane)
+__device__ __forceinline__ void st_global_32bytes(void *p, const uint32_t (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Sixteen neighbouring values of a row of D whose address is a multiple of 32 bytes.
+__device__ __forceinline__ void store16(void *d, int type, long long at, const float (&x)[16])
+{
+    uint32_t r[8];
+    if (type == GEMM_OUT_F32) {
+        float *o = static_cast<float *>(d) + at;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r[i] = __float_as_uint(x[8 * h + i]);
+            st_global_32bytes(o + 8 * h, r);
+        }
+    } else if (type == GEMM_OUT_BF16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            r[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        st_global_32bytes(static_cast<__nv_bfloat16 *>(d) + at, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            r[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        st_global_32bytes(static_cast<__half *>(d) + at, r);
+    }
+}
+
+// Waits for a wide tile's sums and stores one warp's part of them: lane = token
+// (quarter q of this CTA's 128), 64 channels from column block `block`. The
+// channels' scales are fetched before the wait, and the sums taken into
+// registers and the accumulator released before anything is stored. Where rows
+// of D start on 32-byte boundaries every lane writes its token's channels in
+// whole 32-byte sectors (8192^2 x 2048: 179 us with 16-byte pieces and 201 us
+// through shared memory, row by row, which is left to other rows of D). False
+// if the wait gave up.
+__device__ __forceinline__ bool store_wide_tile(const I8Params &p, const I8Waiter &w, const I8Tile &ti, uint32_t bar_acc_full,
+                                                uint32_t acc_phase, uint32_t bar_acc_empty, uint32_t tmem_base, uint32_t stage,
+                                                int rank, int q, int block, int lane)
 {
     const int row0 = ti.m0 + rank * kI8Rows + 32 * q, n0 = ti.n0 + 64 * block;
     const int rows = ti.m1 - row0;
+    const float sa = lane < rows ? p.sa[row0 + lane] : 0.0f;
+    const float *sb = p.sb + static_cast<long long>(ti.expert) * p.N;
+    const float s0 = n0 + lane < p.N ? sb[n0 + lane] : 0.0f, s1 = n0 + 32 + lane < p.N ? sb[n0 + 32 + lane] : 0.0f;
+    const bool ok = w.wait(bar_acc_full, acc_phase, kRoleEpilogue | kWaitAccFull, true);
+    if (!__all_sync(0xffffffffu, ok))
+        return false;
+    tc_fence_after_sync();
     const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(64 * block);
     uint32_t v[2][32];
     tmem_ld_32x32b_x32(src, v[0]);
     tmem_ld_32x32b_x32(src + 32, v[1]);
-    const float sa = lane < rows ? p.sa[row0 + lane] : 0.0f;
     tmem_ld_wait();
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0)
         mbar_arrive_peer(mapa_shared(bar_acc_empty, 0));
     if (rows <= 0)
-        return;
-    const float *sb = p.sb + static_cast<long long>(ti.expert) * p.N;
+        return true;
+    if (p.vec && n0 + 64 <= p.N) {
+        st_shared_f32(stage + 4 * lane, s0);
+        st_shared_f32(stage + 128 + 4 * lane, s1);
+        __syncwarp();
+        const long long at = static_cast<long long>(row0 + lane) * p.ldd + n0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[16];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t sn[4];
+                    ld_shared_v4(stage + 128 * c + 64 * h + 16 * u, sn[0], sn[1], sn[2], sn[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[4 * u + i] = __uint_as_float(v[c][16 * h + 4 * u + i]) * sa * __uint_as_float(sn[i]);
+                }
+                if (lane < rows)
+                    store16(p.d, p.out_type, at + 32 * c + 16 * h, x);
+            }
+        __syncwarp();
+        return true;
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        // through a swizzled tile of 8 tokens x 32 channels, so that rows of D
-        // are written in whole 64- or 128-byte pieces
-        const int lr = lane >> 3, lc = lane & 7;  // row (of four) and four channels of this lane's stores
-        const int nc = n0 + 32 * c, n = nc + (p.vec ? 4 * lc : lane);
-        float4 sn;
-        sn.x = n < p.N ? sb[n] : 0.0f;
-        sn.y = p.vec && n + 1 < p.N ? sb[n + 1] : 0.0f;
-        sn.z = p.vec && n + 2 < p.N ? sb[n + 2] : 0.0f;
-        sn.w = p.vec && n + 3 < p.N ? sb[n + 3] : 0.0f;
+        // eight tokens x 32 channels at a time through a swizzled tile, then a
+        // row at a time, a channel a lane
+        const int n = n0 + 32 * c + lane;
+        const float sn = c ? s1 : s0;
 #pragma unroll 1
-        for (int eight = 0; eight < 4; ++eight) {
+        for (int eight = 0; eight < 4 && 8 * eight < rows; ++eight) {
+            const int lc = lane & 7;
             if ((lane >> 3) == eight) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    st_shared_v4(stage + (lane & 7) * 128 + ((u ^ (lane & 7)) << 4),
+                    st_shared_v4(stage + lc * 128 + ((u ^ lc) << 4),
                                  __float_as_uint(__uint_as_float(v[c][4 * u]) * sa),
                                  __float_as_uint(__uint_as_float(v[c][4 * u + 1]) * sa),
                                  __float_as_uint(__uint_as_float(v[c][4 * u + 2]) * sa),
@@ -507,43 +554,15 @@ __device__ __forceinline__ void wide_epilogue(const I8Params &p, const I8Tile &t
             }
             __syncwarp();
             const long long at = static_cast<long long>(row0 + 8 * eight) * p.ldd + n;
-            if (p.vec) {
-                // four rows at a time, four channels a lane
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = 4 * i + lr;
-                    uint32_t x[4];
-                    ld_shared_v4(stage + row * 128 + ((lc ^ row) << 4), x[0], x[1], x[2], x[3]);
-                    if (8 * eight + row < rows)
-                        store4(p.d, p.out_type, at + row * p.ldd,
-                               make_float4(__uint_as_float(x[0]) * sn.x, __uint_as_float(x[1]) * sn.y,
-                                           __uint_as_float(x[2]) * sn.z, __uint_as_float(x[3]) * sn.w),
-                               p.N - n);
-                }
-            } else {
-                // rows of D start anywhere: a row at a time, a channel a lane
-#pragma unroll
-                for (int row = 0; row < 8; ++row) {
-                    const float x = ld_shared_f32(stage + row * 128 + (((lane >> 2) ^ row) << 4) + 4 * (lane & 3));
-                    if (8 * eight + row < rows && n < p.N)
-                        store1(p.d, p.out_type, at + row * p.ldd, x * sn.x);
-                }
+            for (int row = 0; row < 8; ++row) {
+                const float x = ld_shared_f32(stage + row * 128 + (((lane >> 2) ^ row) << 4) + 4 * (lane & 3));
+                if (8 * eight + row < rows && n < p.N)
+                    store1(p.d, p.out_type, at + row * p.ldd, x * sn);
             }
             __syncwarp();
         }
     }
-}
-
-// Waits for a wide tile's sums and stores this warp's part; false if the wait gave up.
-__device__ __forceinline__ bool store_wide_tile(const I8Params &p, const I8Waiter &w, const I8Tile &ti, uint32_t bar_acc_full,
-                                                uint32_t acc_phase, uint32_t bar_acc_empty, uint32_t tmem_base, uint32_t stage,
-                                                int rank, int q, int block, int lane)
-{
-    const bool ok = w.wait(bar_acc_full, acc_phase, kRoleEpilogue | kWaitAccFull, true);
-    if (!__all_sync(0xffffffffu, ok))
-        return false;
-    tc_fence_after_sync();
-    wide_epilogue(p, ti, tmem_base, bar_acc_empty, stage, rank, q, block, lane);
     return true;
 }
 
@@ -1106,7 +1125,7 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     p.d = D;
     p.ldd = ldd;
     p.out_type = d_type;
-    p.vec = aligned_to(D, 4 * od) && ldd % 4 == 0;
+    p.vec = aligned_to(D, 32) && ldd * od % 32 == 0;
     p.status = status;
     if (K == 0) {
         const int grid = static_cast<int>(std::min<int64_t>(M, 8 * sms));
