@@ -16,9 +16,9 @@
 // MMA reads) where an SM moves 128, which held 8192^3 at 0.48 of the tensor rate.
 //
 // Two shapes of tile:
-//   narrow  128 channels (rows of B) on the M side, 16 to 128 tokens (rows of
-//           A) on the N side, single CTAs: few tokens still use whole 128-row
-//           MMAs and every weight is read once. Such MMAs are short and the
+//   narrow  128 channels (rows of B) on the M side, 16 to 64 tokens (rows of
+//           A) on the N side, or 256 channels and 128 tokens on a CTA pair: few
+//           tokens still use whole MMA rows and every weight is read once. Such MMAs are short and the
 //           issuing thread, about 1000 cycles for the eight of a stage, is
 //           the limit; so two threads issue alternate stages, each into an
 //           accumulator of its own, and the epilogue adds the two. For few
@@ -90,11 +90,11 @@ struct I8Params {
 };
 
 // NS: rows of the N side of one MMA (narrow: tokens; wide: 256 channels).
-// KS: most CTAs sharing one tile's K (1: none do).
+// Tiles of 128 tokens and wide ones are shared by a pair of CTAs. KS: most CTAs sharing one tile's K (1: none do).
 template <int NS, int KS, bool WIDE>
 struct I8Cfg {
-    static constexpr int CG = WIDE ? 2 : 1;
-    static constexpr int TOKENS = WIDE ? 256 : NS, CHANNELS = WIDE ? NS : 128;  // of a tile
+    static constexpr int CG = WIDE || NS == 128 ? 2 : 1;
+    static constexpr int TOKENS = WIDE ? 256 : NS, CHANNELS = WIDE ? NS : 128 * CG;  // of a tile
     static constexpr int SIDE = NS / CG;                                        // N-side rows widened by each CTA
     static constexpr int ISSUERS = WIDE ? 1 : 2;
     static constexpr int EPI_WARPS = WIDE ? 0 : 4;  // of their own
@@ -106,7 +106,7 @@ struct I8Cfg {
     static constexpr int A_COL0 = ACC_BUFS * ISSUERS * ACC_STRIDE;
     static constexpr int A_COLS = kI8K / 2;
     static constexpr int CONV_FIT = (512 - A_COL0) / A_COLS;
-    static constexpr int CONV_MOST = WIDE || NS == 128 ? 2 : 4;  // shared memory has room for
+    static constexpr int CONV_MOST = WIDE ? 2 : 4;  // shared memory has room for
     // Both rings have an even number of stages: the two converter groups (and
     // the two issuers) take alternate blocks, so each stage always belongs to
     // the same one. With an odd number a group that runs ahead would wait for
@@ -137,12 +137,12 @@ struct I8Cfg {
     // out (producer and issuers; epilogue; converters)
     static constexpr int LAUNCH_REGS = WIDE ? 96 : 80;
     static constexpr int ISSUE_REGS = WIDE ? 32 : 48;
-    static constexpr int EPI_REGS = NS == 128 ? 80 : 112;
-    static constexpr int CONV_REGS = WIDE ? 112 : NS == 128 ? 88 : 80;
+    static constexpr int EPI_REGS = 112;
+    static constexpr int CONV_REGS = WIDE ? 112 : 80;
     static constexpr int REG_TOTAL = 128 * (ISSUE_REGS + EPI_WARPS / 4 * EPI_REGS + 4 * CONV_REGS);
     static_assert(REG_TOTAL <= THREADS * LAUNCH_REGS && THREADS * LAUNCH_REGS <= 65536,
                   "the shares add up to no more than the block is launched with");
-    static_assert(!WIDE || (NS == 256 && KS == 1), "wide tiles: 256 channels, no shared K");
+    static_assert((!WIDE || NS == 256) && (CG == 1 || KS == 1), "wide tiles: 256 channels; pairs do not share K");
     static_assert((SIDE & (SIDE - 1)) == 0 && SIDE >= 16 && SIDE <= 128, "unit arithmetic");
     static_assert(8 * NUM_BARS + 16 <= 512, "barriers");
     static_assert(RAW_BYTES % 1024 == 0 && CONV_BYTES % 1024 == 0 && SIDE * kI8K % 1024 == 0,
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_acc_full + 8 * b, C::ISSUERS);
-            mbar_init(bar_acc_empty + 8 * b, WIDE ? 2 * kI8GroupWarps * CG : C::EPI_WARPS);
+            mbar_init(bar_acc_empty + 8 * b, (WIDE ? 2 * kI8GroupWarps : C::EPI_WARPS) * CG);
         }
         mbar_init(bar_drain, C::ISSUERS);
         mbar_init(bar_inject, 1);
@@ -698,7 +698,9 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
                 bool ok = true;
                 for (int t = cluster_id; ok && t < sched.num_tiles; t += clusters) {
                     const I8Tile ti = i8_tile<C::TOKENS, C::CHANNELS>(sched, t);
-                    const int m0 = ti.m0 + (WIDE ? rank * kI8Rows : 0), n0 = ti.n0 + (WIDE ? rank * C::SIDE : 0);
+                    // a pair's CTAs take their own halves of both sides
+                    const int pair_rank = CG == 2 ? rank : 0;
+                    const int m0 = ti.m0 + pair_rank * (WIDE ? kI8Rows : C::SIDE), n0 = ti.n0 + pair_rank * (WIDE ? C::SIDE : kI8Rows);
                     for (int kb = kb0; kb < kb1; ++kb) {
                         ok = w.wait(bar_raw_empty + 8 * stage, phase ^ 1u, kRoleProducer | kWaitEmpty);
                         if (!ok)
@@ -904,10 +906,10 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
             const float *sb = p.sb + static_cast<long long>(ti.expert) * p.N;
             {
                 // lane = channel, column = token
-                const int n = ti.n0 + 32 * q + lane;
+                const int n = ti.n0 + (CG == 2 ? rank * kI8Rows : 0) + 32 * q + lane;
                 const bool live = n < p.N;
                 const float sn = live ? sb[n] : 0.0f;
-                bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull);
+                bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull, CG == 2);
                 if (!__all_sync(0xffffffffu, ok))
                     break;
                 tc_fence_after_sync();
@@ -964,8 +966,12 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar_acc_empty + 8 * acc);
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_peer(mapa_shared(bar_acc_empty + 8 * acc, 0));
+                    else
+                        mbar_arrive(bar_acc_empty + 8 * acc);
+                }
             }
             if (++acc == C::ACC_BUFS) {
                 acc = 0;
@@ -985,6 +991,81 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
         tc_fence_after_sync();
         tmem_dealloc<CG>(tmem_base, 512);
     }
+}
+
+// ---------------------------------------------------------------- few tokens
+//
+// Up to MT tokens against every channel, for which latency counts: a block
+// takes a few channels and its eight warps slices of K, so that all of a
+// block's weights are asked for at once (16 bytes a lane and channel), and
+// dp4a sums them in 32-bit integers, exactly for K < 2^17. No tile to fill, no
+// stages: the weights are read once, the tokens' rows come from L2.
+
+constexpr int kFewWarps = 8;
+constexpr int64_t kFewMaxK = (1 << 17) - 1;
+
+// Bytes k .. k+15 of a row of K: zeros past its end, which is not read past.
+__device__ __forceinline__ int4 load_row16(const int8_t *row, int k, int K)
+{
+    if (k + 16 <= K)
+        return __ldg(reinterpret_cast<const int4 *>(row + k));
+    int4 v = make_int4(0, 0, 0, 0);
+    int8_t *b = reinterpret_cast<int8_t *>(&v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (k + i < K)
+            b[i] = row[k + i];
+    return v;
+}
+
+template <int MT, int ROWS>
+__global__ void __launch_bounds__(32 * kFewWarps)
+    int8_few_kernel(const int8_t *__restrict__ A, long long lda, const int8_t *__restrict__ B, long long ldb, const I8Params p)
+{
+    __shared__ int part[kFewWarps][ROWS * MT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n0 = blockIdx.x * ROWS;
+    int acc[ROWS][MT] = {};
+    for (int k = warp * 512 + lane * 16; k < p.K; k += kFewWarps * 512) {
+        int4 w[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)  // rows past the last repeat it; their sums are not stored
+            w[r] = load_row16(B + static_cast<long long>(min(n0 + r, p.N - 1)) * ldb, k, p.K);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int4 a = load_row16(A + static_cast<long long>(min(m, p.M - 1)) * lda, k, p.K);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+                acc[r][m] = __dp4a(w[r].x, a.x, __dp4a(w[r].y, a.y, __dp4a(w[r].z, a.z, __dp4a(w[r].w, a.w, acc[r][m]))));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int s = __reduce_add_sync(0xffffffffu, acc[r][m]);
+            if (lane == 0)
+                part[warp][m * ROWS + r] = s;
+        }
+    __syncthreads();
+    const int m = threadIdx.x / ROWS, n = n0 + threadIdx.x % ROWS;
+    if (threadIdx.x < ROWS * MT && m < p.M && n < p.N) {
+        int s = 0;
+#pragma unroll
+        for (int i = 0; i < kFewWarps; ++i)
+            s += part[i][threadIdx.x];
+        store1(p.d, p.out_type, m * p.ldd + n, static_cast<float>(s) * p.sa[m] * p.sb[n]);
+    }
+}
+
+// ROWS: channels per block, eight for one token and four for more, whose sums
+// would otherwise take the registers of half the blocks.
+template <int MT, int ROWS = MT == 1 ? 8 : 4>
+gemm_status_t launch_few(const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, const I8Params &p, cudaStream_t st)
+{
+    const unsigned grid = (static_cast<unsigned>(p.N) + ROWS - 1) / ROWS;
+    int8_few_kernel<MT, ROWS><<<grid, 32 * kFewWarps, 0, st>>>(A, lda, B, ldb, p);
+    return host_launched();
 }
 
 // Zeros for K == 0: the rows of every expert, or all M of them.
@@ -1054,7 +1135,8 @@ struct I8Plan {
     bool wide;
     int ns, ks;
     int tokens() const { return wide ? 256 : ns; }
-    int channels() const { return wide ? 256 : 128; }
+    int channels() const { return wide || ns == 128 ? 256 : 128; }
+    int box_tokens() const { return wide ? 128 : ns == 128 ? 64 : ns; }  // tokens one CTA loads
 };
 
 I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms)
@@ -1137,6 +1219,15 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
             int8_zero_kernel<__half><<<grid, 256, 0, st>>>(p);
         return host_launched();
     }
+    // Few tokens, where integers beat tiles, whose work hardly grows with the
+    // tokens (measured us, integers and tiles: 4096 x 4096 weights with 1, 2, 4
+    // and 8 tokens 4.7, 5.8, 7.7 and 11.9 against 10.3; 16384 x 4096 13.4, 15.4,
+    // 19.9 and 27.7 against 16.5; 1024 x 1024 with 4 tokens 2.2 against 6.7).
+    if (E == 0 && K <= kFewMaxK && (M <= 2 || (M <= 4 && N * K <= int64_t(1) << 25) || (M <= 8 && N * K <= int64_t(3) << 22)))
+        return M == 1   ? launch_few<1>(A, lda, B, ldb, p, st)
+               : M == 2 ? launch_few<2>(A, lda, B, ldb, p, st)
+               : M <= 4 ? launch_few<4>(A, lda, B, ldb, p, st)
+                        : launch_few<8>(A, lda, B, ldb, p, st);
     int ms = 0;
     p.inject = host_take_injection(&ms);
     p.timeout_ns = static_cast<unsigned long long>(ms > 0 ? ms : 2000) * 1000000ull;
@@ -1149,7 +1240,7 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     {
         const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(M)};
         const uint64_t strides[1] = {static_cast<uint64_t>(lda)};
-        const uint32_t box[2] = {kI8K, static_cast<uint32_t>(pl.wide ? kI8Rows : pl.ns)};
+        const uint32_t box[2] = {kI8K, static_cast<uint32_t>(pl.box_tokens())};
         if ((s = host_encode_tiled(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) !=
             GEMM_OK)
             return s;

@@ -83,7 +83,7 @@ def test_product_large_tiles(g):
         assert torch.equal(D, y)
 
 
-@pytest.mark.parametrize("M", [1, 8, 16, 32, 64, 128, 200, 600])
+@pytest.mark.parametrize("M", [1, 3, 8, 9, 16, 32, 64, 65, 128, 200, 600])
 @pytest.mark.parametrize("N,K", [(1000, 4096), (20000, 2048), (40960, 1152)])
 def test_long_rows_many_times(g, M, N, K):
     """Many stages and tiles a CTA on every tile shape, launched over and over: every result the same, and right."""
@@ -97,6 +97,37 @@ def test_long_rows_many_times(g, M, N, K):
         g.gemm_int8(M, N, K, ad, K, sa, bd, K, sb, D, N, 0)
     ok(g)
     assert all(torch.equal(D, y) for D in outs)
+
+
+@pytest.mark.parametrize("M,K", [(1, 1), (2, 17), (3, 500), (8, 4097), (5, 9000)])
+def test_few_tokens_tail_is_not_read_past_its_end(g, M, K):
+    """The last row of each operand ends with its allocation's last byte."""
+    rng = np.random.default_rng(K)
+    N = 30
+    ld = up16(K) + 16
+    a = rng.integers(-128, 128, (M - 1) * ld + K).astype(np.int8)
+    b = rng.integers(-128, 128, (N - 1) * ld + K).astype(np.int8)
+    full = [np.concatenate([v, np.zeros(ld - K, np.int8)]).reshape(-1, ld)[:, :K] for v in (a, b)]
+    sa, sb = np.ones(M, np.float32), np.full(N, 0.5, np.float32)
+    D = torch.empty(M, N, device=DEV)
+    g.gemm_int8(M, N, K, torch.from_numpy(a).to(DEV), ld, torch.from_numpy(sa).to(DEV), torch.from_numpy(b).to(DEV), ld,
+                torch.from_numpy(sb).to(DEV), D, N, 0)
+    ok(g)
+    assert torch.equal(D.cpu(), expected(full[0], full[1], sa, sb, 0))
+
+
+def test_few_tokens_sums_are_exact_past_two_to_the_24(g):
+    """Eight tokens and fewer are summed in integers: one rounding, to fp32."""
+    M, N, K = 5, 100, 100000
+    a = torch.full((M, up16(K)), 127, dtype=torch.int8, device=DEV)
+    b = torch.full((N, up16(K)), 127, dtype=torch.int8, device=DEV)
+    b[1] = -128
+    one = torch.ones(N, device=DEV)
+    D = torch.empty(M, N, device=DEV)
+    g.gemm_int8(M, N, K, a, up16(K), one, b, up16(K), one, D, N, 0)
+    ref = torch.full((N,), 127.0 * 127 * K, dtype=torch.float64)
+    ref[1] = -128.0 * 127 * K
+    assert torch.equal(D.cpu(), ref.float().expand(M, N))
 
 
 @pytest.mark.parametrize("M,E", [(96, 64), (1500, 64), (4000, 64), (9000, 33)])
@@ -270,7 +301,7 @@ def test_on_another_stream_and_in_a_graph(g):
 
 
 @pytest.mark.parametrize("role", [1, 2])
-@pytest.mark.parametrize("M", [4, 300])
+@pytest.mark.parametrize("M", [12, 100, 300])
 def test_waits_run_out(g, role, M):
     N, K = 256, 1024
     rng = np.random.default_rng(13)
