@@ -14,6 +14,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/gemm_gb300.h"
 #include "host.h"
@@ -107,9 +108,27 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf(-x)); }
 
 // ---------------------------------------------------------------- routing
+
+// e^x and 1 / x by the special-function unit, for the scores that the choice
+// compares: within about 3e-7 of the sigmoid (softmax: of the largest score),
+// and equal for equal logits. The weights are computed from the chosen logits
+// with expf and correctly rounded divisions.
+__device__ __forceinline__ float fast_exp(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+
+__device__ __forceinline__ float fast_inverse(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 struct RouteParams {
     long long T;
@@ -121,6 +140,7 @@ struct RouteParams {
     int sigmoid, groups, per, group_top, groups_kept, renorm;
     float scale;
     unsigned int per_inv;  // ceil(2^32 / per): e / per = umulhi(e, per_inv) for per >= 2
+    int group_lanes;       // lanes that look through one group
 };
 
 // Order-preserving code of a choice value; 0 for what is never chosen (-inf
@@ -135,9 +155,44 @@ __device__ __forceinline__ uint32_t choice_key(float v)
 
 constexpr int kRouteWarps = 4;
 
+// The value a code stands for.
+__device__ __forceinline__ float choice_value(uint32_t key)
+{
+    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
+// A lane's two best codes among those not taken.
+struct LaneBest {
+    uint32_t key, next;
+    int i, next_i;
+};
+
+template <int NPL>
+__device__ __forceinline__ LaneBest lane_best(const uint32_t (&key)[NPL], uint32_t taken)
+{
+    LaneBest b{0u, 0u, 0, 0};
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const uint32_t v = (taken >> i) & 1u ? 0u : key[i];
+        if (v > b.key) {
+            b.next = b.key;
+            b.next_i = b.i;
+            b.key = v;
+            b.i = i;
+        } else if (v > b.next) {
+            b.next = v;
+            b.next_i = i;
+        }
+    }
+    return b;
+}
+
 // One warp per token; lane l holds experts l, l + 32, ... (NPL of them). The
 // k best are taken one at a time: a warp-wide integer maximum of the lanes'
-// best codes, then the lowest expert index among those equal to it.
+// best codes, then the lowest expert among the lanes that hold it. A lane keeps
+// its two best, so it looks through its codes again only when both are taken.
+// Bound by instructions: 16384 tokens of 256 experts with 8 taken, see the
+// measurements beside kRouteWarps.
 template <typename L, int NPL>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *__restrict__ logits, const RouteParams p)
 {
@@ -154,6 +209,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *__rest
     for (int i = 0; i < NPL; ++i) {
         const int e = lane + 32 * i;
         l[i] = e < p.E ? to_float(row[e]) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
         bad |= l[i] != l[i] || (!p.sigmoid && l[i] == INFINITY);
         top = fmaxf(top, l[i]);
     }
@@ -161,15 +219,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *__rest
     // the softmax over all experts: needed for the weights when they are not
     // renormalised (renormalised ones are a softmax over the chosen), and for
     // the choice when a bias is added to the scores or groups are summed
-    float total = 0.0f;
+    const bool scored = p.bias || p.groups > 1;
+    float s[NPL];
+    float total = 1.0f;
     if (!p.sigmoid) {
         top = warp_max(top);
         if (top == -INFINITY)
             top = 0.0f;
-        if (!p.renorm || p.bias || p.groups > 1) {
+        if (!p.renorm || scored) {
+            total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i)
-                total += l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
+            for (int i = 0; i < NPL; ++i) {
+                s[i] = l[i] > -INFINITY ? (p.renorm ? fast_exp(l[i] - top) : expf(l[i] - top)) : 0.0f;
+                total += s[i];
+            }
             total = warp_sum(total);
             if (total == 0.0f)
                 total = 1.0f;
@@ -177,15 +240,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *__rest
     }
     // what the choice goes by
     uint32_t key[NPL];
-    if (p.bias) {
+    if (scored) {
+        const float inv = fast_inverse(total);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            const int e = lane + 32 * i;
-            key[i] = 0u;
-            if (l[i] > -INFINITY) {
-                const float s = p.sigmoid ? sigmoid(l[i]) : __fdiv_rn(expf(l[i] - top), total);
-                key[i] = choice_key(__fadd_rn(s, p.bias[e]));
+            s[i] = p.sigmoid ? fast_inverse(1.0f + fast_exp(-l[i])) : s[i] * inv;
+            if (p.bias) {
+                const int e = lane + 32 * i;
+                s[i] = e < p.E ? __fadd_rn(s[i], p.bias[e]) : 0.0f;
             }
+            key[i] = l[i] > -INFINITY ? choice_key(p.bias ? s[i] : l[i]) : 0u;
         }
     } else {
 #pragma unroll
@@ -193,39 +257,46 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *__rest
             key[i] = choice_key(l[i]);
     }
     if (p.groups > 1) {
-        const int stride = p.per | 1;  // odd: the lanes reading one value of each group meet distinct banks
+        const int stride = p.per | 1;  // odd: lanes reading one value of each group meet distinct banks
         float *gs = group_smem + warp * p.groups * stride;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int e = lane + 32 * i;
             if (e < p.E) {
-                float v = -INFINITY;
-                if (key[i] != 0u) {
-                    const float s = p.sigmoid ? sigmoid(l[i]) : __fdiv_rn(expf(l[i] - top), total);
-                    v = p.bias ? __fadd_rn(s, p.bias[e]) : s;
-                }
                 const int g = p.per == 1 ? e : static_cast<int>(__umulhi(static_cast<unsigned>(e), p.per_inv));
-                gs[g * stride + e - g * p.per] = v;
+                gs[g * stride + e - g * p.per] = key[i] != 0u ? s[i] : -INFINITY;
             }
         }
         __syncwarp();
-        uint32_t gkey = 0u;
-        if (lane < p.groups) {
-            float a = -INFINITY, b = -INFINITY;
-            for (int i = 0; i < p.per; ++i) {
-                const float v = gs[lane * stride + i];
+        // the two best of each group, by 32 / groups (rounded down to a power of two) lanes
+        const int sub = p.group_lanes, g_of = lane / sub;
+        float a = -INFINITY, b = -INFINITY;
+        if (g_of < p.groups) {
+#pragma unroll 4
+            for (int i = lane % sub; i < p.per; i += sub) {
+                const float v = gs[g_of * stride + i];
                 b = fmaxf(b, fminf(a, v));
                 a = fmaxf(a, v);
             }
-            if (a > -INFINITY)
-                gkey = choice_key(p.group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
         }
+        for (int o = 1; o < sub; o <<= 1) {
+            const float oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+            b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+            a = fmaxf(a, oa);
+        }
+        // lane g takes group g's score
+        uint32_t gkey = 0u;
+        if (a > -INFINITY)
+            gkey = choice_key(p.group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
+        gkey = __shfl_sync(0xffffffffu, gkey, (lane * sub) & 31);
+        if (lane >= p.groups)
+            gkey = 0u;
         int rank = 0;
         for (int g = 0; g < p.groups; ++g) {
             const uint32_t o = __shfl_sync(0xffffffffu, gkey, g);
             rank += o > gkey || (o == gkey && g < lane);
         }
-        const uint32_t kept = __ballot_sync(0xffffffffu, lane < p.groups && gkey != 0u && rank < p.groups_kept);
+        const uint32_t kept = __ballot_sync(0xffffffffu, gkey != 0u && rank < p.groups_kept);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int e = lane + 32 * i;
@@ -238,59 +309,53 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *__rest
     }
     // the k best; lane j keeps the j-th
     int my_id = -1;
-    float my_l = -INFINITY;
-    uint32_t best = 0u;
-    int best_e = INT_MAX;
-    float best_l = 0.0f;
-    auto rescan = [&]() {
-        best = 0u;
-        best_e = INT_MAX;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                best_e = lane + 32 * i;
-                best_l = l[i];
-            }
-    };
-    rescan();
+    uint32_t my_key = 0u, taken = 0u;
+    LaneBest best = lane_best<NPL>(key, 0u);
+    bool fresh = true;  // best.next is known
     for (int j = 0; j < p.k; ++j) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, best.key);
         if (m == 0u)
             break;
-        const int e = static_cast<int>(
-            __reduce_min_sync(0xffffffffu, static_cast<unsigned>(best == m ? best_e : INT_MAX)));
-        const float v = __shfl_sync(0xffffffffu, best_l, e & 31);
+        const uint32_t who = __ballot_sync(0xffffffffu, best.key == m);
+        int e = lane + 32 * best.i;
+        if (who & (who - 1))  // lanes that tie: the lowest expert
+            e = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(best.key == m ? e : INT_MAX)));
+        else
+            e = __shfl_sync(0xffffffffu, e, __ffs(who) - 1);
         if (lane == j) {
             my_id = e;
-            my_l = v;
+            my_key = m;
         }
         if (lane == (e & 31)) {
-#pragma unroll
-            for (int i = 0; i < NPL; ++i)
-                if (lane + 32 * i == e)
-                    key[i] = 0u;
-            rescan();
+            taken |= 1u << best.i;
+            if (fresh) {
+                best.key = best.next;
+                best.i = best.next_i;
+            } else {
+                best = lane_best<NPL>(key, taken);
+            }
+            fresh = !fresh;
         }
     }
     // weights of the chosen, one lane each
-    float s = 0.0f;
+    const float my_l = my_id < 0 ? -INFINITY : p.bias ? to_float(row[my_id]) : choice_value(my_key);
+    float w = 0.0f;
     if (p.sigmoid) {
         if (my_id >= 0)
-            s = sigmoid(my_l);
+            w = sigmoid(my_l);
     } else if (p.renorm) {
         const float m = warp_max(my_l);  // relative to the largest chosen logit: its term is 1, the sum never 0
         if (my_id >= 0)
-            s = expf(my_l - m);
+            w = expf(my_l - m);
     } else if (my_id >= 0) {
-        s = __fdiv_rn(expf(my_l - top), total);
+        w = __fdiv_rn(expf(my_l - top), total);
     }
     if (p.renorm) {
-        const float sum = warp_sum(s);
-        s = __fdiv_rn(s, sum == 0.0f ? 1.0f : sum);
+        const float sum = warp_sum(w);
+        w = __fdiv_rn(w, sum == 0.0f ? 1.0f : sum);
     }
     if (lane < p.k) {
-        p.weights[t * p.k + lane] = bad ? NAN : s * p.scale;
+        p.weights[t * p.k + lane] = bad ? NAN : w * p.scale;
         p.ids[t * p.k + lane] = my_id;
     }
 }
@@ -392,9 +457,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 // warps before it and hands out the rows in order, 32 pairs at a time. One
 // part needs no count kernel.
 
-constexpr int kPlanWarps = 8;
-constexpr int kPlanPart = 1024;      // pairs per block before more blocks are taken
+constexpr int kPlanMaxWarps = 16;
+constexpr int kPlanPart = 2048;      // pairs per block before more blocks are taken
 constexpr int kPlanMaxBlocks = 128;  // every block reads the counts of all: more cost more than they give
+
+// Warps per block: their counts of up to 1024 experts share 48 KB of memory.
+inline int plan_warps(int64_t E) { return E <= 512 ? kPlanMaxWarps : kPlanMaxWarps / 2; }
 
 __host__ __device__ inline int plan_blocks(long long pairs)
 {
@@ -402,7 +470,7 @@ __host__ __device__ inline int plan_blocks(long long pairs)
     return static_cast<int>(b < 1 ? 1 : b > kPlanMaxBlocks ? kPlanMaxBlocks : b);
 }
 
-__global__ void __launch_bounds__(32 * kPlanWarps)
+__global__ void __launch_bounds__(32 * kPlanMaxWarps)
     plan_count_kernel(const int *__restrict__ ids, long long pairs, long long part, int E, int *__restrict__ counts)
 {
     extern __shared__ int plan_smem[];
@@ -420,21 +488,23 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
         counts[static_cast<long long>(blockIdx.x) * E + e] = plan_smem[e];
 }
 
-// Shared memory: kPlanWarps x E counts, then E totals.
-__global__ void __launch_bounds__(32 * kPlanWarps)
+// Shared memory: warps x E counts, E totals, E rows of the parts before.
+__global__ void __launch_bounds__(32 * kPlanMaxWarps)
     plan_scatter_kernel(const int *__restrict__ ids, long long pairs, long long part, int E, int k,
                         const int *__restrict__ counts, int *__restrict__ offsets, int *__restrict__ slots,
                         int *__restrict__ tokens)
 {
     extern __shared__ int plan_smem[];
     int *hist = plan_smem;                  // [warp][E]
-    int *start = plan_smem + kPlanWarps * E;  // first row of each expert
-    __shared__ int warp_total[kPlanWarps];
+    const int warps = static_cast<int>(blockDim.x >> 5);
+    int *start = plan_smem + warps * E;  // first row of each expert
+    int *before = start + E;
+    __shared__ int warp_total[kPlanMaxWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long lo = blockIdx.x * part, hi = min(lo + part, pairs);
-    const long long run = (((hi > lo ? hi - lo : 0) + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+    const long long run = (((hi > lo ? hi - lo : 0) + warps - 1) / warps + 31) / 32 * 32;
     const long long wlo = min(lo + warp * run, hi), whi = min(wlo + run, hi);
-    for (int i = tid; i < kPlanWarps * E; i += blockDim.x)
+    for (int i = tid; i < (warps + 2) * E; i += blockDim.x)
         hist[i] = 0;
     __syncthreads();
     for (long long i = wlo + lane; i < whi; i += 32) {
@@ -443,28 +513,34 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
             atomicAdd(&hist[warp * E + e], 1);
     }
     __syncthreads();
-    // totals of every expert, and of the parts before this one
-    int before[(GEMM_ROUTE_MAX_EXPERTS + 32 * kPlanWarps - 1) / (32 * kPlanWarps)];
-    int r = 0;
-    for (int e = tid; e < E; e += blockDim.x, ++r) {
-        int total = 0, prior = 0;
-        if (gridDim.x == 1) {
-            for (int w = 0; w < kPlanWarps; ++w)
+    // totals of every expert, and of the parts before this one: with several
+    // parts all threads add up the counts, `lanes` of them for each expert
+    if (gridDim.x == 1) {
+        for (int e = tid; e < E; e += blockDim.x) {
+            int total = 0;
+            for (int w = 0; w < warps; ++w)
                 total += hist[w * E + e];
-        } else {
-            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-                const int c = __ldg(counts + static_cast<long long>(b) * E + e);
+            start[e] = total;
+        }
+    } else {
+        const int lanes = max(1, static_cast<int>(blockDim.x) / E);
+        for (int i = tid; i < E * lanes; i += blockDim.x) {
+            const int e = i % E;
+            int total = 0, prior = 0;
+#pragma unroll 16
+            for (int b = i / E; b < static_cast<int>(gridDim.x); b += lanes) {
+                const int c = __ldcg(counts + static_cast<long long>(b) * E + e);
                 total += c;
                 prior += b < static_cast<int>(blockIdx.x) ? c : 0;
             }
+            atomicAdd(&start[e], total);  // whole numbers: the order of the additions does not show
+            atomicAdd(&before[e], prior);
         }
-        start[e] = total;
-        before[r] = prior;
     }
     __syncthreads();
     // exclusive scan of the totals: each warp takes a run of experts, one lane
     // a part of it
-    const int per = (E + 32 * kPlanWarps - 1) / (32 * kPlanWarps);
+    const int per = (E + 32 * warps - 1) / (32 * warps);
     const int e0 = min(tid * per, E), e1 = min(e0 + per, E);
     int sum = 0;
     for (int e = e0; e < e1; ++e)
@@ -480,7 +556,7 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
         warp_total[warp] = incl;
     __syncthreads();
     int base = incl - sum, kept = 0;
-    for (int w = 0; w < kPlanWarps; ++w) {
+    for (int w = 0; w < warps; ++w) {
         if (w < warp)
             base += warp_total[w];
         kept += warp_total[w];
@@ -498,10 +574,9 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
             offsets[E] = kept;
     }
     // first row of each warp's pairs of each expert
-    r = 0;
-    for (int e = tid; e < E; e += blockDim.x, ++r) {
-        int at = start[e] + before[r];
-        for (int w = 0; w < kPlanWarps; ++w) {
+    for (int e = tid; e < E; e += blockDim.x) {
+        int at = start[e] + before[e];
+        for (int w = 0; w < warps; ++w) {
             const int n = hist[w * E + e];
             hist[w * E + e] = at;
             at += n;
@@ -546,41 +621,112 @@ struct QuantParams {
 
 constexpr int kQuantMaxThreads = 512;
 
-template <typename X, bool GATED, bool WIDE>
-__device__ __forceinline__ void quant_load8(const X *row, int c, int K, float (&v)[8])
+// Column of element i of a thread's chunk c: eight neighbours for 16-byte
+// accesses (WIDE), else single elements with the threads side by side.
+template <bool WIDE>
+__device__ __forceinline__ int quant_col(int c, int i)
 {
-    const int n = K - c;
-    if (n <= 0) {
+    const int threads = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x);
+    return WIDE ? 8 * (tid + c * threads) + i : (8 * c + i) * threads + tid;
+}
+
+// A chunk of eight elements of a row: as loaded (PLAIN), so that it takes no
+// more registers than its bytes until it is rounded, or gated.
+template <typename X, bool GATED>
+struct QuantChunk {
+    using Store = typename std::conditional<GATED, float, X>::type;
+    union {
+        uint4 w[sizeof(Store) / 2];
+        Store e[8];
+    };
+    __device__ __forceinline__ QuantChunk() {}
+    __device__ __forceinline__ float at(int i) const { return to_float(e[i]); }
+};
+
+// Columns past K, and rows that do not exist (K 0), are zeros.
+template <typename X, bool GATED, bool WIDE>
+__device__ __forceinline__ void quant_load(const X *row, int c, int K, QuantChunk<X, GATED> &v)
+{
+    using Store = typename QuantChunk<X, GATED>::Store;
+    if constexpr (!GATED && WIDE) {
+        const int at = quant_col<WIDE>(c, 0);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(X) / 2); ++i)
+            v.w[i] = at < K ? __ldg(reinterpret_cast<const uint4 *>(row + at) + i) : make_uint4(0, 0, 0, 0);
+    } else {
+        float g[8], u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = 0.0f;
-        return;
-    }
-    load8<X, WIDE>(row + c, n, v);
-    if constexpr (GATED) {
-        float u[8];
-        load8<X, WIDE>(row + K + c, n, u);
+            g[i] = u[i] = 0.0f;
+        if constexpr (WIDE) {
+            const int at = quant_col<WIDE>(c, 0);
+            if (at < K) {  // K is a multiple of 8
+                load8<X, true>(row + at, 8, g);
+                if constexpr (GATED)
+                    load8<X, true>(row + K + at, 8, u);
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)  // silu(gate) * up
-            v[i] = __fmul_rn(__fdiv_rn(v[i], 1.0f + expf(-v[i])), u[i]);
+            for (int i = 0; i < 8; ++i) {
+                const int at = quant_col<WIDE>(c, i);
+                if (at < K) {
+                    g[i] = to_float(row[at]);
+                    if constexpr (GATED)
+                        u[i] = to_float(row[K + at]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (GATED)  // silu(gate) * up
+                v.e[i] = __fmul_rn(__fdiv_rn(g[i], 1.0f + expf(-g[i])), u[i]);
+            else
+                v.e[i] = from_float<Store>(g[i]);  // was loaded from this type
+        }
     }
 }
 
-__device__ __forceinline__ void quant_store8(int8_t *q, int n, bool wide, const float (&v)[8], float scale)
+// The largest magnitude of a chunk and `top`, as the bits of a nonnegative
+// fp32 number, whose order as integers puts infinities and NaN last.
+template <typename X, bool GATED>
+__device__ __forceinline__ uint32_t quant_top(const QuantChunk<X, GATED> &v, uint32_t top)
 {
-    int b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        b[i] = max(-127, min(127, __float2int_rn(__fdiv_rn(v[i], scale))));
-    if (wide) {
-        const uint32_t lo = (b[0] & 0xFF) | (b[1] & 0xFF) << 8 | (b[2] & 0xFF) << 16 | static_cast<uint32_t>(b[3]) << 24;
-        const uint32_t hi = (b[4] & 0xFF) | (b[5] & 0xFF) << 8 | (b[6] & 0xFF) << 16 | static_cast<uint32_t>(b[7]) << 24;
-        *reinterpret_cast<uint2 *>(q) = make_uint2(lo, hi);
-    } else {
+    if constexpr (sizeof(typename QuantChunk<X, GATED>::Store) == 4) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n)
-                q[i] = static_cast<int8_t>(b[i]);
+            top = max(top, __float_as_uint(v.e[i]) & 0x7fffffffu);
+    } else {
+        // sixteen-bit codes without their signs have the same order
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(v.w);
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        X e;
+        *reinterpret_cast<unsigned short *>(&e) = static_cast<unsigned short>(m);
+        top = max(top, __float_as_uint(to_float(e)) & 0x7fffffffu);
+    }
+    return top;
+}
+
+// round(x / scale) to whole numbers of at most 127, exactly that of the
+// correctly rounded quotient: x times the reciprocal is within 3e-5 of it, so
+// only where that lies near a half is the quotient itself taken. Adding
+// 1.5 * 2^23 rounds to a whole number and leaves it in the low byte.
+__device__ __forceinline__ void quant_round(const float (&x)[8], float scale, float inv, bool exact, uint32_t (&q)[8])
+{
+    const float magic = 12582912.0f;
+    float near_half = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = __fmaf_rn(x[i], inv, magic);
+        near_half = fmaxf(near_half, fabsf(__fmaf_rn(x[i], inv, -__fsub_rn(t, magic))));
+        q[i] = __float_as_uint(t);
+    }
+    if (exact || near_half > 0.4999f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = static_cast<uint32_t>(max(-127, min(127, __float2int_rn(__fdiv_rn(x[i], scale)))));
     }
 }
 
@@ -592,79 +738,77 @@ __global__ void __launch_bounds__(kQuantMaxThreads)
     quantize_kernel(const X *__restrict__ x, int8_t *__restrict__ q, const QuantParams p)
 {
     const long long m = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ float warp_top[kQuantMaxThreads / 32];
-    __shared__ int any_bad;
-    if (tid == 0)
-        any_bad = 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = static_cast<int>(blockDim.x >> 5);
+    __shared__ uint32_t warp_top[kQuantMaxThreads / 32];
     const long long r = p.index ? p.index[m] : m;
     const bool live = r >= 0 && r < p.x_rows;
     const int K = live ? p.K : 0;
     const X *row = x + (live ? r : 0) * p.ldx;
-    float v[CH ? CH : 1][8];
-    float top = 0.0f;
-    bool bad = false;
-    const int step = 8 * blockDim.x;
-    __syncthreads();
+    const int chunks = CH ? CH : (p.K + 8 * static_cast<int>(blockDim.x) - 1) / (8 * static_cast<int>(blockDim.x));
+    QuantChunk<X, GATED> v[CH ? CH : 1];
+    uint32_t top = 0u;
     if constexpr (CH > 0) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-            quant_load8<X, GATED, WIDE>(row, 8 * tid + c * step, K, v[c]);
+            quant_load<X, GATED, WIDE>(row, c, K, v[c]);
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                top = fmaxf(top, fabsf(v[c][i]));
-                bad |= !(fabsf(v[c][i]) < INFINITY);
-            }
+            top = quant_top(v[c], top);
     } else {
-        for (int c = 8 * tid; c < K; c += step) {
-            quant_load8<X, GATED, WIDE>(row, c, K, v[0]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                top = fmaxf(top, fabsf(v[0][i]));
-                bad |= !(fabsf(v[0][i]) < INFINITY);
-            }
+        for (int c = 0; c < chunks; ++c) {
+            quant_load<X, GATED, WIDE>(row, c, K, v[0]);
+            top = quant_top(v[0], top);
         }
     }
-    top = warp_max(top);
-    if (lane == 0)
-        warp_top[warp] = top;
-    if (bad)
-        any_bad = 1;
-    __syncthreads();
-    bad = any_bad != 0;
-    top = 0.0f;
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w)
-        top = fmaxf(top, warp_top[w]);
-    const float scale = __fdiv_rn(top, 127.0f);
-    // a scale that is 0 (also: rounded to 0) divides by 1 and leaves zeros
-    const float by = bad || scale == 0.0f ? 1.0f : scale;
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (warps > 1) {
+        if (lane == 0)
+            warp_top[warp] = top;
+        __syncthreads();
+        top = __reduce_max_sync(0xffffffffu, lane < warps ? warp_top[lane] : 0u);
+    }
+    const bool bad = top >= 0x7f800000u;  // the row holds an infinity or a NaN
+    const float scale = bad ? NAN : __fdiv_rn(__uint_as_float(top), 127.0f);
     if (tid == 0)
-        p.scales[m] = bad ? NAN : scale;
+        p.scales[m] = scale;
+    // a scale that is 0 (also: rounded to 0) divides by 1 and leaves zeros; one
+    // that is subnormal is divided by, its reciprocal being infinite or its
+    // rounding coarse enough for quotients above 127
+    const float by = bad || scale == 0.0f ? 1.0f : scale;
+    const float inv = __frcp_rn(by);
+    const bool exact = by < 1.17549435e-38f;
     int8_t *out = q + m * p.ldq;
-    if constexpr (CH > 0) {
+    auto write = [&](int c, const QuantChunk<X, GATED> &e) {
+        float f[8];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int at = 8 * tid + c * step;
+        for (int i = 0; i < 8; ++i)
+            f[i] = bad ? 0.0f : e.at(i);
+        uint32_t b[8];
+        quant_round(f, by, inv, exact, b);
+        if constexpr (WIDE) {
+            const int at = quant_col<WIDE>(c, 0);
             if (at < p.K) {
-                if (bad) {
+                const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+                const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+                *reinterpret_cast<uint2 *>(out + at) = make_uint2(lo, hi);
+            }
+        } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[c][i] = 0.0f;
-                }
-                quant_store8(out + at, p.K - at, WIDE, v[c], by);
+            for (int i = 0; i < 8; ++i) {
+                const int at = quant_col<WIDE>(c, i);
+                if (at < p.K)
+                    out[at] = static_cast<int8_t>(b[i] & 0xffu);
             }
         }
-    } else {
-        for (int at = 8 * tid; at < p.K; at += step) {
-            quant_load8<X, GATED, WIDE>(row, at, K, v[0]);
-            if (bad) {
+    };
+    if constexpr (CH > 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[0][i] = 0.0f;
-            }
-            quant_store8(out + at, p.K - at, WIDE, v[0], by);
+        for (int c = 0; c < CH; ++c)
+            write(c, v[c]);
+    } else {
+        for (int c = 0; c < chunks; ++c) {
+            quant_load<X, GATED, WIDE>(row, c, K, v[0]);
+            write(c, v[0]);
         }
     }
 }
@@ -813,25 +957,30 @@ gemm_status_t launch_quantize(const void *x, int8_t *q, const QuantParams &p, cu
     const bool wide = aligned_to(x, 16) && aligned_to(q, 8) && p.ldx * static_cast<int64_t>(sizeof(X)) % 16 == 0 &&
                       p.ldq % 8 == 0 && p.K % 8 == 0;
     const int chunks = (p.K + 7) / 8;
-    const int ch = chunks <= kQuantMaxThreads / 2 ? 1 : chunks <= 2 * kQuantMaxThreads ? 2 : chunks <= 4 * kQuantMaxThreads ? 4 : 0;
+    // chunks a thread: small blocks, so that several share an SM and one's loads overlap another's rounding
+    const int ch = chunks <= 256 ? 1 : chunks <= 512 ? 2 : chunks <= 4 * kQuantMaxThreads ? 4 : 0;
     int threads = kQuantMaxThreads;
     if (ch > 0)
         threads = std::max(32, ((chunks + ch - 1) / ch + 31) / 32 * 32);
     const X *xp = static_cast<const X *>(x);
     const unsigned grid = static_cast<unsigned>(p.M);
 #define G300_QUANT(W, C) quantize_kernel<X, GATED, W, C><<<grid, threads, 0, st>>>(xp, q, p)
-    if (wide) {
-        if (ch == 1)
-            G300_QUANT(true, 1);
-        else if (ch == 2)
-            G300_QUANT(true, 2);
-        else if (ch == 4)
-            G300_QUANT(true, 4);
-        else
-            G300_QUANT(true, 0);
-    } else {
-        G300_QUANT(false, 0);
-    }
+#define G300_QUANT_CH(W)                                                                              \
+    do {                                                                                              \
+        if (ch == 1)                                                                                  \
+            G300_QUANT(W, 1);                                                                         \
+        else if (ch == 2)                                                                             \
+            G300_QUANT(W, 2);                                                                         \
+        else if (ch == 4)                                                                             \
+            G300_QUANT(W, 4);                                                                         \
+        else                                                                                          \
+            G300_QUANT(W, 0);                                                                         \
+    } while (0)
+    if (wide)
+        G300_QUANT_CH(true);
+    else
+        G300_QUANT_CH(false);
+#undef G300_QUANT_CH
 #undef G300_QUANT
     return host_launched();
 }
@@ -871,6 +1020,8 @@ gemm_status_t gemm_route(int64_t T, int64_t E, const void *logits, gemm_out_t l_
     p.renorm = r.renormalize != 0;
     p.scale = r.scale;
     p.per_inv = p.per > 1 ? static_cast<unsigned int>(((uint64_t(1) << 32) + p.per - 1) / p.per) : 0u;
+    for (p.group_lanes = 32; p.group_lanes * p.groups > 32;)
+        p.group_lanes /= 2;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return with_type(l_type, [&](auto tag) {
         using L = decltype(tag);
@@ -943,15 +1094,16 @@ gemm_status_t gemm_route_plan(int64_t T, int64_t E, int k, const int32_t *ids, i
     const int64_t pairs = T * k;
     const int blocks = plan_blocks(pairs);
     const long long part = (pairs + blocks - 1) / blocks;
+    const int warps = plan_warps(E);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     int *counts = static_cast<int *>(workspace);
     int launched = 0;
     if (blocks > 1) {
-        plan_count_kernel<<<blocks, 32 * kPlanWarps, E * sizeof(int), st>>>(ids, pairs, part, static_cast<int>(E), counts);
+        plan_count_kernel<<<blocks, 32 * warps, E * sizeof(int), st>>>(ids, pairs, part, static_cast<int>(E), counts);
         if (cudaPeekAtLastError() == cudaSuccess)
             ++launched;
     }
-    plan_scatter_kernel<<<blocks, 32 * kPlanWarps, (kPlanWarps + 1) * E * sizeof(int), st>>>(
+    plan_scatter_kernel<<<blocks, 32 * warps, (warps + 2) * E * sizeof(int), st>>>(
         ids, pairs, part, static_cast<int>(E), k, counts, offsets, slots, tokens);
     return host_launched(launched + 1);
 }
