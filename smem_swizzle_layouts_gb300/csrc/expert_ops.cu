@@ -461,8 +461,13 @@ constexpr int kPlanMaxWarps = 16;
 constexpr int kPlanPart = 2048;      // pairs per block before more blocks are taken
 constexpr int kPlanMaxBlocks = 128;  // every block reads the counts of all: more cost more than they give
 
-// Warps per block: their counts of up to 1024 experts share 48 KB of memory.
-inline int plan_warps(int64_t E) { return E <= 512 ? kPlanMaxWarps : kPlanMaxWarps / 2; }
+// Warps per block: about four steps of 32 pairs for each, and few enough that
+// their counts of all experts share 48 KB of memory.
+inline int plan_warps(int64_t part, int64_t E)
+{
+    const int most = E <= 512 ? kPlanMaxWarps : kPlanMaxWarps / 2;
+    return part <= 512 ? 4 : part <= 1024 ? 8 : most;
+}
 
 __host__ __device__ inline int plan_blocks(long long pairs)
 {
@@ -474,6 +479,7 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps)
     plan_count_kernel(const int *__restrict__ ids, long long pairs, long long part, int E, int *__restrict__ counts)
 {
     extern __shared__ int plan_smem[];
+    cudaTriggerProgrammaticLaunchCompletion();  // plan_scatter_kernel may start its own counting
     for (int e = threadIdx.x; e < E; e += blockDim.x)
         plan_smem[e] = 0;
     __syncthreads();
@@ -523,6 +529,7 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps)
             start[e] = total;
         }
     } else {
+        cudaGridDependencySynchronize();  // the counts of all parts are written
         const int lanes = max(1, static_cast<int>(blockDim.x) / E);
         for (int i = tid; i < E * lanes; i += blockDim.x) {
             const int e = i % E;
@@ -1094,7 +1101,7 @@ gemm_status_t gemm_route_plan(int64_t T, int64_t E, int k, const int32_t *ids, i
     const int64_t pairs = T * k;
     const int blocks = plan_blocks(pairs);
     const long long part = (pairs + blocks - 1) / blocks;
-    const int warps = plan_warps(E);
+    const int warps = plan_warps(part, E);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     int *counts = static_cast<int *>(workspace);
     int launched = 0;
@@ -1103,8 +1110,24 @@ gemm_status_t gemm_route_plan(int64_t T, int64_t E, int k, const int32_t *ids, i
         if (cudaPeekAtLastError() == cudaSuccess)
             ++launched;
     }
-    plan_scatter_kernel<<<blocks, 32 * warps, (warps + 2) * E * sizeof(int), st>>>(
-        ids, pairs, part, static_cast<int>(E), k, counts, offsets, slots, tokens);
+    // the scatter kernel starts while the counts are still being written, and
+    // waits for them before it reads them
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(warps + 2) * E * sizeof(int);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (blocks > 1) {
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&cfg, plan_scatter_kernel, static_cast<const int *>(ids), static_cast<long long>(pairs), part,
+                           static_cast<int>(E), k, static_cast<const int *>(counts), static_cast<int *>(offsets),
+                           static_cast<int *>(slots), static_cast<int *>(tokens)) != cudaSuccess)
+        return GEMM_ERR_CUDA;
     return host_launched(launched + 1);
 }
 
