@@ -47,10 +47,12 @@ __device__ __forceinline__ __half from_float<__half>(float x)
     return __float2half_rn(x);
 }
 
-// Eight neighbouring elements: 16-byte accesses when WIDE (the pointer is
-// 16-byte aligned), else single elements, of which `n` exist.
+// Eight elements of a row of n: neighbours from `at`, by 16-byte accesses, when
+// WIDE (the address is a multiple of 16 bytes and n one of eight elements),
+// else single ones `step` apart, so that the threads lie side by side. Loads
+// past the end give zeros.
 template <typename T, bool WIDE>
-__device__ __forceinline__ void load8(const T *p, int n, float (&v)[8])
+__device__ __forceinline__ void load8(const T *p, int at, int step, int n, float (&v)[8])
 {
     if constexpr (WIDE) {
         union {
@@ -59,19 +61,19 @@ __device__ __forceinline__ void load8(const T *p, int n, float (&v)[8])
         } u;
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-            u.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            u.w[i] = at < n ? reinterpret_cast<const uint4 *>(p + at)[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = to_float(u.e[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = i < n ? to_float(p[i]) : 0.0f;
+            v[i] = at + i * step < n ? to_float(p[at + i * step]) : 0.0f;
     }
 }
 
 template <typename T, bool WIDE>
-__device__ __forceinline__ void store8(T *p, int n, const float (&v)[8])
+__device__ __forceinline__ void store8(T *p, int at, int step, int n, const float (&v)[8])
 {
     if constexpr (WIDE) {
         union {
@@ -81,14 +83,16 @@ __device__ __forceinline__ void store8(T *p, int n, const float (&v)[8])
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             u.e[i] = from_float<T>(v[i]);
+        if (at < n) {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-            reinterpret_cast<uint4 *>(p)[i] = u.w[i];
+            for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+                reinterpret_cast<uint4 *>(p + at)[i] = u.w[i];
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n)
-                p[i] = from_float<T>(v[i]);
+            if (at + i * step < n)
+                p[at + i * step] = from_float<T>(v[i]);
     }
 }
 
@@ -194,11 +198,12 @@ __device__ __forceinline__ LaneBest lane_best(const uint32_t (&key)[NPL], uint32
 // Bound by instructions: 16384 tokens of 256 experts with 8 taken, see the
 // measurements beside kRouteWarps.
 template <typename L, int NPL>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *__restrict__ logits, const RouteParams p)
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *logits, const RouteParams p)
 {
     extern __shared__ float group_smem[];  // per warp: groups x (per | 1) choice values
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp;
+    grid_start();
     if (t >= p.T)
         return;
     const L *row = logits + t * p.ldl;
@@ -372,23 +377,35 @@ struct RouteGradParams {
 
 // One warp per token. The chosen experts' values are computed one lane each
 // and put into a shared-memory row of zeros, which is then written whole;
-// only the softmax over all experts reads the other logits.
-template <typename L>
+// only the softmax over all experts (FULL) reads the other logits, which it
+// holds in registers (NPL a lane) from the maximum to the gradient. Bound by
+// the writing of dlogits.
+template <typename L, int NPL, bool FULL>
 __global__ void __launch_bounds__(32 * kRouteWarps)
-    route_backward_kernel(const L *__restrict__ logits, L *__restrict__ dlogits, const RouteGradParams p)
+    route_backward_kernel(const L *logits, L *__restrict__ dlogits, const RouteGradParams p)
 {
     extern __shared__ float grad_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp;
+    float *ds = grad_smem + warp * p.E;
+    if (t < p.T)
+        for (int e = lane; e < p.E; e += 32)
+            ds[e] = 0.0f;
+    grid_start();
     if (t >= p.T)
         return;
-    float *ds = grad_smem + warp * p.E;
     const L *row = logits + t * p.ldl;
     L *out = dlogits + t * p.lddl;
-    for (int e = lane; e < p.E; e += 32)
-        ds[e] = 0.0f;
     int id = -1;
     float g = 0.0f, x = -INFINITY;
+    float s[NPL];
+    if constexpr (FULL) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            s[i] = e < p.E ? to_float(row[e]) : -INFINITY;
+        }
+    }
     if (lane < p.k) {
         id = p.ids[t * p.k + lane];
         if (id < 0 || id >= p.E)
@@ -399,54 +416,63 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
         }
     }
     __syncwarp();
-    if (p.sigmoid || p.renorm) {
+    if constexpr (FULL) {
+        // dl_e = s_e (ds_e - sum ds s)
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            top = fmaxf(top, s[i]);
+        top = warp_max(top);
+        if (top == -INFINITY)
+            top = 0.0f;
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            s[i] = expf(s[i] - top);
+            total += s[i];
+        }
+        total = warp_sum(total);
+        if (total == 0.0f)
+            total = 1.0f;
+        const float dot = warp_sum(id >= 0 ? g * __fdiv_rn(expf(x - top), total) : 0.0f);
+        if (id >= 0)
+            ds[id] = g;
+        __syncwarp();
+        const float inv = __frcp_rn(total);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            if (e < p.E)
+                out[e] = from_float<L>(s[i] * inv * (ds[e] - dot));
+        }
+    } else {
         // share of the chosen score in the sum, and d score / d logit over the score
-        float s = 0.0f, rest = 1.0f;
+        float c = 0.0f, rest = 1.0f;
         if (p.sigmoid) {
             if (id >= 0) {
-                s = sigmoid(x);
+                c = sigmoid(x);
                 rest = sigmoid(-x);  // 1 - s without its cancellation
             }
         } else {
             const float m = warp_max(x);
             if (id >= 0)
-                s = expf(x - m);
+                c = expf(x - m);
         }
-        float d = g * s * rest;
+        float d = g * c * rest;
         if (p.renorm) {
-            float sum = warp_sum(s);
+            float sum = warp_sum(c);
             if (sum == 0.0f)
                 sum = 1.0f;
-            const float w = __fdiv_rn(s, sum);
+            const float w = __fdiv_rn(c, sum);
             d = w * (g - warp_sum(g * w)) * rest;
         }
         if (id >= 0)
             ds[id] = d;
         __syncwarp();
+#pragma unroll 8
         for (int e = lane; e < p.E; e += 32)
             out[e] = from_float<L>(ds[e]);
-        return;
     }
-    // softmax over all experts: dl_e = s_e (ds_e - sum ds s)
-    float top = -INFINITY;
-    for (int e = lane; e < p.E; e += 32)
-        top = fmaxf(top, to_float(row[e]));
-    top = warp_max(top);
-    if (top == -INFINITY)
-        top = 0.0f;
-    float total = 0.0f;
-    for (int e = lane; e < p.E; e += 32)
-        total += expf(to_float(row[e]) - top);
-    total = warp_sum(total);
-    if (total == 0.0f)
-        total = 1.0f;
-    const float s = id >= 0 ? __fdiv_rn(expf(x - top), total) : 0.0f;
-    const float dot = warp_sum(g * s);
-    if (id >= 0)
-        ds[id] = g;
-    __syncwarp();
-    for (int e = lane; e < p.E; e += 32)
-        out[e] = from_float<L>(__fdiv_rn(expf(to_float(row[e]) - top), total) * (ds[e] - dot));
 }
 
 // ---------------------------------------------------------------- order by expert
@@ -475,19 +501,40 @@ __host__ __device__ inline int plan_blocks(long long pairs)
     return static_cast<int>(b < 1 ? 1 : b > kPlanMaxBlocks ? kPlanMaxBlocks : b);
 }
 
+constexpr int kPlanBatch = 4;  // ids a lane loads at a time
+
+// The ids of pairs i, i + 32, ... below `end`; -1 for those outside 0..E-1.
+__device__ __forceinline__ void plan_load(const int *ids, long long i, long long end, int E, int (&id)[kPlanBatch])
+{
+#pragma unroll
+    for (int u = 0; u < kPlanBatch; ++u)
+        id[u] = i + 32 * u < end ? ids[i + 32 * u] : -1;
+#pragma unroll
+    for (int u = 0; u < kPlanBatch; ++u)
+        if (id[u] < 0 || id[u] >= E)
+            id[u] = -1;
+}
+
 __global__ void __launch_bounds__(32 * kPlanMaxWarps)
-    plan_count_kernel(const int *__restrict__ ids, long long pairs, long long part, int E, int *__restrict__ counts)
+    plan_count_kernel(const int *ids, long long pairs, long long part, int E, int *counts)
 {
     extern __shared__ int plan_smem[];
-    cudaTriggerProgrammaticLaunchCompletion();  // plan_scatter_kernel may start its own counting
+    // the ids are written; only then may plan_scatter_kernel start, which
+    // counts them for itself before it waits for this kernel
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
     for (int e = threadIdx.x; e < E; e += blockDim.x)
         plan_smem[e] = 0;
     __syncthreads();
     const long long lo = blockIdx.x * part, hi = min(lo + part, pairs);
-    for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x) {
-        const int e = ids[i];
-        if (e >= 0 && e < E)
-            atomicAdd(&plan_smem[e], 1);  // a count: the order of the additions does not show
+    const int warp = threadIdx.x >> 5, warps = static_cast<int>(blockDim.x >> 5), lane = threadIdx.x & 31;
+    for (long long i0 = lo + 32 * kPlanBatch * warp; i0 < hi; i0 += 32 * kPlanBatch * warps) {
+        int id[kPlanBatch];
+        plan_load(ids, i0 + lane, hi, E, id);
+#pragma unroll
+        for (int u = 0; u < kPlanBatch; ++u)
+            if (id[u] >= 0)
+                atomicAdd(&plan_smem[id[u]], 1);  // a count: the order of the additions does not show
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x)
@@ -496,9 +543,9 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps)
 
 // Shared memory: warps x E counts, E totals, E rows of the parts before.
 __global__ void __launch_bounds__(32 * kPlanMaxWarps)
-    plan_scatter_kernel(const int *__restrict__ ids, long long pairs, long long part, int E, int k,
-                        const int *__restrict__ counts, int *__restrict__ offsets, int *__restrict__ slots,
-                        int *__restrict__ tokens)
+    plan_scatter_kernel(const int *ids, long long pairs, long long part, int E, int k,
+                        const int *counts, int *offsets, int *slots,
+                        int *tokens)
 {
     extern __shared__ int plan_smem[];
     int *hist = plan_smem;                  // [warp][E]
@@ -510,13 +557,18 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps)
     const long long lo = blockIdx.x * part, hi = min(lo + part, pairs);
     const long long run = (((hi > lo ? hi - lo : 0) + warps - 1) / warps + 31) / 32 * 32;
     const long long wlo = min(lo + warp * run, hi), whi = min(wlo + run, hi);
+    if (gridDim.x == 1)
+        grid_start();
     for (int i = tid; i < (warps + 2) * E; i += blockDim.x)
         hist[i] = 0;
     __syncthreads();
-    for (long long i = wlo + lane; i < whi; i += 32) {
-        const int e = ids[i];
-        if (e >= 0 && e < E)
-            atomicAdd(&hist[warp * E + e], 1);
+    for (long long i0 = wlo; i0 < whi; i0 += 32 * kPlanBatch) {
+        int id[kPlanBatch];
+        plan_load(ids, i0 + lane, whi, E, id);
+#pragma unroll
+        for (int u = 0; u < kPlanBatch; ++u)
+            if (id[u] >= 0)
+                atomicAdd(&hist[warp * E + id[u]], 1);
     }
     __syncthreads();
     // totals of every expert, and of the parts before this one: with several
@@ -529,7 +581,7 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps)
             start[e] = total;
         }
     } else {
-        cudaGridDependencySynchronize();  // the counts of all parts are written
+        grid_start();  // the counts of all parts are written
         const int lanes = max(1, static_cast<int>(blockDim.x) / E);
         for (int i = tid; i < E * lanes; i += blockDim.x) {
             const int e = i % E;
@@ -591,23 +643,26 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps)
     }
     __syncthreads();
     int *mine = hist + warp * E;
-    for (long long i0 = wlo; i0 < whi; i0 += 32) {
-        const long long i = i0 + lane;
-        int e = i < whi ? ids[i] : -1;
-        if (e < 0 || e >= E)
-            e = -1;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        int slot = -1;
-        if (e >= 0)
-            slot = mine[e] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (e >= 0 && (same >> lane) == 1u)  // the last of its expert moves the count on
-            mine[e] = slot + 1;
-        __syncwarp();
-        if (i < whi) {
-            slots[i] = slot;
-            if (slot >= 0)
-                tokens[slot] = static_cast<int>(i / k);
+    for (long long i0 = wlo; i0 < whi; i0 += 32 * kPlanBatch) {
+        int id[kPlanBatch];
+        plan_load(ids, i0 + lane, whi, E, id);
+#pragma unroll
+        for (int u = 0; u < kPlanBatch; ++u) {
+            const long long i = i0 + 32 * u + lane;
+            const int e = id[u];
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            int slot = -1;
+            if (e >= 0)
+                slot = mine[e] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (e >= 0 && (same >> lane) == 1u)  // the last of its expert moves the count on
+                mine[e] = slot + 1;
+            __syncwarp();
+            if (i < whi) {
+                slots[i] = slot;
+                if (slot >= 0)
+                    tokens[slot] = static_cast<int>(i / k);
+            }
         }
     }
     // rows that no pair has
@@ -659,7 +714,7 @@ __device__ __forceinline__ void quant_load(const X *row, int c, int K, QuantChun
         const int at = quant_col<WIDE>(c, 0);
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(X) / 2); ++i)
-            v.w[i] = at < K ? __ldg(reinterpret_cast<const uint4 *>(row + at) + i) : make_uint4(0, 0, 0, 0);
+            v.w[i] = at < K ? reinterpret_cast<const uint4 *>(row + at)[i] : make_uint4(0, 0, 0, 0);
     } else {
         float g[8], u[8];
 #pragma unroll
@@ -667,11 +722,9 @@ __device__ __forceinline__ void quant_load(const X *row, int c, int K, QuantChun
             g[i] = u[i] = 0.0f;
         if constexpr (WIDE) {
             const int at = quant_col<WIDE>(c, 0);
-            if (at < K) {  // K is a multiple of 8
-                load8<X, true>(row + at, 8, g);
-                if constexpr (GATED)
-                    load8<X, true>(row + K + at, 8, u);
-            }
+            load8<X, true>(row, at, 0, K, g);
+            if constexpr (GATED)
+                load8<X, true>(row + K, at, 0, K, u);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -742,11 +795,12 @@ __device__ __forceinline__ void quant_round(const float (&x)[8], float scale, fl
 // twice, the second time from L2). WIDE: 16-byte loads and 8-byte stores.
 template <typename X, bool GATED, bool WIDE, int CH>
 __global__ void __launch_bounds__(kQuantMaxThreads)
-    quantize_kernel(const X *__restrict__ x, int8_t *__restrict__ q, const QuantParams p)
+    quantize_kernel(const X *x, int8_t *__restrict__ q, const QuantParams p)
 {
     const long long m = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = static_cast<int>(blockDim.x >> 5);
     __shared__ uint32_t warp_top[kQuantMaxThreads / 32];
+    grid_start();
     const long long r = p.index ? p.index[m] : m;
     const bool live = r >= 0 && r < p.x_rows;
     const int K = live ? p.K : 0;
@@ -836,10 +890,12 @@ constexpr int kCombineThreads = 128;
 // rows, two of which are in flight at a time.
 template <typename Y, typename D, bool WIDE>
 __global__ void __launch_bounds__(kCombineThreads)
-    combine_kernel(const Y *__restrict__ y, D *__restrict__ d, const CombineParams p, int col_blocks)
+    combine_kernel(const Y *y, D *__restrict__ d, const CombineParams p, int col_blocks)
 {
     const long long t = blockIdx.x / col_blocks;
-    const int c = static_cast<int>(blockIdx.x % col_blocks) * (8 * kCombineThreads) + 8 * threadIdx.x;
+    const int c0 = static_cast<int>(blockIdx.x % col_blocks) * (8 * kCombineThreads);
+    const int c = c0 + (WIDE ? 8 : 1) * static_cast<int>(threadIdx.x);
+    grid_start();
     if (c >= p.N)
         return;
     const int *slots = p.slots + t * p.k;
@@ -847,17 +903,17 @@ __global__ void __launch_bounds__(kCombineThreads)
     float acc[8] = {};
 #pragma unroll 4
     for (int j = 0; j < p.k; ++j) {
-        const int r = __ldg(slots + j);
+        const int r = slots[j];
         if (r >= 0 && r < p.y_rows) {
-            const float w = __ldg(weights + j);
+            const float w = weights[j];
             float v[8];
-            load8<Y, WIDE>(y + r * p.ldy + c, p.N - c, v);
+            load8<Y, WIDE>(y + r * p.ldy, c, kCombineThreads, p.N, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 acc[i] = fmaf(w, v[i], acc[i]);
         }
     }
-    store8<D, WIDE>(d + t * p.ldd + c, p.N - c, acc);
+    store8<D, WIDE>(d + t * p.ldd, c, kCombineThreads, p.N, acc);
 }
 
 struct CombineGradParams {
@@ -875,11 +931,12 @@ constexpr int kCombineGradWarps = 8;
 // row of dY and summing the dot product; a token's warps share dD's row in L1.
 template <typename Y, typename D, bool WIDE>
 __global__ void __launch_bounds__(32 * kCombineGradWarps)
-    combine_backward_kernel(const D *__restrict__ dd, const Y *__restrict__ y, Y *__restrict__ dy,
+    combine_backward_kernel(const D *dd, const Y *y, Y *__restrict__ dy,
                             const CombineGradParams p)
 {
     const int lane = threadIdx.x & 31;
     const long long pair = static_cast<long long>(blockIdx.x) * kCombineGradWarps + (threadIdx.x >> 5);
+    grid_start();
     if (pair >= p.T * p.k)
         return;
     const long long t = pair / p.k;
@@ -891,16 +948,17 @@ __global__ void __launch_bounds__(32 * kCombineGradWarps)
         const Y *yr = y + r * p.ldy;
         Y *o = dy + r * p.lddy;
 #pragma unroll 4
-        for (int c = 8 * lane; c < p.N; c += 256) {
+        for (int c0 = 0; c0 < p.N; c0 += 256) {
+            const int c = c0 + (WIDE ? 8 : 1) * lane;
             float a[8], b[8];
-            load8<D, WIDE>(g + c, p.N - c, a);
-            load8<Y, WIDE>(yr + c, p.N - c, b);
+            load8<D, WIDE>(g, c, 32, p.N, a);
+            load8<Y, WIDE>(yr, c, 32, p.N, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dot = fmaf(a[i], b[i], dot);
                 b[i] = w * a[i];
             }
-            store8<Y, WIDE>(o + c, p.N - c, b);
+            store8<Y, WIDE>(o, c, 32, p.N, b);
         }
     }
     dot = warp_sum(dot);
@@ -954,8 +1012,16 @@ gemm_status_t launch_route(const void *logits, const RouteParams &p, cudaStream_
 {
     const long long blocks = (p.T + kRouteWarps - 1) / kRouteWarps;
     const size_t smem = p.groups > 1 ? sizeof(float) * kRouteWarps * p.groups * (p.per | 1) : 0;
-    route_kernel<L, NPL><<<static_cast<unsigned>(blocks), 32 * kRouteWarps, smem, st>>>(static_cast<const L *>(logits), p);
-    return host_launched();
+    return host_launch(route_kernel<L, NPL>, static_cast<unsigned>(blocks), 32 * kRouteWarps, smem, st, 0,
+                       static_cast<const L *>(logits), p);
+}
+
+template <typename L, int NPL, bool FULL>
+gemm_status_t launch_route_backward(const void *logits, void *dlogits, const RouteGradParams &p, cudaStream_t st)
+{
+    const unsigned blocks = static_cast<unsigned>((p.T + kRouteWarps - 1) / kRouteWarps);
+    return host_launch(route_backward_kernel<L, NPL, FULL>, blocks, 32 * kRouteWarps, sizeof(float) * kRouteWarps * p.E, st, 0,
+                       static_cast<const L *>(logits), static_cast<L *>(dlogits), p);
 }
 
 template <typename X, bool GATED>
@@ -971,7 +1037,7 @@ gemm_status_t launch_quantize(const void *x, int8_t *q, const QuantParams &p, cu
         threads = std::max(32, ((chunks + ch - 1) / ch + 31) / 32 * 32);
     const X *xp = static_cast<const X *>(x);
     const unsigned grid = static_cast<unsigned>(p.M);
-#define G300_QUANT(W, C) quantize_kernel<X, GATED, W, C><<<grid, threads, 0, st>>>(xp, q, p)
+#define G300_QUANT(W, C) return host_launch(quantize_kernel<X, GATED, W, C>, grid, threads, 0, st, 0, xp, q, p)
 #define G300_QUANT_CH(W)                                                                              \
     do {                                                                                              \
         if (ch == 1)                                                                                  \
@@ -989,7 +1055,6 @@ gemm_status_t launch_quantize(const void *x, int8_t *q, const QuantParams &p, cu
         G300_QUANT_CH(false);
 #undef G300_QUANT_CH
 #undef G300_QUANT
-    return host_launched();
 }
 
 }  // namespace
@@ -1070,10 +1135,12 @@ gemm_status_t gemm_route_backward(int64_t T, int64_t E, const void *logits, gemm
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return with_type(l_type, [&](auto tag) {
         using L = decltype(tag);
-        const unsigned blocks = static_cast<unsigned>((T + kRouteWarps - 1) / kRouteWarps);
-        route_backward_kernel<L><<<blocks, 32 * kRouteWarps, sizeof(float) * kRouteWarps * E, st>>>(
-            static_cast<const L *>(logits), static_cast<L *>(dlogits), p);
-        return host_launched();
+        // the softmax over all experts, by the experts a lane holds; the others need none
+        return p.sigmoid || p.renorm ? launch_route_backward<L, 1, false>(logits, dlogits, p, st)
+               : E <= 64             ? launch_route_backward<L, 2, true>(logits, dlogits, p, st)
+               : E <= 256            ? launch_route_backward<L, 8, true>(logits, dlogits, p, st)
+               : E <= 512            ? launch_route_backward<L, 16, true>(logits, dlogits, p, st)
+                                     : launch_route_backward<L, 32, true>(logits, dlogits, p, st);
     });
 }
 
@@ -1104,31 +1171,17 @@ gemm_status_t gemm_route_plan(int64_t T, int64_t E, int k, const int32_t *ids, i
     const int warps = plan_warps(part, E);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     int *counts = static_cast<int *>(workspace);
-    int launched = 0;
     if (blocks > 1) {
-        plan_count_kernel<<<blocks, 32 * warps, E * sizeof(int), st>>>(ids, pairs, part, static_cast<int>(E), counts);
-        if (cudaPeekAtLastError() == cudaSuccess)
-            ++launched;
+        const gemm_status_t c = host_launch(plan_count_kernel, static_cast<unsigned>(blocks), 32 * warps, E * sizeof(int), st, 0,
+                                            ids, pairs, part, static_cast<int>(E), counts);
+        if (c != GEMM_OK)
+            return c;
     }
     // the scatter kernel starts while the counts are still being written, and
     // waits for them before it reads them
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps), 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(warps + 2) * E * sizeof(int);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    if (blocks > 1) {
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    if (cudaLaunchKernelEx(&cfg, plan_scatter_kernel, static_cast<const int *>(ids), static_cast<long long>(pairs), part,
-                           static_cast<int>(E), k, static_cast<const int *>(counts), static_cast<int *>(offsets),
-                           static_cast<int *>(slots), static_cast<int *>(tokens)) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    return host_launched(launched + 1);
+    return host_launch(plan_scatter_kernel, static_cast<unsigned>(blocks), 32 * warps,
+                       static_cast<size_t>(warps + 2) * E * sizeof(int), st, 0, ids, pairs, part, static_cast<int>(E), k, counts,
+                       offsets, slots, tokens);
 }
 
 gemm_status_t gemm_quantize_int8(int64_t M, int64_t K, const void *X, gemm_out_t x_type, int64_t x_rows, int64_t ldx,
@@ -1200,11 +1253,8 @@ gemm_status_t gemm_route_combine(int64_t T, int64_t N, int k, const void *Y, gem
             using D_ = decltype(dtag);
             const Y_ *yp = static_cast<const Y_ *>(Y);
             D_ *dp = static_cast<D_ *>(D);
-            if (wide)
-                combine_kernel<Y_, D_, true><<<grid, kCombineThreads, 0, st>>>(yp, dp, p, static_cast<int>(col_blocks));
-            else
-                combine_kernel<Y_, D_, false><<<grid, kCombineThreads, 0, st>>>(yp, dp, p, static_cast<int>(col_blocks));
-            return host_launched();
+            return host_launch(wide ? combine_kernel<Y_, D_, true> : combine_kernel<Y_, D_, false>, grid, kCombineThreads, 0, st, 0,
+                               yp, dp, p, static_cast<int>(col_blocks));
         });
     });
 }
@@ -1248,11 +1298,8 @@ gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const voi
             const D_ *gp = static_cast<const D_ *>(dD);
             const Y_ *yp = static_cast<const Y_ *>(Y);
             Y_ *op = static_cast<Y_ *>(dY);
-            if (wide)
-                combine_backward_kernel<Y_, D_, true><<<grid, 32 * kCombineGradWarps, 0, st>>>(gp, yp, op, p);
-            else
-                combine_backward_kernel<Y_, D_, false><<<grid, 32 * kCombineGradWarps, 0, st>>>(gp, yp, op, p);
-            return host_launched();
+            return host_launch(wide ? combine_backward_kernel<Y_, D_, true> : combine_backward_kernel<Y_, D_, false>, grid,
+                               32 * kCombineGradWarps, 0, st, 0, gp, yp, op, p);
         });
     });
 }

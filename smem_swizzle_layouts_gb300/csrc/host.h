@@ -27,14 +27,48 @@ int host_take_injection(int *timeout_ms);
 // Counts `n` launched kernels in gemm_launch_count().
 void host_count_launches(int n);
 
-// A launch's status after it was enqueued, counted when it was.
-inline gemm_status_t host_launched(int n = 1)
+// Launches a kernel that may start while the kernel before it on the stream is
+// still running (programmatic dependent launch). Such a kernel calls
+// grid_start() before it touches memory that another kernel writes or reads:
+// only its launch and what it sets up on chip overlap. With `cluster` > 0 it
+// is launched in clusters of that many CTAs.
+template <typename... Params, typename... Args>
+inline gemm_status_t host_launch(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+                                 unsigned cluster, Args... args)
 {
-    if (cudaGetLastError() != cudaSuccess)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...) != cudaSuccess) {
+        (void)cudaGetLastError();
         return GEMM_ERR_CUDA;
-    host_count_launches(n);
+    }
+    host_count_launches(1);
     return GEMM_OK;
 }
+
+#ifdef __CUDACC__
+// The next kernel on the stream may be launched from here on (it waits in its
+// own grid_start); the kernels before this one have finished on return, and
+// their writes are visible. They were not when this kernel started, so it reads
+// what others write with ordinary loads only: no __ldg, no __restrict__ inputs.
+__device__ __forceinline__ void grid_start()
+{
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+}
+#endif
 
 inline int type_bytes(int type) { return type == GEMM_OUT_F32 ? 4 : 2; }
 

@@ -624,6 +624,7 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
         tmem_alloc<CG>(smem_u32(tmem_slot), 512);
         tmem_relinquish<CG>();
     }
+    grid_start();  // what precedes it touches this CTA's own shared memory and TMEM only
     if (warp == kI8FirstEpiWarp && p.experts) {
         // clamped offsets and the first tile of each expert: a running
         // maximum and a running sum, 32 experts at a time
@@ -1005,10 +1006,20 @@ constexpr int kFewWarps = 8;
 constexpr int64_t kFewMaxK = (1 << 17) - 1;
 
 // Bytes k .. k+15 of a row of K: zeros past its end, which is not read past.
+// STREAM: read once, so not kept in L1.
+template <bool STREAM>
 __device__ __forceinline__ int4 load_row16(const int8_t *row, int k, int K)
 {
-    if (k + 16 <= K)
-        return __ldg(reinterpret_cast<const int4 *>(row + k));
+    if (k + 16 <= K) {
+        int4 v;
+        if constexpr (STREAM)
+            asm volatile("ld.global.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "l"(row + k));
+        else
+            v = *reinterpret_cast<const int4 *>(row + k);
+        return v;
+    }
     int4 v = make_int4(0, 0, 0, 0);
     int8_t *b = reinterpret_cast<int8_t *>(&v);
 #pragma unroll
@@ -1020,20 +1031,21 @@ __device__ __forceinline__ int4 load_row16(const int8_t *row, int k, int K)
 
 template <int MT, int ROWS>
 __global__ void __launch_bounds__(32 * kFewWarps)
-    int8_few_kernel(const int8_t *__restrict__ A, long long lda, const int8_t *__restrict__ B, long long ldb, const I8Params p)
+    int8_few_kernel(const int8_t *A, long long lda, const int8_t *B, long long ldb, const I8Params p)
 {
     __shared__ int part[kFewWarps][ROWS * MT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n0 = blockIdx.x * ROWS;
+    grid_start();
     int acc[ROWS][MT] = {};
     for (int k = warp * 512 + lane * 16; k < p.K; k += kFewWarps * 512) {
         int4 w[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)  // rows past the last repeat it; their sums are not stored
-            w[r] = load_row16(B + static_cast<long long>(min(n0 + r, p.N - 1)) * ldb, k, p.K);
+            w[r] = load_row16<true>(B + static_cast<long long>(min(n0 + r, p.N - 1)) * ldb, k, p.K);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const int4 a = load_row16(A + static_cast<long long>(min(m, p.M - 1)) * lda, k, p.K);
+            const int4 a = load_row16<false>(A + static_cast<long long>(min(m, p.M - 1)) * lda, k, p.K);
 #pragma unroll
             for (int r = 0; r < ROWS; ++r)
                 acc[r][m] = __dp4a(w[r].x, a.x, __dp4a(w[r].y, a.y, __dp4a(w[r].z, a.z, __dp4a(w[r].w, a.w, acc[r][m]))));
@@ -1064,14 +1076,15 @@ template <int MT, int ROWS = MT == 1 ? 8 : 4>
 gemm_status_t launch_few(const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb, const I8Params &p, cudaStream_t st)
 {
     const unsigned grid = (static_cast<unsigned>(p.N) + ROWS - 1) / ROWS;
-    int8_few_kernel<MT, ROWS><<<grid, 32 * kFewWarps, 0, st>>>(A, lda, B, ldb, p);
-    return host_launched();
+    return host_launch(int8_few_kernel<MT, ROWS>, grid, 32 * kFewWarps, 0, st, 0, A, static_cast<long long>(lda), B,
+                       static_cast<long long>(ldb), p);
 }
 
 // Zeros for K == 0: the rows of every expert, or all M of them.
 template <typename D>
 __global__ void int8_zero_kernel(const I8Params p)
 {
+    grid_start();
     long long rows = p.M;
     if (p.experts) {
         rows = 0;
@@ -1110,23 +1123,9 @@ gemm_status_t launch_int8(const CUtensorMap &a, const CUtensorMap &b, const I8Pa
     const int64_t tiles_m = (static_cast<int64_t>(p.M) + C::TOKENS - 1) / C::TOKENS + (p.experts ? std::min(p.experts, p.M) : 0);
     const int64_t tiles = tiles_m * p.tiles_n;
     const int cluster = C::CG * ks;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(KS > 1 ? tiles * cluster : std::min<int64_t>(tiles, sms / cluster) * cluster), 1, 1);
-    cfg.blockDim = dim3(C::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = kBase + (p.experts ? 2 * 4 * (p.experts + 1) : 0);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    if (C::CLUSTER > 1) {
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    if (cudaLaunchKernelEx(&cfg, kern, a, b, p, ks) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    return host_launched();
+    const unsigned grid = static_cast<unsigned>(KS > 1 ? tiles * cluster : std::min<int64_t>(tiles, sms / cluster) * cluster);
+    return host_launch(kern, grid, C::THREADS, kBase + (p.experts ? 2 * 4 * (p.experts + 1) : 0), st,
+                       C::CLUSTER > 1 ? static_cast<unsigned>(cluster) : 0u, a, b, p, ks);
 }
 
 // How a product is cut: wide tiles, or narrow ones of `ns` tokens with `ks`
@@ -1211,13 +1210,10 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     p.status = status;
     if (K == 0) {
         const int grid = static_cast<int>(std::min<int64_t>(M, 8 * sms));
-        if (d_type == GEMM_OUT_F32)
-            int8_zero_kernel<float><<<grid, 256, 0, st>>>(p);
-        else if (d_type == GEMM_OUT_BF16)
-            int8_zero_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
-        else
-            int8_zero_kernel<__half><<<grid, 256, 0, st>>>(p);
-        return host_launched();
+        return host_launch(d_type == GEMM_OUT_F32    ? int8_zero_kernel<float>
+                           : d_type == GEMM_OUT_BF16 ? int8_zero_kernel<__nv_bfloat16>
+                                                     : int8_zero_kernel<__half>,
+                           static_cast<unsigned>(grid), 256, 0, st, 0, p);
     }
     // Few tokens, where integers beat tiles, whose work hardly grows with the
     // tokens (measured us, integers and tiles: 4096 x 4096 weights with 1, 2, 4
