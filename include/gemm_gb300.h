@@ -447,7 +447,9 @@ gemm_status_t gemm_bf16_grouped_noalloc(const gemm_problem_t *problems, int num_
  * pointers owned by the caller, no allocation, asynchronous on `stream`,
  * errors returned before anything is enqueued. Unless a rule below says
  * otherwise, pointers need only the alignment of their elements and leading
- * dimensions only the length of a row.
+ * dimensions only the length of a row. The kernels are launched so that each
+ * may start while the kernel before it on the stream ends (programmatic
+ * dependent launch); they wait for it before they touch memory.
  * ------------------------------------------------------------------- */
 
 typedef enum { GEMM_ROUTE_SOFTMAX = 0, GEMM_ROUTE_SIGMOID = 1 } gemm_score_t;
@@ -545,8 +547,10 @@ gemm_status_t gemm_quantize_int8(int64_t M, int64_t K, const void *X, gemm_out_t
  * row (channel) of B. A is M x K, B is N x K (both K-major), D is M x N of
  * d_type. sm_103a has no integer tcgen05 kind: the integers are widened to
  * fp16 on chip, where they and their products are exact, and summed in fp32,
- * exactly while partial sums stay below 2^24 in magnitude (any K <= 1040,
- * and far longer rows of quantised data), and to fp32 rounding beyond.
+ * exactly while partial sums stay below 2^24 in magnitude (any K <= 1024, and
+ * far longer rows of quantised data), and to fp32 rounding beyond. Small
+ * products of at most eight rows of A are summed in 32-bit integers instead,
+ * which are exact for every K they are taken for (K < 2^17).
  * A and B 16-byte aligned, lda and ldb multiples of 16; K == 0 writes zeros.
  */
 gemm_status_t gemm_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a,
@@ -594,7 +598,8 @@ gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const voi
  * read fails). `detail` (may be NULL) receives the raw word: bits 0-7 the
  * role that gave up (1 producer, 2 MMA, 3 epilogue, 4 scale copier of the
  * block-scaled kinds, 5 launch setup: 10 in bits 8-15 means the dynamic
- * shared memory was not 1024-byte aligned), bits 8-15 the wait. */
+ * shared memory was not 1024-byte aligned, 6 a converter warp of the 8-bit
+ * integer products), bits 8-15 the wait. */
 gemm_status_t gemm_last_device_status(gemm_stream_t stream, uint32_t *detail);
 
 const char *gemm_status_string(gemm_status_t status);

@@ -794,7 +794,7 @@ __device__ __forceinline__ void quant_round(const float (&x)[8], float scale, fl
 // between the maximum and the rounding (CH 0: rows too long for that are read
 // twice, the second time from L2). WIDE: 16-byte loads and 8-byte stores.
 template <typename X, bool GATED, bool WIDE, int CH>
-__global__ void __launch_bounds__(kQuantMaxThreads)
+__global__ void __launch_bounds__(kQuantMaxThreads, 3)
     quantize_kernel(const X *x, int8_t *__restrict__ q, const QuantParams p)
 {
     const long long m = blockIdx.x;
