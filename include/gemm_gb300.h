@@ -530,7 +530,9 @@ typedef enum { GEMM_QUANT_PLAIN = 0, GEMM_QUANT_GATED = 1 } gemm_quant_t;
 /*
  * gemm_quantize_int8: rows to 8-bit integers, one scale a row:
  *   scales[m] = max_k |x[m,k]| / 127,  Q[m,k] = round(x[m,k] / scales[m])
- * (ties to even; a row of zeros has scale 0). x[m,:] is row index[m] of X
+ * in fp32, the scale as the product with the fp32 number nearest to 1/127 and
+ * Q from the correctly rounded quotient (ties to even; a row of zeros has
+ * scale 0). x[m,:] is row index[m] of X
  * (row m without an index), X having x_rows rows of x_type with stride ldx.
  * GEMM_QUANT_GATED: X rows are 2K wide, x = silu(X[:, :K]) * X[:, K:].
  * An index outside 0..x_rows-1 gives a row of zeros. A row that holds a

@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kQuantMaxThreads, 3)
         top = __reduce_max_sync(0xffffffffu, lane < warps ? warp_top[lane] : 0u);
     }
     const bool bad = top >= 0x7f800000u;  // the row holds an infinity or a NaN
-    const float scale = bad ? NAN : __fdiv_rn(__uint_as_float(top), 127.0f);
+    const float scale = bad ? NAN : __fmul_rn(__uint_as_float(top), 1.0f / 127.0f);
     if (tid == 0)
         p.scales[m] = scale;
     // a scale that is 0 (also: rounded to 0) divides by 1 and leaves zeros; one

@@ -357,10 +357,10 @@ def test_plan_nothing(g):
 # ------------------------------------------------------------------ quantisation
 
 def quant_ref(x):
-    """In the operator's own arithmetic: fp32 quotients, ties to even."""
+    """In the operator's own arithmetic: the scale by the fp32 reciprocal of 127, fp32 quotients, ties to even."""
     x = x.astype(np.float32)
     top = np.abs(x).max(-1) if x.shape[1] else np.zeros(x.shape[0], np.float32)
-    scale = (top / np.float32(127)).astype(np.float32)
+    scale = (top * (np.float32(1) / np.float32(127))).astype(np.float32)
     by = np.where(scale == 0, np.float32(1), scale)[:, None]
     return np.clip(np.rint(x / by), -127, 127).astype(np.int8), scale
 
