@@ -144,13 +144,14 @@ _current_stream = None
 
 
 def _find_current_stream():
-    """A function that returns the handle of torch's current stream. The raw lookup, where torch has it, takes a
+    """A function that returns the handle of torch's current stream. The raw lookups, where torch has them, take a
     tenth of the time of building a Stream object, which showed on calls of a few microseconds."""
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
+    raw, device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
         return lambda: torch.cuda.current_stream().cuda_stream
-    return lambda: raw(torch.cuda.current_device())
+    torch.cuda.current_stream()  # initialises CUDA, which the raw lookups take as done
+    return lambda: raw(device())
 
 
 def _stream(s) -> int | None:
@@ -353,15 +354,17 @@ def gemm_bf16_grouped_noalloc(problems, a_major, b_major, d_type, alpha, beta, s
                                           _stream(stream)), "gemm_bf16_grouped_noalloc")
 
 
+_ROUTE_FIELDS = frozenset(name for name, _ in GemmRoute._fields_)
+
+
 def _route_rule(route):
     if route is None:
         return None
-    if isinstance(route, GemmRoute):
-        return ctypes.pointer(route)
-    unknown = set(route) - {name for name, _ in GemmRoute._fields_}
-    if unknown:  # ctypes would take them as plain attributes
-        raise TypeError(f"GemmRoute has no field {sorted(unknown)}")
-    return ctypes.pointer(GemmRoute(**route))
+    if not isinstance(route, GemmRoute):
+        if not _ROUTE_FIELDS.issuperset(route):  # ctypes would take others as plain attributes
+            raise TypeError(f"GemmRoute has no field {sorted(set(route) - _ROUTE_FIELDS)}")
+        route = GemmRoute(**route)
+    return ctypes.byref(route)
 
 
 def gemm_route(T, E, logits, l_type, ldl, bias, k, route, weights, ids, stream=None):

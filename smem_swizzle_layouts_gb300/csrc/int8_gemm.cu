@@ -1138,22 +1138,48 @@ struct I8Plan {
     int box_tokens() const { return wide ? 128 : ns == 128 ? 64 : ns; }  // tokens one CTA loads
 };
 
+// CTAs that may share a tile's K: doubled while all tiles still run at once and
+// each CTA keeps some blocks.
+int int8_shares(int64_t tiles, int64_t blocks, int most, int sms)
+{
+    int ks = 1;
+    while (ks < most && tiles * ks * 2 <= sms && blocks >= 4 * ks)
+        ks *= 2;
+    return ks;
+}
+
 I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms)
 {
     const int64_t rows = E ? (M + E - 1) / E : M;  // of one matrix, on average
-    I8Plan pl = {false, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1};
-    if (rows > 128 && N > 128) {
-        pl.wide = true;
+    const int64_t blocks = (K + kI8K - 1) / kI8K;
+    auto tiles = [&](int64_t tokens, int64_t channels) { return (M + tokens - 1) / tokens * ((N + channels - 1) / channels); };
+    if (rows <= 64) {
+        I8Plan pl = {false, rows <= 16 ? 16 : rows <= 32 ? 32 : 64, 1};
+        if (E == 0)
+            pl.ks = int8_shares(tiles(pl.ns, 128), blocks, pl.ns == 16 ? 8 : pl.ns == 32 ? 4 : 2, sms);
         return pl;
     }
-    if (E == 0 && pl.ns <= 64) {
-        const int64_t tiles = (M + pl.ns - 1) / pl.ns * ((N + 127) / 128);
-        const int most = pl.ns == 16 ? 8 : pl.ns == 32 ? 4 : 2;
-        const int64_t blocks = (K + kI8K - 1) / kI8K;
-        while (pl.ks < most && tiles * pl.ks * 2 <= sms && blocks >= 4 * pl.ks)
-            pl.ks *= 2;
-    }
-    return pl;
+    if (E)
+        return {rows > 128 && N > 128, 128, 1};
+    // One matrix and more tokens: the tile whose rounds of the grid take least.
+    // A block of K takes a CTA 0.43 us on 64 x 128 tiles, 0.51 on pairs of 128 x
+    // 256 and 0.66 on wide ones (64, 128 and 768 tokens, 4096 elements of K);
+    // wide tiles are far ahead for each product, but a few of them leave most
+    // of the SMs idle (100 tokens, 4096 x 4096: 18.0 us on pairs).
+    struct Choice {
+        I8Plan pl;
+        int64_t cost;
+    };
+    const int ks = int8_shares(tiles(64, 128), blocks, 2, sms);
+    auto rounds = [](int64_t n, int64_t units) { return (n + units - 1) / units; };
+    const Choice choices[3] = {{{true, 256, 1}, 66 * blocks * rounds(tiles(256, 256), sms / 2)},
+                               {{false, 128, 1}, 51 * blocks * rounds(tiles(128, 256), sms / 2)},
+                               {{false, 64, ks}, 43 * ((blocks + ks - 1) / ks) * rounds(tiles(64, 128) * ks, sms)}};
+    const Choice *best = &choices[0];
+    for (const Choice &c : choices)
+        if (c.cost < best->cost)
+            best = &c;
+    return best->pl;
 }
 
 gemm_status_t launch_int8_plan(const CUtensorMap &a, const CUtensorMap &b, const I8Params &p, const I8Plan &pl, int sms,
