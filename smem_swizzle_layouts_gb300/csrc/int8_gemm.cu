@@ -44,6 +44,16 @@
 //                before it waits for room to write it. The warpgroups share
 //                the registers out by need (setmaxnreg).
 // Every wait is bounded, as in gemm_kernel.cuh.
+//
+// Measured on a GB300, operands not in L2, launches one after another (HBM 6.78
+// TB/s, bf16 products 1919 TFLOP/s): 8192^3 553 us (1990 TFLOP/s), 4096^3 85.7
+// us (256 wide tiles on 76 pairs: 4 rounds for 3.4), 8192^2 x 2048 170-177 us (an
+// epilogue for each sixteen stages), 64 experts with 512 rows each, N 4096, K
+// 2048 335 us; 128 x 16384 x 4096 20.5 us, 16 x 16384 x 4096 15.7 us (about 0.4
+// us a stage on 128 CTAs: the issue of 16-token MMAs and the widening, both
+// ahead of the 10 us of HBM traffic), 96 rows over 64 experts 88 us (0.9 of the
+// HBM rate). What bounds wide tiles: shared memory, 128 to 160 KB a stage
+// (raw writes and reads, fp16 writes, MMA reads) for 1024 MMA cycles.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -910,6 +920,8 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
                 const int n = ti.n0 + (CG == 2 ? rank * kI8Rows : 0) + 32 * q + lane;
                 const bool live = n < p.N;
                 const float sn = live ? sb[n] : 0.0f;
+                const int rows = min(ti.m1 - ti.m0, NS);
+                float sa = lane < rows ? p.sa[ti.m0 + lane] : 0.0f;  // of the first 32 tokens
                 bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull, CG == 2);
                 if (!__all_sync(0xffffffffu, ok))
                     break;
@@ -920,7 +932,6 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
                 const uint32_t src0 = lanes + static_cast<uint32_t>(blocks > 1 ? 0 : first * C::ACC_STRIDE);
                 const uint32_t src1 = lanes + static_cast<uint32_t>(C::ACC_STRIDE);
                 first = (first + blocks) & 1;
-                const int rows = min(ti.m1 - ti.m0, NS);
                 if (KS > 1 && rank > 0) {
                     // this CTA's sums to the first CTA, [rank - 1][token][channel]
                     const uint32_t part = mapa_shared(base + C::PART_OFF, 0) +
@@ -944,7 +955,8 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
                     }
                     for (int c = 0; c < rows; c += 32) {
                         const int left = rows - c;
-                        const float sa = lane < left ? p.sa[ti.m0 + c + lane] : 0.0f;
+                        if (c > 0)
+                            sa = lane < left ? p.sa[ti.m0 + c + lane] : 0.0f;
                         float v[32];
                         load_sums(src0 + c, src1 + c, blocks > 1, v);
                         if constexpr (KS > 1) {
@@ -1000,7 +1012,9 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
 // takes a few channels and its eight warps slices of K, so that all of a
 // block's weights are asked for at once (16 bytes a lane and channel), and
 // dp4a sums them in 32-bit integers, exactly for K < 2^17. No tile to fill, no
-// stages: the weights are read once, the tokens' rows come from L2.
+// stages: the weights are read once, the tokens' rows come from L2. One token
+// against 4096 x 4096 weights takes 4.2 us (4.0 TB/s, 2 us of it latency),
+// against 16384 x 4096 11.7 us (5.8 TB/s).
 
 constexpr int kFewWarps = 8;
 constexpr int64_t kFewMaxK = (1 << 17) - 1;
@@ -1243,8 +1257,8 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     }
     // Few tokens, where integers beat tiles, whose work hardly grows with the
     // tokens (measured us, integers and tiles: 4096 x 4096 weights with 1, 2, 4
-    // and 8 tokens 4.7, 5.8, 7.7 and 11.9 against 10.3; 16384 x 4096 13.4, 15.4,
-    // 19.9 and 27.7 against 16.5; 1024 x 1024 with 4 tokens 2.2 against 6.7).
+    // and 8 tokens 4.2, 5.2, 6.0 and 11.9 against 9.8; 16384 x 4096 11.7, 15.4,
+    // 19.9 and 27.7 against 15.5; 1024 x 1024 with 8 tokens 2.9 against 5.8).
     if (E == 0 && K <= kFewMaxK && (M <= 2 || (M <= 4 && N * K <= int64_t(1) << 25) || (M <= 8 && N * K <= int64_t(3) << 22)))
         return M == 1   ? launch_few<1>(A, lda, B, ldb, p, st)
                : M == 2 ? launch_few<2>(A, lda, B, ldb, p, st)
