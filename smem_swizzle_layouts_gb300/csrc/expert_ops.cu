@@ -199,11 +199,12 @@ __device__ __forceinline__ LaneBest lane_best(const uint32_t (&key)[NPL], uint32
 //
 // s = softmax(l) or sigmoid(l); e is chosen by s_e + bias_e; w = s / sum of the
 // chosen s. For 16384 tokens memory could deliver in 0.4 (64 experts, bf16) to
-// 2.6 us (256, fp32); the kernel takes 8.2 us (k = 6, no bias) and 18.6 us (k =
-// 8 with a bias, 24.9 with 8 groups), about 600 instructions a token: a warp per
+// 2.6 us (256, fp32); the kernel takes 8.2 us (k = 6, no bias; 470 instructions a
+// token) and 15.4 us (k = 8 with a bias, 850; 22.1 us with 8 groups): a warp per
 // token keeps a token's codes in registers and its maxima in the warp. Before
 // the lanes kept two candidates and compared special-function scores it took
-// 25 us. One token takes 2.2 us, launch latency.
+// 25 us, before the bias came with the logits 18.6. One token takes 2.2 us,
+// launch latency.
 template <typename L, int NPL>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *logits, const RouteParams p)
 {
@@ -221,6 +222,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *logits
     for (int i = 0; i < NPL; ++i) {
         const int e = lane + 32 * i;
         l[i] = e < p.E ? to_float(row[e]) : -INFINITY;
+    }
+    float bias[NPL];  // asked for with the logits: one wait for memory
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            bias[i] = lane + 32 * i < p.E ? p.bias[lane + 32 * i] : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
@@ -257,10 +264,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *logits
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             s[i] = p.sigmoid ? fast_inverse(1.0f + fast_exp(-l[i])) : s[i] * inv;
-            if (p.bias) {
-                const int e = lane + 32 * i;
-                s[i] = e < p.E ? __fadd_rn(s[i], p.bias[e]) : 0.0f;
-            }
+            if (p.bias)
+                s[i] = __fadd_rn(s[i], bias[i]);
             key[i] = l[i] > -INFINITY ? choice_key(p.bias ? s[i] : l[i]) : 0u;
         }
     } else {
