@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 // count of every expert; plan_scatter_kernel adds the counts of the parts and
 // warps before it and hands out the rows in order, 32 pairs at a time. One
 // part needs no count kernel. Bound by latency: a chain of counting, a scan and
-// the hand-out, 2.3 us for one token's pairs, 8.5 us for the 131072 of 16384
+// the hand-out, 2.3 us for one token's pairs, 8.0 us for the 131072 of 16384
 // tokens (0.2 us of traffic); the parts' counts were 14 us when each thread
 // added up all parts of its expert.
 
@@ -581,13 +581,18 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps)
     for (int i = tid; i < (warps + 2) * E; i += blockDim.x)
         hist[i] = 0;
     __syncthreads();
+    int first[kPlanBatch];  // the warp's first pairs (mostly all of them) are kept for the hand-out
+    plan_load(ids, wlo + lane, whi, E, first);
     for (long long i0 = wlo; i0 < whi; i0 += 32 * kPlanBatch) {
         int id[kPlanBatch];
-        plan_load(ids, i0 + lane, whi, E, id);
+        if (i0 > wlo)
+            plan_load(ids, i0 + lane, whi, E, id);
 #pragma unroll
-        for (int u = 0; u < kPlanBatch; ++u)
-            if (id[u] >= 0)
-                atomicAdd(&hist[warp * E + id[u]], 1);
+        for (int u = 0; u < kPlanBatch; ++u) {
+            const int e = i0 > wlo ? id[u] : first[u];
+            if (e >= 0)
+                atomicAdd(&hist[warp * E + e], 1);
+        }
     }
     __syncthreads();
     // totals of every expert, and of the parts before this one: with several
@@ -654,21 +659,27 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps)
     // first row of each warp's pairs of each expert
     for (int e = tid; e < E; e += blockDim.x) {
         int at = start[e] + before[e];
-        for (int w = 0; w < warps; ++w) {
-            const int n = hist[w * E + e];
-            hist[w * E + e] = at;
-            at += n;
+        int n[kPlanMaxWarps];
+#pragma unroll
+        for (int w = 0; w < kPlanMaxWarps; ++w)
+            n[w] = w < warps ? hist[w * E + e] : 0;
+#pragma unroll
+        for (int w = 0; w < kPlanMaxWarps; ++w) {
+            if (w < warps)
+                hist[w * E + e] = at;
+            at += n[w];
         }
     }
     __syncthreads();
     int *mine = hist + warp * E;
     for (long long i0 = wlo; i0 < whi; i0 += 32 * kPlanBatch) {
         int id[kPlanBatch];
-        plan_load(ids, i0 + lane, whi, E, id);
+        if (i0 > wlo)
+            plan_load(ids, i0 + lane, whi, E, id);
 #pragma unroll
         for (int u = 0; u < kPlanBatch; ++u) {
             const long long i = i0 + 32 * u + lane;
-            const int e = id[u];
+            const int e = i0 > wlo ? id[u] : first[u];
             const unsigned same = __match_any_sync(0xffffffffu, e);
             int slot = -1;
             if (e >= 0)
@@ -680,7 +691,7 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps)
             if (i < whi) {
                 slots[i] = slot;
                 if (slot >= 0)
-                    tokens[slot] = static_cast<int>(i / k);
+                    tokens[slot] = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(k));
             }
         }
     }
