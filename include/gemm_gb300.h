@@ -501,8 +501,8 @@ gemm_status_t gemm_route(int64_t T, int64_t E, const void *logits, gemm_out_t l_
  * gemm_route_backward: the gradient of the logits from that of the weights,
  * for the ids that gemm_route chose (the choice itself, and with it the bias,
  * has none). dweights: T x k fp32; dlogits: T x E of l_type, row stride lddl,
- * written whole. Ids outside 0..E-1 carry nothing; the others of a token are
- * distinct. k and route as in the forward call (groups play no part).
+ * written whole and not overlapping logits. Ids outside 0..E-1 carry nothing;
+ * the others of a token are distinct. k and route as in the forward call (groups play no part).
  */
 gemm_status_t gemm_route_backward(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl,
                                   int k, const gemm_route_t *route, const int32_t *ids,

@@ -524,3 +524,67 @@ def test_combine_past_two_to_the_31_elements(g):
     g.gemm_quantize_int8(1, N, y, 1, R, N, slots[0], g.QUANT_PLAIN, q, N, s)
     ref_q, ref_s = quant_ref(y[R - 1:].float().cpu().numpy())
     assert (q.cpu().numpy() == ref_q).all() and float(s) == ref_s[0]
+
+
+def test_routing_rows_past_two_to_the_31_elements(g):
+    """Rows of logits, and of their gradient, whose offset passes 2^31 elements."""
+    ld, E, k = 1 << 30, 40, 3
+    buf = torch.empty(2 * ld + E, dtype=torch.bfloat16, device=DEV)
+    x = np.stack([np.roll(np.arange(E), 7 * t) for t in range(3)]) / 8.0
+    rows = buf.as_strided((3, E), (ld, 1))
+    rows.copy_(torch.from_numpy(x))
+    w, ids = torch.empty(3, k, device=DEV), torch.empty(3, k, dtype=torch.int32, device=DEV)
+    r = dict(score=0, renormalize=1)
+    g.gemm_route(3, E, buf, 1, ld, None, k, r, w, ids)
+    w64, ids64 = route64(x, None, k, r)
+    assert (ids.cpu().numpy() == ids64).all()
+    np.testing.assert_allclose(np64(w), w64, rtol=REL)
+    dw = torch.tensor([[1.0, -2.0, 0.5]] * 3, device=DEV)
+    out = torch.empty_like(buf)
+    g.gemm_route_backward(3, E, buf, 1, ld, k, r, ids, dw, out, ld)
+    np.testing.assert_allclose(np64(out.as_strided((3, E), (ld, 1))), route_grad64(x, ids64, np64(dw), r), rtol=REL + HALF_ULP[1], atol=1e-6)
+
+
+def test_combine_backward_past_two_to_the_31_elements(g):
+    N, R = 32768, 70000
+    y = torch.zeros(R, N, dtype=torch.bfloat16, device=DEV)
+    dy = torch.zeros(R, N, dtype=torch.bfloat16, device=DEV)
+    y[R - 1, :8] = 2.0
+    dD = torch.ones(1, N, dtype=torch.bfloat16, device=DEV)
+    slots = torch.tensor([[R - 1]], dtype=torch.int32, device=DEV)
+    dw = torch.empty(1, 1, device=DEV)
+    g.gemm_route_combine_backward(1, N, 1, dD, 1, N, y, 1, R, N, slots, torch.tensor([[0.5]], device=DEV), dy, N, dw)
+    assert float(dw) == 16.0 and (dy[R - 1] == 0.5).all() and (dy[:4] == 0).all()
+
+
+def test_kernels_in_a_row_see_each_other(g):
+    """Each call reads what the one before it wrote; launches overlap the end of the kernel before."""
+    rng = np.random.default_rng(21)
+    T, E, k, N = 3000, 64, 4, 256
+    x = torch.from_numpy(distinct_logits(rng, T, E, 0)).float().to(DEV)
+    ids = torch.empty(T, k, dtype=torch.int32, device=DEV)
+    w = torch.empty(T, k, device=DEV)
+    off = torch.empty(E + 1, dtype=torch.int32, device=DEV)
+    slots, tokens = torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T * k, dtype=torch.int32, device=DEV)
+    n = g.gemm_route_plan_workspace_size(T, E, k)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    q, s = torch.empty(T * k, N, dtype=torch.int8, device=DEV), torch.empty(T * k, device=DEV)
+    y, D = torch.empty(T * k, N, device=DEV), torch.empty(T, N, device=DEV)
+    b = torch.from_numpy(rng.integers(-20, 21, (E, N, N)).astype(np.int8)).to(DEV)
+    sb = torch.ones(E, N, device=DEV)
+    X = torch.from_numpy(rng.standard_normal((T, N))).float().to(DEV)
+    first = None
+    for i in range(20):
+        for t in (ids, w, off, slots, tokens, q, s, y, D):
+            t.fill_(77)
+        g.gemm_route(T, E, x, 0, E, None, k, dict(score=0, renormalize=1), w, ids)
+        g.gemm_route_plan(T, E, k, ids, off, slots, tokens, ws, n)
+        g.gemm_quantize_int8(T * k, N, X, 0, T, N, tokens, g.QUANT_PLAIN, q, N, s)
+        g.gemm_int8_grouped(T * k, N, N, E, off, q, N, s, b, N, N * N, sb, y, N, 0)
+        g.gemm_route_combine(T, N, k, y, 0, T * k, N, slots, w, D, 0, N)
+        if first is None:
+            first = D.clone()
+            assert torch.isfinite(first).all() and (first != 77).any()
+        assert torch.equal(D, first), i
+    o, sl, tk = plan_ref(ids.cpu().numpy(), E)
+    assert (off.cpu().numpy() == o).all() and (slots.cpu().numpy() == sl).all() and (tokens.cpu().numpy() == tk).all()

@@ -275,6 +275,26 @@ def test_experts_past_two_to_the_31_bytes(g):
         assert torch.equal(D[rows], ((ad[rows].double() @ bd.double().t()).float() * 0.01).half())
 
 
+def test_rows_past_two_to_the_31_bytes(g):
+    """Rows of A whose offset passes 2^31 bytes, dense and over experts."""
+    M, lda, K, N = 70000, 32768, 64, 96
+    A = torch.zeros(M, lda, dtype=torch.int8, device=DEV)
+    rng = np.random.default_rng(31)
+    a, ad = int8_matrix(rng, 40, K, K)
+    A[M - 40:, :K] = ad
+    b, bd = int8_matrix(rng, 2 * N, K, K)
+    one = torch.ones(M, device=DEV)
+    D = torch.empty(M, N, device=DEV)
+    g.gemm_int8(M, N, K, A, lda, one, bd, K, one, D, N, 0)
+    ok(g)
+    assert torch.equal(D[M - 40:], (ad.double() @ bd[:N].double().t()).float()) and (D[:M - 40] == 0).all()
+    off = torch.tensor([0, M - 30, M], dtype=torch.int32, device=DEV)
+    g.gemm_int8_grouped(M, N, K, 2, off, A, lda, one, bd, K, N * K, one, D, N, 0)
+    ok(g)
+    assert torch.equal(D[M - 30:], (ad[10:].double() @ bd[N:].double().t()).float())
+    assert torch.equal(D[M - 40:M - 30], (ad[:10].double() @ bd[:N].double().t()).float())
+
+
 # ------------------------------------------------------------------ streams, graphs, waits that run out
 
 def test_on_another_stream_and_in_a_graph(g):
