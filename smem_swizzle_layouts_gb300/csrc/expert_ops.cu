@@ -712,67 +712,125 @@ struct QuantParams {
 };
 
 constexpr int kQuantMaxThreads = 512;
+constexpr int kQuantShared = 256;  // threads of a block of several rows
+constexpr int kQuantMany = 1024;   // rows
 
-// Column of element i of a thread's chunk c: eight neighbours for 16-byte
-// accesses (WIDE), else single elements with the threads side by side.
-template <bool WIDE>
-__device__ __forceinline__ int quant_col(int c, int i)
-{
-    const int threads = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x);
-    return WIDE ? 8 * (tid + c * threads) + i : (8 * c + i) * threads + tid;
-}
-
-// A chunk of eight elements of a row: as loaded (PLAIN), so that it takes no
-// more registers than its bytes until it is rounded, or gated.
-template <typename X, bool GATED>
-struct QuantChunk {
-    using Store = typename std::conditional<GATED, float, X>::type;
+// Eight elements of one type, in registers.
+template <typename T>
+struct Eight {
     union {
-        uint4 w[sizeof(Store) / 2];
-        Store e[8];
+        uint4 w[sizeof(T) / 2];
+        T e[8];
     };
-    __device__ __forceinline__ QuantChunk() {}
-    __device__ __forceinline__ float at(int i) const { return to_float(e[i]); }
+    __device__ __forceinline__ Eight() {}
 };
 
-// Columns past K, and rows that do not exist (K 0), are zeros.
-template <typename X, bool GATED, bool WIDE>
-__device__ __forceinline__ void quant_load(const X *row, int c, int K, QuantChunk<X, GATED> &v)
+// A row's elements at .. at+7 from 16-byte words, its address and `at` a
+// multiple of 16 bytes and of 8; zeros unless `in`.
+template <typename T>
+__device__ __forceinline__ void load_wide(const T *row, int at, bool in, Eight<T> &v)
 {
-    using Store = typename QuantChunk<X, GATED>::Store;
-    if constexpr (!GATED && WIDE) {
-        const int at = quant_col<WIDE>(c, 0);
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(X) / 2); ++i)
-            v.w[i] = at < K ? reinterpret_cast<const uint4 *>(row + at)[i] : make_uint4(0, 0, 0, 0);
-    } else {
-        float g[8], u[8];
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+        v.w[i] = in ? reinterpret_cast<const uint4 *>(row + at)[i] : make_uint4(0, 0, 0, 0);
+}
+
+// Whether the whole 16-byte words around elements at .. at+7 lie inside a row of n, whatever its address.
+template <typename T>
+__device__ __forceinline__ bool inside(int at, int n)
+{
+    constexpr int word = 16 / sizeof(T);
+    return at >= word && at <= n - 8 - word;
+}
+
+// The same elements at any address, from the aligned words around them, which
+// are shifted into place (a neighbour's second word is the next thread's
+// first, in L1): 1000 rows of 8191 bf16 in 9.9 us, 24.4 by single elements.
+// Zeros unless `in`.
+template <typename T>
+__device__ __forceinline__ void load_shifted(const T *row, int at, bool in, Eight<T> &v)
+{
+    constexpr int W = sizeof(T) / 2;
+    const uintptr_t address = reinterpret_cast<uintptr_t>(row + at);
+    const uint4 *from = reinterpret_cast<const uint4 *>(address & ~static_cast<uintptr_t>(15));
+    const uint32_t shift = static_cast<uint32_t>(address) & 15u;
+    uint32_t r[4 * W + 4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            g[i] = u[i] = 0.0f;
+    for (int i = 0; i <= W; ++i) {
+        const uint4 x = in ? from[i] : make_uint4(0, 0, 0, 0);
+        r[4 * i] = x.x;
+        r[4 * i + 1] = x.y;
+        r[4 * i + 2] = x.z;
+        r[4 * i + 3] = x.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * W + 2; ++i)
+        r[i] = shift & 8u ? r[i + 2] : r[i];
+#pragma unroll
+    for (int i = 0; i < 4 * W + 1; ++i)
+        r[i] = shift & 4u ? r[i + 1] : r[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        v.w[i].x = __funnelshift_r(r[4 * i], r[4 * i + 1], 8 * (shift & 3u));
+        v.w[i].y = __funnelshift_r(r[4 * i + 1], r[4 * i + 2], 8 * (shift & 3u));
+        v.w[i].z = __funnelshift_r(r[4 * i + 2], r[4 * i + 3], 8 * (shift & 3u));
+        v.w[i].w = __funnelshift_r(r[4 * i + 3], r[4 * i + 4], 8 * (shift & 3u));
+    }
+}
+
+// The same one by one, zeros past the end: the ends of a row.
+template <typename T>
+__device__ __forceinline__ void load_single(const T *row, int at, int n, Eight<T> &v)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v.e[i] = at + i < n ? row[at + i] : from_float<T>(0.0f);
+}
+
+// A chunk as loaded (PLAIN), so that it takes no more registers than its bytes
+// until it is rounded, or gated.
+template <typename X, bool GATED>
+struct QuantChunk : Eight<typename std::conditional<GATED, float, X>::type> {
+    using Store = typename std::conditional<GATED, float, X>::type;
+    __device__ __forceinline__ float at(int i) const { return to_float(this->e[i]); }
+};
+
+// Columns past K, and rows that do not exist (K 0), are zeros. A PLAIN chunk at
+// the end of a row that is not WIDE is left to quant_end, so that nothing stands
+// between the loads of one chunk and the next.
+template <typename X, bool GATED, bool WIDE>
+__device__ __forceinline__ void quant_load(const X *row, int at, int K, QuantChunk<X, GATED> &v)
+{
+    if constexpr (GATED) {
+        Eight<X> g, u;
         if constexpr (WIDE) {
-            const int at = quant_col<WIDE>(c, 0);
-            load8<X, true>(row, at, 0, K, g);
-            if constexpr (GATED)
-                load8<X, true>(row + K, at, 0, K, u);
+            load_wide(row, at, at < K, g);
+            load_wide(row + K, at, at < K, u);
+        } else if (inside<X>(at, K)) {
+            load_shifted(row, at, true, g);
+            load_shifted(row + K, at, true, u);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int at = quant_col<WIDE>(c, i);
-                if (at < K) {
-                    g[i] = to_float(row[at]);
-                    if constexpr (GATED)
-                        u[i] = to_float(row[K + at]);
-                }
-            }
+            load_single(row, at, K, g);
+            load_single(row + K, at, K, u);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (GATED)  // silu(gate) * up
-                v.e[i] = __fmul_rn(__fdiv_rn(g[i], 1.0f + expf(-g[i])), u[i]);
-            else
-                v.e[i] = from_float<Store>(g[i]);  // was loaded from this type
+        for (int i = 0; i < 8; ++i) {  // silu(gate) * up
+            const float x = to_float(g.e[i]);
+            v.e[i] = __fmul_rn(__fdiv_rn(x, 1.0f + expf(-x)), to_float(u.e[i]));
         }
+    } else if constexpr (WIDE) {
+        load_wide(row, at, at < K, v);
+    } else {
+        load_shifted(row, at, inside<X>(at, K), v);
+    }
+}
+
+template <typename X, bool GATED, bool WIDE>
+__device__ __forceinline__ void quant_end(const X *row, int at, int K, QuantChunk<X, GATED> &v)
+{
+    if constexpr (!GATED && !WIDE) {
+        if (at < K && !inside<X>(at, K))
+            load_single(row, at, K, v);
     }
 }
 
@@ -820,49 +878,59 @@ __device__ __forceinline__ void quant_round(const float (&x)[8], float scale, fl
     }
 }
 
-// One block per row, CH chunks of 8 elements a thread kept in registers
-// between the maximum and the rounding (CH 0: rows too long for that are read
-// twice, the second time from L2). WIDE: 16-byte loads and 8-byte stores.
-// Bound by memory, and by the pause between a row's loads and its stores, which
-// three blocks an SM cover in part: 8192 x 8192 bf16 in 43.8 us (4.6 TB/s; 64
-// with a division for each element, 47 with two blocks an SM), 1536 gated rows
-// of 2048 from fp32 in 7.1 us. Rows of odd length take single-element loads:
-// 4096 x 4001 in 28.9 us.
+// The block's x threads take a row, several rows a block (y) where they are
+// short; CH chunks of 8 elements a thread kept in registers between the maximum
+// and the rounding (CH 0: rows too long for that are read twice, the second
+// time from L2). WIDE: rows of 16-byte words. Bound by memory, and by the pause
+// between a row's loads and its stores, which three blocks an SM cover in part:
+// 8192 x 8192 bf16 in 44.1 us (4.6 TB/s; 64 with a division for each element,
+// 47 with two blocks an SM), 1536 gated rows of 2048 from fp32 in 7.2 us, rows
+// of odd length (4096 x 4001) in 17 us; four chunks a thread of those want the
+// registers of two blocks an SM (1000 x 8191: 11.5 us with three, 9.9 with two).
 template <typename X, bool GATED, bool WIDE, int CH>
-__global__ void __launch_bounds__(kQuantMaxThreads, 3)
+__global__ void __launch_bounds__(kQuantMaxThreads, WIDE || CH < 4 ? 3 : 2)
     quantize_kernel(const X *x, int8_t *__restrict__ q, const QuantParams p)
 {
-    const long long m = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = static_cast<int>(blockDim.x >> 5);
+    const long long m = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    // a thread's chunk c is the eight columns from at0 + c * step
+    const int at0 = 8 * tid, step = 8 * static_cast<int>(blockDim.x);
     __shared__ uint32_t warp_top[kQuantMaxThreads / 32];
     grid_start();
-    const long long r = p.index ? p.index[m] : m;
+    const bool have = m < p.M;
+    const long long r = !have ? -1 : p.index ? p.index[m] : m;
     const bool live = r >= 0 && r < p.x_rows;
     const int K = live ? p.K : 0;
     const X *row = x + (live ? r : 0) * p.ldx;
-    const int chunks = CH ? CH : (p.K + 8 * static_cast<int>(blockDim.x) - 1) / (8 * static_cast<int>(blockDim.x));
+    const int chunks = CH ? CH : (p.K + step - 1) / step;
     QuantChunk<X, GATED> v[CH ? CH : 1];
     uint32_t top = 0u;
     if constexpr (CH > 0) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-            quant_load<X, GATED, WIDE>(row, c, K, v[c]);
+            quant_load<X, GATED, WIDE>(row, at0 + c * step, K, v[c]);
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c) {
+            quant_end<X, GATED, WIDE>(row, at0 + c * step, K, v[c]);
             top = quant_top(v[c], top);
+        }
     } else {
         for (int c = 0; c < chunks; ++c) {
-            quant_load<X, GATED, WIDE>(row, c, K, v[0]);
+            quant_load<X, GATED, WIDE>(row, at0 + c * step, K, v[0]);
+            quant_end<X, GATED, WIDE>(row, at0 + c * step, K, v[0]);
             top = quant_top(v[0], top);
         }
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if (warps > 1) {
+        uint32_t *tops = warp_top + threadIdx.y * warps;
         if (lane == 0)
-            warp_top[warp] = top;
+            tops[warp] = top;
         __syncthreads();
-        top = __reduce_max_sync(0xffffffffu, lane < warps ? warp_top[lane] : 0u);
+        top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0u);
     }
+    if (!have)
+        return;
     const bool bad = top >= 0x7f800000u;  // the row holds an infinity or a NaN
     const float scale = bad ? NAN : __fmul_rn(__uint_as_float(top), 1.0f / 127.0f);
     if (tid == 0)
@@ -874,6 +942,7 @@ __global__ void __launch_bounds__(kQuantMaxThreads, 3)
     const float inv = __frcp_rn(by);
     const bool exact = by < 1.17549435e-38f;
     int8_t *out = q + m * p.ldq;
+    const bool out_wide = (reinterpret_cast<uintptr_t>(out) & 7u) == 0;
     auto write = [&](int c, const QuantChunk<X, GATED> &e) {
         float f[8];
 #pragma unroll
@@ -881,20 +950,16 @@ __global__ void __launch_bounds__(kQuantMaxThreads, 3)
             f[i] = bad ? 0.0f : e.at(i);
         uint32_t b[8];
         quant_round(f, by, inv, exact, b);
-        if constexpr (WIDE) {
-            const int at = quant_col<WIDE>(c, 0);
-            if (at < p.K) {
-                const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-                const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-                *reinterpret_cast<uint2 *>(out + at) = make_uint2(lo, hi);
-            }
-        } else {
+        const int at = at0 + c * step;
+        if (WIDE ? at < p.K : out_wide && at <= p.K - 8) {
+            const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+            const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+            *reinterpret_cast<uint2 *>(out + at) = make_uint2(lo, hi);
+        } else if constexpr (!WIDE) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int at = quant_col<WIDE>(c, i);
-                if (at < p.K)
-                    out[at] = static_cast<int8_t>(b[i] & 0xffu);
-            }
+            for (int i = 0; i < 8; ++i)
+                if (at + i < p.K)
+                    out[at + i] = static_cast<int8_t>(b[i] & 0xffu);
         }
     };
     if constexpr (CH > 0) {
@@ -903,7 +968,8 @@ __global__ void __launch_bounds__(kQuantMaxThreads, 3)
             write(c, v[c]);
     } else {
         for (int c = 0; c < chunks; ++c) {
-            quant_load<X, GATED, WIDE>(row, c, K, v[0]);
+            quant_load<X, GATED, WIDE>(row, at0 + c * step, K, v[0]);
+            quant_end<X, GATED, WIDE>(row, at0 + c * step, K, v[0]);
             write(c, v[0]);
         }
     }
@@ -1069,14 +1135,20 @@ gemm_status_t launch_quantize(const void *x, int8_t *q, const QuantParams &p, cu
     const bool wide = aligned_to(x, 16) && aligned_to(q, 8) && p.ldx * static_cast<int64_t>(sizeof(X)) % 16 == 0 &&
                       p.ldq % 8 == 0 && p.K % 8 == 0;
     const int chunks = (p.K + 7) / 8;
-    // chunks a thread: small blocks, so that several share an SM and one's loads overlap another's rounding
-    const int ch = chunks <= 256 ? 1 : chunks <= 512 ? 2 : chunks <= 4 * kQuantMaxThreads ? 4 : 0;
+    // Chunks a thread: small blocks, so that several share an SM and one's loads
+    // overlap another's rounding. Blocks start at about one a nanosecond, so
+    // many short rows share blocks, and rows of 257 .. 512 columns take a warp
+    // each (16384 x 512: 17.1 us by a block a row, 9.4 by two warps a row, 8.2
+    // by one); few rows spread out (128 x 301: 2.4 us by a warp, 1.9 by two).
+    const bool many = p.M >= kQuantMany;
+    const int ch = many && chunks > 32 && chunks <= 64 ? 2 : chunks <= 256 ? 1 : chunks <= 512 ? 2 : chunks <= 4 * kQuantMaxThreads ? 4 : 0;
     int threads = kQuantMaxThreads;
     if (ch > 0)
         threads = std::max(32, ((chunks + ch - 1) / ch + 31) / 32 * 32);
+    const int rows = many ? std::max(1, kQuantShared / threads) : 1;
     const X *xp = static_cast<const X *>(x);
-    const unsigned grid = static_cast<unsigned>(p.M);
-#define G300_QUANT(W, C) return host_launch(quantize_kernel<X, GATED, W, C>, grid, threads, 0, st, 0, xp, q, p)
+    const unsigned grid = static_cast<unsigned>((p.M + rows - 1) / rows);
+#define G300_QUANT(W, C) return host_launch(quantize_kernel<X, GATED, W, C>, grid, dim3(threads, rows), 0, st, 0, xp, q, p)
 #define G300_QUANT_CH(W)                                                                              \
     do {                                                                                              \
         if (ch == 1)                                                                                  \

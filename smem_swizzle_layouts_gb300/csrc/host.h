@@ -33,12 +33,12 @@ void host_count_launches(int n);
 // only its launch and what it sets up on chip overlap. With `cluster` > 0 it
 // is launched in clusters of that many CTAs.
 template <typename... Params, typename... Args>
-inline gemm_status_t host_launch(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+inline gemm_status_t host_launch(void (*kern)(Params...), unsigned grid, dim3 block, size_t smem, cudaStream_t st,
                                  unsigned cluster, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(block, 1, 1);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];

@@ -419,6 +419,58 @@ def test_quantize_gated(g, x_type, K):
     assert np.abs(q.cpu().numpy() - quotient).max() <= 0.5 + 127 * 2e-6
 
 
+@pytest.mark.parametrize("M", [1023, 1024, 1031, 2049])
+@pytest.mark.parametrize("K", [8, 33, 256, 300, 512, 700, 1024, 1100])
+def test_quantize_many_short_rows(g, M, K):
+    """Numbers of rows that are no multiple of a block's, through an index with rows that do not exist."""
+    rng = np.random.default_rng(M + K)
+    x = torch.from_numpy(rng.standard_normal((M, K)) * np.exp(rng.uniform(-3, 3, (M, 1)))).float()
+    index = rng.permutation(M).astype(np.int32)
+    index[::7] = -1
+    index[M - 1] = 5
+    q = torch.full((M + 9, K), 99, dtype=torch.int8, device=DEV)
+    s = torch.full((M + 9,), -1.0, device=DEV)
+    g.gemm_quantize_int8(M, K, x.to(DEV), 0, M, K, torch.from_numpy(index).to(DEV), g.QUANT_PLAIN, q, K, s)
+    ref_q, ref_s = quant_ref(x.numpy()[np.maximum(index, 0)])
+    ref_q[index < 0], ref_s[index < 0] = 0, 0
+    assert (q[:M].cpu().numpy() == ref_q).all() and (s[:M].cpu().numpy() == ref_s).all()
+    assert (q[M:] == 99).all() and (s[M:] == -1).all()
+
+
+@pytest.mark.parametrize("x_type", [0, 1])
+@pytest.mark.parametrize("K", [1, 7, 8, 9, 23, 31, 256, 261, 4097, 9001])
+@pytest.mark.parametrize("gated", [False, True])
+def test_quantize_at_every_address(g, x_type, K, gated):
+    """Rows at every distance from a 16-byte boundary, between NaN that belong to no row."""
+    rng = np.random.default_rng(K)
+    per = 16 // TYPES[x_type].itemsize
+    W = 2 * K if gated else K
+    mode = g.QUANT_GATED if gated else g.QUANT_PLAIN
+    for first in range(per):
+        ld, M = W + 1, 3
+        x = torch.from_numpy(rng.standard_normal((M, W))).to(TYPES[x_type])
+        store = torch.full((per + M * ld + 8,), math.nan, dtype=TYPES[x_type])
+        store[first: first + M * ld].view(M, ld)[:, :W] = x
+        dev = store.to(DEV)
+        q = torch.full((first + M * (K + 3) + 8,), 99, dtype=torch.int8, device=DEV)
+        s = torch.empty(M, device=DEV)
+        g.gemm_quantize_int8(M, K, dev[first:], x_type, M, ld, None, mode, q[first:], K + 3, s)
+        got = q[first: first + M * (K + 3)].view(M, K + 3).cpu().numpy()
+        assert (got[:, K:] == 99).all() and (q[:first] == 99).all() and (q[first + M * (K + 3):] == 99).all()
+        if gated:                # the same values at aligned addresses
+            want = torch.empty(M, (K + 15) // 16 * 16, dtype=torch.int8, device=DEV)
+            t = torch.empty(M, device=DEV)
+            for m in range(M):
+                g.gemm_quantize_int8(1, K, x[m: m + 1].to(DEV), x_type, 1, W, None, mode, want[m], want.stride(0), t[m:])
+            v = np64(x)
+            v = v[:, :K] / (1 + np.exp(-v[:, :K])) * v[:, K:]
+            np.testing.assert_allclose(np64(s), np.abs(v).max(-1) / 127, rtol=1e-6)
+            assert (got[:, :K] == want.cpu().numpy()[:, :K]).all() and (s == t).all()
+        else:
+            ref_q, ref_s = quant_ref(x.float().numpy())
+            assert (got[:, :K] == ref_q).all() and (s.cpu().numpy() == ref_s).all()
+
+
 def test_quantize_nothing(g):
     s = torch.full((3,), -1.0, device=DEV)
     g.gemm_quantize_int8(3, 0, None, 0, 3, 0, None, g.QUANT_PLAIN, None, 0, s)
@@ -478,6 +530,45 @@ def test_combine_and_backward(g, y_type, d_type, T, N, k, pad):
             assert abs(dw[t, j] - (d64[t] * y64[r]).sum()) <= bound + 1e-30
     untouched = sorted(set(range(R)) - set(used))
     assert (dY[untouched] == 8.0).all() and (dY[:, N:] == 8.0).all()
+
+
+@pytest.mark.parametrize("y_type,d_type", [(0, 0), (1, 1), (0, 1), (2, 0)])
+@pytest.mark.parametrize("N", [1, 8, 23, 255, 264, 523, 1024, 1030, 2041])
+def test_combine_at_every_address(g, y_type, d_type, N):
+    """Rows of every operand at every distance from a 16-byte boundary, between NaN that belong to no row."""
+    rng = np.random.default_rng(N)
+    T, k, R = 3, 2, 6
+    slots = torch.tensor([[5, 0], [2, 1], [3, 4]], dtype=torch.int32, device=DEV)
+    w = torch.from_numpy(rng.standard_normal((T, k))).float()
+    wd = w.to(DEV)
+
+    def put(rows, dtype, first, ld):
+        store = torch.full((first + rows * ld + 8,), math.nan, dtype=dtype, device=DEV)
+        return store, store[first: first + rows * ld].view(rows, ld)
+
+    for first in range(8):
+        y_store, y = put(R, TYPES[y_type], first, N + 1)
+        y[:, :N] = torch.from_numpy(rng.standard_normal((R, N))).to(DEV)
+        d_store, D = put(T, TYPES[d_type], (3 * first) % 8, N + 3)
+        g.gemm_route_combine(T, N, k, y, y_type, R, N + 1, slots, wd, D, d_type, N + 3)
+        y64, w64, sl = np64(y)[:, :N], np64(w), slots.cpu().numpy()
+        terms = w64[:, :, None] * y64[sl]
+        ref, size = terms.sum(1), np.abs(terms).sum(1)
+        assert (np.abs(np64(D)[:, :N] - ref) <= k * 2.0 ** -24 * size + HALF_ULP[d_type] * np.abs(ref) + 2.0 ** -25).all()
+        assert int(torch.isnan(d_store).sum()) == d_store.numel() - T * N
+
+        _, dD = put(T, TYPES[d_type], (5 * first + 1) % 8, N + 2)
+        dD[:, :N] = torch.from_numpy(rng.standard_normal((T, N))).to(DEV)
+        g_store, dY = put(R, TYPES[y_type], (first + 3) % 8, N + 5)
+        dw = torch.full((T, k), 7.0, device=DEV)
+        g.gemm_route_combine_backward(T, N, k, dD, d_type, N + 2, y, y_type, R, N + 1, slots, wd, dY, N + 5, dw)
+        d64 = np64(dD)[:, :N]
+        ref = w64[:, :, None] * d64[:, None]
+        got = np64(dY)[:, :N][sl]
+        assert (np.abs(got - ref) <= (HALF_ULP[y_type] + 2.0 ** -24) * np.abs(ref) + 2.0 ** -25).all()
+        assert int(torch.isnan(g_store).sum()) == g_store.numel() - R * N
+        products = d64[:, None] * y64[sl]
+        assert (np.abs(np64(dw) - products.sum(-1)) <= (N / 32 + 16) * 2.0 ** -24 * np.abs(products).sum(-1) + 1e-30).all()
 
 
 def test_combine_backward_against_differences(g):
