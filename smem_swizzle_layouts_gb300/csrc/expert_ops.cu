@@ -988,8 +988,8 @@ struct CombineParams {
 constexpr int kCombineThreads = 128;
 
 // D_t = sum_j w_tj Y[slot_tj]: one block per token and 1024 columns; each thread
-// sums 8 columns over the k rows, four of which are in flight at a time. Bound
-// by the reading of Y: 4096 tokens, k = 6, N = 4096 bf16 in 41.9 us (0.83 of
+// sums 8 columns over the k rows. Bound
+// by the reading of Y: 4096 tokens, k = 6, N = 4096 bf16 in 41.6 us (0.83 of
 // the HBM rate).
 template <typename Y, typename D, bool WIDE>
 __global__ void __launch_bounds__(kCombineThreads)
@@ -1004,7 +1004,9 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int *slots = p.slots + t * p.k;
     const float *weights = p.weights + t * p.k;
     float acc[8] = {};
-#pragma unroll 4
+    // more rows in flight only where loads are narrow: 256 x 2048, k = 6, fp32 in 4.8 us by two, 5.9 by four;
+    // 4096 x 4001 bf16 in 57.5 and 53.6
+#pragma unroll(WIDE ? 2 : 4)
     for (int j = 0; j < p.k; ++j) {
         const int r = slots[j];
         if (r >= 0 && r < p.y_rows) {
@@ -1028,12 +1030,13 @@ struct CombineGradParams {
     float *dweights;
 };
 
-constexpr int kCombineGradWarps = 8;
+// 256 tokens of 2048, k = 6, fp32: 8.9 us by four warps a block, 9.8 by eight
+constexpr int kCombineGradWarps = 4;
 
 // dY[slot] = w dD, dw = <dD, Y[slot]>: one warp per (token, choice) pair walks
 // the N columns once, writing the row of dY and summing the dot product; a
 // token's warps share dD's row in L1. Bound by memory: 4096 tokens, k = 6, N =
-// 4096 bf16 in 70.7 us (0.91 of the HBM rate).
+// 4096 bf16 in 70.1 us (0.92 of the HBM rate).
 template <typename Y, typename D, bool WIDE>
 __global__ void __launch_bounds__(32 * kCombineGradWarps)
     combine_backward_kernel(const D *dd, const Y *y, Y *__restrict__ dy,
