@@ -80,7 +80,8 @@ constexpr int64_t kSizeLimit = (static_cast<int64_t>(1) << 31) - 1;
 
 inline bool valid_size(int64_t n) { return n >= 0 && n <= kSizeLimit; }
 
-// Strides below 2^40 bytes: row * stride stays within 64 bits.
+// Strides below 2^40 bytes, as tensor maps want them. That the rows which a
+// call names exist, and so lie within 64 bits, is the caller's part.
 inline bool valid_stride(int64_t ld, int esize) { return ld >= 0 && ld < (static_cast<int64_t>(1) << 40) / esize; }
 
 }  // namespace g300

@@ -1225,7 +1225,8 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
     if (K > 0) {
         if (!A || !B || lda < K || ldb < K || !valid_stride(lda, 1) || !valid_stride(ldb, 1))
             return GEMM_ERR_INVALID_ARG;
-        if (E > 1 && (stride_b < 0 || !valid_stride(stride_b, 1) || stride_b < (N - 1) * ldb + K))
+        // by division: the product of two accepted numbers may pass 64 bits
+        if (E > 1 && (stride_b < K || !valid_stride(stride_b, 1) || (N > 1 && (stride_b - K) / (N - 1) < ldb)))
             return GEMM_ERR_INVALID_ARG;
         if (!aligned_to(A, 16) || !aligned_to(B, 16) || lda % 16 != 0 || ldb % 16 != 0 || (E > 1 && stride_b % 16 != 0))
             return GEMM_ERR_ALIGNMENT;

@@ -92,3 +92,13 @@ def test_plan_workspace(g):
 def test_unknown_route_field(g):
     with pytest.raises(TypeError):
         g.gemm_route(**{**CALLS["gemm_route"], "route": dict(top=3)}, stream=0)
+
+
+@pytest.mark.parametrize("change", [
+    dict(N=1 << 28, ldd=1 << 28, ldb=1 << 36, stride_b=1 << 20),  # (N - 1) * ldb passes 64 bits
+    dict(N=1 << 30, ldd=1 << 30, ldb=1 << 38, stride_b=1 << 38),
+    dict(N=64, ldb=128, stride_b=63 * 128 + 48)])  # one unit short
+def test_stride_between_experts_holds_a_matrix(g, change):
+    with pytest.raises(g.GemmError) as e:
+        g.gemm_int8_grouped(**{**CALLS["gemm_int8_grouped"], **change}, stream=0)
+    assert e.value.status == g.ERR_INVALID_ARG
