@@ -447,7 +447,9 @@ gemm_status_t gemm_bf16_grouped_noalloc(const gemm_problem_t *problems, int num_
  * pointers owned by the caller, no allocation, asynchronous on `stream`,
  * errors returned before anything is enqueued. Unless a rule below says
  * otherwise, pointers need only the alignment of their elements and leading
- * dimensions only the length of a row. The kernels are launched so that each
+ * dimensions only the length of a row. Rows that are quantised or summed, and
+ * the sizes of products, end 8192 short of 2^31 (GEMM_ERR_UNSUPPORTED past it).
+ * The kernels are launched so that each
  * may start while the kernel before it on the stream ends (programmatic
  * dependent launch); they wait for it before they touch memory.
  * ------------------------------------------------------------------- */

@@ -1316,6 +1316,8 @@ gemm_status_t gemm_quantize_int8(int64_t M, int64_t K, const void *X, gemm_out_t
         return GEMM_ERR_INVALID_ARG;
     if (!aligned_to(X, es) || !aligned_to(index, 4) || !aligned_to(scales, 4))
         return GEMM_ERR_ALIGNMENT;
+    if (!countable(K))
+        return GEMM_ERR_UNSUPPORTED;
     QuantParams p = {};
     p.M = M;
     p.K = static_cast<int>(K);
@@ -1347,7 +1349,7 @@ gemm_status_t gemm_route_combine(int64_t T, int64_t N, int k, const void *Y, gem
     if (!aligned_to(Y, ey) || !aligned_to(D, ed) || !aligned_to(slots, 4) || !aligned_to(weights, 4))
         return GEMM_ERR_ALIGNMENT;
     const int64_t col_blocks = (N + 8 * kCombineThreads - 1) / (8 * kCombineThreads);
-    if (col_blocks * T > kSizeLimit)
+    if (!countable(N) || col_blocks * T > kSizeLimit)
         return GEMM_ERR_UNSUPPORTED;
     CombineParams p = {};
     p.T = T;
@@ -1390,6 +1392,8 @@ gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const voi
     if (!aligned_to(dD, ed) || !aligned_to(Y, ey) || !aligned_to(dY, ey) || !aligned_to(slots, 4) ||
         !aligned_to(weights, 4) || !aligned_to(dweights, 4))
         return GEMM_ERR_ALIGNMENT;
+    if (!countable(N))
+        return GEMM_ERR_UNSUPPORTED;
     CombineGradParams p = {};
     p.T = T;
     p.N = static_cast<int>(N);

@@ -80,6 +80,10 @@ constexpr int64_t kSizeLimit = (static_cast<int64_t>(1) << 31) - 1;
 
 inline bool valid_size(int64_t n) { return n >= 0 && n <= kSizeLimit; }
 
+// Lengths that a kernel walks with 32-bit counters, whose steps (at most 4096
+// columns) may pass the end once.
+inline bool countable(int64_t n) { return n <= kSizeLimit - 8192; }
+
 // Strides below 2^40 bytes, as tensor maps want them. That the rows which a
 // call names exist, and so lie within 64 bits, is the caller's part.
 inline bool valid_stride(int64_t ld, int esize) { return ld >= 0 && ld < (static_cast<int64_t>(1) << 40) / esize; }

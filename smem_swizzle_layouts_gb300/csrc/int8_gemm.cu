@@ -1231,6 +1231,8 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
         if (!aligned_to(A, 16) || !aligned_to(B, 16) || lda % 16 != 0 || ldb % 16 != 0 || (E > 1 && stride_b % 16 != 0))
             return GEMM_ERR_ALIGNMENT;
     }
+    if (!countable(M) || !countable(N) || !countable(K))
+        return GEMM_ERR_UNSUPPORTED;
     int dev = 0, sms = 0;
     unsigned int *status = nullptr;
     gemm_status_t s = host_device(&dev, &status, &sms);

@@ -102,3 +102,20 @@ def test_stride_between_experts_holds_a_matrix(g, change):
     with pytest.raises(g.GemmError) as e:
         g.gemm_int8_grouped(**{**CALLS["gemm_int8_grouped"], **change}, stream=0)
     assert e.value.status == g.ERR_INVALID_ARG
+
+
+LONG = (1 << 31) - 256  # the step of a 32-bit counter past it would wrap
+
+
+@pytest.mark.parametrize("name,change", [
+    ("gemm_quantize_int8", dict(K=LONG, ldx=LONG, ldq=LONG)),
+    ("gemm_quantize_int8", dict(K=LONG, ldx=2 * LONG, ldq=LONG, mode=1)),
+    ("gemm_route_combine", dict(T=1, N=LONG, ldy=LONG, ldd=LONG)),
+    ("gemm_route_combine_backward", dict(T=1, N=LONG, lddd=LONG, ldy=LONG, lddy=LONG)),
+    ("gemm_int8", dict(M=LONG)), ("gemm_int8", dict(N=LONG, ldd=LONG)), ("gemm_int8", dict(K=LONG, lda=LONG, ldb=LONG)),
+    ("gemm_int8", dict(N=LONG, ldd=LONG, K=0)),
+    ("gemm_int8_grouped", dict(M=LONG)), ("gemm_int8_grouped", dict(E=1, N=LONG, ldd=LONG))])
+def test_lengths_next_to_the_limit(g, name, change):
+    with pytest.raises(g.GemmError) as e:
+        getattr(g, name)(**{**CALLS[name], **change}, stream=0)
+    assert e.value.status == g.ERR_UNSUPPORTED
