@@ -523,11 +523,12 @@ __host__ __device__ inline int plan_blocks(long long pairs)
 constexpr int kPlanBatch = 4;  // ids a lane loads at a time
 
 // The ids of pairs i, i + 32, ... below `end`; -1 for those outside 0..E-1.
+// Through L2: plan_scatter_kernel reads them before its own grid_start().
 __device__ __forceinline__ void plan_load(const int *ids, long long i, long long end, int E, int (&id)[kPlanBatch])
 {
 #pragma unroll
     for (int u = 0; u < kPlanBatch; ++u)
-        id[u] = i + 32 * u < end ? ids[i + 32 * u] : -1;
+        id[u] = i + 32 * u < end ? __ldcg(ids + i + 32 * u) : -1;
 #pragma unroll
     for (int u = 0; u < kPlanBatch; ++u)
         if (id[u] < 0 || id[u] >= E)
