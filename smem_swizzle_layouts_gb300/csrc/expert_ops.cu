@@ -1034,17 +1034,27 @@ struct CombineGradParams {
 // 256 tokens of 2048, k = 6, fp32: 8.9 us by four warps a block, 9.8 by eight
 constexpr int kCombineGradWarps = 4;
 
-// dY[slot] = w dD, dw = <dD, Y[slot]>: one warp per (token, choice) pair walks
-// the N columns once, writing the row of dY and summing the dot product; a
-// token's warps share dD's row in L1. Bound by memory: 4096 tokens, k = 6, N =
+// Few pairs of long rows: each has all warps of a block (SHARED), or a warp
+// would walk its row alone. us with a warp and with a block a pair: 8 pairs of
+// 4096 bf16 5.0, 2.2; 1536 of 2048 bf16 5.4, 3.5, fp32 8.6, 6.6; 4096 of 4096
+// fp32 26.9, 25.1; 3332 odd rows of 2005 17.4, 12.0. More, or shorter, lose by it:
+// 8192 of 2048 bf16 13.8, 16.4; 4096 of 512 3.3, 4.5, of 1024 5.3, 5.5.
+inline bool combine_grad_shared(int64_t pairs, int64_t N) { return N > 256 && pairs <= (N > 1024 ? 4096 : 1024); }
+
+// dY[slot] = w dD, dw = <dD, Y[slot]>: one warp per (token, choice) pair (SHARED:
+// the block's warps in turn) walks the N columns once, writing the row of dY and
+// summing the dot product; a token's warps share dD's row in L1. Rows that do not
+// start on 16-byte words are read by single elements side by side: by the words
+// around them, shifted, 24576 odd rows of 4001 bf16 took 127 us instead of 102. Bound by memory: 4096 tokens, k = 6, N =
 // 4096 bf16 in 70.1 us (0.92 of the HBM rate).
-template <typename Y, typename D, bool WIDE>
+template <typename Y, typename D, bool WIDE, bool SHARED>
 __global__ void __launch_bounds__(32 * kCombineGradWarps)
     combine_backward_kernel(const D *dd, const Y *y, Y *__restrict__ dy,
                             const CombineGradParams p)
 {
-    const int lane = threadIdx.x & 31;
-    const long long pair = static_cast<long long>(blockIdx.x) * kCombineGradWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5);
+    const long long pair = SHARED ? blockIdx.x : static_cast<long long>(blockIdx.x) * kCombineGradWarps + warp;
+    __shared__ float part[kCombineGradWarps];
     grid_start();
     if (pair >= p.T * p.k)
         return;
@@ -1057,7 +1067,7 @@ __global__ void __launch_bounds__(32 * kCombineGradWarps)
         const Y *yr = y + r * p.ldy;
         Y *o = dy + r * p.lddy;
 #pragma unroll 4
-        for (int c0 = 0; c0 < p.N; c0 += 256) {
+        for (int c0 = SHARED ? 256 * warp : 0; c0 < p.N; c0 += SHARED ? 256 * kCombineGradWarps : 256) {
             const int c = c0 + (WIDE ? 8 : 1) * lane;
             float a[8], b[8];
             load8<D, WIDE>(g, c, 32, p.N, a);
@@ -1071,7 +1081,16 @@ __global__ void __launch_bounds__(32 * kCombineGradWarps)
         }
     }
     dot = warp_sum(dot);
-    if (lane == 0)
+    if constexpr (SHARED) {
+        if (lane == 0)
+            part[warp] = dot;
+        __syncthreads();
+        dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kCombineGradWarps; ++i)
+            dot += part[i];
+    }
+    if (lane == 0 && (!SHARED || warp == 0))
         p.dweights[pair] = dot;
 }
 
@@ -1408,7 +1427,8 @@ gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const voi
     p.dweights = dweights;
     const bool wide = N % 8 == 0 && aligned_to(dD, 16) && aligned_to(Y, 16) && aligned_to(dY, 16) &&
                       lddd * ed % 16 == 0 && ldy * ey % 16 == 0 && lddy * ey % 16 == 0;
-    const unsigned grid = static_cast<unsigned>((T * k + kCombineGradWarps - 1) / kCombineGradWarps);
+    const bool shared = combine_grad_shared(T * k, N);
+    const unsigned grid = static_cast<unsigned>(shared ? T * k : (T * k + kCombineGradWarps - 1) / kCombineGradWarps);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return with_type(y_type, [&](auto ytag) {
         using Y_ = decltype(ytag);
@@ -1417,8 +1437,10 @@ gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const voi
             const D_ *gp = static_cast<const D_ *>(dD);
             const Y_ *yp = static_cast<const Y_ *>(Y);
             Y_ *op = static_cast<Y_ *>(dY);
-            return host_launch(wide ? combine_backward_kernel<Y_, D_, true> : combine_backward_kernel<Y_, D_, false>, grid,
-                               32 * kCombineGradWarps, 0, st, 0, gp, yp, op, p);
+            return host_launch(shared ? wide ? combine_backward_kernel<Y_, D_, true, true> : combine_backward_kernel<Y_, D_, false, true>
+                               : wide ? combine_backward_kernel<Y_, D_, true, false>
+                                      : combine_backward_kernel<Y_, D_, false, false>,
+                               grid, 32 * kCombineGradWarps, 0, st, 0, gp, yp, op, p);
         });
     });
 }

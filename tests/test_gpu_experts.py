@@ -571,6 +571,37 @@ def test_combine_at_every_address(g, y_type, d_type, N):
         assert (np.abs(np64(dw) - products.sum(-1)) <= (N / 32 + 16) * 2.0 ** -24 * np.abs(products).sum(-1) + 1e-30).all()
 
 
+@pytest.mark.parametrize("y_type,d_type", [(1, 1), (0, 1), (0, 0)])
+@pytest.mark.parametrize("T,k,N", [(512, 2, 300), (205, 5, 1024), (341, 3, 1024), (205, 5, 1023), (512, 8, 1030), (4097, 1, 1030),
+                                   (241, 17, 2048), (7, 3, 256), (7, 3, 257), (7, 3, 520)])
+@pytest.mark.parametrize("pad", [0, 1, 8])
+def test_combine_backward_of_few_and_many_pairs(g, y_type, d_type, T, k, N, pad):
+    """A row's columns walked by one warp and by several, at the numbers of pairs and columns where that changes."""
+    rng = np.random.default_rng(T + N)
+    R = T * k
+    slots = rng.permutation(R).reshape(T, k)
+    slots[T // 2, 0] = -1
+    y = torch.from_numpy(rng.standard_normal((R, N + pad))).to(TYPES[y_type])
+    dD = torch.from_numpy(rng.standard_normal((T, N + pad))).to(TYPES[d_type])
+    w = rng.standard_normal((T, k)).astype(np.float32)
+    dY = torch.full((R, N + pad), 8.0, dtype=TYPES[y_type], device=DEV)
+    dw = torch.full((T, k), 7.0, device=DEV)
+    g.gemm_route_combine_backward(T, N, k, dD.to(DEV), d_type, N + pad, y.to(DEV), y_type, R, N + pad,
+                                  torch.from_numpy(slots.astype(np.int32)).to(DEV), torch.from_numpy(w).to(DEV), dY, N + pad, dw)
+    dY, dw, d64, y64 = np64(dY), np64(dw), np64(dD)[:, :N], np64(y)[:, :N]
+    assert (dY[:, N:] == 8.0).all() and dw[T // 2, 0] == 0
+    left = (set(range(R)) - set(int(r) for r in slots.reshape(-1))).pop()
+    assert (dY[left] == 8.0).all()
+    for j in range(k):
+        t = np.nonzero(slots[:, j] >= 0)[0]
+        r = slots[t, j]
+        ref = w[t, j].astype(np.float64)[:, None] * d64[t]
+        assert (np.abs(dY[r, :N] - ref) <= (HALF_ULP[y_type] + 2.0 ** -24) * np.abs(ref) + 2.0 ** -25).all()
+        products = d64[t] * y64[r]
+        bound = (N / 32 + 16) * 2.0 ** -24 * np.abs(products).sum(-1) + 1e-30
+        assert (np.abs(dw[t, j] - products.sum(-1)) <= bound).all()
+
+
 def test_combine_backward_against_differences(g):
     """The sum is linear in the rows and in the weights: differences of the forward call are exact up to rounding."""
     rng = np.random.default_rng(8)
