@@ -858,19 +858,45 @@ __device__ __forceinline__ uint32_t quant_top(const QuantChunk<X, GATED> &v, uin
     return top;
 }
 
+// Two fp32 numbers in a register pair, and a * b + c of each.
+__device__ __forceinline__ uint64_t pair_of(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ void pair_to(uint64_t p, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+
 // round(x / scale) to whole numbers of at most 127, exactly that of the
 // correctly rounded quotient: x times the reciprocal is within 3e-5 of it, so
 // only where that lies near a half is the quotient itself taken. Adding
 // 1.5 * 2^23 rounds to a whole number and leaves it in the low byte.
 __device__ __forceinline__ void quant_round(const float (&x)[8], float scale, float inv, bool exact, uint32_t (&q)[8])
 {
-    const float magic = 12582912.0f;
+    const uint64_t magic = pair_of(12582912.0f, 12582912.0f), minus = pair_of(-1.0f, -1.0f), inv2 = pair_of(inv, inv);
     float near_half = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float t = __fmaf_rn(x[i], inv, magic);
-        near_half = fmaxf(near_half, fabsf(__fmaf_rn(x[i], inv, -__fsub_rn(t, magic))));
-        q[i] = __float_as_uint(t);
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t two = pair_of(x[i], x[i + 1]);
+        const uint64_t t = fma_pair(two, inv2, magic);
+        const uint64_t off = fma_pair(two, inv2, fma_pair(t, minus, magic));  // x / scale less the whole number
+        float a, b;
+        pair_to(off, a, b);
+        near_half = fmaxf(near_half, fmaxf(fabsf(a), fabsf(b)));
+        pair_to(t, a, b);
+        q[i] = __float_as_uint(a);
+        q[i + 1] = __float_as_uint(b);
     }
     if (exact || near_half > 0.4999f) {
 #pragma unroll
@@ -884,8 +910,9 @@ __device__ __forceinline__ void quant_round(const float (&x)[8], float scale, fl
 // and the rounding (CH 0: rows too long for that are read twice, the second
 // time from L2). WIDE: rows of 16-byte words. Bound by memory, and by the pause
 // between a row's loads and its stores, which three blocks an SM cover in part:
-// 8192 x 8192 bf16 in 44.1 us (4.6 TB/s; 64 with a division for each element,
-// 47 with two blocks an SM), 1536 gated rows of 2048 from fp32 in 7.2 us, rows
+// 8192 x 8192 bf16 in 42.3 us (4.8 TB/s; 64 with a division for each element,
+// 47 with two blocks an SM, 44.2 without the paired arithmetic of quant_round;
+// a kernel that issues instructions three cycles of four), 1536 gated rows of 2048 from fp32 in 7.2 us, rows
 // of odd length (4096 x 4001) in 17 us; four chunks a thread of those want the
 // registers of two blocks an SM (1000 x 8191: 11.5 us with three, 9.9 with two).
 template <typename X, bool GATED, bool WIDE, int CH>
@@ -948,19 +975,19 @@ __global__ void __launch_bounds__(kQuantMaxThreads, WIDE || CH < 4 ? 3 : 2)
         float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            f[i] = bad ? 0.0f : e.at(i);
+            f[i] = e.at(i);
         uint32_t b[8];
         quant_round(f, by, inv, exact, b);
         const int at = at0 + c * step;
         if (WIDE ? at < p.K : out_wide && at <= p.K - 8) {
             const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
             const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-            *reinterpret_cast<uint2 *>(out + at) = make_uint2(lo, hi);
+            *reinterpret_cast<uint2 *>(out + at) = bad ? make_uint2(0u, 0u) : make_uint2(lo, hi);
         } else if constexpr (!WIDE) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (at + i < p.K)
-                    out[at + i] = static_cast<int8_t>(b[i] & 0xffu);
+                    out[at + i] = bad ? static_cast<int8_t>(0) : static_cast<int8_t>(b[i] & 0xffu);
         }
     };
     if constexpr (CH > 0) {
