@@ -17,6 +17,8 @@ the `cpu_baseline` leg of the default run).
 
 Multi-GPU: the GEMM does not shard here; N ranks run N independent replicas
 (one process per GPU, NCCL only for the barrier and the max-over-ranks time).
+Such ranks run without TMA multicast loads, which the library otherwise plans
+for some single-CTA tiles.
 """
 from __future__ import annotations
 
@@ -306,6 +308,15 @@ class _DeviceSet:
         return self._outs
 
 
+def rank_options(options, world_size):
+    """A rank's GEMM options: with several GPUs no plan may share operands by TMA multicast."""
+    if world_size <= 1:
+        return options
+    if (options or {}).get("multicast_b", 0) > 0:
+        raise ValueError("multicast_b is for runs on one GPU")
+    return dict(options or {}, multicast_b=-1)
+
+
 class GemmJob:
     """One GEMM per step through gemm_ex."""
 
@@ -462,6 +473,7 @@ def _run_ours(args, wl_name, wl, ws, rank, local):
     options = wl.get("options")
     if args.options:
         options = dict(options or {}, **json.loads(args.options))
+    options = rank_options(options, ws)
     job = (GroupedJob if wl.get("kind") == "grouped" else GemmJob)(wl, dev, stream, options)
 
     def barrier():
