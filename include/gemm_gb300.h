@@ -558,6 +558,8 @@ gemm_status_t gemm_quantize_int8(int64_t M, int64_t K, const void *X, gemm_out_t
  * products of at most eight rows of A are summed in 32-bit integers instead,
  * which are exact for every K they are taken for (K < 2^17).
  * A and B 16-byte aligned, lda and ldb multiples of 16; K == 0 writes zeros.
+ * Waits inside the tile kernels end after 2 s and 10 us for each 128 elements
+ * of K that a CTA walks (GEMM_ERR_TIMEOUT by gemm_last_device_status).
  */
 gemm_status_t gemm_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a,
                         const int8_t *B, int64_t ldb, const float *scale_b,
@@ -677,6 +679,15 @@ gemm_status_t gemm_debug_plan(int64_t M, int64_t N, int64_t K, int kind, int a_m
  */
 int gemm_debug_streamk_units(int mode, int64_t tiles, int clusters, int kb_per_tile, int cluster,
                              int32_t *out, int max_units);
+
+/*
+ * Host-side plan of gemm_int8 (E = 0) and gemm_int8_grouped on a device with
+ * `sms` SMs (no GPU needed). Writes 5 int32: kind (0 the integer kernel for few
+ * tokens, 1 tiles with channels on the MMA's M side, 2 wide tiles), tokens and
+ * channels of a tile, CTAs that share a tile's K, and the bound of a wait in
+ * ms. Kind 0 has no tiles and no waits: M tokens, the others 0.
+ */
+gemm_status_t gemm_debug_int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms, int32_t *out);
 
 /* Test hook: the next GEMM launch makes its MMA warp wait on a barrier
  * that nothing arrives at, with a wait bound of `timeout_ms`; every role

@@ -89,6 +89,8 @@ _lib.gemm_debug_plan.argtypes = [_i64, _i64, _i64, _int, _int, _int, _int, ctype
 _lib.gemm_debug_plan.restype = _int
 _lib.gemm_debug_streamk_units.argtypes = [_int, _i64, _int, _int, _int, ctypes.POINTER(ctypes.c_int32), _int]
 _lib.gemm_debug_streamk_units.restype = _int
+_lib.gemm_debug_int8_plan.argtypes = [_i64, _i64, _i64, _i64, _int, ctypes.POINTER(ctypes.c_int32)]
+_lib.gemm_debug_int8_plan.restype = _int
 _lib.gemm_debug_inject_timeout.argtypes = [_int]
 _lib.gemm_debug_inject_timeout.restype = None
 _lib.gemm_debug_inject_timeout_at.argtypes = [_int, _int]
@@ -123,7 +125,7 @@ EXPORTED = ("gemm_bf16", "gemm_f16", "gemm_ex", "gemm_fp8", "gemm_fp8_ex", "gemm
             "gemm_quantize_int8", "gemm_int8", "gemm_int8_grouped", "gemm_route_combine", "gemm_route_combine_backward",
             "gemm_f16_grouped", "gemm_bf16_grouped_noalloc", "gemm_last_device_status", "gemm_status_string", "gemm_launch_count",
             "gemm_debug_descriptors", "gemm_debug_stage_image", "gemm_debug_plan", "gemm_debug_streamk_units",
-            "gemm_debug_inject_timeout", "gemm_debug_inject_timeout_at")
+            "gemm_debug_int8_plan", "gemm_debug_inject_timeout", "gemm_debug_inject_timeout_at")
 
 
 class GemmError(RuntimeError):
@@ -292,6 +294,16 @@ def gemm_debug_plan(M, N, K, kind=0, a_major=0, b_major=0, grouped=False, option
     _check(_lib.gemm_debug_plan(M, N, K, kind, a_major, b_major, int(grouped), _opts(options), sms, out),
            "gemm_debug_plan")
     return dict(zip(PLAN_FIELDS, list(out)))
+
+
+INT8_PLAN_FIELDS = ("kind", "tokens", "channels", "shares", "wait_ms")
+
+
+def gemm_debug_int8_plan(M, N, K, E=0, sms=152):
+    """The tiles an 8-bit integer product would launch (host only), as a dict; kind 0 integers, 1 narrow, 2 wide."""
+    out = (ctypes.c_int32 * 5)()
+    _check(_lib.gemm_debug_int8_plan(M, N, K, E, sms, out), "gemm_debug_int8_plan")
+    return dict(zip(INT8_PLAN_FIELDS, list(out)))
 
 
 def gemm_debug_streamk_units(mode, tiles, clusters, kb_per_tile, cluster):

@@ -43,7 +43,7 @@
 //                stages; a group reads and widens a stage into registers
 //                before it waits for room to write it. The warpgroups share
 //                the registers out by need (setmaxnreg).
-// Every wait is bounded, as in gemm_kernel.cuh.
+// Every wait is bounded, as in gemm_kernel.cuh, here by the length of K.
 //
 // Measured on a GB300, operands not in L2, launches one after another (HBM 6.78
 // TB/s, bf16 products 1919 TFLOP/s): 8192^3 553 us (1990 TFLOP/s), 4096^3 85.7
@@ -1206,6 +1206,23 @@ I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms)
     return best->pl;
 }
 
+// Few tokens, where integers beat tiles, whose work hardly grows with the
+// tokens (measured us, integers and tiles: 4096 x 4096 weights with 1, 2, 4
+// and 8 tokens 4.2, 5.2, 6.0 and 11.9 against 9.8; 16384 x 4096 11.7, 15.4,
+// 19.9 and 27.7 against 15.5; 1024 x 1024 with 8 tokens 2.9 against 5.8).
+bool int8_few(int64_t M, int64_t N, int64_t K, int64_t E)
+{
+    return E == 0 && K <= kFewMaxK &&
+           (M <= 2 || (M <= 4 && N * K <= int64_t(1) << 25) || (M <= 8 && N * K <= int64_t(3) << 22));
+}
+
+// How long a wait may take: a role may wait for another to walk all of a tile's
+// K, for which a block has 10 us (0.4 to 0.7 measured), and 2 s beside it.
+int int8_wait_ms(int64_t K, const I8Plan &pl)
+{
+    return static_cast<int>(2000 + (K / kI8K + 1) / pl.ks / 100);
+}
+
 gemm_status_t launch_int8_plan(const CUtensorMap &a, const CUtensorMap &b, const I8Params &p, const I8Plan &pl, int sms,
                                cudaStream_t st)
 {
@@ -1268,19 +1285,15 @@ gemm_status_t run_int8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t
                                                      : int8_zero_kernel<__half>,
                            static_cast<unsigned>(grid), 256, 0, st, 0, p);
     }
-    // Few tokens, where integers beat tiles, whose work hardly grows with the
-    // tokens (measured us, integers and tiles: 4096 x 4096 weights with 1, 2, 4
-    // and 8 tokens 4.2, 5.2, 6.0 and 11.9 against 9.8; 16384 x 4096 11.7, 15.4,
-    // 19.9 and 27.7 against 15.5; 1024 x 1024 with 8 tokens 2.9 against 5.8).
-    if (E == 0 && K <= kFewMaxK && (M <= 2 || (M <= 4 && N * K <= int64_t(1) << 25) || (M <= 8 && N * K <= int64_t(3) << 22)))
+    if (int8_few(M, N, K, E))
         return M == 1   ? launch_few<1>(A, lda, B, ldb, p, st)
                : M == 2 ? launch_few<2>(A, lda, B, ldb, p, st)
                : M <= 4 ? launch_few<4>(A, lda, B, ldb, p, st)
                         : launch_few<8>(A, lda, B, ldb, p, st);
+    const I8Plan pl = int8_plan(M, N, K, E, sms);
     int ms = 0;
     p.inject = host_take_injection(&ms);
-    p.timeout_ns = static_cast<unsigned long long>(ms > 0 ? ms : 2000) * 1000000ull;
-    const I8Plan pl = int8_plan(M, N, K, E, sms);
+    p.timeout_ns = static_cast<unsigned long long>(ms > 0 ? ms : int8_wait_ms(K, pl)) * 1000000ull;
     const int64_t tiles_n = (N + pl.channels() - 1) / pl.channels();
     if (tiles_n * ((M + pl.tokens() - 1) / pl.tokens() + (E ? std::min(E, M) : 0)) > kSizeLimit)
         return GEMM_ERR_UNSUPPORTED;
@@ -1325,6 +1338,23 @@ gemm_status_t gemm_int8_grouped(int64_t M, int64_t N, int64_t K, int64_t E, cons
         return GEMM_ERR_INVALID_ARG;
     return g300::run_int8(M, N, K, E, offsets, A, lda, scale_a, B, ldb, stride_b, scale_b, D, ldd, d_type,
                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_debug_int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms, int32_t *out)
+{
+    using namespace g300;
+    if (!out || sms <= 0 || M < 1 || N < 1 || K < 1 || E < 0 || E > GEMM_ROUTE_MAX_EXPERTS)
+        return GEMM_ERR_INVALID_ARG;
+    if (!countable(M) || !countable(N) || !countable(K))
+        return GEMM_ERR_UNSUPPORTED;
+    const bool few = int8_few(M, N, K, E);
+    const I8Plan pl = int8_plan(M, N, K, E, sms);
+    out[0] = few ? 0 : pl.wide ? 2 : 1;
+    out[1] = few ? static_cast<int32_t>(M) : pl.tokens();
+    out[2] = few ? 0 : pl.channels();
+    out[3] = few ? 0 : pl.ks;
+    out[4] = few ? 0 : int8_wait_ms(K, pl);
+    return GEMM_OK;
 }
 
 }  // extern "C"
