@@ -495,7 +495,8 @@ typedef struct {
  * A logit (or bias) of -inf or NaN is never chosen. Where fewer than k
  * experts are left (a padded token has none), the remaining ids are -1 and
  * their weights 0. A NaN logit, or under softmax one of +inf, makes all
- * weights of its token NaN; the ids stay valid.
+ * weights of its token NaN; the ids stay valid (the choice takes a softmax
+ * score of +inf as 1, that of the others beside it as 0).
  */
 gemm_status_t gemm_route(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl,
                          const float *bias, int k, const gemm_route_t *route,

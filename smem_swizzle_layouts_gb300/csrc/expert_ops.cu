@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *logits
             total = 0.0f;
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
-                s[i] = l[i] > -INFINITY ? (p.renorm ? fast_exp(l[i] - top) : expf(l[i] - top)) : 0.0f;
+                // a logit of +inf counts as 1 beside others of 0, so that the choice has its order
+                s[i] = l[i] == top ? 1.0f : l[i] > -INFINITY ? (p.renorm ? fast_exp(l[i] - top) : expf(l[i] - top)) : 0.0f;
                 total += s[i];
             }
             total = warp_sum(total);
