@@ -487,8 +487,9 @@ typedef struct {
  * of the chosen s). The bias (E fp32 values, or NULL) steers the choice and
  * is no part of the weights. Equal values go to the lower index; without a
  * bias the choice goes by the logits, whose order is that of the scores. The
- * scores that a choice with a bias (or between groups) compares are good to
- * about 3e-7, the weights to fp32 rounding.
+ * scores that a choice with a bias (or between groups) compares and the
+ * weights are good to fp32 rounding (a few units in the last place; a sigmoid
+ * below 2^-126 counts as 0 in the weights).
  *   logits: T x E of l_type, row stride ldl. weights: T x k fp32; ids: T x k
  *   int32. 1 <= k <= min(E, GEMM_ROUTE_MAX_K), E <= GEMM_ROUTE_MAX_EXPERTS,
  *   k at most the experts of the kept groups.

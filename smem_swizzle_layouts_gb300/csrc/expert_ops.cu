@@ -117,22 +117,12 @@ __device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf
 
 // ---------------------------------------------------------------- routing
 
-// e^x and 1 / x by the special-function unit, for the scores that the choice
-// compares: within about 3e-7 of the sigmoid (softmax: of the largest score),
-// and equal for equal logits. The weights are computed from the chosen logits
-// with expf and correctly rounded divisions.
-__device__ __forceinline__ float fast_exp(float x)
+// The sigmoid as a choice compares it: to fp32 rounding down to the smallest
+// subnormal number, where 1 / (1 + e^-x) would be 0 from x = -88.7 on.
+__device__ __forceinline__ float choice_sigmoid(float x)
 {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
-    return y;
-}
-
-__device__ __forceinline__ float fast_inverse(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+    const float e = expf(-fabsf(x)), r = __frcp_rn(1.0f + e);
+    return x < 0.0f ? e * r : r;
 }
 
 struct RouteParams {
@@ -198,13 +188,14 @@ __device__ __forceinline__ LaneBest lane_best(const uint32_t (&key)[NPL], uint32
 // its two best, so it looks through its codes again only when both are taken.
 //
 // s = softmax(l) or sigmoid(l); e is chosen by s_e + bias_e; w = s / sum of the
-// chosen s. For 16384 tokens memory could deliver in 0.4 (64 experts, bf16) to
-// 2.6 us (256, fp32); the kernel takes 8.2 us (k = 6, no bias; 470 instructions a
-// token) and 15.4 us (k = 8 with a bias, 850; 22.1 us with 8 groups): a warp per
-// token keeps a token's codes in registers and its maxima in the warp. Before
-// the lanes kept two candidates and compared special-function scores it took
-// 25 us, before the bias came with the logits 18.6. One token takes 2.2 us,
-// launch latency.
+// chosen s. Both the compared scores and the weights are fp32, by expf. For
+// 16384 tokens memory could deliver in 0.4 (64 experts, bf16) to 2.6 us (256,
+// fp32); the kernel takes 8.2 us (k = 6, no bias; 467 instructions a token) and
+// 17.4 us (k = 8 with a bias; 24.2 us with 8 groups): held by the instructions it
+// issues, of which the k rounds of maxima across the warp are most. Before the
+// lanes kept two candidates the second took 25 us. Special-function scores took
+// 14.6 and 21.5 us, but flushed those below 2^-126 and tied their experts. One
+// token takes 2.4 us, launch latency.
 template <typename L, int NPL>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *logits, const RouteParams p)
 {
@@ -250,7 +241,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *logits
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
                 // a logit of +inf counts as 1 beside others of 0, so that the choice has its order
-                s[i] = l[i] == top ? 1.0f : l[i] > -INFINITY ? (p.renorm ? fast_exp(l[i] - top) : expf(l[i] - top)) : 0.0f;
+                s[i] = l[i] == top ? 1.0f : l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
                 total += s[i];
             }
             total = warp_sum(total);
@@ -261,10 +252,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const L *logits
     // what the choice goes by
     uint32_t key[NPL];
     if (scored) {
-        const float inv = fast_inverse(total);
+        const float inv = __frcp_rn(total);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            s[i] = p.sigmoid ? fast_inverse(1.0f + fast_exp(-l[i])) : s[i] * inv;
+            s[i] = p.sigmoid ? choice_sigmoid(l[i]) : s[i] * inv;
             if (p.bias)
                 s[i] = __fadd_rn(s[i], bias[i]);
             key[i] = l[i] > -INFINITY ? choice_key(p.bias ? s[i] : l[i]) : 0u;
