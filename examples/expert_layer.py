@@ -20,6 +20,13 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import smem_swizzle_layouts_gb300 as g  # noqa: E402
 
 
+def expect(name: str, t: torch.Tensor, dtype: torch.dtype, *shape: int) -> None:
+    """The library reads bare pointers: another type, size or order of a tensor's elements is refused here."""
+    if t.dtype != dtype or tuple(t.shape) != shape or (t.shape[-1] > 1 and t.numel() > 0 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: {dtype} {list(shape)} with neighbouring elements in a row, not "
+                         f"{t.dtype} {list(t.shape)} with strides {list(t.stride())}")
+
+
 def quantize_weights(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     """(int8 values, scale per channel) of weights [E, N, K]; K is a multiple of 16."""
     E, N, K = w.shape
@@ -41,6 +48,9 @@ class ExpertLayer:
         dev = w1.device
         self.E, two_f, self.H = w1.shape
         self.F, self.k, self.rule, self.tokens = two_f // 2, k, rule, tokens
+        self.T = 0  # of the last call
+        if two_f % 2 or tuple(w2.shape) != (self.E, self.H, self.F):
+            raise ValueError(f"w1 [E, 2F, H] {list(w1.shape)} and w2 [E, H, F] {list(w2.shape)} do not fit")
         self.q1, self.s1 = quantize_weights(w1)
         self.q2, self.s2 = quantize_weights(w2)
         rows = tokens * k
@@ -60,6 +70,11 @@ class ExpertLayer:
         T, (E, k, H, F) = x.shape[0], (self.E, self.k, self.H, self.F)
         if T > self.tokens:
             raise ValueError(f"{T} tokens in a layer of {self.tokens}")
+        expect("x", x, torch.bfloat16, T, H)
+        expect("logits", logits, torch.float32, T, E)
+        if bias is not None:
+            expect("bias", bias, torch.float32, E)
+        self.T = T
         rows = T * k
         out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
         g.gemm_route(T, E, logits, g.OUT_F32, logits.stride(0), bias, k, self.rule, self.weights, self.ids)
@@ -78,7 +93,9 @@ class ExpertLayer:
 
     def router_gradient(self, logits: torch.Tensor, d_out: torch.Tensor) -> torch.Tensor:
         """The gradient of the logits of the last call, from that of its output ([T, H] bf16)."""
-        T, k, H, rows = logits.shape[0], self.k, self.H, logits.shape[0] * self.k
+        T, k, H, rows = self.T, self.k, self.H, self.T * self.k
+        expect("logits", logits, torch.float32, T, self.E)
+        expect("d_out", d_out, torch.bfloat16, T, H)
         d_rows, d_weights = torch.empty_like(self.y2), torch.empty(T, k, device=logits.device)
         g.gemm_route_combine_backward(T, H, k, d_out, g.OUT_BF16, d_out.stride(0), self.y2, g.OUT_F32, rows, H,
                                       self.slots, self.weights, d_rows, H, d_weights)
