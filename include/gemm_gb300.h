@@ -697,8 +697,13 @@ gemm_status_t gemm_debug_int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, i
 void gemm_debug_inject_timeout(int timeout_ms);
 
 /* The same for a chosen role: 1 the TMA producer (in both CTAs of a pair,
- * before it issues any load), 2 the MMA issuer. Other roles are ignored. The
- * status word then names that role with wait code 6 (injected). */
+ * before it issues any load), 2 the MMA issuer; in the tiles of the 8-bit
+ * integer products also 3 the epilogue of tiles that are not wide, and 6 the
+ * converters (a launch that has no such role is not affected). Other roles
+ * are ignored. The status word then names that role
+ * with wait code 6 (injected), in the integer products' tiles that or a role
+ * that waits for it. Where CTAs share a tile's K, role 3 instead leaves out the
+ * others' sums, and the first CTA's epilogue gives up on them (wait code 13). */
 void gemm_debug_inject_timeout_at(int timeout_ms, int role);
 
 #ifdef __cplusplus

@@ -453,5 +453,6 @@ def gemm_debug_stage_image(src, major, swizzle, rows_total, k_total, ld, rows, b
 
 
 def gemm_debug_inject_timeout(timeout_ms: int, role: int = 2) -> None:
-    """Make the next launch's MMA issuer (role 2) or producer (role 1) wait until `timeout_ms` runs out."""
+    """Make the next launch's MMA issuer (role 2) or producer (role 1) wait until `timeout_ms` runs out; in 8-bit
+    integer products also the epilogue (3) or the converters (6)."""
     _lib.gemm_debug_inject_timeout_at(timeout_ms, role)

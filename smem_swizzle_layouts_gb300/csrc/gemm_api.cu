@@ -565,9 +565,10 @@ void fill_common(KParams &p, const Plan &pl, const InFmt &f, int a_mn, int b_mn,
     p.flags = pl.flags;
     p.stats = pl.stats;
     p.status = status;
-    const int inj = g_inject_timeout_ms.exchange(0);
-    p.inject_timeout = inj > 0 ? g_inject_role.load() : 0;
-    if (inj > 0)
+    const int inj = g_inject_timeout_ms.exchange(0), role = g_inject_role.load();
+    const bool known = inj > 0 && (role == kRoleProducer || role == kRoleMma);
+    p.inject_timeout = known ? role : 0;
+    if (known)
         p.timeout_ns = static_cast<unsigned long long>(inj) * 1000000ull;
 }
 
@@ -1347,7 +1348,7 @@ void gemm_debug_inject_timeout(int timeout_ms) { gemm_debug_inject_timeout_at(ti
 
 void gemm_debug_inject_timeout_at(int timeout_ms, int role)
 {
-    if (role != kRoleProducer && role != kRoleMma)
+    if (role != kRoleProducer && role != kRoleMma && role != kRoleEpilogue && role != kRoleConvert)
         return;
     g_inject_role.store(role);
     g_inject_timeout_ms.store(timeout_ms > 0 ? timeout_ms : 0);

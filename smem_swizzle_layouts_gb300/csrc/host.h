@@ -20,6 +20,10 @@ gemm_status_t host_encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, int ra
                                 const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
                                 CUtensorMapSwizzle swz);
 
+// Role code of the converters of the 8-bit integer products in the status word,
+// beside those of gemm_kernel.cuh.
+constexpr unsigned int kRoleConvert = 6;
+
 // Takes a pending timeout injection (gemm_debug_inject_timeout): the role
 // that shall wait and its bound in ms, or 0.
 int host_take_injection(int *timeout_ms);

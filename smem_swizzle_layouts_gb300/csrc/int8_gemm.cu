@@ -78,7 +78,6 @@ constexpr int kI8FirstEpiWarp = 4;
 constexpr int kI8MaxSmem = 232448;
 
 enum : uint32_t {
-    kRoleConvert = 6,
     kWaitRawFull = 11 << 8,
     kWaitConvEmpty = 12 << 8,
     kWaitSplit = 13 << 8,
@@ -94,7 +93,7 @@ struct I8Params {
     long long ldd;
     int out_type;
     int vec;     // rows of D start on multiples of 32 bytes
-    int inject;  // test hook: the role that waits on a barrier nothing arrives at
+    int inject;  // test hook: the role that waits on a barrier nothing arrives at (see the epilogue for its own)
     unsigned long long timeout_ns;
     unsigned int *status;
 };
@@ -821,7 +820,9 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
         int rs = group % C::RAW_STAGES, cs = group % C::CONV_STAGES;
         uint32_t rphase = 0, cphase = 1;
         int skip = group;  // blocks of the tile before the group's next one
-        bool ok = true;
+        bool ok = p.inject != kRoleConvert;
+        if (!ok)
+            w.wait(bar_inject, 0u, kRoleConvert | kWaitInjected);
         // wide: the tile whose sums are still to be stored, and the parity of its accumulator
         int done = -1;
         uint32_t acc_phase = 0;
@@ -922,7 +923,11 @@ __global__ void __launch_bounds__(I8Cfg<NS, KS, WIDE>::THREADS, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         int first = 0;  // narrow: the issuer of the tile's first block
-        for (int t = cluster_id; t < sched.num_tiles; t += clusters) {
+        // the injected epilogue waits, or where CTAs share K keeps its sums from the first CTA, which waits for them
+        const bool injected = p.inject == kRoleEpilogue && (cluster == CG || rank > 0);
+        if (injected && cluster == CG)
+            w.wait(bar_inject, 0u, kRoleEpilogue | kWaitInjected);
+        for (int t = cluster_id; !injected && t < sched.num_tiles; t += clusters) {
             const I8Tile ti = i8_tile<C::TOKENS, C::CHANNELS>(sched, t);
             const float *sb = p.sb + static_cast<long long>(ti.expert) * p.N;
             {

@@ -108,6 +108,32 @@ def test_experts_on_pairs_of_ctas(g, tile, M, N, K, offsets, d_type, sectors):
     assert torch.equal(D, want)
 
 
+INJECTED, SPLIT = 6, 13  # wait codes
+
+
+@pytest.mark.parametrize("role,tile,M,N,K,wait", [
+    *[(role, WIDE, 200, 20000, 2048, INJECTED) for role in (1, 2, 6)], *[(role, PAIR, 128, 20000, 2048, INJECTED) for role in (1, 2, 3, 6)],
+    (6, (1, 16, 1), 16, 20000, 1024, INJECTED), (3, (1, 64, 1), 64, 20000, 1024, INJECTED),
+    *[(3, (1, t, ks), t, 300, 4096, SPLIT) for t, ks in ((16, 8), (32, 4), (64, 2))], (6, (1, 32, 4), 32, 300, 4096, INJECTED),
+    (1, (1, 16, 8), 16, 300, 4096, INJECTED), (2, (1, 64, 2), 64, 300, 4096, INJECTED)])
+def test_waits_run_out_on_every_tile(g, role, tile, M, N, K, wait):
+    """A role that waits in vain ends the launch, and the next launch is sound."""
+    assert plan(g, M, N, K) == tile
+    gen = torch.Generator(device=DEV).manual_seed(role)
+    a, b = matrix(gen, M, K, K, limit(K)), matrix(gen, N, K, K, limit(K))
+    one = torch.ones(M + N, device=DEV)
+    D = torch.empty(M, N, device=DEV)
+    g.gemm_debug_inject_timeout(30, role)
+    g.gemm_int8(M, N, K, a, K, one, b, K, one, D, N, 0)
+    st, word = g.gemm_last_device_status()
+    assert st == g.ERR_TIMEOUT and word != 0  # of the injected role, or of one that waits for it
+    if wait == SPLIT:
+        assert (word & 255, word >> 8) == (role, SPLIT)
+    g.gemm_int8(M, N, K, a, K, one, b, K, one, D, N, 0)
+    ok(g)
+    assert torch.equal(D, scaled(a, b, one[:M], one[:N], 0))
+
+
 def test_a_tile_that_takes_longer_than_two_seconds(g):
     """One tile of 2^23 blocks of K, about 0.35 us each: waits for it last as long as it does."""
     K = 1 << 30
