@@ -451,7 +451,9 @@ gemm_status_t gemm_bf16_grouped_noalloc(const gemm_problem_t *problems, int num_
  * the sizes of products, end 8192 short of 2^31 (GEMM_ERR_UNSUPPORTED past it).
  * The kernels are launched so that each
  * may start while the kernel before it on the stream ends (programmatic
- * dependent launch); they wait for it before they touch memory.
+ * dependent launch); they wait for it before they touch memory. The second of
+ * gemm_route_plan's two kernels reads the ids before it waits for the first,
+ * which lets it start only when what came before both has ended.
  * ------------------------------------------------------------------- */
 
 typedef enum { GEMM_ROUTE_SOFTMAX = 0, GEMM_ROUTE_SIGMOID = 1 } gemm_score_t;

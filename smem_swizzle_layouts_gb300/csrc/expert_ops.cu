@@ -3,8 +3,10 @@
 // weighted sum of the experts' rows with its gradient. Contracts are in
 // include/gemm_gb300.h.
 //
-// All of them read their inputs once. Sums and softmax statistics are fp32 and
-// results are rounded once, on the store. Times in the comments are of one
+// They read their inputs once, but for the chosen logits of a routing with a
+// bias, the ids of an order in several parts (counted, then handed out) and rows
+// too long for a block's registers in the quantisation. Sums and softmax
+// statistics are fp32 and results are rounded once, on the store. Times in the comments are of one
 // launch among others on a GB300 with operands that are not in L2; the HBM
 // rate they are set against is 6.78 TB/s.
 #include <cuda_bf16.h>

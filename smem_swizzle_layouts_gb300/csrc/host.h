@@ -34,8 +34,10 @@ void host_count_launches(int n);
 // Launches a kernel that may start while the kernel before it on the stream is
 // still running (programmatic dependent launch). Such a kernel calls
 // grid_start() before it touches memory that another kernel writes or reads:
-// only its launch and what it sets up on chip overlap. With `cluster` > 0 it
-// is launched in clusters of that many CTAs.
+// only its launch and what it sets up on chip overlap. (One reads earlier:
+// plan_scatter_kernel its ids. The kernel before it, plan_count_kernel, lets it
+// start after its own wait, so that what wrote the ids has ended.) With
+// `cluster` > 0 it is launched in clusters of that many CTAs.
 template <typename... Params, typename... Args>
 inline gemm_status_t host_launch(void (*kern)(Params...), unsigned grid, dim3 block, size_t smem, cudaStream_t st,
                                  unsigned cluster, Args... args)

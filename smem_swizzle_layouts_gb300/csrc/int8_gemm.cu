@@ -46,10 +46,11 @@
 // Every wait is bounded, as in gemm_kernel.cuh, here by the length of K.
 //
 // Measured on a GB300, operands not in L2, launches one after another (HBM 6.78
-// TB/s, bf16 products 1919 TFLOP/s): 8192^3 553 us (1990 TFLOP/s), 4096^3 85.7
-// us (256 wide tiles on 76 pairs: 4 rounds for 3.4), 8192^2 x 2048 170-177 us (an
+// TB/s, bf16 products 1932 TFLOP/s): 8192^3 547 us in a burst of 20 launches
+// (2010 TFLOP/s) and 620 us in a long run under the power cap (1770), 4096^3 86
+// us (256 wide tiles on 76 pairs: 4 rounds for 3.4), 8192^2 x 2048 167 us (an
 // epilogue for each sixteen stages), 64 experts with 512 rows each, N 4096, K
-// 2048 335 us; 128 x 16384 x 4096 20.5 us, 16 x 16384 x 4096 15.7 us (about 0.4
+// 2048 335 us; 128 x 16384 x 4096 20.5-21.6 us, 16 x 16384 x 4096 15.7 us (about 0.4
 // us a stage on 128 CTAs: the issue of 16-token MMAs and the widening, both
 // ahead of the 10 us of HBM traffic), 96 rows over 64 experts 88 us (0.9 of the
 // HBM rate). What bounds wide tiles: shared memory, 128 to 160 KB a stage
