@@ -193,8 +193,8 @@ __device__ __forceinline__ LaneBest lane_best(const uint32_t (&key)[NPL], uint32
 // chosen s. Both the compared scores and the weights are fp32, by expf. For
 // 16384 tokens memory could deliver in 0.4 (64 experts, bf16) to 2.6 us (256,
 // fp32); the kernel takes 8.2 us (k = 6, no bias; 467 instructions a token) and
-// 17.4 us (k = 8 with a bias; 24.2 us with 8 groups): held by the instructions it
-// issues, of which the k rounds of maxima across the warp are most. Before the
+// 17.4 us (k = 8 with a bias, 1003; 24.2 us with 8 groups): held by the instructions
+// it issues, of which the k rounds of maxima across the warp are most. Before the
 // lanes kept two candidates the second took 25 us. Special-function scores took
 // 14.6 and 21.5 us, but flushed those below 2^-126 and tied their experts. One
 // token takes 2.4 us, launch latency.
