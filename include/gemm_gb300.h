@@ -605,6 +605,126 @@ gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const voi
                                           int64_t ldy, const int32_t *slots, const float *weights,
                                           void *dY, int64_t lddy, float *dweights, gemm_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * The ends of a training step: rows of a token table, the loss of a linear head
+ * over a large vocabulary, and the balance loss of the routers. The rules of the expert-layer calls above hold (element types,
+ * alignment, errors, overlapping launches), but for what is said here.
+ * ------------------------------------------------------------------- */
+
+/*
+ * gemm_cross_entropy: softmax cross entropy of the logits l = X W^T, which are
+ * never written to memory:
+ *   lse[t] = log sum_v exp(l[t,v]),  losses[t] = lse[t] - l[t, targets[t]]
+ * X is T x K, W is V x K, of in_type (0 fp16, 1 bf16; both row-major and
+ * 16-byte aligned, ldx and ldw multiples of 8, as for gemm_ex). A token whose
+ * target is outside 0..V-1 (padding, a prompt that is not trained on) has no
+ * loss: losses[t] and lse[t] are 0, whatever its row of X holds. Logits are
+ * summed in fp32; sums of exponentials, lse and losses are fp32, the loss
+ * without the rounding of lse. A logit of +inf makes lse +inf, one of NaN NaN.
+ * workspace: gemm_cross_entropy_workspace_size(T, V) bytes, 16-byte aligned,
+ * in no particular state.
+ */
+size_t gemm_cross_entropy_workspace_size(int64_t T, int64_t V);
+
+gemm_status_t gemm_cross_entropy(int in_type, int64_t T, int64_t V, int64_t K, const void *X, int64_t ldx,
+                                 const void *W, int64_t ldw, const int32_t *targets, float *losses, float *lse,
+                                 void *workspace, size_t workspace_bytes, gemm_stream_t stream);
+
+/*
+ * gemm_cross_entropy_backward: gradients of sum_t dlosses[t] * losses[t] +
+ * dlse[t] * lse[t] (dlse NULL: no gradient of lse; a penalty on the normaliser
+ * has one) from the lse that the forward call wrote:
+ *   dl[t,v] = exp(l[t,v] - lse[t]) * (dlosses[t] + dlse[t]) - [v = targets[t]] * dlosses[t]
+ *   dX = dl W  (T x K of dx_type),   dW = dl^T X  (V x K of dw_type; accumulate
+ *   nonzero: added to what dW holds, the sum rounded once)
+ * dX or dW may be NULL, when only the other is wanted. Both are written whole,
+ * 16-byte aligned with rows of a multiple of 16 bytes; they do not overlap the
+ * inputs. Tokens without a loss carry nothing: their rows of dX are 0 (for a
+ * finite W), and what their rows of X, dlosses and dlse hold has no part in dW.
+ * dl is computed for a piece of the vocabulary at a time and rounded to the
+ * inputs' type for the tensor cores, after a division by the largest
+ * |dlosses| + |dlse| (found on the GPU: any scaling of the loss gives the same
+ * gradients, times it). Products are summed in fp32. T == 0 leaves dX and writes
+ * zeros to dW (nothing with accumulate).
+ * workspace: 256-byte aligned, in no particular state. The call takes the widest
+ * pieces that it has room for, 16384 columns at most:
+ * gemm_cross_entropy_backward_workspace_size(T, V, K, columns) bytes for pieces
+ * of `columns` columns (rounded up to a multiple of 256, the least; 0: the
+ * widest), on the current device; 0 for bad arguments or without a device. The
+ * widths' order of sums differs, so gradients may differ in their last bits.
+ */
+size_t gemm_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t K, int64_t columns);
+
+gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int64_t K, const void *X, int64_t ldx,
+                                          const void *W, int64_t ldw, const int32_t *targets, const float *lse,
+                                          const float *dlosses, const float *dlse, void *dX, gemm_out_t dx_type,
+                                          int64_t lddx, void *dW, gemm_out_t dw_type, int64_t lddw, int accumulate,
+                                          void *workspace, size_t workspace_bytes, gemm_stream_t stream);
+
+/*
+ * gemm_route_balance: counts per expert and the balance loss of a router, for
+ * each of S sequences (tokens offsets[s] .. offsets[s+1]-1; offsets: S + 1 int32
+ * in device memory that do not fall, those outside 0..T taken as its ends; NULL:
+ * S is 1 and the sequence is all T tokens). Of the tokens of a sequence those
+ * are live that have an id in 0..E-1 (padded tokens, as gemm_route leaves them,
+ * have none); for its n live tokens
+ *   counts[s,e] = number of ids that are e,      tokens[s] = n,
+ *   means[s,e]  = mean of p[t,e],
+ *   losses[s]   = E * sum_e counts[s,e] / (k n) * means[s,e]
+ * with p the token's softmax over the E experts, or its sigmoid scores over their
+ * sum (route->score; its other fields, and a bias, have no part; NULL: softmax).
+ * A perfect balance has loss 1; a sequence without live tokens has zeros.
+ * ids: T x k int32 as gemm_route writes them; logits: T x E of l_type, row
+ * stride ldl. counts and means: S x E; all fp32 or int32. E, k as for gemm_route.
+ * workspace: gemm_route_balance_workspace_size(T, E, S) bytes, 16-byte aligned,
+ * in no particular state (may be NULL where that is 0). Sums have a fixed order.
+ */
+size_t gemm_route_balance_workspace_size(int64_t T, int64_t E, int64_t S);
+
+gemm_status_t gemm_route_balance(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl, int k,
+                                 const gemm_route_t *route, const int32_t *ids, int64_t S, const int32_t *offsets,
+                                 int32_t *counts, int32_t *tokens, float *means, float *losses, void *workspace,
+                                 size_t workspace_bytes, gemm_stream_t stream);
+
+/*
+ * gemm_route_balance_backward: the gradient of the logits from that of the
+ * losses (S fp32 values), with the counts and tokens that the forward call wrote;
+ * counts carry no gradient. dlogits: T x E of l_type, row stride lddl, not
+ * overlapping logits. accumulate nonzero: added to what dlogits holds (such as
+ * gemm_route_backward's gradient). Rows of tokens that are not live get zeros
+ * (accumulate: stay as they are); rows of tokens in no sequence are not written.
+ */
+gemm_status_t gemm_route_balance_backward(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl,
+                                          int k, const gemm_route_t *route, const int32_t *ids, int64_t S,
+                                          const int32_t *offsets, const int32_t *counts, const int32_t *tokens,
+                                          const float *dlosses, void *dlogits, int64_t lddl, int accumulate,
+                                          gemm_stream_t stream);
+
+/*
+ * gemm_embed: D[t,:] = scale * table[ids[t],:], rows of N values; zeros where
+ * the id is outside 0..V-1. table: V x N of t_type, row stride ldt; D: T x N of
+ * d_type, row stride ldd; ids: T int32. The product is rounded once.
+ */
+gemm_status_t gemm_embed(int64_t T, int64_t N, int64_t V, const int32_t *ids, const void *table, gemm_out_t t_type,
+                         int64_t ldt, float scale, void *D, gemm_out_t d_type, int64_t ldd, gemm_stream_t stream);
+
+/*
+ * gemm_embed_backward: dtable[v,:] = scale * sum of dD[t,:] over the tokens t
+ * with ids[t] = v, in a fixed order, in fp32, rounded once. dtable is V x N of
+ * t_type, written whole (rows that no id names get zeros); accumulate nonzero:
+ * the sums are added to what it holds (a tied head's dW, say) and rows that no
+ * id names are not touched. dD: T x N of d_type, row stride lddd. Ids outside
+ * 0..V-1 carry nothing. scale is finite.
+ * workspace: gemm_embed_backward_workspace_size(T, N, V) bytes, 256-byte
+ * aligned, in no particular state (may be NULL where that is 0).
+ */
+size_t gemm_embed_backward_workspace_size(int64_t T, int64_t N, int64_t V);
+
+gemm_status_t gemm_embed_backward(int64_t T, int64_t N, int64_t V, const int32_t *ids, const void *dD,
+                                  gemm_out_t d_type, int64_t lddd, float scale, void *dtable, gemm_out_t t_type,
+                                  int64_t lddt, int accumulate, void *workspace, size_t workspace_bytes,
+                                  gemm_stream_t stream);
+
 /* Synchronises `stream`, reads the device status word of this library,
  * clears it, and returns GEMM_OK or GEMM_ERR_TIMEOUT (GEMM_ERR_CUDA if the
  * read fails). `detail` (may be NULL) receives the raw word: bits 0-7 the

@@ -13,6 +13,9 @@ from ._lib import (  # noqa: F401
     QUANT_GATED, QUANT_PLAIN, ROUTE_MAX_EXPERTS, ROUTE_MAX_K, ROUTE_SIGMOID, ROUTE_SOFTMAX, GemmRoute, gemm_int8, gemm_int8_grouped,
     gemm_quantize_int8, gemm_route, gemm_route_backward, gemm_route_combine, gemm_route_combine_backward, gemm_route_plan,
     gemm_route_plan_workspace_size,
+    gemm_embed, gemm_embed_backward, gemm_embed_backward_workspace_size, gemm_route_balance, gemm_route_balance_backward,
+    gemm_route_balance_workspace_size,
+    gemm_cross_entropy, gemm_cross_entropy_backward, gemm_cross_entropy_backward_workspace_size, gemm_cross_entropy_workspace_size,
     GemmCall, GemmError, GemmOptions, GemmProblem, gemm_bf16, gemm_bf16_grouped, gemm_bf16_grouped_noalloc, gemm_debug_descriptors,
     gemm_debug_inject_timeout, gemm_debug_stage_image, gemm_debug_int8_plan, gemm_debug_streamk_units, gemm_ex, gemm_f16, gemm_f16_grouped, gemm_fp4, gemm_fp4_scale_bytes, gemm_fp8, gemm_fp8_ex,
     gemm_grouped_ex, gemm_grouped_workspace_size, gemm_mx_scale_bytes, gemm_mxfp8, gemm_streamk_workspace_size, gemm_last_device_status, gemm_launch_count, gemm_status_string,

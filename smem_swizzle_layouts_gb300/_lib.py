@@ -108,7 +108,27 @@ _lib.gemm_int8_grouped.argtypes = [_i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, 
 _lib.gemm_route_combine.argtypes = [_i64, _i64, _int, _vp, _int, _i64, _i64, _vp, _vp, _vp, _int, _i64, _vp]
 _lib.gemm_route_combine_backward.argtypes = [_i64, _i64, _int, _vp, _int, _i64, _vp, _int, _i64, _i64, _vp, _vp, _vp,
                                              _i64, _vp, _vp]
-for _name in ("gemm_route", "gemm_route_backward", "gemm_route_plan", "gemm_quantize_int8", "gemm_int8",
+_head = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]
+_lib.gemm_cross_entropy_workspace_size.argtypes = [_i64, _i64]
+_lib.gemm_cross_entropy_workspace_size.restype = ctypes.c_size_t
+_lib.gemm_cross_entropy.argtypes = _head + [_vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.gemm_cross_entropy_backward_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
+_lib.gemm_cross_entropy_backward_workspace_size.restype = ctypes.c_size_t
+_lib.gemm_cross_entropy_backward.argtypes = _head + [_vp, _vp, _vp, _vp, _int, _i64, _vp, _int, _i64, _int, _vp,
+                                                     ctypes.c_size_t, _vp]
+_balance = [_i64, _i64, _vp, _int, _i64, _int, _route, _vp, _i64, _vp, _vp, _vp]
+_lib.gemm_route_balance_workspace_size.argtypes = [_i64, _i64, _i64]
+_lib.gemm_route_balance_workspace_size.restype = ctypes.c_size_t
+_lib.gemm_route_balance.argtypes = _balance + [_vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.gemm_route_balance_backward.argtypes = _balance + [_vp, _vp, _i64, _int, _vp]
+_lib.gemm_embed.argtypes = [_i64, _i64, _i64, _vp, _vp, _int, _i64, _f, _vp, _int, _i64, _vp]
+_lib.gemm_embed_backward_workspace_size.argtypes = [_i64, _i64, _i64]
+_lib.gemm_embed_backward_workspace_size.restype = ctypes.c_size_t
+_lib.gemm_embed_backward.argtypes = [_i64, _i64, _i64, _vp, _vp, _int, _i64, _f, _vp, _int, _i64, _int, _vp,
+                                     ctypes.c_size_t, _vp]
+for _name in ("gemm_route_balance", "gemm_route_balance_backward", "gemm_embed", "gemm_embed_backward",
+              "gemm_cross_entropy", "gemm_cross_entropy_backward",
+              "gemm_route", "gemm_route_backward", "gemm_route_plan", "gemm_quantize_int8", "gemm_int8",
               "gemm_int8_grouped", "gemm_route_combine", "gemm_route_combine_backward",
               "gemm_bf16", "gemm_f16", "gemm_ex", "gemm_fp8", "gemm_fp8_ex", "gemm_mxfp8", "gemm_fp4", "gemm_bf16_grouped",
               "gemm_f16_grouped",
@@ -123,6 +143,10 @@ EXPORTED = ("gemm_bf16", "gemm_f16", "gemm_ex", "gemm_fp8", "gemm_fp8_ex", "gemm
             "gemm_bf16_grouped", "gemm_grouped_ex",
             "gemm_route", "gemm_route_backward", "gemm_route_plan", "gemm_route_plan_workspace_size",
             "gemm_quantize_int8", "gemm_int8", "gemm_int8_grouped", "gemm_route_combine", "gemm_route_combine_backward",
+            "gemm_cross_entropy", "gemm_cross_entropy_workspace_size", "gemm_cross_entropy_backward",
+            "gemm_cross_entropy_backward_workspace_size",
+            "gemm_route_balance", "gemm_route_balance_workspace_size", "gemm_route_balance_backward",
+            "gemm_embed", "gemm_embed_backward", "gemm_embed_backward_workspace_size",
             "gemm_f16_grouped", "gemm_bf16_grouped_noalloc", "gemm_last_device_status", "gemm_status_string", "gemm_launch_count",
             "gemm_debug_descriptors", "gemm_debug_stage_image", "gemm_debug_plan", "gemm_debug_streamk_units",
             "gemm_debug_int8_plan", "gemm_debug_inject_timeout", "gemm_debug_inject_timeout_at")
@@ -431,6 +455,66 @@ def gemm_route_combine_backward(T, N, k, dD, d_type, lddd, Y, y_type, y_rows, ld
     _check(_lib.gemm_route_combine_backward(T, N, k, _addr(dD), d_type, lddd, _addr(Y), y_type, y_rows, ldy,
                                             _addr(slots), _addr(weights), _addr(dY), lddy, _addr(dweights),
                                             _stream(stream)), "gemm_route_combine_backward")
+
+
+def gemm_cross_entropy_workspace_size(T: int, V: int) -> int:
+    return int(_lib.gemm_cross_entropy_workspace_size(T, V))
+
+
+def gemm_cross_entropy(in_type, T, V, K, X, ldx, W, ldw, targets, losses, lse, workspace, workspace_bytes, stream=None):
+    """Each token's loss and normaliser under the softmax of X W^T, whose values are never kept."""
+    _check(_lib.gemm_cross_entropy(in_type, T, V, K, _addr(X), ldx, _addr(W), ldw, _addr(targets), _addr(losses), _addr(lse),
+                                   _addr(workspace), workspace_bytes, _stream(stream)), "gemm_cross_entropy")
+
+
+def gemm_cross_entropy_backward_workspace_size(T: int, V: int, K: int, columns: int = 0) -> int:
+    return int(_lib.gemm_cross_entropy_backward_workspace_size(T, V, K, columns))
+
+
+def gemm_cross_entropy_backward(in_type, T, V, K, X, ldx, W, ldw, targets, lse, dlosses, dlse, dX, dx_type, lddx, dW,
+                                dw_type, lddw, accumulate, workspace, workspace_bytes, stream=None):
+    """The gradients of the rows and of the head's weights (None: not wanted) from those of the losses and normalisers."""
+    _check(_lib.gemm_cross_entropy_backward(in_type, T, V, K, _addr(X), ldx, _addr(W), ldw, _addr(targets), _addr(lse),
+                                            _addr(dlosses), _addr(dlse), _addr(dX), dx_type, lddx, _addr(dW), dw_type,
+                                            lddw, accumulate, _addr(workspace), workspace_bytes, _stream(stream)),
+           "gemm_cross_entropy_backward")
+
+
+def gemm_route_balance_workspace_size(T: int, E: int, S: int) -> int:
+    return int(_lib.gemm_route_balance_workspace_size(T, E, S))
+
+
+def gemm_route_balance(T, E, logits, l_type, ldl, k, route, ids, S, offsets, counts, tokens, means, losses, workspace,
+                       workspace_bytes, stream=None):
+    """Counts per expert, mean scores and the balance loss of each sequence. ``route``: as for gemm_route (its score)."""
+    _check(_lib.gemm_route_balance(T, E, _addr(logits), l_type, ldl, k, _route_rule(route), _addr(ids), S, _addr(offsets),
+                                   _addr(counts), _addr(tokens), _addr(means), _addr(losses), _addr(workspace),
+                                   workspace_bytes, _stream(stream)), "gemm_route_balance")
+
+
+def gemm_route_balance_backward(T, E, logits, l_type, ldl, k, route, ids, S, offsets, counts, tokens, dlosses, dlogits, lddl,
+                                accumulate, stream=None):
+    """The gradient of the router's logits from that of the balance losses."""
+    _check(_lib.gemm_route_balance_backward(T, E, _addr(logits), l_type, ldl, k, _route_rule(route), _addr(ids), S,
+                                            _addr(offsets), _addr(counts), _addr(tokens), _addr(dlosses), _addr(dlogits),
+                                            lddl, accumulate, _stream(stream)), "gemm_route_balance_backward")
+
+
+def gemm_embed(T, N, V, ids, table, t_type, ldt, scale, D, d_type, ldd, stream=None):
+    """The table's rows that ``ids`` names, times ``scale``."""
+    _check(_lib.gemm_embed(T, N, V, _addr(ids), _addr(table), t_type, ldt, scale, _addr(D), d_type, ldd, _stream(stream)),
+           "gemm_embed")
+
+
+def gemm_embed_backward_workspace_size(T: int, N: int, V: int) -> int:
+    return int(_lib.gemm_embed_backward_workspace_size(T, N, V))
+
+
+def gemm_embed_backward(T, N, V, ids, dD, d_type, lddd, scale, dtable, t_type, lddt, accumulate, workspace, workspace_bytes,
+                        stream=None):
+    """The table's gradient: each token's rows summed in a fixed order."""
+    _check(_lib.gemm_embed_backward(T, N, V, _addr(ids), _addr(dD), d_type, lddd, scale, _addr(dtable), t_type, lddt,
+                                    accumulate, _addr(workspace), workspace_bytes, _stream(stream)), "gemm_embed_backward")
 
 
 def gemm_last_device_status(stream=None) -> tuple[int, int]:

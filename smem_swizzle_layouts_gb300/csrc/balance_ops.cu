@@ -1,0 +1,489 @@
+// The balance loss of a router and its counts per expert, with the gradient of
+// its logits. Contracts are in include/gemm_gb300.h.
+//
+//   n_e = choices of e among the n live tokens of a sequence, P_e = mean of p_te
+//   loss = E sum_e n_e / (k n) P_e
+//   c_e = dloss E n_e / (k n^2);  softmax: dl = p (c - sum p c),
+//   sigmoid scores over their sum, p = s / Z: dl = s (1 - s) / Z (c - sum p c)
+//
+// The tokens are cut into equal parts, one for each block, whatever the
+// sequences' lengths. A part and a sequence that meet have a slot of the
+// workspace, part + sequence (one of the two grows from each meeting to the
+// next), where the block leaves its counts and sums; a sequence's slots are
+// added in their order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/gemm_gb300.h"
+#include "elements.cuh"
+#include "host.h"
+
+using namespace g300;
+
+namespace {
+
+struct BalanceParams {
+    long long T, S;
+    int E, k, sigmoid;
+    long long ldl, lddl;
+    const int *ids, *offsets;
+    int *counts, *tokens;
+    float *means, *losses;
+    long long part;  // tokens of a block
+    int blocks;
+    int *slot_counts, *slot_tokens;
+    float *slot_sums;
+    long long ld_slot;
+    const float *dlosses;
+    int accumulate;
+};
+
+// The tokens of sequence s, inside 0..T.
+struct Sequence {
+    long long lo, hi;
+};
+
+__device__ __forceinline__ Sequence sequence(const BalanceParams &p, long long s)
+{
+    if (!p.offsets)
+        return {0, p.T};
+    Sequence q;
+    q.lo = min(max(static_cast<long long>(__ldcg(p.offsets + s)), 0ll), p.T);
+    q.hi = min(max(static_cast<long long>(__ldcg(p.offsets + s + 1)), q.lo), p.T);
+    return q;
+}
+
+// The last sequence that begins at token t or before it (0 if none does).
+__device__ __forceinline__ long long sequence_of(const BalanceParams &p, long long t)
+{
+    if (!p.offsets)
+        return 0;
+    long long lo = 0, hi = p.S - 1;
+    while (lo < hi) {
+        const long long mid = (lo + hi + 1) / 2;
+        if (__ldcg(p.offsets + mid) <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Scores of a token, expert lane + 32 i in v[i]: p unnormalised, and the
+// factor that normalises it.
+template <typename L, int NPL>
+__device__ __forceinline__ float scores(const L *row, int E, int lane, bool sigmoid, float (&x)[NPL], float (&v)[NPL])
+{
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane + 32 * i;
+        x[i] = e < E ? to_float(row[e]) : -INFINITY;
+    }
+    float total = 0.0f;
+    if (sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            v[i] = __frcp_rn(1.0f + expf(-x[i]));  // -inf: 1 / inf
+    } else {
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < NPL; ++i)
+            top = fmaxf(top, x[i]);
+        top = warp_max(top);
+        if (top == -INFINITY)
+            top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            v[i] = expf(x[i] - top);
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+        total += v[i];
+    total = warp_sum(total);
+    return __frcp_rn(total == 0.0f ? 1.0f : total);
+}
+
+// Warps of a block: their sums of all experts take 32 KB of shared memory.
+template <int NPL>
+constexpr int kBalanceWarps = NPL <= 8 ? 32 : NPL == 16 ? 16 : 8;
+
+// Counts, means and loss of one sequence from sums and counts in shared memory.
+__device__ void balance_finish(const BalanceParams &p, long long s, const float *sums, const int *counts, int n)
+{
+    __shared__ float warp_part[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = static_cast<int>(blockDim.x >> 5);
+    const float live = static_cast<float>(max(n, 1));
+    float loss = 0.0f;
+    for (int e = tid; e < p.E; e += blockDim.x) {
+        const float mean = __fdiv_rn(sums[e], live);
+        const int c = counts[e];
+        p.counts[s * p.E + e] = c;
+        p.means[s * p.E + e] = mean;
+        loss = fmaf(__fdiv_rn(static_cast<float>(c), static_cast<float>(p.k) * live), mean, loss);
+    }
+    loss = warp_sum(loss);
+    if (lane == 0)
+        warp_part[warp] = loss;
+    __syncthreads();
+    if (tid == 0) {
+        loss = 0.0f;
+        for (int w = 0; w < warps; ++w)
+            loss += warp_part[w];
+        p.losses[s] = static_cast<float>(p.E) * loss;
+        p.tokens[s] = n;
+    }
+    __syncthreads();
+}
+
+// One block's part of the tokens, one warp a token. With one part alone it
+// finishes the sequences itself.
+template <typename L, int NPL>
+__global__ void __launch_bounds__(32 * kBalanceWarps<NPL>) balance_kernel(const L *logits, const BalanceParams p)
+{
+    constexpr int WARPS = kBalanceWarps<NPL>;
+    __shared__ float sums[WARPS][32 * NPL];
+    __shared__ int counts[32 * NPL], tokens;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_start();
+    const long long lo = blockIdx.x * p.part, hi = min(lo + p.part, p.T);
+    for (long long s = p.blocks == 1 ? 0 : sequence_of(p, lo); s < p.S; ++s) {
+        const Sequence q = sequence(p, s);
+        if (q.lo >= hi && p.blocks > 1)
+            return;
+        const long long a = max(lo, q.lo), b = min(hi, q.hi);
+        if (a >= b && p.blocks > 1)
+            continue;
+        for (int e = tid; e < 32 * NPL; e += 32 * WARPS)
+            counts[e] = 0;
+        if (tid == 0)
+            tokens = 0;
+        __syncthreads();
+        float sum[NPL] = {};
+        int mine = 0;
+        for (long long t = a + warp; t < b; t += WARPS) {
+            int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
+            if (id >= p.E)
+                id = -1;
+            float x[NPL], v[NPL];
+            const float inv = scores<L, NPL>(logits + t * p.ldl, p.E, lane, p.sigmoid != 0, x, v);
+            if (__any_sync(0xffffffffu, id >= 0)) {
+                ++mine;
+                if (id >= 0)
+                    atomicAdd(&counts[id], 1);  // a count: the order of the additions does not show
+#pragma unroll
+                for (int i = 0; i < NPL; ++i)
+                    sum[i] = fmaf(v[i], inv, sum[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            sums[warp][lane + 32 * i] = sum[i];
+        if (lane == 0)
+            atomicAdd(&tokens, mine);
+        __syncthreads();
+        for (int e = tid; e < p.E; e += 32 * WARPS) {
+            float total = sums[0][e];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w)
+                total += sums[w][e];
+            sums[0][e] = total;
+        }
+        __syncthreads();
+        if (p.blocks == 1) {
+            balance_finish(p, s, sums[0], counts, tokens);
+        } else {
+            const long long slot = blockIdx.x + s;
+            for (int e = tid; e < p.E; e += 32 * WARPS) {
+                p.slot_sums[slot * p.ld_slot + e] = sums[0][e];
+                p.slot_counts[slot * p.ld_slot + e] = counts[e];
+            }
+            if (tid == 0)
+                p.slot_tokens[slot] = tokens;
+            __syncthreads();
+        }
+    }
+}
+
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinGroups = 32;  // at most
+
+// A sequence's slots, added by groups of threads that take every so-manieth
+// one; then the groups in their order.
+__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const BalanceParams p)
+{
+    __shared__ float sums[4 * kJoinThreads];
+    __shared__ int counts[4 * kJoinThreads], tokens;
+    const int tid = threadIdx.x;
+    const int words = static_cast<int>(p.ld_slot / 4), groups = min(kJoinThreads / words, kJoinGroups);
+    const int group = tid / words, word = tid - group * words;
+    if (tid == 0)
+        tokens = 0;
+    grid_start();
+    __syncthreads();
+    const long long s = blockIdx.x;
+    const Sequence q = sequence(p, s);
+    long long first = 0, end = 0;
+    if (q.lo < q.hi) {
+        first = q.lo / p.part + s;
+        end = (q.hi - 1) / p.part + s + 1;
+    }
+    if (group < groups) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        int4 c = make_int4(0, 0, 0, 0);
+#pragma unroll 4
+        for (long long i = first + group; i < end; i += groups) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.slot_sums + i * p.ld_slot) + word);
+            const int4 n = __ldcg(reinterpret_cast<const int4 *>(p.slot_counts + i * p.ld_slot) + word);
+            f.x += v.x;
+            f.y += v.y;
+            f.z += v.z;
+            f.w += v.w;
+            c.x += n.x;
+            c.y += n.y;
+            c.z += n.z;
+            c.w += n.w;
+        }
+        reinterpret_cast<float4 *>(sums)[tid] = f;
+        reinterpret_cast<int4 *>(counts)[tid] = c;
+    }
+    int n = 0;
+    for (long long i = first + tid; i < end; i += kJoinThreads)
+        n += __ldcg(p.slot_tokens + i);
+    if (n)
+        atomicAdd(&tokens, n);
+    __syncthreads();
+    for (int e = tid; e < p.E; e += kJoinThreads) {
+        float f = sums[e];
+        int c = counts[e];
+        for (int g = 1; g < groups; ++g) {
+            f += sums[g * p.ld_slot + e];
+            c += counts[g * p.ld_slot + e];
+        }
+        sums[e] = f;
+        counts[e] = c;
+    }
+    __syncthreads();
+    balance_finish(p, s, sums, counts, tokens);
+}
+
+constexpr int kBalanceGradWarps = 8;
+constexpr int kBalanceGradRun = 4;  // tokens of a warp, neighbours, which mostly share a sequence
+
+// One warp a token: its scores, their mean gradient, and the logits' gradients.
+template <typename L, int NPL>
+__global__ void __launch_bounds__(32 * kBalanceGradWarps) balance_backward_kernel(const L *logits, L *dlogits, const BalanceParams p)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t0 = (static_cast<long long>(blockIdx.x) * kBalanceGradWarps + warp) * kBalanceGradRun;
+    grid_start();
+    if (t0 >= p.T)
+        return;
+    long long s = -1;
+    Sequence q = {0, 0};
+    float c[NPL];
+    for (long long t = t0; t < min(t0 + kBalanceGradRun, p.T); ++t) {
+        if (s < 0 || t >= q.hi) {
+            s = sequence_of(p, t);
+            q = sequence(p, s);
+            const float n = static_cast<float>(max(__ldcg(p.tokens + s), 1));
+            const float by = __ldcg(p.dlosses + s) * static_cast<float>(p.E);
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const int e = lane + 32 * i;
+                const float count = e < p.E ? static_cast<float>(__ldcg(p.counts + s * p.E + e)) : 0.0f;
+                c[i] = __fdiv_rn(__fdiv_rn(by * count, static_cast<float>(p.k) * n), n);
+            }
+        }
+        if (t < q.lo || t >= q.hi)
+            continue;  // a token of no sequence
+        const int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
+        const bool live = __any_sync(0xffffffffu, id >= 0 && id < p.E);
+        L *out = dlogits + t * p.lddl;
+        float d[NPL];
+        if (live) {
+            float x[NPL], v[NPL];
+            const float inv = scores<L, NPL>(logits + t * p.ldl, p.E, lane, p.sigmoid != 0, x, v);
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                dot = fmaf(v[i] * inv, c[i], dot);
+            dot = warp_sum(dot);
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                d[i] = v[i] * inv * (c[i] - dot);
+                if (p.sigmoid)
+                    d[i] *= __frcp_rn(1.0f + expf(x[i]));  // 1 - s without its cancellation
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                d[i] = 0.0f;
+            if (p.accumulate)
+                continue;
+        }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            if (e < p.E)
+                out[e] = from_float<L>(p.accumulate ? to_float(out[e]) + d[i] : d[i]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr int kBalanceBlocks = 152;  // parts of the tokens at most: one for each SM of the GPU this is built for
+constexpr int kBalancePart = 32;     // tokens of a part at least
+
+struct BalancePlan {
+    int blocks;
+    int64_t part, ld;
+    size_t counts, tokens, bytes;  // offsets; the sums come first
+};
+
+BalancePlan balance_plan(int64_t T, int64_t E, int64_t S)
+{
+    BalancePlan b = {};
+    b.part = std::max<int64_t>(kBalancePart, (T + kBalanceBlocks - 1) / kBalanceBlocks);
+    b.blocks = static_cast<int>((T + b.part - 1) / b.part);
+    b.ld = (E + 3) / 4 * 4;
+    if (b.blocks <= 1)
+        return b;
+    const int64_t slots = b.blocks + S - 1;
+    const size_t one = static_cast<size_t>((slots * b.ld * 4 + 255) / 256 * 256);
+    b.counts = one;
+    b.tokens = 2 * one;
+    b.bytes = 2 * one + static_cast<size_t>((slots * 4 + 255) / 256 * 256);
+    return b;
+}
+
+// What both calls check, and the parameters that they share.
+gemm_status_t check_balance(int64_t T, int64_t E, const void *logits, int l_type, int64_t ldl, int k, const gemm_route_t *route,
+                            const int32_t *ids, int64_t S, const int32_t *offsets, BalanceParams *p)
+{
+    const int score = route ? route->score : GEMM_ROUTE_SOFTMAX;
+    if (!valid_size(T) || !valid_type(l_type) || E < 1 || E > GEMM_ROUTE_MAX_EXPERTS || k < 1 || k > GEMM_ROUTE_MAX_K || k > E ||
+        (score != GEMM_ROUTE_SOFTMAX && score != GEMM_ROUTE_SIGMOID) || S < 0 || S > kSizeLimit / E || (!offsets && S != 1))
+        return GEMM_ERR_INVALID_ARG;
+    const int es = type_bytes(l_type);
+    if (T > 0 && (!logits || !ids || ldl < E || !valid_stride(ldl, es)))
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned_to(logits, es) || !aligned_to(ids, 4) || !aligned_to(offsets, 4))
+        return GEMM_ERR_ALIGNMENT;
+    *p = BalanceParams{};
+    p->T = T;
+    p->S = S;
+    p->E = static_cast<int>(E);
+    p->k = k;
+    p->sigmoid = score == GEMM_ROUTE_SIGMOID;
+    p->ldl = ldl;
+    p->ids = ids;
+    p->offsets = offsets;
+    return GEMM_OK;
+}
+
+template <typename L, int NPL>
+gemm_status_t launch_balance(const void *logits, const BalanceParams &p, cudaStream_t st)
+{
+    return host_launch(balance_kernel<L, NPL>, static_cast<unsigned>(p.blocks), 32 * kBalanceWarps<NPL>, 0, st, 0,
+                       static_cast<const L *>(logits), p);
+}
+
+template <typename L, int NPL>
+gemm_status_t launch_balance_backward(const void *logits, void *dlogits, const BalanceParams &p, cudaStream_t st)
+{
+    const int64_t tokens = kBalanceGradWarps * kBalanceGradRun;
+    return host_launch(balance_backward_kernel<L, NPL>, static_cast<unsigned>((p.T + tokens - 1) / tokens), 32 * kBalanceGradWarps, 0, st, 0,
+                       static_cast<const L *>(logits), static_cast<L *>(dlogits), p);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- C ABI
+
+extern "C" {
+
+size_t gemm_route_balance_workspace_size(int64_t T, int64_t E, int64_t S)
+{
+    if (T < 1 || T > kSizeLimit || E < 1 || E > GEMM_ROUTE_MAX_EXPERTS || S < 1 || S > kSizeLimit / E)
+        return 0;
+    return balance_plan(T, E, S).bytes;
+}
+
+gemm_status_t gemm_route_balance(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl, int k, const gemm_route_t *route,
+                                 const int32_t *ids, int64_t S, const int32_t *offsets, int32_t *counts, int32_t *tokens, float *means,
+                                 float *losses, void *workspace, size_t workspace_bytes, gemm_stream_t stream)
+{
+    BalanceParams p;
+    gemm_status_t s = check_balance(T, E, logits, l_type, ldl, k, route, ids, S, offsets, &p);
+    if (s != GEMM_OK || S == 0)
+        return s;
+    if (!counts || !tokens || !means || !losses)
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned_to(counts, 4) || !aligned_to(tokens, 4) || !aligned_to(means, 4) || !aligned_to(losses, 4))
+        return GEMM_ERR_ALIGNMENT;
+    const BalancePlan b = balance_plan(std::max<int64_t>(T, 1), E, S);
+    if (b.bytes > 0 && (!workspace || workspace_bytes < b.bytes))
+        return GEMM_ERR_INVALID_ARG;
+    if (b.bytes > 0 && !aligned_to(workspace, 16))
+        return GEMM_ERR_ALIGNMENT;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.counts = counts;
+    p.tokens = tokens;
+    p.means = means;
+    p.losses = losses;
+    p.part = b.part;
+    p.blocks = b.blocks;
+    p.slot_sums = reinterpret_cast<float *>(ws);
+    p.slot_counts = reinterpret_cast<int *>(ws + b.counts);
+    p.slot_tokens = reinterpret_cast<int *>(ws + b.tokens);
+    p.ld_slot = b.ld;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    s = with_type(l_type, [&](auto tag) {
+        using L = decltype(tag);
+        return E <= 64    ? launch_balance<L, 2>(logits, p, st)
+               : E <= 128 ? launch_balance<L, 4>(logits, p, st)
+               : E <= 256 ? launch_balance<L, 8>(logits, p, st)
+               : E <= 512 ? launch_balance<L, 16>(logits, p, st)
+                          : launch_balance<L, 32>(logits, p, st);
+    });
+    if (s != GEMM_OK || b.blocks == 1)
+        return s;
+    return host_launch(balance_join_kernel, static_cast<unsigned>(S), kJoinThreads, 0, st, 0, p);
+}
+
+gemm_status_t gemm_route_balance_backward(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl, int k,
+                                          const gemm_route_t *route, const int32_t *ids, int64_t S, const int32_t *offsets,
+                                          const int32_t *counts, const int32_t *tokens, const float *dlosses, void *dlogits, int64_t lddl,
+                                          int accumulate, gemm_stream_t stream)
+{
+    BalanceParams p;
+    const gemm_status_t s = check_balance(T, E, logits, l_type, ldl, k, route, ids, S, offsets, &p);
+    if (s != GEMM_OK || S == 0 || T == 0)
+        return s;
+    const int es = type_bytes(l_type);
+    if (!counts || !tokens || !dlosses || !dlogits || lddl < E || !valid_stride(lddl, es))
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned_to(counts, 4) || !aligned_to(tokens, 4) || !aligned_to(dlosses, 4) || !aligned_to(dlogits, es))
+        return GEMM_ERR_ALIGNMENT;
+    p.counts = const_cast<int *>(counts);
+    p.tokens = const_cast<int *>(tokens);
+    p.dlosses = dlosses;
+    p.lddl = lddl;
+    p.accumulate = accumulate != 0;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return with_type(l_type, [&](auto tag) {
+        using L = decltype(tag);
+        return E <= 64    ? launch_balance_backward<L, 2>(logits, dlogits, p, st)
+               : E <= 128 ? launch_balance_backward<L, 4>(logits, dlogits, p, st)
+               : E <= 256 ? launch_balance_backward<L, 8>(logits, dlogits, p, st)
+               : E <= 512 ? launch_balance_backward<L, 16>(logits, dlogits, p, st)
+                          : launch_balance_backward<L, 32>(logits, dlogits, p, st);
+    });
+}
+
+}  // extern "C"
