@@ -59,28 +59,25 @@ enum : int { kEpiSoftmax = 0, kEpiLogitGrad = 1, kEpiProduct = 2 };
 
 // Offsets behind the stages: staging chunks, then barriers.
 constexpr int kHeadStageBytes = kHeadWarps * kEpiBufBytes;
-constexpr int kHeadBars = 2 * kHeadMaxStages + 4 + 2;
+constexpr int kHeadBars = 2 * kHeadMaxStages + 4 + 2 + 8;
+constexpr int kHeadHalves = 128 * 8;  // forward: a partial softmax for each row of a tile
 constexpr int kHeadTail = kHeadBars * 8 + 16;
 
-struct HeadParams {
-    int M, N, K;  // of this product: rows, columns, length of the sums
-    int tiles_m, tiles_n, units;
-    int kb_unit;  // K blocks of one unit: units = tiles * splits of K
-    int kb_part;  // K blocks that the tensor cores sum before the epilogue takes the sum (a unit's, or fewer)
-    int bn;       // columns of a tile
-    int a_rows;   // rows of A that a CTA loads (all 128, or fewer for few tokens)
-    int a_mn, b_mn, in_bf16;
-    int stages, group_m;
-    unsigned long long timeout_ns;
-    int inject;
-    unsigned int *status;
-    // softmax and its gradient: column v0 + n of the vocabulary
-    const int *targets;
-    int V, v0;
-    float2 *partials;  // [2 * tiles_n][M]: reference and sum, base 2
-    float *picked;     // the targets' logits
-    const float *lse, *dlosses, *dlse;
-    float *scale;      // {what dl is multiplied by, its inverse}
+// One product of a launch. Its units are tiles (in rasters of group_m tile
+// rows), one split of K after another.
+struct HeadJob {
+    int M, N, K;  // rows, columns, length of the sums
+    int tiles_m, tiles_n, units, group_m;
+    int kb_all, kb_unit;  // K blocks of the whole product and of a unit
+    int kb_part;          // those that the tensor cores sum before the epilogue takes the sum (a unit's, or fewer)
+    int bn;               // columns of a tile
+    int a_mn, b_mn;
+    int epi;
+    // the units are dealt out in turn to all clusters, but for the first
+    // `extra` rounds, which go to the clusters from `behind` on: those that have
+    // one unit less of the job before
+    int behind, extra;
+    int v0;  // first column of the piece of the vocabulary
     // products
     int out_type;
     int scaled;              // multiply by scale[1]
@@ -92,6 +89,29 @@ struct HeadParams {
     long long ld_raw;
     const void *c_typed;     // values of the output's type to add after it, or null
     long long ld_typed;
+};
+
+constexpr int kMaxJobs = 3;
+
+struct HeadMaps {
+    CUtensorMap a[kMaxJobs], b[kMaxJobs], d[kMaxJobs];
+};
+
+struct HeadParams {
+    HeadJob jobs[kMaxJobs];
+    int num_jobs;
+    int a_rows, b_rows;  // rows of the operands' places in a stage
+    int in_bf16, stages;
+    unsigned long long timeout_ns;
+    int inject;
+    unsigned int *status;
+    // softmax and its gradient
+    const int *targets;
+    int T, V;
+    float2 *partials;  // [tiles_n][T]: reference and sum, base 2
+    float *picked;     // the targets' logits
+    const float *lse, *dlosses, *dlse;
+    float *scale;      // {what dl is multiplied by, its inverse}
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -106,62 +126,97 @@ template <int CG>
 constexpr int kHeadBK = CG == 2 ? 128 : 64;
 
 struct HeadUnit {
+    int job;
     int m_blk, n_blk, split, kb0, kb1;
 };
 
-// Units in rasters of group_m tile rows (as decode_tile), one split of K after another.
-__device__ __forceinline__ HeadUnit head_unit(int tiles_m, int tiles_n, int group_m, int kb_unit, int kb_all, int u)
-{
-    HeadUnit h;
-    const int tiles = tiles_m * tiles_n;
-    h.split = u / tiles;
-    const int local = u - h.split * tiles;
-    const int per_group = group_m * tiles_n;
-    const int g = local / per_group;
-    const int rows = min(tiles_m - g * group_m, group_m);
-    const int r = local - g * per_group;
-    h.m_blk = g * group_m + r % rows;
-    h.n_blk = r / rows;
-    h.kb0 = h.split * kb_unit;
-    h.kb1 = min(kb_all, h.kb0 + kb_unit);
-    return h;
-}
+// A cluster's units, job after job: every role of both CTAs walks the same.
+struct HeadUnits {
+    const HeadParams &p;
+    int c, G;
+    int job = 0, round = 0;
+
+    __device__ __forceinline__ HeadUnits(const HeadParams &params, int cluster, int clusters) : p(params), c(cluster), G(clusters) {}
+
+    __device__ __forceinline__ bool next(HeadUnit &h)
+    {
+        while (job < p.num_jobs) {
+            const HeadJob &j = p.jobs[job];
+            const int late = G - j.behind;  // clusters that are behind
+            int u = -1;
+            if (round < j.extra) {
+                if (c >= j.behind)
+                    u = round * late + c - j.behind;
+                else
+                    round = j.extra;
+            }
+            if (u < 0)
+                u = j.extra * late + (round - j.extra) * G + c;
+            ++round;
+            if (u >= j.units) {
+                if (round <= j.extra) {
+                    round = j.extra;
+                    continue;
+                }
+                ++job;
+                round = 0;
+                continue;
+            }
+            h.job = job;
+            const int tiles = j.tiles_m * j.tiles_n;
+            h.split = u / tiles;
+            const int local = u - h.split * tiles;
+            const int per_group = j.group_m * j.tiles_n;
+            const int g = local / per_group;
+            const int rows = min(j.tiles_m - g * j.group_m, j.group_m);
+            const int r = local - g * per_group;
+            h.m_blk = g * j.group_m + r % rows;
+            h.n_blk = r / rows;
+            h.kb0 = h.split * j.kb_unit;
+            h.kb1 = min(j.kb_all, h.kb0 + j.kb_unit);
+            return true;
+        }
+        return false;
+    }
+};
 
 template <int CG>
-__device__ ProducerTail head_producer(const HeadParams &p, const CUtensorMap *tmA, const CUtensorMap *tmB, uint32_t smem,
-                                      uint32_t bar_full, uint32_t bar_empty, uint32_t bar_inject, uint32_t rank, const Waiter &w)
+__device__ ProducerTail head_producer(const HeadParams &p, const HeadMaps &maps, uint32_t smem, uint32_t bar_full, uint32_t bar_empty,
+                                      uint32_t bar_inject, uint32_t rank, const Waiter &w)
 {
     constexpr int BK = kHeadBK<CG>;
     if (p.inject == kRoleProducer) {
         w.wait(bar_inject, 0u, kRoleProducer | kWaitInjected);
         return ProducerTail{0, 0, 0u};
     }
-    const int tiles_m = p.tiles_m, tiles_n = p.tiles_n, units = p.units, group_m = p.group_m, kb_unit = p.kb_unit;
-    const int bn = p.bn, stages = p.stages, kb_all = ceil_div_i(p.K, BK);
-    const OperandBoxes box_a = operand_boxes(p.a_mn, 3, p.a_rows, BK, 2);
-    const OperandBoxes box_b = operand_boxes(p.b_mn, 3, bn / CG, BK, 2);
-    const uint32_t a_bytes = static_cast<uint32_t>(p.a_rows) * BK * 2, b_bytes = static_cast<uint32_t>(bn / CG) * BK * 2;
-    const int nbox = max(box_a.nbox, box_b.nbox);
+    const int stages = p.stages, a_rows = p.a_rows;
+    const uint32_t a_bytes = static_cast<uint32_t>(a_rows) * BK * 2, stage_bytes = a_bytes + static_cast<uint32_t>(p.b_rows) * BK * 2;
     const uint32_t full_target = CG == 2 ? mapa_shared(bar_full, 0) : bar_full;
-    const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
     int stage = 0, issued = 0;
     uint32_t phase = 0;
-    for (int u = cluster; u < units; u += clusters) {
-        const HeadUnit h = head_unit(tiles_m, tiles_n, group_m, kb_unit, kb_all, u);
+    HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
+    HeadUnit h;
+    while (units.next(h)) {
+        const HeadJob &j = p.jobs[h.job];
+        const CUtensorMap *const map_a = &maps.a[h.job], *const map_b = &maps.b[h.job];
+        const int b_cols = j.bn / CG;
+        const OperandBoxes box_a = operand_boxes(j.a_mn, 3, a_rows, BK, 2), box_b = operand_boxes(j.b_mn, 3, b_cols, BK, 2);
+        const uint32_t tx = CG * (a_bytes + static_cast<uint32_t>(b_cols) * BK * 2);
+        const int nbox = max(box_a.nbox, box_b.nbox);
         const int m0 = (h.m_blk * CG + static_cast<int>(rank)) * 128;
-        const int n0 = h.n_blk * bn + (bn / CG) * static_cast<int>(rank);
+        const int n0 = h.n_blk * j.bn + b_cols * static_cast<int>(rank);
         for (int kb = h.kb0; kb < h.kb1; ++kb) {
             if (!w.wait(bar_empty + 8 * stage, phase ^ 1u, kRoleProducer | kWaitEmpty, rank != 0))
                 return ProducerTail{min(issued, stages), stage, phase};
             if (rank == 0)
-                mbar_arrive_expect_tx(bar_full + 8 * stage, CG * (a_bytes + b_bytes));
-            const uint32_t sa = smem + static_cast<uint32_t>(stage) * (a_bytes + b_bytes);
+                mbar_arrive_expect_tx(bar_full + 8 * stage, tx);
+            const uint32_t sa = smem + static_cast<uint32_t>(stage) * stage_bytes;
             const uint32_t fb = full_target + 8 * stage;
             for (int b = 0; b < nbox; ++b) {
                 if (b < box_a.nbox)
-                    issue_box<CG>(tmA, sa, fb, box_a, b, m0, kb * BK);
+                    issue_box<CG>(map_a, sa, fb, box_a, b, m0, kb * BK);
                 if (b < box_b.nbox)
-                    issue_box<CG>(tmB, sa + a_bytes, fb, box_b, b, n0, kb * BK);
+                    issue_box<CG>(map_b, sa + a_bytes, fb, box_b, b, n0, kb * BK);
             }
             ++issued;
             if (++stage == stages) {
@@ -182,24 +237,25 @@ __device__ void head_mma(const HeadParams &p, uint32_t smem, uint32_t bar_full, 
         w.wait(bar_inject, 0u, kRoleMma | kWaitInjected);
         return;
     }
-    const int tiles_m = p.tiles_m, tiles_n = p.tiles_n, units = p.units, group_m = p.group_m, kb_unit = p.kb_unit;
-    const int bn = p.bn, stages = p.stages, kb_part = p.kb_part, kb_all = ceil_div_i(p.K, BK);
-    const uint32_t idesc = make_idesc_f16(128 * CG, bn, p.in_bf16, p.a_mn, p.b_mn);
-    const OperandPacking pa = operand_packing(p.a_mn, 3, p.a_rows, BK), pb = operand_packing(p.b_mn, 3, bn / CG, BK);
-    const uint32_t a_bytes = static_cast<uint32_t>(p.a_rows) * BK * 2, b_bytes = static_cast<uint32_t>(bn / CG) * BK * 2;
-    const uint64_t a_desc0 = make_smem_desc(smem, pa.lbo, pa.sbo, pa.swz);
-    const uint64_t b_desc0 = make_smem_desc(smem + a_bytes, pb.lbo, pb.sbo, pb.swz);
-    uint32_t a_off[SLICES], b_off[SLICES];
-#pragma unroll
-    for (int j = 0; j < SLICES; ++j) {
-        a_off[j] = slice_byte_offset(p.a_mn, 3, p.a_rows, j) >> 4;
-        b_off[j] = slice_byte_offset(p.b_mn, 3, bn / CG, j) >> 4;
-    }
-    const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+    const int stages = p.stages, a_rows = p.a_rows;
+    const uint32_t a_bytes = static_cast<uint32_t>(a_rows) * BK * 2, stage_bytes = a_bytes + static_cast<uint32_t>(p.b_rows) * BK * 2;
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
-    for (int u = cluster; u < units; u += clusters) {
-        const HeadUnit h = head_unit(tiles_m, tiles_n, group_m, kb_unit, kb_all, u);
+    HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
+    HeadUnit h;
+    while (units.next(h)) {
+        const HeadJob &j = p.jobs[h.job];
+        const int b_cols = j.bn / CG, kb_part = j.kb_part;
+        const uint32_t idesc = make_idesc_f16(128 * CG, j.bn, p.in_bf16, j.a_mn, j.b_mn);
+        const OperandPacking pa = operand_packing(j.a_mn, 3, a_rows, BK), pb = operand_packing(j.b_mn, 3, b_cols, BK);
+        const uint64_t a_desc0 = make_smem_desc(smem, pa.lbo, pa.sbo, pa.swz);
+        const uint64_t b_desc0 = make_smem_desc(smem + a_bytes, pb.lbo, pb.sbo, pb.swz);
+        uint32_t a_off[SLICES], b_off[SLICES];
+#pragma unroll
+        for (int i = 0; i < SLICES; ++i) {
+            a_off[i] = slice_byte_offset(j.a_mn, 3, a_rows, i) >> 4;
+            b_off[i] = slice_byte_offset(j.b_mn, 3, b_cols, i) >> 4;
+        }
         for (int part = h.kb0; part < h.kb1; part += kb_part) {
             if (!w.wait(bar_acc_empty + 8 * acc, acc_phase ^ 1u, kRoleMma | kWaitAccEmpty, CG == 2))
                 return;
@@ -210,10 +266,10 @@ __device__ void head_mma(const HeadParams &p, uint32_t smem, uint32_t bar_full, 
                 if (!mbar_try_wait(bar_full + 8 * stage, phase) && !w.wait(bar_full + 8 * stage, phase, kRoleMma | kWaitFull))
                     return;
                 tc_fence_after_sync();
-                const uint64_t at = (static_cast<uint32_t>(stage) * (a_bytes + b_bytes)) >> 4;
+                const uint64_t at = (static_cast<uint32_t>(stage) * stage_bytes) >> 4;
 #pragma unroll
-                for (int j = 0; j < SLICES; ++j)
-                    mma_f16<CG>(d, a_desc0 + at + a_off[j], b_desc0 + at + b_off[j], idesc, ((kb - part) | j) != 0);
+                for (int i = 0; i < SLICES; ++i)
+                    mma_f16<CG>(d, a_desc0 + at + a_off[i], b_desc0 + at + b_off[i], idesc, ((kb - part) | i) != 0);
                 if constexpr (CG == 2)
                     mma_commit_pair_multicast(bar_empty + 8 * stage);
                 else
@@ -285,6 +341,18 @@ struct RunningSoftmax {
         s = s * ex2(r - ref) + ((t[0] + t[1]) + (t[2] + t[3]));
         r = top == INFINITY ? 0.0f : top;
     }
+
+    // Another part of the row. A sum of 0 or infinity stays what it is whatever
+    // its reference.
+    __device__ __forceinline__ void join(float2 o)
+    {
+        const float top = fmaxf(r, o.x);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        const float a = r == ref || s == 0.0f || s == INFINITY ? s : s * ex2(r - ref);
+        const float b = o.x == ref || o.y == 0.0f || o.y == INFINITY ? o.y : o.y * ex2(o.x - ref);
+        r = top;
+        s = a + b;
+    }
 };
 
 // The value of `v` at place `at`, where that is one of its 32.
@@ -304,10 +372,10 @@ struct RowGrad {
     bool live = false;
 };
 
-__device__ __forceinline__ RowGrad row_grad(const HeadParams &p, int row)
+__device__ __forceinline__ RowGrad row_grad(const HeadParams &p, int row, int v0)
 {
     RowGrad g;
-    if (row < p.M) {
+    if (row < p.T) {
         const int y = __ldcg(p.targets + row);
         g.live = static_cast<unsigned>(y) < static_cast<unsigned>(p.V);
         if (g.live) {
@@ -315,7 +383,7 @@ __device__ __forceinline__ RowGrad row_grad(const HeadParams &p, int row)
             g.a = (d + z) * by;
             g.b = d * by;
             g.lse2 = __ldcg(p.lse + row) * kLog2e;
-            g.target = y - p.v0;
+            g.target = y - v0;
         }
     }
     return g;
@@ -401,190 +469,255 @@ __device__ __forceinline__ void store_tail(const uint32_t (&o)[32], void *row, i
     }
 }
 
-// A chunk in the output's type.
+// Columns 32 i .. +31 of a chunk in the output's type.
 template <int CW>
-__device__ __forceinline__ void pack_chunk(const float (&v)[CW], int out_type, uint32_t (&o)[32])
+__device__ __forceinline__ void pack32(const float (&v)[32], int i, int out_type, uint32_t (&o)[32])
 {
     if constexpr (CW == 32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            o[i] = __float_as_uint(v[i]);
+        for (int k = 0; k < 32; ++k)
+            o[k] = __float_as_uint(v[k]);
     } else {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
             uint32_t four[4];
             pack_out(v + 8 * u, out_type, four);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[4 * u + i] = four[i];
+            for (int k = 0; k < 4; ++k)
+                o[16 * i + 4 * u + k] = four[k];
         }
     }
 }
 
-template <int CG, int EPI, int CW>
-__device__ void head_epilogue(const HeadParams &p, const CUtensorMap *tmD, uint32_t sbuf, uint32_t bar_acc_full,
-                              uint32_t bar_acc_empty, uint32_t tmem, uint32_t rank, int warp, int lane, const Waiter &w)
-{
-    constexpr int BK = kHeadBK<CG>;
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const int tiles_m = p.tiles_m, tiles_n = p.tiles_n, units = p.units, group_m = p.group_m, kb_unit = p.kb_unit;
-    const int M = p.M, N = p.N, bn = p.bn, kb_all = ceil_div_i(p.K, BK);
-    const uint32_t acc_empty_target = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
-    const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+// An epilogue warp's view of the accumulators: waits for the next one and hands
+// it back. Warp w has TMEM lanes 32 (w mod 4) .. +31 and half of the columns.
+template <int CG>
+struct Accumulators {
+    uint32_t bar_full, bar_empty, tmem;  // bar_empty: the even CTA's
     int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int u = cluster; u < units; u += clusters) {
-        const HeadUnit h = head_unit(tiles_m, tiles_n, group_m, kb_unit, kb_all, u);
-        const int m0 = (h.m_blk * CG + static_cast<int>(rank)) * 128 + 32 * q;
-        const int row = m0 + lane;
-        const int n0 = h.n_blk * bn, cols = min(bn, N - n0);
-        RowGrad g;
-        int y = -1;
-        if constexpr (EPI == kEpiLogitGrad)
-            g = row_grad(p, row);
-        if constexpr (EPI == kEpiSoftmax)
-            y = row < M ? __ldcg(p.targets + row) - n0 : -1;
-        // waits for an accumulator, and hands it back
-        auto take = [&]() {
-            const bool ok = w.wait(bar_acc_full + 8 * acc, acc_phase, kRoleEpilogue | kWaitAccFull, rank != 0);
-            tc_fence_after_sync();
-            return __all_sync(0xffffffffu, ok) != 0;
-        };
-        auto release = [&]() {
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 2)
-                    mbar_arrive_cluster(acc_empty_target + 8 * acc);
-                else
-                    mbar_arrive(bar_acc_empty + 8 * acc);
-            }
-            acc ^= 1;
-            acc_phase ^= acc == 0 ? 1u : 0u;
-        };
-        auto columns = [&](int c) {
-            return tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc * kAccStride + c);
-        };
-        const bool rows = m0 < M;  // the same for the whole warp
-        if constexpr (EPI == kEpiSoftmax) {
-            // the parts of the sums over K, added up in registers with fp32 rounding
-            float v[4][32] = {};
-            for (int part = h.kb0; part < h.kb1; part += p.kb_part) {
-                if (!take())
-                    return;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (rows && 32 * half + 64 * j < cols) {
-                        add_acc16(columns(32 * half + 64 * j), v[j]);
-                        add_acc16(columns(32 * half + 64 * j + 16), v[j] + 16);
-                    }
-                }
-                release();
-            }
-            RunningSoftmax sm;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = 32 * half + 64 * j;
-                if (rows && c < cols) {
-                    if (c + 32 > cols) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[j][i] = c + i < cols ? v[j][i] : -INFINITY;
-                    }
-                    sm.add(v[j]);
-                    const bool mine = y >= c && y < min(c + 32, cols);
-                    if (__any_sync(0xffffffffu, mine)) {
-                        const float x = pick32(v[j], y - c);
-                        if (mine)
-                            p.picked[row] = x;
-                    }
-                }
-            }
-            if (row < M)
-                p.partials[static_cast<long long>(2 * h.n_blk + half) * M + row] = make_float2(sm.r, sm.s);
-        } else {
-            if (!take())
-                return;
-            if (rows) {
-                for (int c = CW * half; c < cols; c += 2 * CW) {
-                    float v[CW];
-                    const int col = n0 + c;
-                    if constexpr (EPI == kEpiLogitGrad) {
-#pragma unroll
-                        for (int j = 0; j < CW / 32; ++j) {
-                            float x[32];
-                            load_acc32(columns(c + 32 * j), x);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[32 * j + i] = g.live ? ex2(fmaf(x[i], kLog2e, -g.lse2)) * g.a : 0.0f;
-                        }
-                        const bool mine = g.target >= col && g.target < col + CW;
-                        if (__any_sync(0xffffffffu, mine)) {
-#pragma unroll
-                            for (int i = 0; i < CW; ++i)
-                                v[i] -= mine && g.target == col + i ? g.b : 0.0f;
-                        }
-                        uint32_t o[32];
-                        pack_chunk<CW>(v, p.in_bf16 ? 1 : 2, o);
-                        stage_and_store<CW>(o, sbuf, lane, tmD, col, m0, 0);
-                    } else {
-                        const float by = p.scaled ? __ldcg(p.scale + 1) : 1.0f;
-#pragma unroll
-                        for (int j = 0; j < CW / 32; ++j) {
-                            float x[32];
-                            uint32_t raw[32];
-                            if (p.c_raw)
-                                load_row<float, 32>(p.c_raw + (h.split * p.slot_rows + row) * p.ld_raw, col + 32 * j, N, row < M, raw);
-                            __syncwarp();
-                            load_acc32(columns(c + 32 * j), x);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[32 * j + i] = (p.c_raw ? x[i] + __uint_as_float(raw[i]) : x[i]) * by;
-                        }
-                        if (p.c_typed) {
-                            uint32_t old[32];
-                            if constexpr (CW == 32) {
-                                load_row<float, 32>(static_cast<const float *>(p.c_typed) + row * p.ld_typed, col, N, row < M, old);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    v[i] += __uint_as_float(old[i]);
-                            } else {
-                                load_row<__half, 64>(static_cast<const __half *>(p.c_typed) + row * p.ld_typed, col, N, row < M, old);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    const uint32_t four[4] = {old[4 * k], old[4 * k + 1], old[4 * k + 2], old[4 * k + 3]};
-                                    float f[8];
-                                    unpack_in(four, p.out_type, f);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        v[8 * k + i] += f[i];
-                                }
-                            }
-                        }
-                        uint32_t o[32];
-                        pack_chunk<CW>(v, p.out_type, o);
-                        if (col < p.whole)
-                            stage_and_store<CW>(o, sbuf, lane, tmD, col, m0, h.split);
-                        if (col + CW > p.whole && p.whole < N && row < M)
-                            store_tail<CW>(o, static_cast<char *>(p.d) + row * p.ldd * (CW == 32 ? 4 : 2), col, p.whole, N);
-                    }
-                }
-            }
-            release();
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ bool take(const Waiter &w, uint32_t rank)
+    {
+        const bool ok = w.wait(bar_full + 8 * acc, phase, kRoleEpilogue | kWaitAccFull, rank != 0);
+        tc_fence_after_sync();
+        return __all_sync(0xffffffffu, ok) != 0;
+    }
+
+    __device__ __forceinline__ void release(int lane)
+    {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+            if constexpr (CG == 2)
+                mbar_arrive_cluster(bar_empty + 8 * acc);
+            else
+                mbar_arrive(bar_empty + 8 * acc);
         }
+        acc ^= 1;
+        phase ^= acc == 0 ? 1u : 0u;
     }
-    if constexpr (EPI != kEpiSoftmax) {
-        if (lane == 0)
-            bulk_wait_group<0>();
+
+    __device__ __forceinline__ uint32_t columns(int q, int c) const
+    {
+        return tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc * kAccStride + c);
     }
+};
+
+// Forward: each tile's partial softmax. The two warps that share a row join
+// theirs through shared memory.
+template <int CG>
+__device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t bar_halves, Accumulators<CG> a, uint32_t rank, int warp, int lane,
+                                 const Waiter &w)
+{
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    float2 *const slot = halves + 32 * q + lane;
+    const uint32_t bar_ready = bar_halves + 16 * q, bar_free = bar_ready + 8;
+    uint32_t phase = 0;
+    HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
+    HeadUnit h;
+    while (units.next(h)) {
+        const HeadJob &j = p.jobs[0];
+        const int m0 = (h.m_blk * CG + static_cast<int>(rank)) * 128 + 32 * q, row = m0 + lane;
+        const int n0 = h.n_blk * j.bn, cols = min(j.bn, j.N - n0);
+        const int y = row < p.T ? __ldcg(p.targets + row) - n0 : -1;
+        const bool rows = m0 < p.T;  // the same for both warps
+        // the parts of the sums over K, added up in registers with fp32 rounding
+        float v[4][32] = {};
+        for (int part = h.kb0; part < h.kb1; part += j.kb_part) {
+            if (!a.take(w, rank))
+                return;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (rows && 32 * half + 64 * i < cols) {
+                    add_acc16(a.columns(q, 32 * half + 64 * i), v[i]);
+                    add_acc16(a.columns(q, 32 * half + 64 * i + 16), v[i] + 16);
+                }
+            }
+            a.release(lane);
+        }
+        if (!rows)
+            continue;
+        RunningSoftmax sm;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = 32 * half + 64 * i;
+            if (c < cols) {
+                if (c + 32 > cols) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        v[i][k] = c + k < cols ? v[i][k] : -INFINITY;
+                }
+                sm.add(v[i]);
+                const bool mine = y >= c && y < min(c + 32, cols);
+                if (__any_sync(0xffffffffu, mine)) {
+                    const float x = pick32(v[i], y - c);
+                    if (mine)
+                        p.picked[row] = x;
+                }
+            }
+        }
+        if (half == 1) {
+            if (!__all_sync(0xffffffffu, w.wait(bar_free, phase ^ 1u, kRoleEpilogue | kWaitPartial)))
+                return;
+            *slot = make_float2(sm.r, sm.s);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_ready);
+        } else {
+            if (!__all_sync(0xffffffffu, w.wait(bar_ready, phase, kRoleEpilogue | kWaitPartial)))
+                return;
+            sm.join(*slot);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_free);
+            if (row < p.T)
+                p.partials[static_cast<long long>(h.n_blk) * p.T + row] = make_float2(sm.r, sm.s);
+        }
+        phase ^= 1u;
+    }
+}
+
+// One tile of dl.
+template <int CG>
+__device__ __forceinline__ void logit_grad_tile(const HeadParams &p, const HeadJob &j, const CUtensorMap *map, const RowGrad &g,
+                                                const Accumulators<CG> &a, int q, int half, int m0, int n0, int cols, uint32_t sbuf, int lane)
+{
+    for (int c = 64 * half; c < cols; c += 128) {
+        uint32_t o[32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float v[32];
+            load_acc32(a.columns(q, c + 32 * i), v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                v[k] = g.live ? ex2(fmaf(v[k], kLog2e, -g.lse2)) * g.a : 0.0f;
+            const int at = g.target - (n0 + c + 32 * i);
+            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    v[k] -= at == k ? g.b : 0.0f;
+            }
+            pack32<64>(v, i, p.in_bf16 ? 1 : 2, o);
+        }
+        stage_and_store<64>(o, sbuf, lane, map, n0 + c, m0, 0);
+    }
+}
+
+// One tile of a gradient, in chunks of 32 (fp32) or 64 columns.
+template <int CG, int CW>
+__device__ __forceinline__ void product_tile(const HeadParams &p, const HeadJob &j, const CUtensorMap *map, const Accumulators<CG> &a, int q,
+                                             int half, int m0, int n0, int cols, int split, uint32_t sbuf, int lane)
+{
+    const int row = m0 + lane;
+    const bool have = row < j.M;
+    const float by = j.scaled ? __ldcg(p.scale + 1) : 1.0f;
+    for (int c = CW * half; c < cols; c += 2 * CW) {
+        uint32_t o[32];
+        const int col = n0 + c;
+#pragma unroll
+        for (int i = 0; i < CW / 32; ++i) {
+            float v[32];
+            uint32_t old[32];
+            const int at = col + 32 * i;
+            if (j.c_raw)
+                load_row<float, 32>(j.c_raw + (split * j.slot_rows + row) * j.ld_raw, at, j.N, have, old);
+            __syncwarp();
+            load_acc32(a.columns(q, c + 32 * i), v);
+            if (j.c_raw) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    v[k] += __uint_as_float(old[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                v[k] *= by;
+            if (j.c_typed) {
+                if constexpr (CW == 32) {
+                    load_row<float, 32>(static_cast<const float *>(j.c_typed) + row * j.ld_typed, at, j.N, have, old);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        v[k] += __uint_as_float(old[k]);
+                } else {
+                    uint32_t two[16];
+                    load_row<__half, 32>(static_cast<const __half *>(j.c_typed) + row * j.ld_typed, at, j.N, have, two);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t four[4] = {two[4 * u], two[4 * u + 1], two[4 * u + 2], two[4 * u + 3]};
+                        float f[8];
+                        unpack_in(four, j.out_type, f);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[8 * u + k] += f[k];
+                    }
+                }
+            }
+            pack32<CW>(v, i, j.out_type, o);
+        }
+        if (col < j.whole)
+            stage_and_store<CW>(o, sbuf, lane, map, col, m0, split);
+        if (col + CW > j.whole && j.whole < j.N && have)
+            store_tail<CW>(o, static_cast<char *>(j.d) + row * j.ldd * (CW == 32 ? 4 : 2), col, j.whole, j.N);
+    }
+}
+
+// Backward: tiles of dl, dX and dW.
+template <int CG>
+__device__ void gradient_epilogue(const HeadParams &p, const HeadMaps &maps, uint32_t sbuf, Accumulators<CG> a, uint32_t rank, int warp,
+                                  int lane, const Waiter &w)
+{
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
+    HeadUnit h;
+    while (units.next(h)) {
+        const HeadJob &j = p.jobs[h.job];
+        const CUtensorMap *const map = &maps.d[h.job];
+        const int m0 = (h.m_blk * CG + static_cast<int>(rank)) * 128 + 32 * q;
+        const int n0 = h.n_blk * j.bn, cols = min(j.bn, j.N - n0);
+        const bool of_logits = j.epi == kEpiLogitGrad;
+        RowGrad g;
+        if (of_logits)
+            g = row_grad(p, m0 + lane, j.v0);
+        if (!a.take(w, rank))
+            return;
+        if (m0 < j.M) {  // the same for the whole warp
+            if (of_logits)
+                logit_grad_tile<CG>(p, j, map, g, a, q, half, m0, n0, cols, sbuf, lane);
+            else if (j.out_type == 0)
+                product_tile<CG, 32>(p, j, map, a, q, half, m0, n0, cols, h.split, sbuf, lane);
+            else
+                product_tile<CG, 64>(p, j, map, a, q, half, m0, n0, cols, h.split, sbuf, lane);
+        }
+        a.release(lane);
+    }
+    if (lane == 0)
+        bulk_wait_group<0>();
 }
 
 // ---------------------------------------------------------------- kernel
 
-template <int CG, int EPI>
-__global__ void __launch_bounds__(kHeadThreads, 1)
-    head_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const __grid_constant__ CUtensorMap tmD, const __grid_constant__ HeadParams p)
+template <int CG, bool FORWARD>
+__global__ void __launch_bounds__(kHeadThreads, 1) head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -593,13 +726,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
     const uint32_t rank = CG == 2 ? cluster_ctarank() & 1u : 0u;
     const int stages = p.stages;
-    const uint32_t stage_bytes = static_cast<uint32_t>(p.a_rows + p.bn / CG) * kHeadBK<CG> * 2;
-    const uint32_t staging = base + static_cast<uint32_t>(stages) * stage_bytes;
-    const uint32_t bars = staging + (EPI == kEpiSoftmax ? 0 : kHeadStageBytes);
+    const uint32_t staging = base + static_cast<uint32_t>(stages) * static_cast<uint32_t>(p.a_rows + p.b_rows) * kHeadBK<CG> * 2;
+    const uint32_t bars = staging + (FORWARD ? kHeadHalves : kHeadStageBytes);
     const uint32_t bar_full = bars, bar_empty = bar_full + 8 * kHeadMaxStages;
     const uint32_t bar_acc_full = bar_empty + 8 * kHeadMaxStages, bar_acc_empty = bar_acc_full + 16;
     const uint32_t bar_drain = bar_acc_empty + 16, bar_inject = bar_drain + 8;
-    const uint32_t misc = bar_inject + 8;
+    const uint32_t bar_halves = bar_inject + 8, misc = bar_halves + 64;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + (misc - base));
     volatile uint32_t *abort_flag = tmem_slot + 1;
     if (threadIdx.x == 0) {
@@ -613,12 +745,16 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         }
         mbar_init(bar_drain, 1);
         mbar_init(bar_inject, 1);
+        for (int i = 0; i < 8; ++i)
+            mbar_init(bar_halves + 8 * i, 1);
         *abort_flag = 0u;
         fence_mbar_init();
-        prefetch_tensormap(&tmA);
-        prefetch_tensormap(&tmB);
-        if constexpr (EPI != kEpiSoftmax)
-            prefetch_tensormap(&tmD);
+        for (int j = 0; j < p.num_jobs; ++j) {
+            prefetch_tensormap(&maps.a[j]);
+            prefetch_tensormap(&maps.b[j]);
+            if constexpr (!FORWARD)
+                prefetch_tensormap(&maps.d[j]);
+        }
     }
     if (warp == 1) {
         tmem_alloc<CG>(smem_u32(tmem_slot), 2 * kAccStride);
@@ -642,7 +778,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         if (lane == 0) {
             // what kernels before this one wrote by ordinary stores is read by TMA
             asm volatile("fence.proxy.async;" ::: "memory");
-            tail = head_producer<CG>(p, &tmA, &tmB, base, bar_full, bar_empty, bar_inject, rank, w);
+            tail = head_producer<CG>(p, maps, base, bar_full, bar_empty, bar_inject, rank, w);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
@@ -651,15 +787,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
             w.drain(bar_drain, 0u, 100000000ull);
         }
     } else {
-        const uint32_t sbuf = staging + static_cast<uint32_t>((warp - 2) * kEpiBufBytes);
-        if constexpr (EPI == kEpiProduct) {
-            if (p.out_type == 0)
-                head_epilogue<CG, EPI, 32>(p, &tmD, sbuf, bar_acc_full, bar_acc_empty, tmem, rank, warp, lane, w);
-            else
-                head_epilogue<CG, EPI, 64>(p, &tmD, sbuf, bar_acc_full, bar_acc_empty, tmem, rank, warp, lane, w);
-        } else {
-            head_epilogue<CG, EPI, 64>(p, &tmD, sbuf, bar_acc_full, bar_acc_empty, tmem, rank, warp, lane, w);
-        }
+        const Accumulators<CG> a{bar_acc_full, CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty, tmem};
+        if constexpr (FORWARD)
+            softmax_epilogue<CG>(p, reinterpret_cast<float2 *>(smem + (staging - base)), bar_halves, a, rank, warp, lane, w);
+        else
+            gradient_epilogue<CG>(p, maps, staging + static_cast<uint32_t>((warp - 2) * kEpiBufBytes), a, rank, warp, lane, w);
     }
     __syncwarp();
     __syncthreads();  // every role has returned: the abort flag is final
@@ -692,54 +824,54 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
 
 // ---------------------------------------------------------------- around the products
 
-// The normaliser and loss of each token from its partial softmaxes. ROWS 32: a
-// block has 32 tokens, its warps every eighth partial; ROWS 1: a block has one
-// token, its threads the partials. r is a maximum over the partials, so that
-// the sum is in range; the loss is taken in base 2, where the target's logit
-// cancels against r before anything is rounded.
+// The normaliser and loss of each token from its partial softmaxes: a block has
+// ROWS tokens (32, or 1 where tokens are few), its warps share the partials. r
+// is a maximum over the partials, so that the sum is in range; the loss is taken
+// in base 2, where the target's logit cancels against r before anything is
+// rounded.
+constexpr int kCombineWarps = 16;
+
 template <int ROWS>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kCombineWarps)
     head_combine_kernel(const float2 *partials, int parts, long long T, const int *targets, int V, float *losses, float *lse)
 {
-    __shared__ float2 part[8][32];
+    __shared__ float2 part[kCombineWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row = ROWS == 32 ? blockIdx.x * 32ll + lane : static_cast<long long>(blockIdx.x);
-    const int first = ROWS == 32 ? warp : static_cast<int>(threadIdx.x), step = ROWS == 32 ? 8 : 256;
+    const int first = ROWS == 32 ? warp : static_cast<int>(threadIdx.x), step = ROWS == 32 ? kCombineWarps : 32 * kCombineWarps;
     grid_start();
-    float r = -INFINITY, s = 0.0f;
-    auto join = [&](float2 o) {
-        const float top = fmaxf(r, o.x);
-        const float ref = top == -INFINITY ? 0.0f : top;
-        // a sum of 0 or infinity stays what it is whatever its reference
-        const float a = r == ref || s == 0.0f || s == INFINITY ? s : s * ex2(r - ref);
-        const float b = o.x == ref || o.y == 0.0f || o.y == INFINITY ? o.y : o.y * ex2(o.x - ref);
-        r = top;
-        s = a + b;
-    };
+    RunningSoftmax sm;
     if (row < T) {
-#pragma unroll 8
-        for (int i = first; i < parts; i += step)
-            join(__ldcg(partials + i * T + row));
+        for (int i = first; i < parts; i += 8 * step) {
+            float2 o[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                o[u] = i + u * step < parts ? __ldcg(partials + (i + u * step) * T + row) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                sm.join(o[u]);
+        }
     }
     if constexpr (ROWS == 1) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             float2 other;
-            other.x = __shfl_xor_sync(0xffffffffu, r, o);
-            other.y = __shfl_xor_sync(0xffffffffu, s, o);
-            join(other);
+            other.x = __shfl_xor_sync(0xffffffffu, sm.r, o);
+            other.y = __shfl_xor_sync(0xffffffffu, sm.s, o);
+            sm.join(other);
         }
     }
-    part[warp][lane] = make_float2(r, s);
+    part[warp][lane] = make_float2(sm.r, sm.s);
     __syncthreads();
     if (warp != 0 || (ROWS == 1 && lane != 0) || row >= T)
         return;
-    for (int i = 1; i < 8; ++i)
-        join(part[i][lane]);
+#pragma unroll
+    for (int i = 1; i < kCombineWarps; ++i)
+        sm.join(part[i][lane]);
     const int y = __ldcg(targets + row);
     const bool live = static_cast<unsigned>(y) < static_cast<unsigned>(V);
-    const float ref = r == -INFINITY ? 0.0f : r;
-    const float log2s = log2f(s);
+    const float ref = sm.r == -INFINITY ? 0.0f : sm.r;
+    const float log2s = log2f(sm.s);
     lse[row] = live ? (ref + log2s) * kLn2 : 0.0f;
     losses[row] = live ? (fmaf(-__ldcg(losses + row), kLog2e, ref) + log2s) * kLn2 : 0.0f;
 }
@@ -750,25 +882,27 @@ __global__ void __launch_bounds__(256)
 // 2^14 for fp16, whose small probabilities would otherwise be subnormal);
 // the other blocks copy X with the rows of tokens without a loss zeroed, so
 // that what such a row holds (a NaN, say) does not reach dW as 0 * NaN.
-__global__ void __launch_bounds__(256)
+constexpr int kPrepareThreads = 512;
+
+__global__ void __launch_bounds__(kPrepareThreads)
     head_prepare_kernel(const uint4 *x, long long ldx16, uint4 *xs, long long ld16, int K, long long T, const int *targets, int V,
                         const float *dlosses, const float *dlse, float c, float *scale)
 {
     grid_start();
     if (blockIdx.x == 0) {
-        __shared__ float top[8];
+        __shared__ float top[kPrepareThreads / 32];
         float m = 0.0f;
-        for (long long t = threadIdx.x; t < T; t += 256)
-            if (static_cast<unsigned>(__ldcg(targets + t)) < static_cast<unsigned>(V))
-                m = fmaxf(m, fabsf(__ldcg(dlosses + t)) + (dlse ? fabsf(__ldcg(dlse + t)) : 0.0f));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 4
+        for (long long t = threadIdx.x; t < T; t += kPrepareThreads) {
+            const float d = fabsf(__ldcg(dlosses + t)) + (dlse ? fabsf(__ldcg(dlse + t)) : 0.0f);
+            m = fmaxf(m, static_cast<unsigned>(__ldcg(targets + t)) < static_cast<unsigned>(V) ? d : 0.0f);
+        }
+        m = warp_max(m);
         if ((threadIdx.x & 31) == 0)
             top[threadIdx.x >> 5] = m;
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int i = 1; i < 8; ++i)
+            for (int i = 1; i < kPrepareThreads / 32; ++i)
                 m = fmaxf(m, top[i]);
             m = fminf(fmaxf(m, 1e-30f), 3e38f);
             scale[0] = c / m;
@@ -779,8 +913,8 @@ __global__ void __launch_bounds__(256)
     if (!xs)
         return;
     const int words = (K + 7) / 8;
-    const long long all = T * words, step = (gridDim.x - 1ll) * 256;
-    for (long long i = (blockIdx.x - 1ll) * 256 + threadIdx.x; i < all; i += step) {
+    const long long all = T * words, step = (gridDim.x - 1ll) * kPrepareThreads;
+    for (long long i = (blockIdx.x - 1ll) * kPrepareThreads + threadIdx.x; i < all; i += step) {
         const long long t = i / words;
         const int k = static_cast<int>(i - t * words);
         const bool live = static_cast<unsigned>(__ldcg(targets + t)) < static_cast<unsigned>(V);
@@ -872,117 +1006,162 @@ struct Operand {
     int64_t ld;
 };
 
-// Tiles of a product: single CTAs of up to 128 rows, or pairs of 256; `bn`
-// columns; K in `splits` parts.
-struct HeadTiles {
-    int cg, bn, splits;
+// A product of a launch as the host builds it.
+struct Job {
+    HeadJob j;
+    CUtensorMap a, b, d;
+    int64_t cost;  // of a unit
 };
 
-template <int CG, int EPI>
-std::atomic<uint64_t> head_attribute_set[2] = {{0}, {0}};
+// What a block of K costs on a tile `bn` wide, in columns: a pair's time goes
+// with the operands' bytes, which the tiles' 256 rows share (4096 x 16384 x 4096:
+// 14.0 us a round of 128 columns, 20.9 of 256); few tokens leave the SMs waiting
+// for the weights alone.
+int64_t tile_cost(int cg, int bn) { return cg == 2 ? bn + 160 : bn; }
 
-template <int CG, int EPI>
-gemm_status_t launch_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &d, HeadParams &p, int sms, cudaStream_t st)
+template <int CG>
+gemm_status_t make_job(Job *job, int bn, int splits, int64_t M, int64_t N, int64_t K, int in_bf16, const Operand &A, const Operand &B, int a_rows)
 {
     constexpr int BK = kHeadBK<CG>;
-    const int stage_bytes = (p.a_rows + p.bn / CG) * BK * 2;
-    const int rest = (EPI == kEpiSoftmax ? 0 : kHeadStageBytes) + kHeadTail;
-    p.stages = std::min(kHeadMaxStages, (kHeadSmem - rest) / stage_bytes);
-    const int smem = p.stages * stage_bytes + rest + 1024;
-    auto kern = head_kernel<CG, EPI>;
-    if (ensure_smem_attribute(kern, kHeadSmem + 1024, head_attribute_set<CG, EPI>) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    const unsigned grid = static_cast<unsigned>(std::min(p.units, std::max(1, sms / CG)) * CG);
-    return host_launch(kern, grid, kHeadThreads, static_cast<size_t>(smem), st, CG == 2 ? 2u : 0u, a, b, d, p);
+    HeadJob &j = job->j;
+    const int64_t tiles_m = (M + 128 * CG - 1) / (128 * CG), tiles_n = (N + bn - 1) / bn;
+    const int64_t kb = (K + BK - 1) / BK, unit = (kb + splits - 1) / splits, parts = (kb + unit - 1) / unit;
+    if (tiles_m * tiles_n * parts > kSizeLimit)
+        return GEMM_ERR_UNSUPPORTED;
+    j.M = static_cast<int>(M);
+    j.N = static_cast<int>(N);
+    j.K = static_cast<int>(K);
+    j.tiles_m = static_cast<int>(tiles_m);
+    j.tiles_n = static_cast<int>(tiles_n);
+    j.units = static_cast<int>(tiles_m * tiles_n * parts);
+    j.group_m = 8;
+    j.kb_all = static_cast<int>(kb);
+    j.kb_unit = static_cast<int>(unit);
+    j.kb_part = static_cast<int>(unit);
+    j.bn = bn;
+    j.a_mn = A.mn_major;
+    j.b_mn = B.mn_major;
+    // an epilogue that no other unit's products cover costs about four blocks
+    job->cost = (unit + 4) * tile_cost(CG, bn);
+    gemm_status_t s = encode_16(&job->a, in_bf16, A.ptr, A.mn_major, M, K, A.ld, a_rows, BK);
+    if (s == GEMM_OK)
+        s = encode_16(&job->b, in_bf16, B.ptr, B.mn_major, N, K, B.ld, bn / CG, BK);
+    return s;
 }
 
-// Fills in the shape of a product and launches it.
-template <int EPI>
-gemm_status_t run_head(HeadParams p, const HeadTiles &t, int64_t M, int64_t N, int64_t K, int in_bf16, const Operand &A, const Operand &B,
-                       const CUtensorMap *d, int sms, cudaStream_t st)
+template <int CG, bool FORWARD>
+std::atomic<uint64_t> head_attribute_set[2] = {{0}, {0}};
+
+// Deals the units of the jobs, the longest first, out to the clusters and
+// launches them together.
+template <int CG, bool FORWARD>
+gemm_status_t launch_head(HeadParams p, Job *jobs, int n, int sms, cudaStream_t st)
 {
-    const int bk = t.cg == 2 ? kHeadBK<2> : kHeadBK<1>;
-    p.M = static_cast<int>(M);
-    p.N = static_cast<int>(N);
-    p.K = static_cast<int>(K);
-    p.bn = t.bn;
-    p.a_rows = t.cg == 2 || A.mn_major ? 128 : static_cast<int>(std::min<int64_t>(128, round_up(M, 8)));
-    p.a_mn = A.mn_major;
-    p.b_mn = B.mn_major;
-    p.in_bf16 = in_bf16;
-    p.group_m = 8;
-    const int64_t tiles_m = (M + 128 * t.cg - 1) / (128 * t.cg), tiles_n = (N + t.bn - 1) / t.bn;
-    const int64_t kb = (K + bk - 1) / bk, unit = (kb + t.splits - 1) / t.splits, splits = (kb + unit - 1) / unit;
-    if (tiles_m * tiles_n * splits > kSizeLimit)
-        return GEMM_ERR_UNSUPPORTED;
-    p.tiles_m = static_cast<int>(tiles_m);
-    p.tiles_n = static_cast<int>(tiles_n);
-    p.kb_unit = static_cast<int>(unit);
-    p.kb_part = EPI == kEpiSoftmax ? kSumPart / bk : static_cast<int>(unit);
-    p.units = static_cast<int>(tiles_m * tiles_n * splits);
+    constexpr int BK = kHeadBK<CG>;
+    std::sort(jobs, jobs + n, [](const Job &x, const Job &y) { return x.cost > y.cost; });
+    int64_t units = 0, longest = 0;
+    int bn = 0;
+    for (int i = 0; i < n; ++i) {
+        units += jobs[i].j.units;
+        longest = std::max<int64_t>(longest, jobs[i].j.kb_unit);
+        bn = std::max(bn, jobs[i].j.bn);
+    }
+    const int64_t clusters = std::min<int64_t>(units, std::max(1, sms / CG));
+    HeadMaps maps;
+    int64_t behind = 0, gap = 0;  // clusters from `behind` on have `gap` less to do
+    for (int i = 0; i < n; ++i) {
+        HeadJob &j = jobs[i].j;
+        const int64_t cost = jobs[i].cost, late = clusters - behind;
+        j.behind = static_cast<int>(behind);
+        j.extra = behind > 0 ? static_cast<int>((gap + cost / 2) / cost) : 0;
+        const int64_t rest = j.units - j.extra * late;
+        if (rest <= 0) {
+            gap -= j.units / late * cost;
+        } else if (rest % clusters != 0) {
+            behind = rest % clusters;
+            gap = cost;
+        } else {
+            behind = gap = 0;
+        }
+        p.jobs[i] = j;
+        maps.a[i] = jobs[i].a;
+        maps.b[i] = jobs[i].b;
+        maps.d[i] = jobs[i].d;
+    }
+    for (int i = n; i < kMaxJobs; ++i) {
+        p.jobs[i] = p.jobs[0];
+        maps.a[i] = maps.a[0];
+        maps.b[i] = maps.b[0];
+        maps.d[i] = maps.d[0];
+    }
+    p.num_jobs = n;
+    p.b_rows = bn / CG;
     int ms = 0;
     p.inject = host_take_injection(&ms);
     // a role may wait for another to walk all of a unit's K: 10 us a block beside 2 s
-    p.timeout_ns = ms > 0 ? static_cast<unsigned long long>(ms) * 1000000ull : 2000000000ull + static_cast<unsigned long long>(unit) * 10000ull;
-    CUtensorMap a, b;
-    gemm_status_t s = encode_16(&a, in_bf16, A.ptr, A.mn_major, M, K, A.ld, p.a_rows, bk);
-    if (s != GEMM_OK || (s = encode_16(&b, in_bf16, B.ptr, B.mn_major, N, K, B.ld, t.bn / t.cg, bk)) != GEMM_OK)
-        return s;
-    const CUtensorMap &out = d ? *d : a;
-    return t.cg == 2 ? launch_head<2, EPI>(a, b, out, p, sms, st) : launch_head<1, EPI>(a, b, out, p, sms, st);
+    p.timeout_ns = ms > 0 ? static_cast<unsigned long long>(ms) * 1000000ull : 2000000000ull + static_cast<unsigned long long>(longest) * 10000ull;
+    const int stage_bytes = (p.a_rows + p.b_rows) * BK * 2;
+    const int rest = (FORWARD ? kHeadHalves : kHeadStageBytes) + kHeadTail;
+    p.stages = std::min(kHeadMaxStages, (kHeadSmem - rest) / stage_bytes);
+    const int smem = p.stages * stage_bytes + rest + 1024;
+    auto kern = head_kernel<CG, FORWARD>;
+    if (ensure_smem_attribute(kern, kHeadSmem + 1024, head_attribute_set<CG, FORWARD>) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    return host_launch(kern, static_cast<unsigned>(clusters * CG), kHeadThreads, static_cast<size_t>(smem), st, CG == 2 ? 2u : 0u, maps, p);
 }
 
-// Rounds of the grid that `units` take, as a share of it that they fill.
-double filled(int64_t units, int64_t slots) { return static_cast<double>(units) / static_cast<double>((units + slots - 1) / slots * slots); }
-
-// Tiles of the logits: 256 columns, or the width (a multiple of `step`) whose
-// rounds of the grid cost least where there are few.
-HeadTiles logit_tiles(int64_t T, int64_t V, int step, int sms)
+// Columns of the tiles of the logits: 256, or the width whose rounds of the grid
+// cost least where there are few. A tile of few rows of A is at least so wide
+// that the 128 rows the tensor cores read of a stage lie inside it.
+int logit_columns(int cg, int64_t T, int64_t V, int a_rows, int step, int sms)
 {
-    HeadTiles t = {T <= 128 ? 1 : 2, 256, 1};
-    const int64_t slots = std::max(1, sms / t.cg), tiles_m = (T + 128 * t.cg - 1) / (128 * t.cg);
-    int64_t best = 0;
-    for (int bn = 256; bn >= 128; bn -= step) {
-        const int64_t units = tiles_m * ((V + bn - 1) / bn), cost = (units + slots - 1) / slots * bn;
-        if (best == 0 || cost < best) {
-            best = cost;
-            t.bn = bn;
+    const int64_t slots = std::max(1, sms / cg), tiles_m = (T + 128 * cg - 1) / (128 * cg);
+    const int least = cg == 2 ? 128 : std::max(64, 128 - a_rows);
+    int best = 256;
+    int64_t best_cost = 0;
+    for (int bn = 256; bn >= least; bn -= step) {
+        const int64_t rounds = (tiles_m * ((V + bn - 1) / bn) + slots - 1) / slots, cost = rounds * tile_cost(cg, bn);
+        if (best_cost == 0 || cost < best_cost) {
+            best_cost = cost;
+            best = bn;
         }
     }
-    return t;
+    return best;
 }
 
-// Vocabulary columns of a piece, slots for parts of dX, and the places of all
-// that in the workspace.
+// Vocabulary columns of a piece, parts of dX, and the places of all that in the
+// workspace.
 struct BackPlan {
-    int64_t piece, ldp;  // columns of a piece (a multiple of 256 but for the only one), elements of its rows
-    int64_t ldk;         // elements of a row of X's copy and of dX's parts
-    HeadTiles dx;
-    size_t xs, dl, parts, bytes;  // offsets
+    int cg;
+    int64_t piece, pieces, ldp;  // columns of a piece (a multiple of 256 but for the only one), their number, elements of its rows
+    int64_t ldk;                 // elements of a row of X's copy and of dX's parts
+    int dx_bn, dx_splits;
+    size_t xs, dl[2], parts, bytes;  // offsets
 };
 
 constexpr int64_t kPieceColumns = 16384;
 
-BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t piece, int sms)
+BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
 {
     BackPlan b = {};
-    b.piece = std::min(V, piece);
+    b.cg = T <= 128 ? 1 : 2;
+    b.pieces = (V + columns - 1) / columns;
+    b.piece = b.pieces == 1 ? V : round_up((V + b.pieces - 1) / b.pieces, 256);
+    b.pieces = (V + b.piece - 1) / b.piece;
     b.ldp = round_up(b.piece, 64);
     b.ldk = round_up(K, 8);
-    b.dx.cg = T <= 128 ? 1 : 2;
-    b.dx.bn = K <= 128 ? 128 : 256;
-    const int64_t slots = std::max(1, sms / b.dx.cg);
-    const int64_t tiles = (T + 128 * b.dx.cg - 1) / (128 * b.dx.cg) * ((K + b.dx.bn - 1) / b.dx.bn);
-    // parts of the vocabulary that fill the grid best: each costs T K sums in
-    // fp32, written and read once more
-    int best = 1;
-    for (int s = 2; s <= 152 && s * 512 <= b.piece; ++s)
-        if (s <= 4 || tiles * s <= slots)
-            if (filled(tiles * s, slots) > filled(tiles * best, slots) + 0.04)
-                best = s;
-    // as many as whole blocks of K make, so that no later, shorter piece has more
-    const int64_t bk = b.dx.cg == 2 ? kHeadBK<2> : kHeadBK<1>, kb = (b.piece + bk - 1) / bk, unit = (kb + best - 1) / best;
-    b.dx.splits = static_cast<int>((kb + unit - 1) / unit);
+    b.dx_bn = K <= 128 ? 128 : 256;
+    // dX has few tiles with long sums over the piece: in parts, where one would
+    // take more than a third of what a cluster has to do in all
+    const int bk = b.cg == 2 ? kHeadBK<2> : kHeadBK<1>, rows = 128 * b.cg;
+    const int64_t slots = std::max(1, sms / b.cg);
+    auto blocks = [&](int64_t n) { return (n + bk - 1) / bk; };
+    auto tiles = [&](int64_t m, int64_t n, int bn) { return (m + rows - 1) / rows * ((n + bn - 1) / bn); };
+    const int64_t x_tiles = tiles(T, K, b.dx_bn), kb = blocks(b.piece);
+    const int64_t work = x_tiles * kb + tiles(b.piece, K, b.dx_bn) * (blocks(T) + 4) + (b.pieces > 1 ? tiles(T, b.piece, 256) * (blocks(K) + 4) : 0);
+    const int64_t most = std::max<int64_t>(8, work / slots / 3);
+    const int64_t wanted = std::min<int64_t>((kb + most - 1) / most, std::max<int64_t>(1, 2 * slots / x_tiles)), unit = (kb + wanted - 1) / wanted;
+    b.dx_splits = static_cast<int>((kb + unit - 1) / unit);
     size_t at = 256;
     auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -990,10 +1169,19 @@ BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t piece, int sms)
         return o;
     };
     b.xs = take(static_cast<size_t>(T) * b.ldk * 2);
-    b.dl = take(static_cast<size_t>(T) * b.ldp * 2);
-    b.parts = take(static_cast<size_t>(T) * b.ldk * 4 * b.dx.splits);
+    b.dl[0] = take(static_cast<size_t>(T) * b.ldp * 2);
+    b.dl[1] = b.pieces > 1 ? take(static_cast<size_t>(T) * b.ldp * 2) : b.dl[0];
+    b.parts = take(static_cast<size_t>(T) * b.ldk * 4 * b.dx_splits);
     b.bytes = at;
     return b;
+}
+
+// Widest pieces that are taken for a shape. Few tokens wait for memory: what a
+// launch reads and writes of the weights and their gradient (three pieces) shall
+// stay in L2, where the next launch reads one of them again.
+int64_t widest_piece(int64_t T, int64_t K)
+{
+    return T > 512 ? kPieceColumns : std::max<int64_t>(2048, std::min<int64_t>(kPieceColumns, (int64_t(16) << 20) / K / 256 * 256));
 }
 
 // What both calls check of their shape.
@@ -1013,8 +1201,112 @@ gemm_status_t check_head(int in_type, int64_t T, int64_t V, int64_t K, const voi
     return GEMM_OK;
 }
 
-// Room for partial softmaxes on any GPU: two for each tile of at least 128 columns.
-size_t forward_bytes(int64_t T, int64_t V) { return static_cast<size_t>(T) * static_cast<size_t>((V + 127) / 128) * 2 * sizeof(float2); }
+// Room for partial softmaxes on any GPU: one for each tile, which has at least 64 columns.
+size_t forward_bytes(int64_t T, int64_t V) { return static_cast<size_t>(T) * static_cast<size_t>((V + 63) / 64) * sizeof(float2); }
+
+template <int CG>
+gemm_status_t run_forward(HeadParams p, int64_t T, int64_t V, int64_t K, int in_type, const Operand &X, const Operand &W, int *tiles, int sms,
+                          cudaStream_t st)
+{
+    p.a_rows = CG == 2 ? 128 : static_cast<int>(std::min<int64_t>(128, round_up(T, 8)));
+    Job job;
+    const int bn = logit_columns(CG, T, V, p.a_rows, CG == 2 ? 32 : 16, sms);
+    const gemm_status_t s = make_job<CG>(&job, bn, 1, T, V, K, in_type, X, W, p.a_rows);
+    if (s != GEMM_OK)
+        return s;
+    job.d = job.a;
+    job.j.epi = kEpiSoftmax;
+    job.j.kb_part = kSumPart / kHeadBK<CG>;
+    *tiles = job.j.tiles_n;
+    return launch_head<CG, true>(p, &job, 1, sms, st);
+}
+
+// The arguments of a backward call that its launches need.
+struct BackArgs {
+    int in_type;
+    int64_t T, V, K;
+    Operand X, W;
+    void *dX, *dW;
+    int dx_type, dw_type;
+    int64_t lddx, lddw;
+    bool accumulate;
+    uint8_t *ws;
+};
+
+// One launch for each piece: its gradients and the next piece's dl, which do not
+// wait for one another, so that the units of one product fill what the rounds of
+// the others leave of the grid.
+template <int CG>
+gemm_status_t run_backward(HeadParams p, const BackArgs &g, const BackPlan &b, int sms, cudaStream_t st)
+{
+    p.a_rows = 128;
+    const int ew = type_bytes(g.dw_type);
+    float *parts = reinterpret_cast<float *>(g.ws + b.parts);
+    for (int64_t i = -1; i < b.pieces; ++i) {
+        Job jobs[kMaxJobs];
+        int n = 0;
+        gemm_status_t s;
+        const int64_t v0 = i * b.piece, cols = std::min(b.piece, g.V - v0);
+        if (i >= 0 && g.dX) {
+            Job &job = jobs[n++];
+            if ((s = make_job<CG>(&job, b.dx_bn, b.dx_splits, g.T, g.K, cols, g.in_type, {g.ws + b.dl[i & 1], 0, b.ldp},
+                                  {static_cast<const char *>(g.W.ptr) + v0 * g.W.ld * 2, 1, g.W.ld}, 128)) != GEMM_OK)
+                return s;
+            const bool last = i == b.pieces - 1 && b.dx_splits == 1;
+            HeadJob &j = job.j;
+            j.epi = kEpiProduct;
+            j.out_type = last ? g.dx_type : GEMM_OUT_F32;
+            j.scaled = last;
+            j.slot_rows = g.T;
+            j.c_raw = i > 0 ? parts : nullptr;
+            j.ld_raw = b.ldk;
+            j.c_typed = nullptr;
+            j.ld_typed = 0;
+            j.whole = static_cast<int>(last ? whole_words(g.K, g.dx_type) : b.ldk);
+            j.d = g.dX;
+            j.ldd = g.lddx;
+            if ((s = encode_out(&job.d, j.out_type, last ? g.dX : parts, g.T, j.whole, last ? g.lddx : b.ldk, last ? 1 : b.dx_splits)) != GEMM_OK)
+                return s;
+        }
+        if (i >= 0 && g.dW) {
+            Job &job = jobs[n++];
+            if ((s = make_job<CG>(&job, b.dx_bn, 1, cols, g.K, g.T, g.in_type, {g.ws + b.dl[i & 1], 1, b.ldp}, {g.ws + b.xs, 1, b.ldk}, 128)) != GEMM_OK)
+                return s;
+            char *o = static_cast<char *>(g.dW) + v0 * g.lddw * ew;
+            HeadJob &j = job.j;
+            j.epi = kEpiProduct;
+            j.out_type = g.dw_type;
+            j.scaled = 1;
+            j.slot_rows = 0;
+            j.c_raw = nullptr;
+            j.ld_raw = 0;
+            j.c_typed = g.accumulate ? o : nullptr;
+            j.ld_typed = g.lddw;
+            j.whole = static_cast<int>(whole_words(g.K, g.dw_type));
+            j.d = o;
+            j.ldd = g.lddw;
+            if ((s = encode_out(&job.d, g.dw_type, o, cols, j.whole, g.lddw)) != GEMM_OK)
+                return s;
+        }
+        if (i + 1 < b.pieces) {
+            Job &job = jobs[n++];
+            const int64_t w0 = (i + 1) * b.piece, next = std::min(b.piece, g.V - w0);
+            // where it has a launch of its own, by its own rounds of the grid
+            const int bn = n == 1 ? logit_columns(CG, g.T, next, 128, 64, sms) : 256;
+            if ((s = make_job<CG>(&job, bn, 1, g.T, next, g.K, g.in_type, g.X, {static_cast<const char *>(g.W.ptr) + w0 * g.W.ld * 2, 0, g.W.ld}, 128)) !=
+                GEMM_OK)
+                return s;
+            job.j.epi = kEpiLogitGrad;
+            job.j.v0 = static_cast<int>(w0);
+            if ((s = encode_out(&job.d, g.in_type == 1 ? GEMM_OUT_BF16 : GEMM_OUT_F16, g.ws + b.dl[(i + 1) & 1], g.T, round_up(next, 8), b.ldp)) !=
+                GEMM_OK)
+                return s;
+        }
+        if ((s = launch_head<CG, false>(p, jobs, n, sms, st)) != GEMM_OK)
+            return s;
+    }
+    return GEMM_OK;
+}
 
 }  // namespace
 
@@ -1042,18 +1334,21 @@ gemm_status_t gemm_cross_entropy(int in_type, int64_t T, int64_t V, int64_t K, c
     HeadParams p = {};
     if ((s = host_device(&dev, &p.status, &sms)) != GEMM_OK)
         return s;
-    const HeadTiles t = logit_tiles(T, V, 32, sms);
     p.targets = targets;
+    p.T = static_cast<int>(T);
     p.V = static_cast<int>(V);
+    p.in_bf16 = in_type;
     p.partials = static_cast<float2 *>(workspace);
     p.picked = losses;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if ((s = run_head<kEpiSoftmax>(p, t, T, V, K, in_type, {X, 0, ldx}, {W, 0, ldw}, nullptr, sms, st)) != GEMM_OK)
+    int parts = 0;
+    s = T <= 128 ? run_forward<1>(p, T, V, K, in_type, {X, 0, ldx}, {W, 0, ldw}, &parts, sms, st)
+                 : run_forward<2>(p, T, V, K, in_type, {X, 0, ldx}, {W, 0, ldw}, &parts, sms, st);
+    if (s != GEMM_OK)
         return s;
-    const int parts = 2 * static_cast<int>((V + t.bn - 1) / t.bn);
-    if (T <= 64)
-        return host_launch(head_combine_kernel<1>, static_cast<unsigned>(T), 256, 0, st, 0, p.partials, parts, T, targets, p.V, losses, lse);
-    return host_launch(head_combine_kernel<32>, static_cast<unsigned>((T + 31) / 32), 256, 0, st, 0, p.partials, parts, T, targets, p.V,
+    if (T <= 512)
+        return host_launch(head_combine_kernel<1>, static_cast<unsigned>(T), 32 * kCombineWarps, 0, st, 0, p.partials, parts, T, targets, p.V, losses, lse);
+    return host_launch(head_combine_kernel<32>, static_cast<unsigned>((T + 31) / 32), 32 * kCombineWarps, 0, st, 0, p.partials, parts, T, targets, p.V,
                        losses, lse);
 }
 
@@ -1065,7 +1360,8 @@ size_t gemm_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t 
     unsigned int *status = nullptr;
     if (host_device(&dev, &status, &sms) != GEMM_OK)
         return 0;
-    return back_plan(T, V, K, columns ? round_up(columns, 256) : kPieceColumns, sms).bytes;
+    const int64_t widest = widest_piece(T, K);
+    return back_plan(T, V, K, columns ? std::min(widest, round_up(columns, 256)) : widest, sms).bytes;
 }
 
 gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int64_t K, const void *X, int64_t ldx, const void *W,
@@ -1100,7 +1396,7 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
         return s;
     // the largest pieces that the workspace has room for, up to the usual ones
     BackPlan b = {};
-    for (int64_t piece = kPieceColumns; piece >= 256; piece -= 256) {
+    for (int64_t piece = widest_piece(T, K); piece >= 256; piece -= 256) {
         b = back_plan(T, V, K, piece, sms);
         if (b.bytes <= workspace_bytes)
             break;
@@ -1109,70 +1405,25 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
         return GEMM_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *scale = reinterpret_cast<float *>(ws);
-    void *xs = ws + b.xs, *dl = ws + b.dl;
-    float *parts = reinterpret_cast<float *>(ws + b.parts);
-    const unsigned copies = dW ? static_cast<unsigned>(std::min<int64_t>((T * ((K + 7) / 8) + 1023) / 1024, 4 * sms)) : 0;
-    if ((s = host_launch(head_prepare_kernel, 1 + copies, 256, 0, st, 0, static_cast<const uint4 *>(X), ldx / 8,
-                         dW ? static_cast<uint4 *>(xs) : nullptr, b.ldk / 8, static_cast<int>(K), T, targets, static_cast<int>(V), dlosses, dlse,
-                         in_type == 1 ? 1.0f : 16384.0f, scale)) != GEMM_OK)
+    const unsigned copies = dW ? static_cast<unsigned>(std::min<int64_t>((T * ((K + 7) / 8) + 2047) / 2048, 2 * sms)) : 0;
+    if ((s = host_launch(head_prepare_kernel, 1 + copies, kPrepareThreads, 0, st, 0, static_cast<const uint4 *>(X), ldx / 8,
+                         dW ? reinterpret_cast<uint4 *>(ws + b.xs) : nullptr, b.ldk / 8, static_cast<int>(K), T, targets,
+                         static_cast<int>(V), dlosses, dlse, in_type == 1 ? 1.0f : 16384.0f, scale)) != GEMM_OK)
         return s;
     p.targets = targets;
+    p.T = static_cast<int>(T);
     p.V = static_cast<int>(V);
+    p.in_bf16 = in_type;
     p.lse = lse;
     p.dlosses = dlosses;
     p.dlse = dlse;
     p.scale = scale;
-    const int64_t pieces = (V + b.piece - 1) / b.piece;
-    const int splits = b.dx.splits;
-    for (int64_t i = 0; i < pieces; ++i) {
-        const int64_t v0 = i * b.piece, n = std::min(b.piece, V - v0);
-        const char *w = static_cast<const char *>(W) + v0 * ldw * 2;
-        CUtensorMap d;
-        HeadParams q = p;
-        q.v0 = static_cast<int>(v0);
-        if ((s = encode_out(&d, in_type == 1 ? GEMM_OUT_BF16 : GEMM_OUT_F16, dl, T, round_up(n, 8), b.ldp)) != GEMM_OK)
-            return s;
-        if ((s = run_head<kEpiLogitGrad>(q, logit_tiles(T, n, 64, sms), T, n, K, in_type, {X, 0, ldx}, {w, 0, ldw}, &d, sms, st)) != GEMM_OK)
-            return s;
-        if (dX) {
-            q = p;
-            const bool last = i == pieces - 1 && splits == 1;
-            q.out_type = last ? dx_type : GEMM_OUT_F32;
-            q.scaled = last;
-            q.slot_rows = T;
-            if (i > 0) {
-                q.c_raw = parts;
-                q.ld_raw = b.ldk;
-            }
-            q.whole = static_cast<int>(last ? whole_words(K, dx_type) : b.ldk);
-            q.d = dX;
-            q.ldd = lddx;
-            if ((s = encode_out(&d, q.out_type, last ? dX : parts, T, q.whole, last ? lddx : b.ldk, last ? 1 : splits)) != GEMM_OK)
-                return s;
-            if ((s = run_head<kEpiProduct>(q, b.dx, T, K, n, in_type, {dl, 0, b.ldp}, {w, 1, ldw}, &d, sms, st)) != GEMM_OK)
-                return s;
-        }
-        if (dW) {
-            q = p;
-            q.out_type = dw_type;
-            q.scaled = 1;
-            char *o = static_cast<char *>(dW) + v0 * lddw * ew;
-            if (accumulate) {
-                q.c_typed = o;
-                q.ld_typed = lddw;
-            }
-            q.whole = static_cast<int>(whole_words(K, dw_type));
-            q.d = o;
-            q.ldd = lddw;
-            if ((s = encode_out(&d, dw_type, o, n, q.whole, lddw)) != GEMM_OK)
-                return s;
-            const HeadTiles t = {2, K <= 128 ? 128 : 256, 1};
-            if ((s = run_head<kEpiProduct>(q, t, n, K, T, in_type, {dl, 1, b.ldp}, {xs, 1, b.ldk}, &d, sms, st)) != GEMM_OK)
-                return s;
-        }
-    }
-    if (!dX || splits == 1)
-        return GEMM_OK;
+    const BackArgs args = {in_type, T, V, K, {X, 0, ldx}, {W, 0, ldw}, dX, dW, dx_type, dw_type, lddx, lddw, accumulate != 0, ws};
+    s = b.cg == 1 ? run_backward<1>(p, args, b, sms, st) : run_backward<2>(p, args, b, sms, st);
+    const int splits = b.dx_splits;
+    if (s != GEMM_OK || !dX || splits == 1)
+        return s;
+    const float *parts = reinterpret_cast<const float *>(ws + b.parts);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((T * ((K + 3) / 4) + 255) / 256, 8 * sms));
     const int k = static_cast<int>(K);
     const long long stride = T * b.ldk;
