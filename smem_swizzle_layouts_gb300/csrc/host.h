@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/gemm_gb300.h"
@@ -30,6 +31,27 @@ int host_take_injection(int *timeout_ms);
 
 // Counts `n` launched kernels in gemm_launch_count().
 void host_count_launches(int n);
+
+// Opt a kernel into its dynamic shared memory once per device (the attribute
+// is per device; setting it on every launch costs host time on short GEMMs).
+// `done` is the caller's per-variant record: one bit per device 0..127.
+template <typename Kern>
+cudaError_t ensure_smem_attribute(Kern kern, int bytes, std::atomic<uint64_t> (&done)[2])
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 128)
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done[dev >> 6].load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        done[dev >> 6].fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
 
 // Launches a kernel that may start while the kernel before it on the stream is
 // still running (programmatic dependent launch). Such a kernel calls

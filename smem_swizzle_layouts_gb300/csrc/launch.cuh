@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "gemm_kernel.cuh"
+#include "host.h"
 
 namespace g300 {
 
@@ -18,27 +19,6 @@ struct LaunchArgs {
     int grid;  // CTAs (a multiple of the cluster size)
     cudaStream_t stream;
 };
-
-// Opt a kernel into its dynamic shared memory once per device (the attribute
-// is per device; setting it on every launch costs host time on short GEMMs).
-// `done` is the caller's per-variant record: one bit per device 0..127.
-template <typename Kern>
-cudaError_t ensure_smem_attribute(Kern kern, int bytes, std::atomic<uint64_t> (&done)[2])
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
-    if (dev < 0 || dev >= 128)
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (done[dev >> 6].load(std::memory_order_acquire) & bit)
-        return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        done[dev >> 6].fetch_or(bit, std::memory_order_acq_rel);
-    return e;
-}
 
 // One record per kernel variant.
 template <int CG, int BN, int BK, int STAGES, bool GROUPED, int ESIZE, int BMT, int SF, int MODE>
