@@ -647,9 +647,9 @@ gemm_status_t gemm_cross_entropy(int in_type, int64_t T, int64_t V, int64_t K, c
  * gradients, times it). Products are summed in fp32. T == 0 leaves dX and writes
  * zeros to dW (nothing with accumulate).
  * workspace: 256-byte aligned, in no particular state. The call takes the widest
- * pieces that it has room for, 16384 columns at most:
- * gemm_cross_entropy_backward_workspace_size(T, V, K, columns) bytes for pieces
- * of `columns` columns (rounded up to a multiple of 256, the least; 0: the
+ * pieces that it has room for, of at most 2^27 / T columns (a piece's dl then has
+ * 256 MB): gemm_cross_entropy_backward_workspace_size(T, V, K, columns) bytes for
+ * pieces of `columns` columns (rounded up to a multiple of 256, the least; 0: the
  * widest), on the current device; 0 for bad arguments or without a device. The
  * widths' order of sums differs, so gradients may differ in their last bits.
  */

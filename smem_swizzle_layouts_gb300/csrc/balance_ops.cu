@@ -176,8 +176,20 @@ __global__ void __launch_bounds__(32 * kBalanceWarps<NPL>) balance_kernel(const 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_start();
     const long long lo = blockIdx.x * p.part, hi = min(lo + p.part, p.T);
-    for (long long s = p.blocks == 1 ? 0 : sequence_of(p, lo); s < p.S; ++s) {
-        const Sequence q = sequence(p, s);
+    // up to 31 sequences: each lane has the end of one
+    const bool few = p.offsets && p.S < 32;
+    const long long mine_end = few && lane <= p.S ? min(max(static_cast<long long>(__ldcg(p.offsets + lane)), 0ll), p.T) : p.T;
+    long long s = 0;
+    if (p.blocks > 1)
+        s = few ? max(0, __popc(__ballot_sync(0xffffffffu, lane < p.S && mine_end <= lo)) - 1) : sequence_of(p, lo);
+    for (; s < p.S; ++s) {
+        Sequence q;
+        if (few) {
+            q.lo = __shfl_sync(0xffffffffu, mine_end, static_cast<int>(s));
+            q.hi = max(q.lo, __shfl_sync(0xffffffffu, mine_end, static_cast<int>(s) + 1));
+        } else {
+            q = sequence(p, s);
+        }
         if (q.lo >= hi && p.blocks > 1)
             return;
         const long long a = max(lo, q.lo), b = min(hi, q.hi);
@@ -350,7 +362,7 @@ constexpr int kBalanceGradWarps = 8;
 // Tokens of a warp: neighbours, which mostly share a sequence, and whose logits
 // are all asked for at the start.
 template <int NPL>
-constexpr int kBalanceGradRun = NPL <= 8 ? 4 : 1;
+constexpr int kBalanceGradRun = NPL <= 2 ? 4 : NPL <= 8 ? 2 : 1;
 
 // One warp a token: its scores, their mean gradient, and the logits' gradients.
 template <typename L, int NPL>
@@ -393,12 +405,11 @@ __global__ void __launch_bounds__(32 * kBalanceGradWarps) balance_backward_kerne
                 q = sequence(p, s);
             }
             const float n = static_cast<float>(max(__ldcg(p.tokens + s), 1));
-            const float by = __ldcg(p.dlosses + s) * static_cast<float>(p.E);
+            const float by = __fdiv_rn(__fdiv_rn(__ldcg(p.dlosses + s) * static_cast<float>(p.E), static_cast<float>(p.k) * n), n);
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
                 const int e = lane + 32 * i;
-                const float count = e < p.E ? static_cast<float>(__ldcg(p.counts + s * p.E + e)) : 0.0f;
-                c[i] = __fdiv_rn(__fdiv_rn(by * count, static_cast<float>(p.k) * n), n);
+                c[i] = e < p.E ? by * static_cast<float>(__ldcg(p.counts + s * p.E + e)) : 0.0f;
             }
         }
         if (t < q.lo || t >= q.hi)

@@ -63,11 +63,25 @@ constexpr int kHeadBars = 2 * kHeadMaxStages + 4 + 2 + 8;
 constexpr int kHeadHalves = 128 * 8;  // forward: a partial softmax for each row of a tile
 constexpr int kHeadTail = kHeadBars * 8 + 16;
 
+// Division of n < 2^31 by a number that the host knows: with 2^shift < d <=
+// 2^(shift + 1) and m = ceil(2^(32 + shift) / d), n m / 2^(32 + shift) is above
+// n / d by less than 2^-(shift + 1) <= 1 / d. Short units would otherwise wait
+// for the divisions of their places.
+struct Divisor {
+    unsigned d, m;
+    int shift;
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return d == 1 ? n : static_cast<int>(__umulhi(static_cast<unsigned>(n), m) >> shift);
+    }
+};
+
 // One product of a launch. Its units are tiles (in rasters of group_m tile
 // rows), one split of K after another.
 struct HeadJob {
     int M, N, K;  // rows, columns, length of the sums
     int tiles_m, tiles_n, units, group_m;
+    Divisor by_tiles, by_group, by_rows, by_last_rows;  // tiles, tiles of a raster group, its rows, those of the last group
     int kb_all, kb_unit;  // K blocks of the whole product and of a unit
     int kb_part;          // those that the tensor cores sum before the epilogue takes the sum (a unit's, or fewer)
     int bn;               // columns of a tile
@@ -163,15 +177,13 @@ struct HeadUnits {
                 continue;
             }
             h.job = job;
-            const int tiles = j.tiles_m * j.tiles_n;
-            h.split = u / tiles;
-            const int local = u - h.split * tiles;
-            const int per_group = j.group_m * j.tiles_n;
-            const int g = local / per_group;
-            const int rows = min(j.tiles_m - g * j.group_m, j.group_m);
-            const int r = local - g * per_group;
-            h.m_blk = g * j.group_m + r % rows;
-            h.n_blk = r / rows;
+            h.split = j.by_tiles(u);
+            const int local = u - h.split * static_cast<int>(j.by_tiles.d);
+            const int g = j.by_group(local), r = local - g * static_cast<int>(j.by_group.d);
+            const int left = j.tiles_m - g * j.group_m;
+            const Divisor &rows = left < j.group_m ? j.by_last_rows : j.by_rows;
+            h.n_blk = rows(r);
+            h.m_blk = g * j.group_m + r - h.n_blk * static_cast<int>(rows.d);
             h.kb0 = h.split * j.kb_unit;
             h.kb1 = min(j.kb_all, h.kb0 + j.kb_unit);
             return true;
@@ -196,15 +208,25 @@ __device__ ProducerTail head_producer(const HeadParams &p, const HeadMaps &maps,
     uint32_t phase = 0;
     HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
     HeadUnit h;
+    const CUtensorMap *map_a = nullptr, *map_b = nullptr;
+    OperandBoxes box_a = {}, box_b = {};
+    int last_job = -1, bn = 0, b_cols = 0, nbox = 0;
+    uint32_t tx = 0;
     while (units.next(h)) {
-        const HeadJob &j = p.jobs[h.job];
-        const CUtensorMap *const map_a = &maps.a[h.job], *const map_b = &maps.b[h.job];
-        const int b_cols = j.bn / CG;
-        const OperandBoxes box_a = operand_boxes(j.a_mn, 3, a_rows, BK, 2), box_b = operand_boxes(j.b_mn, 3, b_cols, BK, 2);
-        const uint32_t tx = CG * (a_bytes + static_cast<uint32_t>(b_cols) * BK * 2);
-        const int nbox = max(box_a.nbox, box_b.nbox);
+        if (h.job != last_job) {
+            const HeadJob &j = p.jobs[h.job];
+            last_job = h.job;
+            map_a = &maps.a[h.job];
+            map_b = &maps.b[h.job];
+            bn = j.bn;
+            b_cols = bn / CG;
+            box_a = operand_boxes(j.a_mn, 3, a_rows, BK, 2);
+            box_b = operand_boxes(j.b_mn, 3, b_cols, BK, 2);
+            tx = CG * (a_bytes + static_cast<uint32_t>(b_cols) * BK * 2);
+            nbox = max(box_a.nbox, box_b.nbox);
+        }
         const int m0 = (h.m_blk * CG + static_cast<int>(rank)) * 128;
-        const int n0 = h.n_blk * j.bn + b_cols * static_cast<int>(rank);
+        const int n0 = h.n_blk * bn + b_cols * static_cast<int>(rank);
         for (int kb = h.kb0; kb < h.kb1; ++kb) {
             if (!w.wait(bar_empty + 8 * stage, phase ^ 1u, kRoleProducer | kWaitEmpty, rank != 0))
                 return ProducerTail{min(issued, stages), stage, phase};
@@ -243,18 +265,24 @@ __device__ void head_mma(const HeadParams &p, uint32_t smem, uint32_t bar_full, 
     uint32_t phase = 0, acc_phase = 0;
     HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
     HeadUnit h;
+    int last_job = -1, kb_part = 1;
+    uint32_t idesc = 0, a_off[SLICES], b_off[SLICES];
+    uint64_t a_desc0 = 0, b_desc0 = 0;
     while (units.next(h)) {
-        const HeadJob &j = p.jobs[h.job];
-        const int b_cols = j.bn / CG, kb_part = j.kb_part;
-        const uint32_t idesc = make_idesc_f16(128 * CG, j.bn, p.in_bf16, j.a_mn, j.b_mn);
-        const OperandPacking pa = operand_packing(j.a_mn, 3, a_rows, BK), pb = operand_packing(j.b_mn, 3, b_cols, BK);
-        const uint64_t a_desc0 = make_smem_desc(smem, pa.lbo, pa.sbo, pa.swz);
-        const uint64_t b_desc0 = make_smem_desc(smem + a_bytes, pb.lbo, pb.sbo, pb.swz);
-        uint32_t a_off[SLICES], b_off[SLICES];
+        if (h.job != last_job) {
+            const HeadJob &j = p.jobs[h.job];
+            const int b_cols = j.bn / CG;
+            last_job = h.job;
+            kb_part = j.kb_part;
+            idesc = make_idesc_f16(128 * CG, j.bn, p.in_bf16, j.a_mn, j.b_mn);
+            const OperandPacking pa = operand_packing(j.a_mn, 3, a_rows, BK), pb = operand_packing(j.b_mn, 3, b_cols, BK);
+            a_desc0 = make_smem_desc(smem, pa.lbo, pa.sbo, pa.swz);
+            b_desc0 = make_smem_desc(smem + a_bytes, pb.lbo, pb.sbo, pb.swz);
 #pragma unroll
-        for (int i = 0; i < SLICES; ++i) {
-            a_off[i] = slice_byte_offset(j.a_mn, 3, a_rows, i) >> 4;
-            b_off[i] = slice_byte_offset(j.b_mn, 3, b_cols, i) >> 4;
+            for (int i = 0; i < SLICES; ++i) {
+                a_off[i] = slice_byte_offset(j.a_mn, 3, a_rows, i) >> 4;
+                b_off[i] = slice_byte_offset(j.b_mn, 3, b_cols, i) >> 4;
+            }
         }
         for (int part = h.kb0; part < h.kb1; part += kb_part) {
             if (!w.wait(bar_acc_empty + 8 * acc, acc_phase ^ 1u, kRoleMma | kWaitAccEmpty, CG == 2))
@@ -291,15 +319,14 @@ __device__ void head_mma(const HeadParams &p, uint32_t smem, uint32_t bar_full, 
 
 // ---------------------------------------------------------------- epilogues
 
-// This thread's 32 values of a row from TMEM.
-__device__ __forceinline__ void load_acc32(uint32_t taddr, float (&v)[32])
+// 32 values of a thread's row from TMEM: there after tmem_ld_wait().
+__device__ __forceinline__ void fetch_acc32(uint32_t taddr, float *v)
 {
-    uint32_t r[32];
-    tmem_ld_32x32b_x32(taddr, r);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] = __uint_as_float(r[i]);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 // 16 values of a row from TMEM, added to `v`. By 16 rather than 32: beside the
@@ -326,20 +353,32 @@ __device__ __forceinline__ void add_acc16(uint32_t taddr, float *v)
 struct RunningSoftmax {
     float r = -INFINITY, s = 0.0f;
 
-    __device__ __forceinline__ void add(const float (&v)[32])
+    // All of a thread's values of a tile, the first that it sees.
+    __device__ __forceinline__ void take(const float (&v)[4][32])
     {
-        float m = v[0];
+        float m[8];
 #pragma unroll
-        for (int i = 1; i < 32; ++i)
-            m = fmaxf(m, v[i]);
-        const float top = fmaxf(r, m * kLog2e);
-        const float ref = fabsf(top) == INFINITY ? 0.0f : top;
+        for (int i = 0; i < 8; ++i)
+            m[i] = fmaxf(fmaxf(v[0][i], v[1][i]), fmaxf(v[2][i], v[3][i]));
+#pragma unroll
+        for (int i = 8; i < 32; ++i)
+            m[i & 7] = fmaxf(fmaxf(m[i & 7], fmaxf(v[0][i], v[1][i])), fmaxf(v[2][i], v[3][i]));
+        const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7]))) * kLog2e;
+        const float ref = fabsf(top) < INFINITY ? top : 0.0f;
+        // by eights, so that small terms gather before they meet a large one
         float t[4] = {};
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            t[i & 3] += ex2(fmaf(v[i], kLog2e, -ref));
-        s = s * ex2(r - ref) + ((t[0] + t[1]) + (t[2] + t[3]));
-        r = top == INFINITY ? 0.0f : top;
+        for (int i = 0; i < 32; i += 2) {
+            float e[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                e[k] = ex2(fmaf(v[k][i], kLog2e, -ref));
+                e[4 + k] = ex2(fmaf(v[k][i + 1], kLog2e, -ref));
+            }
+            t[(i >> 1) & 3] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        }
+        s = (t[0] + t[1]) + (t[2] + t[3]);
+        r = top == INFINITY ? 0.0f : fmaxf(top, -INFINITY);  // NaN, of a row of nothing else, to -inf
     }
 
     // Another part of the row. A sum of 0 or infinity stays what it is whatever
@@ -372,19 +411,32 @@ struct RowGrad {
     bool live = false;
 };
 
-__device__ __forceinline__ RowGrad row_grad(const HeadParams &p, int row, int v0)
+// A row's values as they come from memory: asked for a unit ahead, since an
+// epilogue that is behind has nothing to wait with.
+struct RowValues {
+    int y;
+    float lse, d, z, by;
+
+    __device__ __forceinline__ void load(const HeadParams &p, int row)
+    {
+        const int at = min(row, p.T - 1);
+        y = __ldcg(p.targets + at);
+        lse = __ldcg(p.lse + at);
+        d = __ldcg(p.dlosses + at);
+        z = p.dlse ? __ldcg(p.dlse + at) : 0.0f;
+        by = __ldcg(p.scale);
+    }
+};
+
+__device__ __forceinline__ RowGrad row_grad(const HeadParams &p, const RowValues &r, int v0)
 {
     RowGrad g;
-    if (row < p.T) {
-        const int y = __ldcg(p.targets + row);
-        g.live = static_cast<unsigned>(y) < static_cast<unsigned>(p.V);
-        if (g.live) {
-            const float by = __ldcg(p.scale), d = __ldcg(p.dlosses + row), z = p.dlse ? __ldcg(p.dlse + row) : 0.0f;
-            g.a = (d + z) * by;
-            g.b = d * by;
-            g.lse2 = __ldcg(p.lse + row) * kLog2e;
-            g.target = y - v0;
-        }
+    g.live = static_cast<unsigned>(r.y) < static_cast<unsigned>(p.V);
+    if (g.live) {
+        g.a = (r.d + r.z) * r.by;
+        g.b = r.d * r.by;
+        g.lse2 = r.lse * kLog2e;
+        g.target = r.y - v0;
     }
     return g;
 }
@@ -432,8 +484,9 @@ __device__ __forceinline__ void load_row(const T *row, int col, int cols, bool h
 }
 
 // 64 (16-bit) or 32 (fp32) values of a thread's row into its warp's staging
-// chunk (SW128 rows) and on to global memory by TMA. A TMA store writes whole
-// 16-byte words, also the one in which a row ends, so that the map ends before
+// chunk (SW128 rows) and on to global memory by TMA (32-byte stores from
+// registers: 1 x 131072 x 4096 backward 680 us instead of 600). A TMA store
+// writes whole 16-byte words, also the one in which a row ends, so that the map ends before
 // it and store_tail writes the rest.
 template <int CW>
 __device__ __forceinline__ void stage_and_store(const uint32_t (&o)[32], uint32_t sbuf, int lane, const CUtensorMap *tmD, int col, int row,
@@ -535,48 +588,55 @@ __device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t b
     const uint32_t bar_ready = bar_halves + 16 * q, bar_free = bar_ready + 8;
     uint32_t phase = 0;
     HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
+    const HeadJob &j = p.jobs[0];
     HeadUnit h;
     while (units.next(h)) {
-        const HeadJob &j = p.jobs[0];
         const int m0 = (h.m_blk * CG + static_cast<int>(rank)) * 128 + 32 * q, row = m0 + lane;
         const int n0 = h.n_blk * j.bn, cols = min(j.bn, j.N - n0);
         const int y = row < p.T ? __ldcg(p.targets + row) - n0 : -1;
         const bool rows = m0 < p.T;  // the same for both warps
         // the parts of the sums over K, added up in registers with fp32 rounding
-        float v[4][32] = {};
-        for (int part = h.kb0; part < h.kb1; part += j.kb_part) {
+        float v[4][32];
+        for (int part = 0; part < j.kb_all; part += j.kb_part) {
             if (!a.take(w, rank))
                 return;
+            if (part == 0) {
+                // all of them: columns past the tile's lie in TMEM too, and are masked below
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (rows && 32 * half + 64 * i < cols) {
-                    add_acc16(a.columns(q, 32 * half + 64 * i), v[i]);
-                    add_acc16(a.columns(q, 32 * half + 64 * i + 16), v[i] + 16);
+                for (int i = 0; i < 4; ++i)
+                    fetch_acc32(a.columns(q, 32 * half + 64 * i), v[i]);
+                tmem_ld_wait();
+            } else if (rows) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 32 * half + 64 * i;
+                    if (c < cols) {
+                        add_acc16(a.columns(q, c), v[i]);
+                        add_acc16(a.columns(q, c + 16), v[i] + 16);
+                    }
                 }
             }
             a.release(lane);
         }
         if (!rows)
             continue;
-        RunningSoftmax sm;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c = 32 * half + 64 * i;
-            if (c < cols) {
-                if (c + 32 > cols) {
+            if (c + 32 > cols) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        v[i][k] = c + k < cols ? v[i][k] : -INFINITY;
-                }
-                sm.add(v[i]);
-                const bool mine = y >= c && y < min(c + 32, cols);
-                if (__any_sync(0xffffffffu, mine)) {
-                    const float x = pick32(v[i], y - c);
-                    if (mine)
-                        p.picked[row] = x;
-                }
+                for (int k = 0; k < 32; ++k)
+                    v[i][k] = c + k < cols ? v[i][k] : -INFINITY;
+            }
+            const bool mine = y >= c && y < min(c + 32, cols);
+            if (__any_sync(0xffffffffu, mine)) {
+                const float x = pick32(v[i], y - c);
+                if (mine)
+                    p.picked[row] = x;
             }
         }
+        RunningSoftmax sm;
+        sm.take(v);
         if (half == 1) {
             if (!__all_sync(0xffffffffu, w.wait(bar_free, phase ^ 1u, kRoleEpilogue | kWaitPartial)))
                 return;
@@ -600,15 +660,18 @@ __device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t b
 
 // One tile of dl.
 template <int CG>
-__device__ __forceinline__ void logit_grad_tile(const HeadParams &p, const HeadJob &j, const CUtensorMap *map, const RowGrad &g,
-                                                const Accumulators<CG> &a, int q, int half, int m0, int n0, int cols, uint32_t sbuf, int lane)
+__device__ __forceinline__ void logit_grad_tile(const HeadParams &p, const CUtensorMap *map, const RowGrad &g, const Accumulators<CG> &a, int q,
+                                                int half, int m0, int n0, int cols, uint32_t sbuf, int lane)
 {
     for (int c = 64 * half; c < cols; c += 128) {
         uint32_t o[32];
+        float x[2][32];
+        fetch_acc32(a.columns(q, c), x[0]);
+        fetch_acc32(a.columns(q, c + 32), x[1]);
+        tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float v[32];
-            load_acc32(a.columns(q, c + 32 * i), v);
+            float (&v)[32] = x[i];
 #pragma unroll
             for (int k = 0; k < 32; ++k)
                 v[k] = g.live ? ex2(fmaf(v[k], kLog2e, -g.lse2)) * g.a : 0.0f;
@@ -643,7 +706,8 @@ __device__ __forceinline__ void product_tile(const HeadParams &p, const HeadJob 
             if (j.c_raw)
                 load_row<float, 32>(j.c_raw + (split * j.slot_rows + row) * j.ld_raw, at, j.N, have, old);
             __syncwarp();
-            load_acc32(a.columns(q, c + 32 * i), v);
+            fetch_acc32(a.columns(q, c + 32 * i), v);
+            tmem_ld_wait();
             if (j.c_raw) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
@@ -688,30 +752,33 @@ __device__ void gradient_epilogue(const HeadParams &p, const HeadMaps &maps, uin
 {
     const int q = warp & 3, half = (warp - 2) >> 2;
     HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
+    auto first_row = [&](const HeadUnit &u) { return (u.m_blk * CG + static_cast<int>(rank)) * 128 + 32 * q; };
     HeadUnit h;
-    while (units.next(h)) {
+    RowValues values = {}, next_values = {};
+    bool more = units.next(h);
+    if (more && p.jobs[h.job].epi == kEpiLogitGrad)
+        next_values.load(p, first_row(h) + lane);
+    while (more) {
         const HeadJob &j = p.jobs[h.job];
         const CUtensorMap *const map = &maps.d[h.job];
-        const int m0 = (h.m_blk * CG + static_cast<int>(rank)) * 128 + 32 * q;
+        const int m0 = first_row(h), split = h.split;
         const int n0 = h.n_blk * j.bn, cols = min(j.bn, j.N - n0);
-        const bool of_logits = j.epi == kEpiLogitGrad;
-        RowGrad g;
-        if (of_logits)
-            g = row_grad(p, m0 + lane, j.v0);
+        values = next_values;
+        more = units.next(h);
+        if (more && p.jobs[h.job].epi == kEpiLogitGrad)
+            next_values.load(p, first_row(h) + lane);
         if (!a.take(w, rank))
             return;
         if (m0 < j.M) {  // the same for the whole warp
-            if (of_logits)
-                logit_grad_tile<CG>(p, j, map, g, a, q, half, m0, n0, cols, sbuf, lane);
+            if (j.epi == kEpiLogitGrad)
+                logit_grad_tile<CG>(p, map, row_grad(p, values, j.v0), a, q, half, m0, n0, cols, sbuf, lane);
             else if (j.out_type == 0)
-                product_tile<CG, 32>(p, j, map, a, q, half, m0, n0, cols, h.split, sbuf, lane);
+                product_tile<CG, 32>(p, j, map, a, q, half, m0, n0, cols, split, sbuf, lane);
             else
-                product_tile<CG, 64>(p, j, map, a, q, half, m0, n0, cols, h.split, sbuf, lane);
+                product_tile<CG, 64>(p, j, map, a, q, half, m0, n0, cols, split, sbuf, lane);
         }
         a.release(lane);
     }
-    if (lane == 0)
-        bulk_wait_group<0>();
 }
 
 // ---------------------------------------------------------------- kernel
@@ -792,6 +859,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_kernel(const __grid_cons
             softmax_epilogue<CG>(p, reinterpret_cast<float2 *>(smem + (staging - base)), bar_halves, a, rank, warp, lane, w);
         else
             gradient_epilogue<CG>(p, maps, staging + static_cast<uint32_t>((warp - 2) * kEpiBufBytes), a, rank, warp, lane, w);
+        if (!FORWARD && lane == 0)
+            bulk_wait_group<0>();  // stores have finished reading shared memory
     }
     __syncwarp();
     __syncthreads();  // every role has returned: the abort flag is final
@@ -1006,6 +1075,17 @@ struct Operand {
     int64_t ld;
 };
 
+Divisor divisor(int64_t d)
+{
+    Divisor v = {static_cast<unsigned>(d), 0u, 0};
+    if (d > 1) {
+        while ((int64_t(1) << (v.shift + 1)) < d)
+            ++v.shift;  // 2^shift < d <= 2^(shift + 1)
+        v.m = static_cast<unsigned>(((uint64_t(1) << (32 + v.shift)) + d - 1) / d);
+    }
+    return v;
+}
+
 // A product of a launch as the host builds it.
 struct Job {
     HeadJob j;
@@ -1015,9 +1095,11 @@ struct Job {
 
 // What a block of K costs on a tile `bn` wide, in columns: a pair's time goes
 // with the operands' bytes, which the tiles' 256 rows share (4096 x 16384 x 4096:
-// 14.0 us a round of 128 columns, 20.9 of 256); few tokens leave the SMs waiting
-// for the weights alone.
-int64_t tile_cost(int cg, int bn) { return cg == 2 ? bn + 160 : bn; }
+// 14.0 us a round of 128 columns, 20.9 of 256). Few tokens leave the SMs waiting
+// for the weights, and a little for each tile: 1 x 131072 x 4096 took 168 us by
+// six tiles of 144 columns a CTA and 161 by four of 224, 77 x 50001 x 2001 52.5
+// by three of 112 and 43.8 by two of 176.
+int64_t tile_cost(int cg, int bn) { return cg == 2 ? bn + 160 : bn + 16; }
 
 template <int CG>
 gemm_status_t make_job(Job *job, int bn, int splits, int64_t M, int64_t N, int64_t K, int in_bf16, const Operand &A, const Operand &B, int a_rows)
@@ -1026,7 +1108,7 @@ gemm_status_t make_job(Job *job, int bn, int splits, int64_t M, int64_t N, int64
     HeadJob &j = job->j;
     const int64_t tiles_m = (M + 128 * CG - 1) / (128 * CG), tiles_n = (N + bn - 1) / bn;
     const int64_t kb = (K + BK - 1) / BK, unit = (kb + splits - 1) / splits, parts = (kb + unit - 1) / unit;
-    if (tiles_m * tiles_n * parts > kSizeLimit)
+    if (tiles_m * tiles_n * parts > kSizeLimit / 2)  // a cluster's last step may pass the end once
         return GEMM_ERR_UNSUPPORTED;
     j.M = static_cast<int>(M);
     j.N = static_cast<int>(N);
@@ -1034,7 +1116,11 @@ gemm_status_t make_job(Job *job, int bn, int splits, int64_t M, int64_t N, int64
     j.tiles_m = static_cast<int>(tiles_m);
     j.tiles_n = static_cast<int>(tiles_n);
     j.units = static_cast<int>(tiles_m * tiles_n * parts);
-    j.group_m = 8;
+    j.group_m = static_cast<int>(std::min<int64_t>(8, tiles_m));
+    j.by_tiles = divisor(tiles_m * tiles_n);
+    j.by_group = divisor(j.group_m * tiles_n);
+    j.by_rows = divisor(j.group_m);
+    j.by_last_rows = divisor(tiles_m % j.group_m ? tiles_m % j.group_m : j.group_m);
     j.kb_all = static_cast<int>(kb);
     j.kb_unit = static_cast<int>(unit);
     j.kb_part = static_cast<int>(unit);
@@ -1139,8 +1225,6 @@ struct BackPlan {
     size_t xs, dl[2], parts, bytes;  // offsets
 };
 
-constexpr int64_t kPieceColumns = 16384;
-
 BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
 {
     BackPlan b = {};
@@ -1176,12 +1260,14 @@ BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
     return b;
 }
 
-// Widest pieces that are taken for a shape. Few tokens wait for memory: what a
-// launch reads and writes of the weights and their gradient (three pieces) shall
-// stay in L2, where the next launch reads one of them again.
-int64_t widest_piece(int64_t T, int64_t K)
+// Widest pieces that are taken: a piece's dl has 256 MB at most. Few tokens wait
+// for memory, and have all of the vocabulary in one piece: pieces small enough
+// to stay in L2 from one launch to the next left most SMs without tiles (1 x
+// 131072 x 4096: 1140 us in pieces of 8192, WHOLE1 in one; 128 x 131072 x 2048:
+// 499 and WHOLE128).
+int64_t widest_piece(int64_t T)
 {
-    return T > 512 ? kPieceColumns : std::max<int64_t>(2048, std::min<int64_t>(kPieceColumns, (int64_t(16) << 20) / K / 256 * 256));
+    return std::max<int64_t>(256, (int64_t(1) << 27) / std::max<int64_t>(T, 1) / 256 * 256);
 }
 
 // What both calls check of their shape.
@@ -1239,7 +1325,6 @@ struct BackArgs {
 template <int CG>
 gemm_status_t run_backward(HeadParams p, const BackArgs &g, const BackPlan &b, int sms, cudaStream_t st)
 {
-    p.a_rows = 128;
     const int ew = type_bytes(g.dw_type);
     float *parts = reinterpret_cast<float *>(g.ws + b.parts);
     for (int64_t i = -1; i < b.pieces; ++i) {
@@ -1247,6 +1332,8 @@ gemm_status_t run_backward(HeadParams p, const BackArgs &g, const BackPlan &b, i
         int n = 0;
         gemm_status_t s;
         const int64_t v0 = i * b.piece, cols = std::min(b.piece, g.V - v0);
+        // dl alone: places of few rows leave the stages to the weights
+        p.a_rows = CG == 1 && i < 0 ? static_cast<int>(std::min<int64_t>(128, round_up(g.T, 8))) : 128;
         if (i >= 0 && g.dX) {
             Job &job = jobs[n++];
             if ((s = make_job<CG>(&job, b.dx_bn, b.dx_splits, g.T, g.K, cols, g.in_type, {g.ws + b.dl[i & 1], 0, b.ldp},
@@ -1291,9 +1378,10 @@ gemm_status_t run_backward(HeadParams p, const BackArgs &g, const BackPlan &b, i
         if (i + 1 < b.pieces) {
             Job &job = jobs[n++];
             const int64_t w0 = (i + 1) * b.piece, next = std::min(b.piece, g.V - w0);
-            // where it has a launch of its own, by its own rounds of the grid
-            const int bn = n == 1 ? logit_columns(CG, g.T, next, 128, 64, sms) : 256;
-            if ((s = make_job<CG>(&job, bn, 1, g.T, next, g.K, g.in_type, g.X, {static_cast<const char *>(g.W.ptr) + w0 * g.W.ld * 2, 0, g.W.ld}, 128)) !=
+            // by its own rounds of the grid, where it has a launch to itself or too few wide tiles for all clusters
+            const int64_t wide = (g.T + 128 * CG - 1) / (128 * CG) * ((next + 255) / 256);
+            const int bn = n == 1 || wide < 2 * sms / CG ? logit_columns(CG, g.T, next, p.a_rows, 64, sms) : 256;
+            if ((s = make_job<CG>(&job, bn, 1, g.T, next, g.K, g.in_type, g.X, {static_cast<const char *>(g.W.ptr) + w0 * g.W.ld * 2, 0, g.W.ld}, p.a_rows)) !=
                 GEMM_OK)
                 return s;
             job.j.epi = kEpiLogitGrad;
@@ -1360,7 +1448,7 @@ size_t gemm_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t 
     unsigned int *status = nullptr;
     if (host_device(&dev, &status, &sms) != GEMM_OK)
         return 0;
-    const int64_t widest = widest_piece(T, K);
+    const int64_t widest = std::min(round_up(V, 256), widest_piece(T));
     return back_plan(T, V, K, columns ? std::min(widest, round_up(columns, 256)) : widest, sms).bytes;
 }
 
@@ -1396,11 +1484,15 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
         return s;
     // the largest pieces that the workspace has room for, up to the usual ones
     BackPlan b = {};
-    for (int64_t piece = widest_piece(T, K); piece >= 256; piece -= 256) {
-        b = back_plan(T, V, K, piece, sms);
-        if (b.bytes <= workspace_bytes)
-            break;
+    int64_t low = 1, high = std::min(round_up(V, 256), widest_piece(T)) / 256;
+    while (low < high) {
+        const int64_t mid = (low + high + 1) / 2;
+        if (back_plan(T, V, K, 256 * mid, sms).bytes <= workspace_bytes)
+            low = mid;
+        else
+            high = mid - 1;
     }
+    b = back_plan(T, V, K, 256 * low, sms);
     if (b.bytes > workspace_bytes)
         return GEMM_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);

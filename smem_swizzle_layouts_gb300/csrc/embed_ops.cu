@@ -65,13 +65,14 @@ union Vector {
     }
 };
 
-// An item is 16 bytes of the output (WIDE: rows of 16-byte words) or a single
-// element. Bound by memory. I: a type that counts all items.
-template <typename S, typename D, bool WIDE, typename I>
+// Rows of 16-byte words: an item is 16 bytes of the output. Bound by memory:
+// 8192 rows of 4096 bf16 in 13.6 us, to fp32 27.6 us. I: a type that counts all
+// items.
+template <typename S, typename D, typename I>
 __global__ void __launch_bounds__(kEmbedThreads)
     embed_kernel(const S *table, long long ldt, const int *ids, D *d, long long ldd, unsigned items, I all, int V, float scale)
 {
-    constexpr int VEC = WIDE ? 16 / static_cast<int>(sizeof(D)) : 1;
+    constexpr int VEC = 16 / static_cast<int>(sizeof(D));
     grid_start();
     const I first = static_cast<I>(blockIdx.x) * (kEmbedThreads * kEmbedItems) + threadIdx.x;
     Vector<S, VEC> v[kEmbedItems];
@@ -107,11 +108,31 @@ __global__ void __launch_bounds__(kEmbedThreads)
     }
 }
 
-// ---------------------------------------------------------------- order by id
+// Other rows, by single elements side by side: the block's x threads walk a row.
+template <typename S, typename D>
+__global__ void __launch_bounds__(kEmbedThreads)
+    embed_narrow_kernel(const S *table, long long ldt, const int *ids, D *d, long long ldd, long long T, int N, int V, float scale)
+{
+    const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    grid_start();
+    if (t >= T)
+        return;
+    const int id = ids[t];
+    const bool have = static_cast<unsigned>(id) < static_cast<unsigned>(V);
+    const S *from = table + (have ? id : 0) * ldt;
+    D *to = d + t * ldd;
+    const int step = static_cast<int>(blockDim.x);
+    for (int c = threadIdx.x; c < N; c += 8 * step) {
+        float v[8];
+        load8<S, false>(from, c, step, have ? N : 0, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] *= scale;
+        store8<D, false>(to, c, step, N, v);
+    }
+}
 
-constexpr int kBlockWarps = 32;
-constexpr int kBlockSteps = 16;                             // of 32 entries for each warp
-constexpr int kBlockMost = 32 * kBlockWarps * kBlockSteps;  // entries that one block sorts
+// ---------------------------------------------------------------- order by id
 
 constexpr int kSortWarps = 16;
 constexpr int kSortMaxBins = 512;
@@ -126,7 +147,7 @@ struct SortPass {
     const int *tokens;  // null: an entry's own place
     int *ids_out, *tokens_out;
     long long n;        // of the first pass
-    int *kept;          // entries that are left after it
+    int *kept;          // entries that are left after it; behind it a counter for the sums, which starts at 0
     int *counts;        // [block][bins]
     int V, shift, bits, bins, blocks;
     bool first;
@@ -150,23 +171,22 @@ SortPlan sort_plan(int64_t T, int64_t V)
     SortPlan p;
     p.passes = (bits + 8) / 9;
     p.bits = (bits + p.passes - 1) / p.passes;
-    p.blocks = T <= kBlockMost ? 1 : static_cast<int>(std::min<int64_t>(kSortMaxBlocks, (T + kSortPart - 1) / kSortPart));
+    p.blocks = static_cast<int>(std::min<int64_t>(kSortMaxBlocks, (T + kSortPart - 1) / kSortPart));
     return p;
 }
 
 template <typename U>
-__device__ __forceinline__ void write_zeros(U *d, long long ld, long long row, long long lo, long long hi, int block, int blocks)
+__device__ __forceinline__ void write_zeros(U *d, long long ld, long long row, long long lo, long long hi, int thread, int threads)
 {
-    const long long step = static_cast<long long>(blocks) * blockDim.x;
     const U zero = {};
-    long long i = lo + static_cast<long long>(block) * blockDim.x + threadIdx.x;
+    long long i = lo + thread;
     if (ld == row) {
-#pragma unroll 4
-        for (; i < hi; i += step)
+#pragma unroll 8
+        for (; i < hi; i += threads)
             d[i] = zero;
         return;
     }
-    for (; i < hi; i += step)
+    for (; i < hi; i += threads)
         d[i / row * ld + i % row] = zero;
 }
 
@@ -176,11 +196,12 @@ __device__ __forceinline__ bool sort_zeros(const SortPass &p)
     const int block = static_cast<int>(blockIdx.x) - p.blocks;
     if (block < 0)
         return false;
-    const int blocks = static_cast<int>(gridDim.x) - p.blocks;
+    const int threads = (static_cast<int>(gridDim.x) - p.blocks) * static_cast<int>(blockDim.x);
+    const int thread = block * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
     if (p.wide)
-        write_zeros(static_cast<uint4 *>(p.zeros), p.ld, p.row, p.lo, p.hi, block, blocks);
+        write_zeros(static_cast<uint4 *>(p.zeros), p.ld, p.row, p.lo, p.hi, thread, threads);
     else
-        write_zeros(static_cast<uint16_t *>(p.zeros), p.ld, p.row, p.lo, p.hi, block, blocks);
+        write_zeros(static_cast<uint16_t *>(p.zeros), p.ld, p.row, p.lo, p.hi, thread, threads);
     return true;
 }
 
@@ -200,8 +221,7 @@ __device__ __forceinline__ void sort_load(const SortPass &p, long long i, long l
 __device__ __forceinline__ int sort_digit(const SortPass &p, int id) { return (id >> p.shift) & (p.bins - 1); }
 
 // The lanes that have this lane's digit: a ballot for each of its bits, which is
-// quicker than a match over the warp's 32 values (16384 entries of 15 bits,
-// sorted by one block: MATCH_US us by matches).
+// quicker than a match over the warp's 32 values.
 __device__ __forceinline__ unsigned sort_peers(int digit, int bits, bool valid)
 {
     unsigned same = __ballot_sync(0xffffffffu, valid);
@@ -302,8 +322,10 @@ __device__ void sort_scatter(const SortPass &p, int *hist, int *start, int *befo
         at += w < warp ? warp_total[w] : 0;
         kept += warp_total[w];
     }
-    if (p.first && blockIdx.x == 0 && tid == 0)
-        *p.kept = kept;
+    if (p.first && blockIdx.x == 0 && tid == 0) {
+        p.kept[0] = kept;
+        p.kept[1] = 0;
+    }
     // first place of each warp's entries of each bin
     if (tid < bins) {
         at += before[tid];
@@ -348,125 +370,208 @@ __global__ void __launch_bounds__(32 * kSortWarps) sort_scatter_kernel(const Sor
     sort_scatter(p, sort_smem, sort_smem + kSortWarps * p.bins, sort_smem + (kSortWarps + 1) * p.bins);
 }
 
-// All passes of a list that one block sorts: the entries are held in registers
-// from counting to handing out, and go from pass to pass through shared memory.
-// Several launches of more blocks wait longer for one another than they save
-// (16384 entries: 30 us by four launches, all but hidden behind 134 MB of zeros
-// by this one).
-__global__ void __launch_bounds__(32 * kBlockWarps) sort_block_kernel(const SortPass p, int passes, int *ids_out, int *tokens_out)
+// Up to 16384 tokens: one launch. Each block has a range of ids and looks through
+// all of the list (which L2 holds) for those of its range: it counts the ids
+// below the range, which is where its own begin in the order, and its own by
+// warp and id; then it hands them out, each warp its run of the list. Of a
+// gradient that is written whole, warps of their own zero its range's rows
+// meanwhile. Blocks need nothing of one another. (A counting sort by digits
+// takes four launches that wait for one another; by one block of 32 warps it
+// took 35 us for 16384 tokens of 32768 ids.)
+constexpr int kRangeWarps = 16;
+constexpr int kRangeBatch = 16;         // entries a lane has in flight
+constexpr int kRangeBlocks = 152;       // at least: one for each SM of the GPU this is built for
+constexpr int kRangeMostIds = 1024;     // of a block
+constexpr int kRangeMostBlocks = 1024;
+constexpr int64_t kRangeMostTokens = 16384;
+constexpr int kZeroWarps = 16;          // of a block that writes its range's zeros meanwhile
+
+inline bool sort_by_range(int64_t T, int64_t V) { return T <= kRangeMostTokens && V <= static_cast<int64_t>(kRangeMostIds) * kRangeMostBlocks; }
+
+struct RangePass {
+    const int *ids;
+    int *ids_out, *tokens_out, *kept;
+    int T, V, per;  // ids of a block
+    void *zeros;    // the table, or null: rows as in SortPass
+    bool wide;
+    long long ld, row, all;
+};
+
+// The sorting warps' barrier.
+__device__ __forceinline__ void range_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kRangeWarps) : "memory"); }
+
+__global__ void __launch_bounds__(32 * (kRangeWarps + kZeroWarps)) sort_range_kernel(const RangePass p)
 {
-    extern __shared__ int sort_smem[];
-    __shared__ int warp_total[kBlockWarps];
-    const int bits = p.bits, bins = p.bins, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int *hist = sort_smem;                                        // [warp][bin]
-    int *list = hist + kBlockWarps * bins;                        // ids between two passes
-    uint16_t *places = reinterpret_cast<uint16_t *>(list + p.n);  // and their tokens
-    grid_start();
-    if (sort_zeros(p))
+    extern __shared__ int range_smem[];
+    __shared__ int warp_total[kRangeWarps], below_all, all_kept;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *hist = range_smem;  // [warp][id of the range]
+    const int first = static_cast<int>(blockIdx.x) * p.per, n = min(p.per, p.V - first);
+    if (warp >= kRangeWarps) {
+        grid_start();
+        // all blocks walk the table side by side
+        const int thread = tid - 32 * kRangeWarps + static_cast<int>(blockIdx.x) * (32 * kZeroWarps), threads = static_cast<int>(gridDim.x) * (32 * kZeroWarps);
+        if (p.wide)
+            write_zeros(static_cast<uint4 *>(p.zeros), p.ld, p.row, 0, p.all, thread, threads);
+        else
+            write_zeros(static_cast<uint16_t *>(p.zeros), p.ld, p.row, 0, p.all, thread, threads);
         return;
-    int n = static_cast<int>(p.n), id[kBlockSteps], token[kBlockSteps];
-    for (int pass = 0; pass < passes; ++pass) {
-        const int steps = (n + 32 * kBlockWarps - 1) / (32 * kBlockWarps), lo = warp * 32 * steps + lane;
+    }
+    for (int i = tid; i < kRangeWarps * n; i += 32 * kRangeWarps)
+        hist[i] = 0;
+    if (tid == 0)
+        below_all = all_kept = 0;
+    grid_start();
+    range_sync();
+    // the warp's run of the list, whole steps of 32
+    const int run = ((p.T + kRangeWarps - 1) / kRangeWarps + 31) / 32 * 32;
+    const int lo = min(warp * run, p.T), hi = min(lo + run, p.T);
+    int *mine = hist + warp * n;
+    int below = 0, kept = 0;
+    for (int i0 = lo; i0 < hi; i0 += 32 * kRangeBatch) {
+        int id[kRangeBatch];
 #pragma unroll
-        for (int u = 0; u < kBlockSteps; ++u) {
-            const int i = lo + 32 * u;
-            id[u] = -1;
-            if (u < steps && i < n) {
-                id[u] = pass == 0 ? __ldcg(p.ids + i) : list[i];
-                token[u] = pass == 0 ? i : places[i];
+        for (int u = 0; u < kRangeBatch; ++u)
+            id[u] = i0 + 32 * u + lane < hi ? __ldcg(p.ids + i0 + 32 * u + lane) : -1;
+#pragma unroll
+        for (int u = 0; u < kRangeBatch; ++u) {
+            if (static_cast<unsigned>(id[u]) < static_cast<unsigned>(p.V)) {
+                ++kept;
+                below += id[u] < first;
+                if (static_cast<unsigned>(id[u] - first) < static_cast<unsigned>(n))
+                    atomicAdd(&mine[id[u] - first], 1);  // a count: the order of the additions does not show
             }
         }
-        for (int i = tid; i < kBlockWarps * bins; i += 32 * kBlockWarps)
-            hist[i] = 0;
-        __syncthreads();
-        const int shift = pass * bits;
-        int *mine = hist + warp * bins;
+    }
+    below = __reduce_add_sync(0xffffffffu, below);
+    kept = __reduce_add_sync(0xffffffffu, kept);
+    if (lane == 0) {
+        atomicAdd(&below_all, below);
+        atomicAdd(&all_kept, kept);
+    }
+    range_sync();
+    if (blockIdx.x == 0 && tid == 0) {
+        p.kept[0] = all_kept;
+        p.kept[1] = 0;
+    }
+    // where each id's entries begin, two ids a thread, and each warp's of them
+    static_assert(kRangeMostIds <= 2 * 32 * kRangeWarps, "two ids a thread");
+    int total[2] = {};
 #pragma unroll
-        for (int u = 0; u < kBlockSteps; ++u) {
-            if (static_cast<unsigned>(id[u]) >= static_cast<unsigned>(p.V))
-                id[u] = -1;
-            if (id[u] >= 0)
-                atomicAdd(&mine[(id[u] >> shift) & (bins - 1)], 1);  // a count: the order of the additions does not show
-        }
-        __syncthreads();
-        int total = 0;  // of bin tid
-        if (tid < bins) {
-#pragma unroll 8
-            for (int w = 0; w < kBlockWarps; ++w)
-                total += hist[w * bins + tid];
-        }
-        int incl = total;
+    for (int k = 0; k < 2; ++k)
+        if (2 * tid + k < n) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += v;
+            for (int w = 0; w < kRangeWarps; ++w)
+                total[k] += hist[w * n + 2 * tid + k];
         }
-        if (lane == 31)
-            warp_total[warp] = incl;
-        __syncthreads();
-        int at = incl - total, kept = 0;
-#pragma unroll 8
-        for (int w = 0; w < kBlockWarps; ++w) {
-            at += w < warp ? warp_total[w] : 0;
-            kept += warp_total[w];
-        }
-        if (tid < bins) {
-#pragma unroll 8
-            for (int w = 0; w < kBlockWarps; ++w) {
-                const int c = hist[w * bins + tid];
-                hist[w * bins + tid] = at;
+    const int sum = total[0] + total[1];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += v;
+    }
+    if (lane == 31)
+        warp_total[warp] = incl;
+    range_sync();
+    int at = below_all + incl - sum, own = 0;
+#pragma unroll
+    for (int w = 0; w < kRangeWarps; ++w) {
+        at += w < warp ? warp_total[w] : 0;
+        own += warp_total[w];
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (2 * tid + k < n) {
+            const int id = 2 * tid + k;
+#pragma unroll
+            for (int w = 0; w < kRangeWarps; ++w) {
+                const int c = hist[w * n + id];
+                hist[w * n + id] = at;
                 at += c;
             }
         }
-        __syncthreads();
+    range_sync();
+    if (own == 0)
+        return;
+    for (int i0 = lo; i0 < hi; i0 += 32 * kRangeBatch) {
+        int id[kRangeBatch];
 #pragma unroll
-        for (int u = 0; u < kBlockSteps; ++u) {
-            if (u < steps) {
-                const int b = (id[u] >> shift) & (bins - 1);
-                const unsigned same = sort_peers(b, bits, id[u] >= 0);
-                int place = -1;
-                if (id[u] >= 0)
-                    place = mine[b] + __popc(same & ((1u << lane) - 1u));
-                __syncwarp();
-                if (id[u] >= 0 && (same >> lane) == 1u)  // the last of its bin moves the count on
-                    mine[b] = place + 1;
-                __syncwarp();
-                if (place >= 0) {
-                    if (pass == passes - 1) {
-                        ids_out[place] = id[u];
-                        tokens_out[place] = token[u];
-                    } else {
-                        list[place] = id[u];
-                        places[place] = static_cast<uint16_t>(token[u]);
-                    }
+        for (int u = 0; u < kRangeBatch; ++u)
+            id[u] = i0 + 32 * u + lane < hi ? __ldcg(p.ids + i0 + 32 * u + lane) - first : -1;
+#pragma unroll
+        for (int u = 0; u < kRangeBatch; ++u) {
+            unsigned left = __ballot_sync(0xffffffffu, static_cast<unsigned>(id[u]) < static_cast<unsigned>(n));
+            while (left) {  // an id at a time: a block has few of 32 entries, or the same ones often
+                const int who = __shfl_sync(0xffffffffu, id[u], __ffs(left) - 1);
+                const unsigned same = __ballot_sync(0xffffffffu, id[u] == who) & left;
+                const int place = mine[who];
+                if (id[u] == who) {
+                    const int to = place + __popc(same & ((1u << lane) - 1u));
+                    p.ids_out[to] = who + first;
+                    p.tokens_out[to] = i0 + 32 * u + lane;
                 }
+                __syncwarp();
+                if (lane == 0)
+                    mine[who] = place + __popc(same);
+                __syncwarp();
+                left &= ~same;
             }
         }
-        n = kept;
-        __syncthreads();
     }
-    if (tid == 0)
-        *p.kept = n;
 }
 
-std::atomic<uint64_t> sort_attribute_set[2] = {{0}, {0}};
+std::atomic<uint64_t> range_attribute_set[2] = {{0}, {0}};
 
 // ---------------------------------------------------------------- sums
 
 constexpr int kMaxChunk = 32;       // sorted entries of a block at most
 constexpr int kSumThreads = 128;    // of eight columns each
 constexpr int kSumColumns = 8 * kSumThreads;
-constexpr int kJoinGroups = 4;      // threads that share a column when chunks are joined
 constexpr int kSumBlocks = 608;     // four for each SM of the GPU this is built for
+constexpr int kJoinBlocks = 152;   // one for each
+constexpr int kJoinGroups = 4;      // of kSumThreads threads in a block that joins chunks
+constexpr int kJoinAlone = 8;       // parts that one group joins by itself
 
 struct SumParams {
+    long long T;
     const int *ids, *tokens, *kept;
+    int *crossing, *crossings;  // the chunks in which a run begins that passes their end, in any order, and their number
     long long lddd, ldt;
     int N, accumulate, col_blocks, chunk;
     float scale;
     float *parts;  // [2 * chunks][N8]: a chunk's first run where it began before, its last where it goes on
     long long ld_parts;
+};
+
+// Eight elements of a row as load8 takes them, not yet widened.
+template <typename T>
+struct Eight {
+    union {
+        uint4 w[sizeof(T) / 2];
+        T e[8];
+    };
+    __device__ __forceinline__ Eight() {}
+    template <bool WIDE>
+    __device__ __forceinline__ void load(const T *p, int at, int step, int n)
+    {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+                w[i] = at < n ? reinterpret_cast<const uint4 *>(p + at)[i] : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                e[i] = at + i * step < n ? p[at + i * step] : from_float<T>(0.0f);
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = to_float(e[i]);
+    }
 };
 
 // dtable[id] = scale * sum (+ what it holds)
@@ -486,120 +591,172 @@ __device__ __forceinline__ void finish_row(W *row, int c, int N, float (&acc)[8]
 template <typename D, typename W, bool WIDE>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const D *dd, W *dtable, const SumParams p)
 {
-    __shared__ int ids[kMaxChunk + 2], tokens[kMaxChunk];  // with the entries before and behind
+    constexpr int ROWS = WIDE && sizeof(D) == 2 ? 8 : 4;  // in flight: as many as registers hold
+    __shared__ int ids[kMaxChunk + 2];                    // with the entries before and behind
+    __shared__ long long rows[kMaxChunk];
     const int tid = threadIdx.x;
     const long long chunk = blockIdx.x / p.col_blocks;
-    const int c = static_cast<int>(blockIdx.x - chunk * p.col_blocks) * kSumColumns + (WIDE ? 8 : 1) * tid;
+    const int col_block = static_cast<int>(blockIdx.x - chunk * p.col_blocks);
+    const int c = col_block * kSumColumns + (WIDE ? 8 : 1) * tid;
     grid_start();
-    const long long kept = __ldcg(p.kept), lo = chunk * p.chunk;
+    const long long lo = chunk * p.chunk, i = lo + tid - 1;
+    // asked for together; what lies past the kept entries is not looked at
+    const bool near = tid < p.chunk + 2 && i >= 0 && i < p.T;
+    const int id = near ? __ldcg(p.ids + i) : -1, token = near ? __ldcg(p.tokens + i) : 0;
+    const long long kept = __ldcg(p.kept);
     if (lo >= kept)
         return;
     const int n = static_cast<int>(min(kept - lo, static_cast<long long>(p.chunk)));
-    if (tid < p.chunk + 2) {
-        const long long i = lo + tid - 1;
-        ids[tid] = i >= 0 && i < kept ? __ldcg(p.ids + i) : -1;
-        if (tid < n)
-            tokens[tid] = __ldcg(p.tokens + lo + tid);
-    }
+    if (tid < p.chunk + 2)
+        ids[tid] = i < kept ? id : -1;
+    // places past the last name the first row, which is not added for them
+    if (tid > 0 && tid <= p.chunk)
+        rows[tid - 1] = (tid <= n ? token : 0) * p.lddd;
     __syncthreads();
     if (c >= p.N)
         return;
     float acc[8] = {};
     int run = ids[1];
     bool before = ids[0] == run;  // the run began in an earlier chunk
-    auto flush = [&](bool behind) {
-        if (!before && !behind) {
+    auto part = [&](int which) { store8<float, WIDE>(p.parts + (2 * chunk + which) * p.ld_parts, c, kSumThreads, p.N, acc); };
+    auto flush = [&]() {
+        if (before)
+            part(0);
+        else
             finish_row<W, WIDE>(dtable + run * p.ldt, c, p.N, acc, p.scale, p.accumulate);
-        } else {
-            float *part = p.parts + (2 * chunk + (before ? 0 : 1)) * p.ld_parts;
-            store8<float, WIDE>(part, c, kSumThreads, p.N, acc);
-        }
     };
-    for (int j0 = 0; j0 < n; j0 += 4) {
-        float v[4][8];
+    for (int j0 = 0; j0 < n; j0 += ROWS) {
+        Eight<D> raw[ROWS];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            load8<D, WIDE>(dd + (j0 + u < n ? tokens[j0 + u] : 0) * p.lddd, c, kSumThreads, j0 + u < n ? p.N : 0, v[u]);
+        for (int u = 0; u < ROWS; ++u)
+            raw[u].template load<WIDE>(dd + rows[j0 + u], c, kSumThreads, p.N);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (j0 + u < n) {
-                const int id = ids[1 + j0 + u];
-                if (id != run) {
-                    flush(false);
-                    run = id;
-                    before = false;
+        for (int u = 0; u < ROWS; ++u) {
+            if (j0 + u >= n)
+                break;
+            float v[8];
+            raw[u].values(v);
+            const int next = ids[1 + j0 + u];
+            if (next != run) {
+                flush();
+                run = next;
+                before = false;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        acc[i] = v[u][i];
-                } else {
+                for (int k = 0; k < 8; ++k)
+                    acc[k] = v[k];
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        acc[i] += v[u][i];
-                }
+                for (int k = 0; k < 8; ++k)
+                    acc[k] += v[k];
             }
         }
     }
-    flush(n == p.chunk && ids[p.chunk + 1] == run);
+    if (n == p.chunk && ids[p.chunk + 1] == run && !before) {
+        part(1);  // the run goes on behind the chunk
+        if (col_block == 0 && tid == 0)
+            p.crossing[atomicAdd(p.crossings, 1)] = static_cast<int>(chunk);
+    } else {
+        flush();
+    }
 }
 
 // Joins the parts of each run that passes a chunk's end, in the order of the
-// chunks: a block for the chunk in which the run begins, its groups of threads
-// for equal shares of the chunks behind it.
+// chunks. A group of threads takes a run (1024 columns of it) of the list, whose
+// order does not show, as its sums' orders are its own; where it has many
+// parts, all groups of the block take equal shares of it.
 template <typename W, bool WIDE>
 __global__ void __launch_bounds__(kSumThreads * kJoinGroups) embed_join_kernel(W *dtable, const SumParams p)
 {
-    __shared__ float part[kJoinGroups - 1][8][kSumThreads];
-    const int tid = threadIdx.x, group = threadIdx.y;
-    const long long chunk = blockIdx.x / p.col_blocks;
-    const int c = static_cast<int>(blockIdx.x - chunk * p.col_blocks) * kSumColumns + (WIDE ? 8 : 1) * tid;
+    __shared__ float share_sums[kJoinGroups - 1][8][kSumThreads];
+    __shared__ int long_chunk[kJoinGroups], long_cols[kJoinGroups];
+    __shared__ long long long_more[kJoinGroups];
+    const int tid = threadIdx.x, group = threadIdx.y, lane = tid & 31;
     grid_start();
-    const long long kept = __ldcg(p.kept), next = (chunk + 1) * p.chunk;
-    if (next >= kept)
-        return;
-    const int run = __ldcg(p.ids + next);
-    if (__ldcg(p.ids + next - 1) != run || (chunk > 0 && __ldcg(p.ids + next - p.chunk - 1) == run))
-        return;  // no run that begins in this chunk passes its end
-    // chunks behind this one that begin with the run: each warp narrows them
-    // down to a 32nd at a time
-    long long more = 0, most = (kept - next + p.chunk - 1) / p.chunk;  // the first `more` do, those from `most` on do not
-    while (more < most) {
-        const long long step = (most - more + 31) / 32, i = more + (tid & 31) * step;
-        const unsigned yes = __ballot_sync(0xffffffffu, i < most && __ldcg(p.ids + next + min(i, most - 1) * p.chunk) == run);
-        const int hits = __popc(yes);  // of ascending i: the first ones
-        most = min(most, more + hits * step);
-        if (hits > 0)
-            more += (hits - 1) * step + 1;
+    const int items = __ldcg(p.crossings) * p.col_blocks;
+    for (int first = blockIdx.x * kJoinGroups; first < items; first += kJoinBlocks * kJoinGroups) {
+        const int item = first + group;
+        if (tid == 0)
+            long_more[group] = 0;
+        __syncthreads();
+        if (item < items) {
+            const int chunk = __ldcg(p.crossing + item / p.col_blocks), col_block = item % p.col_blocks;
+            const long long next = (chunk + 1ll) * p.chunk, kept = __ldcg(p.kept);
+            const long long all = (kept - next + p.chunk - 1) / p.chunk;  // chunks behind this one
+            const int run = __ldcg(p.ids + next);
+            // those that begin with the run: each warp narrows them down, 32 at
+            // a time at first: the first `more` do, those from `most` on do not
+            long long more = 0, most = all;
+            for (long long step = 1; more < most; step = (most - more + 31) / 32) {
+                const long long at = more + lane * step;
+                const unsigned yes = __ballot_sync(0xffffffffu, at < most && __ldcg(p.ids + next + min(at, most - 1) * p.chunk) == run);
+                const int hits = __popc(yes);  // of ascending places: the first ones
+                if (hits < 32)
+                    most = min(most, more + hits * step);
+                if (hits > 0)
+                    more += (hits - 1) * step + 1;
+            }
+            if (more > kJoinAlone) {
+                if (tid == 0) {
+                    long_chunk[group] = chunk;
+                    long_cols[group] = col_block;
+                    long_more[group] = more;
+                }
+            } else {
+                const int c = col_block * kSumColumns + (WIDE ? 8 : 1) * tid;
+                float acc[8], v[kJoinAlone][8];
+                load8<float, WIDE>(p.parts + (2ll * chunk + 1) * p.ld_parts, c, kSumThreads, p.N, acc);
+#pragma unroll
+                for (int k = 0; k < kJoinAlone; ++k)
+                    load8<float, WIDE>(p.parts + 2 * (chunk + 1 + (k < more ? k : 0)) * p.ld_parts, c, kSumThreads, k < more ? p.N : 0, v[k]);
+#pragma unroll
+                for (int k = 0; k < kJoinAlone; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        acc[j] += v[k][j];
+                if (c < p.N)
+                    finish_row<W, WIDE>(dtable + run * p.ldt, c, p.N, acc, p.scale, p.accumulate);
+            }
+        }
+        __syncthreads();
+        for (int g = 0; g < kJoinGroups; ++g) {
+            const long long more = long_more[g];
+            if (more == 0)
+                continue;
+            const long long chunk = long_chunk[g];
+            const int c = long_cols[g] * kSumColumns + (WIDE ? 8 : 1) * tid;
+            const long long share = (more + kJoinGroups - 1) / kJoinGroups;
+            const long long from = chunk + 1 + group * share, to = min(from + share, chunk + 1 + more);
+            float acc[8] = {};
+            if (group == 0)
+                load8<float, WIDE>(p.parts + (2 * chunk + 1) * p.ld_parts, c, kSumThreads, p.N, acc);
+            for (long long k = from; k < to; k += kJoinAlone) {
+                float v[kJoinAlone][8];
+#pragma unroll
+                for (int u = 0; u < kJoinAlone; ++u)
+                    load8<float, WIDE>(p.parts + 2 * min(k + u, to - 1) * p.ld_parts, c, kSumThreads, k + u < to ? p.N : 0, v[u]);
+#pragma unroll
+                for (int u = 0; u < kJoinAlone; ++u)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        acc[j] += v[u][j];
+            }
+            if (group > 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    share_sums[group - 1][j][tid] = acc[j];
+            }
+            __syncthreads();
+            if (group == 0 && c < p.N) {
+#pragma unroll
+                for (int k = 0; k < kJoinGroups - 1; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        acc[j] += share_sums[k][j][tid];
+                finish_row<W, WIDE>(dtable + __ldcg(p.ids + (chunk + 1) * p.chunk) * p.ldt, c, p.N, acc, p.scale, p.accumulate);
+            }
+            __syncthreads();
+        }
     }
-    const long long share = (more + kJoinGroups - 1) / kJoinGroups;
-    const long long first = chunk + 1 + group * share, end = min(first + share, chunk + 1 + more);
-    float acc[8] = {};
-    if (group == 0)
-        load8<float, WIDE>(p.parts + (2 * chunk + 1) * p.ld_parts, c, kSumThreads, p.N, acc);
-    for (long long k = first; k < end; k += 4) {
-        float v[4][8];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            load8<float, WIDE>(p.parts + 2 * min(k + u, end - 1) * p.ld_parts, c, kSumThreads, k + u < end ? p.N : 0, v[u]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                acc[i] += v[u][i];
-    }
-    if (group > 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            part[group - 1][i][tid] = acc[i];
-    }
-    __syncthreads();
-    if (group > 0 || c >= p.N)
-        return;
-#pragma unroll
-    for (int g = 0; g < kJoinGroups - 1; ++g)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            acc[i] += part[g][i][tid];
-    finish_row<W, WIDE>(dtable + run * p.ldt, c, p.N, acc, p.scale, p.accumulate);
 }
 
 // ---------------------------------------------------------------- zeros
@@ -614,7 +771,7 @@ struct EmbedPlan {
     SortPlan sort;
     int chunk;
     int64_t chunks;
-    size_t kept, counts, ids_a, tokens_a, ids_b, tokens_b, parts, bytes;  // offsets
+    size_t kept, crossing, counts, ids_a, tokens_a, ids_b, tokens_b, parts, bytes;  // offsets
     int64_t ld_parts;
 };
 
@@ -633,19 +790,20 @@ EmbedPlan embed_plan(int64_t T, int64_t N, int64_t V)
         at += static_cast<size_t>((bytes + 255) / 256 * 256);
         return o;
     };
-    e.kept = take(4);
-    e.counts = take(e.sort.blocks > 1 ? static_cast<int64_t>(e.sort.blocks) * 4 << e.sort.bits : 0);
+    e.kept = take(8);
+    e.crossing = take(4 * e.chunks);
+    const bool range = sort_by_range(T, V);
+    e.counts = take(range ? 0 : static_cast<int64_t>(e.sort.blocks) * 4 << e.sort.bits);
     e.ids_a = take(4 * T);
     e.tokens_a = take(4 * T);
-    const bool again = e.sort.passes > 1 && e.sort.blocks > 1;  // one block passes them on through shared memory
-    e.ids_b = take(again ? 4 * T : 0);
-    e.tokens_b = take(again ? 4 * T : 0);
+    e.ids_b = take(!range && e.sort.passes > 1 ? 4 * T : 0);
+    e.tokens_b = take(!range && e.sort.passes > 1 ? 4 * T : 0);
     e.parts = take(e.chunks > 1 ? 2 * e.chunks * e.ld_parts * 4 : 0);
     e.bytes = at;
     return e;
 }
 
-constexpr int kZeroBlocks = 304;  // of 512 threads, beside the sort's; half as many of 1024, of which an SM holds one
+constexpr int kZeroBlocks = 304;  // beside the sort's
 
 gemm_status_t launch_sort(const EmbedPlan &e, SortPass p, int64_t T, int64_t V, const int32_t *ids, uint8_t *ws, cudaStream_t st)
 {
@@ -660,16 +818,8 @@ gemm_status_t launch_sort(const EmbedPlan &e, SortPass p, int64_t T, int64_t V, 
     p.bins = 1 << e.sort.bits;
     p.blocks = e.sort.blocks;
     const int64_t zeros = p.hi;  // of the whole table
-    const int64_t beside = p.blocks == 1 ? kZeroBlocks / 2 - 1 : kZeroBlocks;
-    const unsigned grid = static_cast<unsigned>(p.blocks + (zeros > 0 ? std::min(beside, (zeros + 511) / 512) : 0));
+    const unsigned grid = static_cast<unsigned>(p.blocks + (zeros > 0 ? std::min<int64_t>(kZeroBlocks, (zeros + 511) / 512) : 0));
     const size_t smem = static_cast<size_t>(kSortWarps + 2) * p.bins * sizeof(int);
-    if (p.blocks == 1) {
-        const int most = kBlockWarps * kSortMaxBins * 4 + kBlockMost * 6;
-        if (ensure_smem_attribute(sort_block_kernel, most, sort_attribute_set) != cudaSuccess)
-            return GEMM_ERR_CUDA;
-        return host_launch(sort_block_kernel, grid, 32 * kBlockWarps, static_cast<size_t>(kBlockWarps) * p.bins * 4 + static_cast<size_t>(T) * 6, st,
-                           0, p, e.sort.passes, at[0], at[1]);
-    }
     int launch = 0;
     auto share = [&]() {  // equal shares of the zeros for every launch
         p.lo = zeros * launch / (2 * e.sort.passes);
@@ -726,11 +876,12 @@ gemm_status_t gemm_embed(int64_t T, int64_t N, int64_t V, const int32_t *ids, co
     if (s != GEMM_OK || T == 0 || N == 0)
         return s;
     const bool wide = wide_rows(table, ldt, N, type_bytes(t_type)) && wide_rows(D, ldd, N, type_bytes(d_type));
-    const int64_t items = wide ? N * type_bytes(d_type) / 16 : N, all = T * items, block = kEmbedThreads * kEmbedItems;
+    const int64_t items = N * type_bytes(d_type) / 16, all = T * items, block = kEmbedThreads * kEmbedItems;
     const int64_t blocks = (all + block - 1) / block;
-    if (blocks > kSizeLimit)
+    // threads of a narrow row, eight columns each, and rows of a block
+    const int x = static_cast<int>(std::min<int64_t>(kEmbedThreads, ((N + 7) / 8 + 31) / 32 * 32)), y = kEmbedThreads / x;
+    if (wide && blocks > kSizeLimit)
         return GEMM_ERR_UNSUPPORTED;
-    const bool narrow = blocks * block <= UINT32_MAX;  // items are counted in 32 bits
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return with_type(t_type, [&](auto ttag) {
         using S = decltype(ttag);
@@ -738,13 +889,14 @@ gemm_status_t gemm_embed(int64_t T, int64_t N, int64_t V, const int32_t *ids, co
             using D_ = decltype(dtag);
             const S *from = static_cast<const S *>(table);
             D_ *to = static_cast<D_ *>(D);
-            const unsigned grid = static_cast<unsigned>(blocks), row = static_cast<unsigned>(items);
             const int v = static_cast<int>(V);
-            if (narrow)
-                return host_launch(wide ? embed_kernel<S, D_, true, unsigned> : embed_kernel<S, D_, false, unsigned>, grid, kEmbedThreads, 0, st, 0,
-                                   from, ldt, ids, to, ldd, row, all, v, scale);
-            return host_launch(wide ? embed_kernel<S, D_, true, unsigned long long> : embed_kernel<S, D_, false, unsigned long long>, grid,
-                               kEmbedThreads, 0, st, 0, from, ldt, ids, to, ldd, row, all, v, scale);
+            if (!wide)
+                return host_launch(embed_narrow_kernel<S, D_>, static_cast<unsigned>((T + y - 1) / y), dim3(x, y), 0, st, 0, from, ldt, ids, to, ldd,
+                                   T, static_cast<int>(N), v, scale);
+            const unsigned grid = static_cast<unsigned>(blocks), row = static_cast<unsigned>(items);
+            if (blocks * block <= UINT32_MAX)  // items are counted in 32 bits
+                return host_launch(embed_kernel<S, D_, unsigned>, grid, kEmbedThreads, 0, st, 0, from, ldt, ids, to, ldd, row, all, v, scale);
+            return host_launch(embed_kernel<S, D_, unsigned long long>, grid, kEmbedThreads, 0, st, 0, from, ldt, ids, to, ldd, row, all, v, scale);
         });
     });
 }
@@ -788,12 +940,37 @@ gemm_status_t gemm_embed_backward(int64_t T, int64_t N, int64_t V, const int32_t
     if (T == 0)
         return accumulate ? GEMM_OK : host_launch(embed_zero_kernel, 2u * kZeroBlocks, 512, 0, st, 0, sort);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    if ((s = launch_sort(e, sort, T, V, ids, ws, st)) != GEMM_OK)
+    if (sort_by_range(T, V)) {
+        RangePass r = {};
+        r.ids = ids;
+        r.ids_out = reinterpret_cast<int *>(ws + e.ids_a);
+        r.tokens_out = reinterpret_cast<int *>(ws + e.tokens_a);
+        r.kept = reinterpret_cast<int *>(ws + e.kept);
+        r.T = static_cast<int>(T);
+        r.V = static_cast<int>(V);
+        r.per = static_cast<int>(std::min<int64_t>(kRangeMostIds, (V + kRangeBlocks - 1) / kRangeBlocks));
+        r.zeros = sort.zeros;
+        r.wide = sort.wide;
+        r.ld = sort.ld;
+        r.row = sort.row;
+        r.all = sort.hi;
+        const size_t smem = static_cast<size_t>(kRangeWarps) * r.per * sizeof(int);
+        if (ensure_smem_attribute(sort_range_kernel, kRangeWarps * kRangeMostIds * 4, range_attribute_set) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+        s = host_launch(sort_range_kernel, static_cast<unsigned>((V + r.per - 1) / r.per), 32 * (kRangeWarps + (accumulate ? 0 : kZeroWarps)), smem, st,
+                        0, r);
+    } else {
+        s = launch_sort(e, sort, T, V, ids, ws, st);
+    }
+    if (s != GEMM_OK)
         return s;
     SumParams p = {};
+    p.T = T;
     p.ids = reinterpret_cast<int *>(ws + e.ids_a);
     p.tokens = reinterpret_cast<int *>(ws + e.tokens_a);
     p.kept = reinterpret_cast<int *>(ws + e.kept);
+    p.crossings = reinterpret_cast<int *>(ws + e.kept) + 1;
+    p.crossing = reinterpret_cast<int *>(ws + e.crossing);
     p.lddd = lddd;
     p.ldt = lddt;
     p.N = static_cast<int>(N);
@@ -814,8 +991,8 @@ gemm_status_t gemm_embed_backward(int64_t T, int64_t N, int64_t V, const int32_t
             gemm_status_t r = host_launch(wide ? embed_sum_kernel<D, W, true> : embed_sum_kernel<D, W, false>, grid, kSumThreads, 0, st, 0, from, to, p);
             if (r != GEMM_OK || e.chunks == 1)
                 return r;
-            return host_launch(wide ? embed_join_kernel<W, true> : embed_join_kernel<W, false>, grid, dim3(kSumThreads, kJoinGroups), 0, st, 0,
-                               to, p);
+            return host_launch(wide ? embed_join_kernel<W, true> : embed_join_kernel<W, false>, kJoinBlocks, dim3(kSumThreads, kJoinGroups), 0, st,
+                               0, to, p);
         });
     });
 }

@@ -363,3 +363,70 @@ def test_waits_that_run_out_are_reported(g, T, role):
     losses, _ = forward(g, X, W, y)
     assert bool(((losses - forward64(X, W, y)[0]).abs() < 1e-4).all())
     status_ok(g)
+
+
+@pytest.mark.parametrize("role", [1, 2])
+@pytest.mark.parametrize("T,columns", [(64, 0), (300, 0), (300, 256)])
+def test_waits_of_the_gradients_that_run_out_are_reported(g, T, columns, role):
+    X, W, y = make(T, 2000, 128, torch.bfloat16, seed=20)
+    lse = forward64(X, W, y)[1].float()
+    dl = torch.ones(T, device=DEV)
+    good = backward(g, X, W, y, lse, dl, None, columns=columns)
+    status_ok(g)
+    g.gemm_debug_inject_timeout(20, role)
+    backward(g, X, W, y, lse, dl, None, columns=columns)
+    status, word = g.gemm_last_device_status()
+    assert status == g.ERR_TIMEOUT and word & 0xFF in (1, 2, 3)
+    again = backward(g, X, W, y, lse, dl, None, columns=columns)
+    assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
+    status_ok(g)
+
+
+def test_two_calls_side_by_side(g):
+    """Two streams, each with its own workspace: neither sees the other."""
+    cases = [make(400, 6000, 192, torch.bfloat16, seed=s, masked=0.1) for s in (21, 22)]
+    dl = torch.rand(400, device=DEV)
+    want = []
+    for X, W, y in cases:
+        losses, lse = forward(g, X, W, y)
+        want.append((losses, lse) + backward(g, X, W, y, lse, dl, None))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for (X, W, y), stream in zip(cases, streams):
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                losses, lse = forward(g, X, W, y)
+                out = (losses, lse) + backward(g, X, W, y, lse, dl, None)
+            got.append(out)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, z) for x, z in zip(a, b))
+
+
+def test_more_than_32_bits_of_weights_and_gradients(g):
+    """A head of over 2^31 elements; sampled rows against float64."""
+    T, V, K = 40, 262145, 8200
+    X = torch.randn(T, K, device=DEV).bfloat16()
+    W = torch.empty(V, K, dtype=torch.bfloat16, device=DEV)
+    for a in range(0, V, 32768):
+        W[a:a + 32768] = torch.randn(min(32768, V - a), K, device=DEV) * (1.5 / math.sqrt(K))
+    y = torch.randint(V - 1000, V, (T,), device=DEV, dtype=torch.int32)
+    losses, lse = forward(g, X, W, y)
+    logits = torch.cat([X.double() @ W[a:a + 16384].double().t() for a in range(0, V, 16384)], 1)
+    want_lse = torch.logsumexp(logits, -1)
+    want = want_lse - logits.gather(1, y.long()[:, None])[:, 0]
+    assert bool(((losses - want).abs() < 2e-5).all()) and bool(((lse - want_lse).abs() < 2e-5).all())
+    dl = torch.ones(T, device=DEV)
+    dX, dW = backward(g, X, W, y, lse, dl, None)
+    p = torch.exp(logits - lse.double()[:, None])
+    p[torch.arange(T, device=DEV), y.long()] -= 1.0
+    rows = torch.cat([torch.tensor([0, 1, 131072, V - 1], device=DEV), y.long()[:8]])
+    pick = p[:, rows]
+    want_rows = (pick.t() @ X.double(), pick.abs().t() @ X.double().abs(), float((pick.square().t() @ X.double().square()).sum().sqrt()),
+                 X.double().abs().sum(0))
+    near(dW[rows], want_rows, X.dtype)
+    wx = sum(p[:, a:a + 16384] @ W[a:a + 16384].double() for a in range(0, V, 16384))
+    sx = sum(p[:, a:a + 16384].abs() @ W[a:a + 16384].double().abs() for a in range(0, V, 16384))
+    nx = math.sqrt(sum(float((p[:, a:a + 16384].square() @ W[a:a + 16384].double().square()).sum()) for a in range(0, V, 16384)))
+    near(dX, (wx, sx, nx, torch.zeros(K, dtype=torch.float64, device=DEV)), X.dtype)
