@@ -26,6 +26,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/gemm_gb300.h"
 #include "elements.cuh"
@@ -1036,6 +1037,290 @@ __global__ void __launch_bounds__(256) head_zero_kernel(uint8_t *d, long long ld
             *reinterpret_cast<uint16_t *>(d + r * ld_bytes + i) = 0;
 }
 
+// ---------------------------------------------------------------- few tokens, backward
+
+// One or two tokens: one pass over the weights by fp32 arithmetic. A group of
+// threads has R words at a time, each thread eight columns of them: their dot
+// products with the tokens' rows, summed over the group, give dl, with which
+// the same registers make the words' rows of dW and add to dX. Bound by memory,
+// which holds the weights once and their gradient once (the tiles of the
+// products read the weights twice): 1 x 131072 x 4096 in 375 us, of 322 at the
+// copy rate, 2 x 131072 x 4096 in 368, 1 x 32000 x 1024 in 33 (by tiles 607, 610
+// and 60). Four tokens, of which registers hold two words at a time, took as
+// long as by tiles.
+constexpr int kFewThreads = 512;  // K <= 8 * 512
+constexpr int kFewBlocks = 152;   // one for each SM of the GPU this is built for
+
+struct FewParams {
+    const void *x, *w;
+    void *dw;
+    float *parts;  // [block][T][ld_parts], or null
+    long long ldx, ldw, lddw, ld_parts;
+    int T, V, K, x_threads, dw_type, accumulate;
+    const int *targets;
+    const float *lse, *dlosses, *dlse;
+};
+
+// Pairs of fp32 numbers, worked on by one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 pair_to(uint64_t p)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Eight 16-bit values as pairs.
+template <typename I>
+__device__ __forceinline__ void widen(const uint4 &v, uint64_t (&o)[4])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<I, __nv_bfloat16>::value) {
+            o[i] = pair_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            o[i] = pair_of(f.x, f.y);
+        }
+    }
+}
+
+// Eight 16-bit values of a row from column k on, zeros past its end.
+__device__ __forceinline__ uint4 load_eight(const uint16_t *row, int k, int K, bool have)
+{
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (have && k + 8 <= K) {
+        v = __ldcg(reinterpret_cast<const uint4 *>(row + k));
+    } else if (have && k < K) {
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k + i < K)
+                w[i / 2] |= static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short *>(row) + k + i)) << (16 * (i & 1));
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return v;
+}
+
+template <typename D>
+__device__ __forceinline__ void store_eight(void *row, int k, int K, int accumulate, float (&v)[8])
+{
+    D *p = static_cast<D *>(row) + k;
+    if (k + 8 <= K) {
+        float old[8];
+        if (accumulate) {
+            load8<D, true>(p, 0, 1, 8, old);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] += old[i];
+        }
+        store8<D, true>(p, 0, 1, 8, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k + i < K)
+                p[i] = from_float<D>(accumulate ? v[i] + to_float(p[i]) : v[i]);
+    }
+}
+
+template <typename I, int TT>
+__global__ void __launch_bounds__(kFewThreads, 1) head_few_kernel(const FewParams p)
+{
+    constexpr int R = 8 / TT, N = R * TT;  // words at a time; their dot products
+    extern __shared__ float few_smem[];             // [TT][8 * x threads] of dX at the end
+    __shared__ float dots[2][kFewThreads / 32][N];
+    const int tid = threadIdx.x, group = threadIdx.y, lane = tid & 31, k = 8 * tid;
+    const int warps = p.x_threads / 32, warp = tid >> 5;  // of the group
+    const int groups = static_cast<int>(blockDim.y);
+    grid_start();
+    uint64_t x[TT][4], acc[TT][4] = {};
+    // lane j has the constants of token j % TT
+    const int t_of = lane % TT;
+    RowGrad g;
+    if (t_of < p.T) {
+        const int y = __ldcg(p.targets + t_of);
+        g.live = static_cast<unsigned>(y) < static_cast<unsigned>(p.V);
+        if (g.live) {
+            const float d = __ldcg(p.dlosses + t_of);
+            g.a = d + (p.dlse ? __ldcg(p.dlse + t_of) : 0.0f);
+            g.b = d;
+            g.lse2 = __ldcg(p.lse + t_of) * kLog2e;
+            g.target = y;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const bool live = __shfl_sync(0xffffffffu, g.live, t);
+        widen<I>(load_eight(static_cast<const uint16_t *>(p.x) + (t < p.T ? t : 0) * p.ldx, k, p.K, live), x[t]);
+    }
+    const uint16_t *weights = static_cast<const uint16_t *>(p.w);
+    const long long step = static_cast<long long>(gridDim.x) * groups * R;
+    long long v0 = (static_cast<long long>(blockIdx.x) * groups + group) * R;
+    uint4 next[R];  // asked for a step ahead
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        next[r] = load_eight(weights + (v0 + r) * p.ldw, k, p.K, v0 + r < p.V);
+    for (int turn = 0; v0 < p.V; v0 += step, turn ^= 1) {
+        uint4 w[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            w[r] = next[r];
+            next[r] = load_eight(weights + (v0 + step + r) * p.ldw, k, p.K, v0 + step + r < p.V);
+        }
+        float dot[N];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint64_t words[4];
+            widen<I>(w[r], words);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                uint64_t s = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s = fma_pair(x[t][i], words[i], s);
+                const float2 two = pair_to(s);
+                dot[r * TT + t] = two.x + two.y;
+            }
+        }
+        // the warp's sums: halves of the values change places until a lane has one
+        int at = 0;
+#pragma unroll
+        for (int m = N / 2, o = 16; o > 0; o >>= 1, m /= 2) {
+            if (m > 0) {
+                const bool upper = lane & o;
+                at += upper ? m : 0;
+#pragma unroll
+                for (int i = 0; i < m; ++i) {
+                    const float send = upper ? dot[i] : dot[i + m];
+                    const float keep = upper ? dot[i + m] : dot[i];
+                    dot[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                }
+            } else {
+                dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
+            }
+        }
+        if (lane % (32 / N) == 0)
+            dots[turn][group * warps + warp][at] = dot[0];
+        if (warps == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(p.x_threads) : "memory");
+        // dl of word (lane % N) / TT and token lane % TT, in every warp
+        float l = 0.0f;
+        for (int i = lane / N; i < warps; i += 32 / N)
+            l += dots[turn][group * warps + i][lane % N];
+#pragma unroll
+        for (int o = N; o < 32; o <<= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+        const long long v = v0 + (lane % N) / TT;
+        const float dl = g.live && v < p.V ? ex2(fmaf(l, kLog2e, -g.lse2)) * g.a - (v == g.target ? g.b : 0.0f) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint64_t words[4], sums[4] = {};
+            widen<I>(w[r], words);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const float d = __shfl_sync(0xffffffffu, dl, r * TT + t);
+                const uint64_t two = pair_of(d, d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sums[i] = fma_pair(two, x[t][i], sums[i]);
+                    acc[t][i] = fma_pair(two, words[i], acc[t][i]);
+                }
+            }
+            float out[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 two = pair_to(sums[i]);
+                out[2 * i] = two.x;
+                out[2 * i + 1] = two.y;
+            }
+            if (p.dw && v0 + r < p.V && k < p.K) {
+                if (p.dw_type == GEMM_OUT_F32)
+                    store_eight<float>(static_cast<float *>(p.dw) + (v0 + r) * p.lddw, k, p.K, p.accumulate, out);
+                else if (p.dw_type == GEMM_OUT_BF16)
+                    store_eight<__nv_bfloat16>(static_cast<__nv_bfloat16 *>(p.dw) + (v0 + r) * p.lddw, k, p.K, p.accumulate, out);
+                else
+                    store_eight<__half>(static_cast<__half *>(p.dw) + (v0 + r) * p.lddw, k, p.K, p.accumulate, out);
+            }
+        }
+    }
+    if (!p.parts)
+        return;
+    // dX of the block's groups, in their order
+    float mine[TT][8];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 two = pair_to(acc[t][j]);
+            mine[t][2 * j] = two.x;
+            mine[t][2 * j + 1] = two.y;
+        }
+    for (int i = 0; i < groups; ++i) {
+        __syncthreads();
+        if (group == i) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float *s = few_smem + (t * 8 + j) * p.x_threads + tid;
+                    if (i > 0)
+                        mine[t][j] += *s;
+                    if (i + 1 < groups)
+                        *s = mine[t][j];
+                }
+        }
+    }
+    if (group == groups - 1 && k < p.K) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+                if (t < p.T)
+                    *reinterpret_cast<float4 *>(p.parts + (static_cast<long long>(blockIdx.x) * p.T + t) * p.ld_parts + k + j) =
+                        make_float4(mine[t][j], mine[t][j + 1], mine[t][j + 2], mine[t][j + 3]);
+    }
+}
+
+// dX from the blocks' parts: eight threads share an element's parts, in a fixed order.
+template <typename D>
+__global__ void __launch_bounds__(256) head_few_sum_kernel(const float *parts, int n, long long ld, int T, int K, D *d, long long ldd)
+{
+    __shared__ float sums[8][32];
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+    const int k = static_cast<int>(blockIdx.x) * 32 + lane, t = static_cast<int>(blockIdx.y);
+    grid_start();
+    float s = 0.0f;
+    if (k < K) {
+#pragma unroll 8
+        for (int i = part; i < n; i += 8)
+            s += __ldcg(parts + (static_cast<long long>(i) * T + t) * ld + k);
+    }
+    sums[part][lane] = s;
+    __syncthreads();
+    if (part == 0 && k < K) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            s += sums[i][lane];
+        d[t * ldd + k] = from_float<D>(s);
+    }
+}
+
 // ---------------------------------------------------------------- host
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
@@ -1307,6 +1592,12 @@ gemm_status_t run_forward(HeadParams p, int64_t T, int64_t V, int64_t K, int in_
     return launch_head<CG, true>(p, &job, 1, sms, st);
 }
 
+constexpr int kFewTokens = 2;
+
+bool few_tokens(int64_t T, int64_t K) { return T <= kFewTokens && K <= 8 * kFewThreads; }
+
+size_t few_bytes(int64_t T, int64_t K) { return static_cast<size_t>(kFewBlocks) * T * round_up(K, 8) * 4; }
+
 // The arguments of a backward call that its launches need.
 struct BackArgs {
     int in_type;
@@ -1318,6 +1609,50 @@ struct BackArgs {
     bool accumulate;
     uint8_t *ws;
 };
+
+template <typename I, int TT>
+std::atomic<uint64_t> few_attribute_set[2] = {{0}, {0}};
+
+template <typename I, int TT>
+gemm_status_t launch_few(FewParams p, int groups, cudaStream_t st)
+{
+    const size_t smem = groups > 1 ? static_cast<size_t>(TT) * 8 * p.x_threads * 4 : 0;
+    if (ensure_smem_attribute(head_few_kernel<I, TT>, TT * 4 * 8 * kFewThreads, few_attribute_set<I, TT>) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    return host_launch(head_few_kernel<I, TT>, kFewBlocks, dim3(p.x_threads, groups), smem, st, 0, p);
+}
+
+gemm_status_t run_few(const BackArgs &g, FewParams p, cudaStream_t st)
+{
+    p.x = g.X.ptr;
+    p.w = g.W.ptr;
+    p.dw = g.dW;
+    p.parts = g.dX ? reinterpret_cast<float *>(g.ws) : nullptr;
+    p.ldx = g.X.ld;
+    p.ldw = g.W.ld;
+    p.lddw = g.lddw;
+    p.ld_parts = round_up(g.K, 8);
+    p.T = static_cast<int>(g.T);
+    p.V = static_cast<int>(g.V);
+    p.K = static_cast<int>(g.K);
+    p.x_threads = static_cast<int>(round_up((g.K + 7) / 8, 32));
+    p.dw_type = g.dw_type;
+    p.accumulate = g.accumulate;
+    // barriers 1 to 15 are the groups' own; those of one warp need none
+    const int groups = kFewThreads / p.x_threads;
+    gemm_status_t s;
+    if (g.in_type == 1)
+        s = g.T == 1 ? launch_few<__nv_bfloat16, 1>(p, groups, st) : launch_few<__nv_bfloat16, 2>(p, groups, st);
+    else
+        s = g.T == 1 ? launch_few<__half, 1>(p, groups, st) : launch_few<__half, 2>(p, groups, st);
+    if (s != GEMM_OK || !g.dX)
+        return s;
+    return with_type(g.dx_type, [&](auto tag) {
+        using D = decltype(tag);
+        return host_launch(head_few_sum_kernel<D>, dim3(static_cast<unsigned>((g.K + 31) / 32), static_cast<unsigned>(g.T)), 256, 0, st, 0, p.parts,
+                           kFewBlocks, p.ld_parts, p.T, p.K, static_cast<D *>(g.dX), g.lddx);
+    });
+}
 
 // One launch for each piece: its gradients and the next piece's dl, which do not
 // wait for one another, so that the units of one product fill what the rounds of
@@ -1444,6 +1779,8 @@ size_t gemm_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t 
 {
     if (T < 1 || V < 1 || K < 1 || columns < 0 || !countable(T) || !countable(V) || !countable(K))
         return 0;
+    if (few_tokens(T, K))
+        return few_bytes(T, K);
     int dev = 0, sms = 0;
     unsigned int *status = nullptr;
     if (host_device(&dev, &status, &sms) != GEMM_OK)
@@ -1478,6 +1815,18 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
         return GEMM_ERR_INVALID_ARG;
     if (!aligned_to(lse, 4) || !aligned_to(dlosses, 4) || !aligned_to(dlse, 4) || !aligned_to(workspace, 256))
         return GEMM_ERR_ALIGNMENT;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const BackArgs args = {in_type, T, V, K, {X, 0, ldx}, {W, 0, ldw}, dX, dW, dx_type, dw_type, lddx, lddw, accumulate != 0, ws};
+    if (few_tokens(T, K)) {
+        if (workspace_bytes < few_bytes(T, K))
+            return GEMM_ERR_INVALID_ARG;
+        FewParams f = {};
+        f.targets = targets;
+        f.lse = lse;
+        f.dlosses = dlosses;
+        f.dlse = dlse;
+        return run_few(args, f, st);
+    }
     int dev = 0, sms = 0;
     HeadParams p = {};
     if ((s = host_device(&dev, &p.status, &sms)) != GEMM_OK)
@@ -1495,7 +1844,6 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
     b = back_plan(T, V, K, 256 * low, sms);
     if (b.bytes > workspace_bytes)
         return GEMM_ERR_INVALID_ARG;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *scale = reinterpret_cast<float *>(ws);
     const unsigned copies = dW ? static_cast<unsigned>(std::min<int64_t>((T * ((K + 7) / 8) + 2047) / 2048, 2 * sms)) : 0;
     if ((s = host_launch(head_prepare_kernel, 1 + copies, kPrepareThreads, 0, st, 0, static_cast<const uint4 *>(X), ldx / 8,
@@ -1510,7 +1858,6 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
     p.dlosses = dlosses;
     p.dlse = dlse;
     p.scale = scale;
-    const BackArgs args = {in_type, T, V, K, {X, 0, ldx}, {W, 0, ldw}, dX, dW, dx_type, dw_type, lddx, lddw, accumulate != 0, ws};
     s = b.cg == 1 ? run_backward<1>(p, args, b, sms, st) : run_backward<2>(p, args, b, sms, st);
     const int splits = b.dx_splits;
     if (s != GEMM_OK || !dX || splits == 1)

@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(32 * kSortWarps) sort_scatter_kernel(const Sor
 // takes four launches that wait for one another; by one block of 32 warps it
 // took 35 us for 16384 tokens of 32768 ids.)
 constexpr int kRangeWarps = 16;
-constexpr int kRangeBatch = 16;         // entries a lane has in flight
+constexpr int kRangeBatch = 8;          // entries a lane has in flight
 constexpr int kRangeBlocks = 152;       // at least: one for each SM of the GPU this is built for
 constexpr int kRangeMostIds = 1024;     // of a block
 constexpr int kRangeMostBlocks = 1024;

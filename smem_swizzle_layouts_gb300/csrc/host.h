@@ -61,11 +61,11 @@ cudaError_t ensure_smem_attribute(Kern kern, int bytes, std::atomic<uint64_t> (&
 // start after its own wait, so that what wrote the ids has ended.) With
 // `cluster` > 0 it is launched in clusters of that many CTAs.
 template <typename... Params, typename... Args>
-inline gemm_status_t host_launch(void (*kern)(Params...), unsigned grid, dim3 block, size_t smem, cudaStream_t st,
+inline gemm_status_t host_launch(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                                  unsigned cluster, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;

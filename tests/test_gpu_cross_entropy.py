@@ -152,7 +152,7 @@ def check_backward(g, T, V, K, type, seed=0, masked=0.0, z=False, factor=1.0, x_
     status_ok(g)
 
 
-BACKWARD = [(1, 1, 1), (1, 1000, 64), (2, 257, 63), (8, 4096, 512), (33, 5000, 200), (77, 20001, 129), (128, 2048, 1024), (129, 2047, 72),
+BACKWARD = [(1, 1, 1), (1, 30001, 2048), (2, 5000, 4096), (1, 3000, 4097), (2, 1217, 1500), (3, 2000, 700), (1, 7, 4090), (1, 1000, 64), (2, 257, 63), (8, 4096, 512), (33, 5000, 200), (77, 20001, 129), (128, 2048, 1024), (129, 2047, 72),
             (256, 256, 128), (257, 8200, 65), (700, 3001, 1001), (1500, 12345, 96), (300, 40000, 256)]
 
 
@@ -168,6 +168,8 @@ def test_gradients(g, T, V, K, type):
 def test_gradient_types(g, x_type, w_type, accumulate):
     check_backward(g, 300, 2500, 172, "bf16", seed=5, masked=0.1, x_type=x_type, w_type=w_type, accumulate=accumulate)
     check_backward(g, 60, 700, 333, "f16", seed=6, masked=0.1, x_type=x_type, w_type=w_type, accumulate=accumulate, z=True)
+    check_backward(g, 2, 3001, 203, "bf16", seed=7, x_type=x_type, w_type=w_type, accumulate=accumulate, z=True)
+    check_backward(g, 1, 900, 96, "f16", seed=8, x_type=x_type, w_type=w_type, accumulate=accumulate)
 
 
 @pytest.mark.parametrize("columns", [256, 512, 1024, 4096])
@@ -186,10 +188,11 @@ def test_any_scaling_of_the_loss(g, type, factor):
 
 
 @pytest.mark.parametrize("want", ["x", "w"])
-def test_one_gradient_alone(g, want):
-    X, W, y = make(270, 3000, 136, torch.bfloat16, seed=10, masked=0.2)
+@pytest.mark.parametrize("T", [1, 2, 270])
+def test_one_gradient_alone(g, T, want):
+    X, W, y = make(T, 3000, 136, torch.bfloat16, seed=10, masked=0.2)
     lse = forward64(X, W, y)[1].float()
-    dl = torch.rand(270, device=DEV)
+    dl = torch.rand(T, device=DEV)
     both = backward(g, X, W, y, lse, dl, None)
     alone = backward(g, X, W, y, lse, dl, None, want=want)
     i = "xw".index(want)
@@ -213,6 +216,22 @@ def test_rows_without_a_loss(g):
     Xc, dl, dz = X.clone(), dl.clone(), dz.clone()
     Xc[dead], dl[dead], dz[dead] = 0.0, 0.0, 0.0
     want_x, want_w = backward64(Xc, W, y, lse, dl, dz)
+    near(dX, want_x, X.dtype)
+    near(dW, want_w, X.dtype)
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_few_tokens_without_a_loss(g, T):
+    X, W, y = make(T, 700, 264, torch.bfloat16, seed=12)
+    y[0] = -1
+    X[0] = math.nan
+    lse = forward(g, X, W, y)[1]
+    dl = torch.full((T,), 0.5, device=DEV)
+    dl[0] = math.inf
+    dX, dW = backward(g, X, W, y, lse, dl, None)
+    assert not dX[0].any()
+    X[0], dl[0] = 0.0, 0.0
+    want_x, want_w = backward64(X, W, y, lse, dl, None)
     near(dX, want_x, X.dtype)
     near(dW, want_w, X.dtype)
 
