@@ -136,6 +136,42 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// Pairs of fp32 numbers, worked on by one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 pair_to(uint64_t p)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Elements of K in a stage.
 template <int CG>
 constexpr int kHeadBK = CG == 2 ? 128 : 64;
@@ -366,19 +402,30 @@ struct RunningSoftmax {
             m[i & 7] = fmaxf(fmaxf(m[i & 7], fmaxf(v[0][i], v[1][i])), fmaxf(v[2][i], v[3][i]));
         const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7]))) * kLog2e;
         const float ref = fabsf(top) < INFINITY ? top : 0.0f;
-        // by eights, so that small terms gather before they meet a large one
-        float t[4] = {};
+        // a tree of sums, so that a term passes seven additions, and small ones
+        // gather before they meet a large one: level l waits for its other half
+        const uint64_t by = pair_of(kLog2e, kLog2e), less = pair_of(-ref, -ref);
+        uint64_t level[5];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            float e[8];
+        for (int i = 0; i < 16; ++i) {
+            uint64_t e[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                e[k] = ex2(fmaf(v[k][i], kLog2e, -ref));
-                e[4 + k] = ex2(fmaf(v[k][i + 1], kLog2e, -ref));
+                const float2 l = pair_to(fma_pair(pair_of(v[k][2 * i], v[k][2 * i + 1]), by, less));
+                e[k] = pair_of(ex2(l.x), ex2(l.y));
             }
-            t[(i >> 1) & 3] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            uint64_t sum = add_pair(add_pair(e[0], e[1]), add_pair(e[2], e[3]));
+#pragma unroll
+            for (int l = 0; l < 4; ++l)
+                if (((i + 1) & ((2 << l) - 1)) == 0)
+                    sum = add_pair(level[l], sum);
+#pragma unroll
+            for (int l = 0; l < 5; ++l)
+                if (((i + 1) & ((2 << l) - 1)) == (1 << l))
+                    level[l] = sum;
         }
-        s = (t[0] + t[1]) + (t[2] + t[3]);
+        const float2 u = pair_to(level[4]);
+        s = u.x + u.y;
         r = top == INFINITY ? 0.0f : fmaxf(top, -INFINITY);  // NaN, of a row of nothing else, to -inf
     }
 
@@ -629,6 +676,13 @@ __device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t b
                 for (int k = 0; k < 32; ++k)
                     v[i][k] = c + k < cols ? v[i][k] : -INFINITY;
             }
+        }
+        RunningSoftmax sm;
+        sm.take(v);
+        // the target comes last: it has been on its way from memory meanwhile
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = 32 * half + 64 * i;
             const bool mine = y >= c && y < min(c + 32, cols);
             if (__any_sync(0xffffffffu, mine)) {
                 const float x = pick32(v[i], y - c);
@@ -636,8 +690,6 @@ __device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t b
                     p.picked[row] = x;
             }
         }
-        RunningSoftmax sm;
-        sm.take(v);
         if (half == 1) {
             if (!__all_sync(0xffffffffu, w.wait(bar_free, phase ^ 1u, kRoleEpilogue | kWaitPartial)))
                 return;
@@ -664,6 +716,7 @@ template <int CG>
 __device__ __forceinline__ void logit_grad_tile(const HeadParams &p, const CUtensorMap *map, const RowGrad &g, const Accumulators<CG> &a, int q,
                                                 int half, int m0, int n0, int cols, uint32_t sbuf, int lane)
 {
+    const uint64_t by = pair_of(kLog2e, kLog2e), less = pair_of(-g.lse2, -g.lse2), scale = pair_of(g.a, g.a);
     for (int c = 64 * half; c < cols; c += 128) {
         uint32_t o[32];
         float x[2][32];
@@ -674,8 +727,12 @@ __device__ __forceinline__ void logit_grad_tile(const HeadParams &p, const CUten
         for (int i = 0; i < 2; ++i) {
             float (&v)[32] = x[i];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                v[k] = g.live ? ex2(fmaf(v[k], kLog2e, -g.lse2)) * g.a : 0.0f;
+            for (int k = 0; k < 32; k += 2) {
+                const float2 l = pair_to(fma_pair(pair_of(v[k], v[k + 1]), by, less));
+                const float2 d = pair_to(mul_pair(pair_of(ex2(l.x), ex2(l.y)), scale));
+                v[k] = d.x;
+                v[k + 1] = d.y;
+            }
             const int at = g.target - (n0 + c + 32 * i);
             if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
 #pragma unroll
@@ -684,6 +741,9 @@ __device__ __forceinline__ void logit_grad_tile(const HeadParams &p, const CUten
             }
             pack32<64>(v, i, p.in_bf16 ? 1 : 2, o);
         }
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            o[k] = g.live ? o[k] : 0u;  // whatever the row of a token without a loss made of them
         stage_and_store<64>(o, sbuf, lane, map, n0 + c, m0, 0);
     }
 }
@@ -715,8 +775,11 @@ __device__ __forceinline__ void product_tile(const HeadParams &p, const HeadJob 
                     v[k] += __uint_as_float(old[k]);
             }
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                v[k] *= by;
+            for (int k = 0; k < 32; k += 2) {
+                const float2 d = pair_to(mul_pair(pair_of(v[k], v[k + 1]), pair_of(by, by)));
+                v[k] = d.x;
+                v[k + 1] = d.y;
+            }
             if (j.c_typed) {
                 if constexpr (CW == 32) {
                     load_row<float, 32>(static_cast<const float *>(j.c_typed) + row * j.ld_typed, at, j.N, have, old);
@@ -1060,28 +1123,6 @@ struct FewParams {
     const int *targets;
     const float *lse, *dlosses, *dlse;
 };
-
-// Pairs of fp32 numbers, worked on by one instruction.
-__device__ __forceinline__ uint64_t pair_of(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ float2 pair_to(uint64_t p)
-{
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-    return v;
-}
-
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 
 // Eight 16-bit values as pairs.
 template <typename I>
