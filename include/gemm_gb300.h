@@ -607,8 +607,9 @@ gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const voi
 
 /* ---------------------------------------------------------------------
  * The ends of a training step: rows of a token table, the loss of a linear head
- * over a large vocabulary, and the balance loss of the routers. The rules of the expert-layer calls above hold (element types,
- * alignment, errors, overlapping launches), but for what is said here.
+ * over a large vocabulary, and the balance loss of the routers. The rules of the
+ * expert-layer calls above hold (element types, alignment, errors, overlapping
+ * launches), but for what is said here.
  * ------------------------------------------------------------------- */
 
 /*
@@ -644,7 +645,7 @@ gemm_status_t gemm_cross_entropy(int in_type, int64_t T, int64_t V, int64_t K, c
  * dl is computed for a piece of the vocabulary at a time and rounded to the
  * inputs' type for the tensor cores, after a division by the largest
  * |dlosses| + |dlse| (found on the GPU: any scaling of the loss gives the same
- * gradients, times it). Products are summed in fp32. T == 0 leaves dX and writes
+ * gradients, times it); for one or two tokens of K <= 4096 it is not rounded. Products are summed in fp32. T == 0 leaves dX and writes
  * zeros to dW (nothing with accumulate).
  * workspace: 256-byte aligned, in no particular state. The call takes the widest
  * pieces that it has room for, of at most 2^27 / T columns (a piece's dl then has

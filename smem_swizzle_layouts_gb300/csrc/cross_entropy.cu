@@ -12,6 +12,18 @@
 // dl rounded to the inputs' type (backward, a piece of the vocabulary at a
 // time into the workspace: the logits are computed a second time, 2 T V K of
 // the 6 T V K operations of the backward pass), or the gradients themselves.
+// Backward, one launch has up to three products: a piece's dX and dW, and the
+// next piece's dl, whose units fill what the others' rounds leave of the grid
+// (4096 x 32768 x 4096: 1958 us instead of 2234 by a launch for each). One or
+// two tokens have a kernel of their own below.
+//
+// Many tokens are bound by the tensor cores, whose rate the power limit holds:
+// 8192 x 65536 x 4096 forward took 2554 to 2583 us (1.7 PFLOP/s; of the measured
+// peak 2280 in a burst, 2500 sustained), 4096 x 32768 x 4096 backward 1963 (1710).
+// Few are bound by the weights' bytes: 1 x 131072 x 4096 in 161 us, at the rate of
+// a copy. Small K is bound by the epilogue, one exponential and
+// some additions for each logit, against K products: 8192 x 32768 x 256 forward
+// 151 us of 71, backward 395 of 214.
 //
 // Roles, barriers and waits are those of gemm_kernel.cuh (whose operand
 // geometry, descriptors and bounded waits are used here); the tiles' widths,
@@ -1092,11 +1104,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // Zeros for dW when there is no token.
-__global__ void __launch_bounds__(256) head_zero_kernel(uint8_t *d, long long ld_bytes, long long rows, int row_bytes)
+__global__ void __launch_bounds__(256) head_zero_kernel(uint8_t *d, long long ld_bytes, long long rows, long long row_bytes)
 {
     grid_start();
     for (long long r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int i = 2 * static_cast<int>(threadIdx.x); i < row_bytes; i += 512)
+        for (long long i = 2 * static_cast<int>(threadIdx.x); i < row_bytes; i += 512)
             *reinterpret_cast<uint16_t *>(d + r * ld_bytes + i) = 0;
 }
 
@@ -1570,7 +1582,8 @@ BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
     const int64_t x_tiles = tiles(T, K, b.dx_bn), kb = blocks(b.piece);
     const int64_t work = x_tiles * kb + tiles(b.piece, K, b.dx_bn) * (blocks(T) + 4) + (b.pieces > 1 ? tiles(T, b.piece, 256) * (blocks(K) + 4) : 0);
     const int64_t most = std::max<int64_t>(8, work / slots / 3);
-    const int64_t wanted = std::min<int64_t>((kb + most - 1) / most, std::max<int64_t>(1, 2 * slots / x_tiles)), unit = (kb + wanted - 1) / wanted;
+    const int64_t most_splits = std::max<int64_t>(1, 2 * slots / x_tiles);
+    const int64_t wanted = std::min<int64_t>((kb + most - 1) / most, most_splits), unit = (kb + wanted - 1) / wanted;
     b.dx_splits = static_cast<int>((kb + unit - 1) / unit);
     size_t at = 256;
     auto take = [&](size_t bytes) {
@@ -1581,7 +1594,9 @@ BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
     b.xs = take(static_cast<size_t>(T) * b.ldk * 2);
     b.dl[0] = take(static_cast<size_t>(T) * b.ldp * 2);
     b.dl[1] = b.pieces > 1 ? take(static_cast<size_t>(T) * b.ldp * 2) : b.dl[0];
-    b.parts = take(static_cast<size_t>(T) * b.ldk * 4 * b.dx_splits);
+    // room for the most parts that any piece would have: narrower pieces, of which
+    // some have more, never need more room than wider ones
+    b.parts = take(static_cast<size_t>(T) * b.ldk * 4 * std::min(most_splits, blocks(V)));
     b.bytes = at;
     return b;
 }
@@ -1589,8 +1604,8 @@ BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
 // Widest pieces that are taken: a piece's dl has 256 MB at most. Few tokens wait
 // for memory, and have all of the vocabulary in one piece: pieces small enough
 // to stay in L2 from one launch to the next left most SMs without tiles (1 x
-// 131072 x 4096: 1140 us in pieces of 8192, WHOLE1 in one; 128 x 131072 x 2048:
-// 499 and WHOLE128).
+// 131072 x 4096: 1140 us by tiles in pieces of 8192, 607 in one; 128 x 131072 x
+// 2048: 499 and 338).
 int64_t widest_piece(int64_t T)
 {
     return std::max<int64_t>(256, (int64_t(1) << 27) / std::max<int64_t>(T, 1) / 256 * 256);
@@ -1850,7 +1865,7 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
         if (!dW || accumulate)
             return GEMM_OK;
         return host_launch(head_zero_kernel, static_cast<unsigned>(std::min<int64_t>(V, 4096)), 256, 0, st, 0, static_cast<uint8_t *>(dW),
-                           lddw * ew, V, static_cast<int>(K * ew));
+                           lddw * ew, V, K * ew);
     }
     if (!lse || !dlosses || !workspace)
         return GEMM_ERR_INVALID_ARG;
@@ -1872,9 +1887,14 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
     HeadParams p = {};
     if ((s = host_device(&dev, &p.status, &sms)) != GEMM_OK)
         return s;
-    // the largest pieces that the workspace has room for, up to the usual ones
+    // the widest pieces that the workspace has room for; the only piece has one
+    // dl, and may need less than two pieces do
     BackPlan b = {};
     int64_t low = 1, high = std::min(round_up(V, 256), widest_piece(T)) / 256;
+    if (back_plan(T, V, K, 256 * high, sms).bytes <= workspace_bytes)
+        low = high;
+    else
+        high = std::max<int64_t>(1, high - 1);
     while (low < high) {
         const int64_t mid = (low + high + 1) / 2;
         if (back_plan(T, V, K, 256 * mid, sms).bytes <= workspace_bytes)

@@ -258,6 +258,13 @@ def test_no_tokens(g):
         assert bool((dW[:, :64] == want).all()) and bool((dW[:, 64:] == 7.0).all())
 
 
+def test_no_tokens_and_rows_of_more_than_32_bits_of_bytes(g):
+    K = 2 ** 29 + 8
+    dW = torch.full((1, K), 3.0, device=DEV)
+    g.gemm_cross_entropy_backward(1, 0, 1, K, None, 0, None, 0, None, None, None, None, None, 0, 0, dW, 0, K, 0, None, 0)
+    assert int(torch.count_nonzero(dW)) == 0
+
+
 def test_columns_behind_the_rows_are_left_alone(g):
     X, W, y = make(70, 500, 100, torch.bfloat16, seed=13)
     lse = forward64(X, W, y)[1].float()
