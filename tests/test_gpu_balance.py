@@ -135,6 +135,15 @@ def test_ragged_sequences(g, T, cuts, score, type):
     check(g, T, 72, 4, score, cuts, type, seed=len(cuts), padded=0.15)
 
 
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("T,S", [(1, 9), (5, 9), (32, 40), (30, 31), (20, 700), (300, 700), (2000, 33)])
+def test_many_sequences_most_of_them_empty(g, T, S, score):
+    gen = torch.Generator().manual_seed(T + S)
+    cuts = torch.randint(0, min(T, 25) + 1, (S + 1,), generator=gen).sort().values
+    cuts[-(S // 3):] = T  # a run of empty ones at the end, others between
+    check(g, T, 12, 2, score, cuts.tolist(), seed=S, padded=0.1)
+
+
 def test_padded_tokens_may_hold_anything(g):
     logits, ids = make(600, 64, 6, padded=0.3, seed=3)
     dead = (ids < 0).all(-1)
