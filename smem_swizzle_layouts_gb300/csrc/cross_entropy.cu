@@ -22,8 +22,8 @@
 // peak 2280 in a burst, 2500 sustained), 4096 x 32768 x 4096 backward 1963 (1710).
 // Few are bound by the weights' bytes: 1 x 131072 x 4096 in 161 us, at the rate of
 // a copy. Small K is bound by the epilogue, one exponential and
-// some additions for each logit, against K products: 8192 x 32768 x 256 forward
-// 151 us of 71, backward 395 of 214.
+// some additions for each logit, against K products, and backward by dl's bytes:
+// 8192 x 32768 x 256 forward 112 us of 71, backward 352 of 214.
 //
 // Roles, barriers and waits are those of gemm_kernel.cuh (whose operand
 // geometry, descriptors and bounded waits are used here); the tiles' widths,
@@ -53,8 +53,15 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int kHeadWarps = 8;                      // epilogue warps: a lane quarter and half of the columns each
-constexpr int kHeadThreads = 64 + 32 * kHeadWarps;
+// Epilogue warps: a lane quarter each, and a half or (a pair's softmax) a quarter
+// of the columns. The softmax has no staging buffers, and while some of its 16
+// warps wait for TMEM others have work: 7252 x 118755 x 128 forward 346 us (384
+// by 8), 8192 x 32768 x 256 112 (123); 2048 x 32768 x 1024 78.7 (77.3). A single
+// CTA's few rows leave most warps without any: 1 x 131072 x 4096 167 (157).
+template <int CG, bool FORWARD>
+constexpr int kHeadWarps = CG == 2 && FORWARD ? 16 : 8;
+template <int CG, bool FORWARD>
+constexpr int kHeadThreads = 64 + 32 * kHeadWarps<CG, FORWARD>;
 constexpr int kHeadMaxStages = 12;
 constexpr int kAccStride = 256;                    // TMEM columns from one accumulator to the next
 constexpr int kHeadSmem = 232448 - 1024;           // less the slack that rounds the base up to 1024 bytes
@@ -71,9 +78,9 @@ constexpr int kSumPart = 512;
 enum : int { kEpiSoftmax = 0, kEpiLogitGrad = 1, kEpiProduct = 2 };
 
 // Offsets behind the stages: staging chunks, then barriers.
-constexpr int kHeadStageBytes = kHeadWarps * kEpiBufBytes;
+constexpr int kHeadStageBytes = kHeadWarps<2, false> * kEpiBufBytes;
 constexpr int kHeadBars = 2 * kHeadMaxStages + 4 + 2 + 8;
-constexpr int kHeadHalves = 128 * 8;  // forward: a partial softmax for each row of a tile
+constexpr int kHeadShares = 3 * 128 * 8;  // forward: partial softmaxes of up to three quarters of a tile's columns for each of its rows
 constexpr int kHeadTail = kHeadBars * 8 + 16;
 
 // Division of n < 2^31 by a number that the host knows: with 2^shift < d <=
@@ -403,30 +410,33 @@ struct RunningSoftmax {
     float r = -INFINITY, s = 0.0f;
 
     // All of a thread's values of a tile, the first that it sees.
-    __device__ __forceinline__ void take(const float (&v)[4][32])
+    template <int N>
+    __device__ __forceinline__ void take(const float (&v)[N][32])
     {
         float m[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            m[i] = fmaxf(fmaxf(v[0][i], v[1][i]), fmaxf(v[2][i], v[3][i]));
+            m[i] = fmaxf(v[0][i], v[1][i]);
 #pragma unroll
-        for (int i = 8; i < 32; ++i)
-            m[i & 7] = fmaxf(fmaxf(m[i & 7], fmaxf(v[0][i], v[1][i])), fmaxf(v[2][i], v[3][i]));
+        for (int i = 8; i < 16 * N; ++i)
+            m[i & 7] = fmaxf(m[i & 7], fmaxf(v[i / 32 * 2][i & 31], v[i / 32 * 2 + 1][i & 31]));
         const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7]))) * kLog2e;
         const float ref = fabsf(top) < INFINITY ? top : 0.0f;
-        // a tree of sums, so that a term passes seven additions, and small ones
+        // a tree of sums, so that a term passes seven additions at most, and small ones
         // gather before they meet a large one: level l waits for its other half
         const uint64_t by = pair_of(kLog2e, kLog2e), less = pair_of(-ref, -ref);
         uint64_t level[5];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            uint64_t e[4];
+            uint64_t e[N];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < N; ++k) {
                 const float2 l = pair_to(fma_pair(pair_of(v[k][2 * i], v[k][2 * i + 1]), by, less));
                 e[k] = pair_of(ex2(l.x), ex2(l.y));
             }
-            uint64_t sum = add_pair(add_pair(e[0], e[1]), add_pair(e[2], e[3]));
+            uint64_t sum = add_pair(e[0], e[1]);
+            if constexpr (N == 4)
+                sum = add_pair(sum, add_pair(e[2], e[3]));
 #pragma unroll
             for (int l = 0; l < 4; ++l)
                 if (((i + 1) & ((2 << l) - 1)) == 0)
@@ -602,6 +612,19 @@ __device__ __forceinline__ void pack32(const float (&v)[32], int i, int out_type
     }
 }
 
+// Arrive on the even CTA's barrier for an accumulator this warp has read. The
+// reads of TMEM have completed (tcgen05.wait::ld), and nothing that the warp has
+// stored is the MMA's to read, so that the release is confined to this CTA's
+// shared memory: one of all memory waits for the stores to global memory that
+// are on their way (forward 8192 x 32768 x 256 151 us, 7252 x 118755 x 128 441;
+// confined 112 and 346).
+__device__ __forceinline__ void mbar_arrive_read(uint32_t cluster_bar)
+{
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
+                 "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+                 : "memory");
+}
+
 // An epilogue warp's view of the accumulators: waits for the next one and hands
 // it back. Warp w has TMEM lanes 32 (w mod 4) .. +31 and half of the columns.
 template <int CG>
@@ -623,7 +646,7 @@ struct Accumulators {
         __syncwarp();
         if (lane == 0) {
             if constexpr (CG == 2)
-                mbar_arrive_cluster(bar_empty + 8 * acc);
+                mbar_arrive_read(bar_empty + 8 * acc);
             else
                 mbar_arrive(bar_empty + 8 * acc);
         }
@@ -637,15 +660,16 @@ struct Accumulators {
     }
 };
 
-// Forward: each tile's partial softmax. The two warps that share a row join
+// Forward: each tile's partial softmax. The warps that share a row join
 // theirs through shared memory.
 template <int CG>
-__device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t bar_halves, Accumulators<CG> a, uint32_t rank, int warp, int lane,
+__device__ void softmax_epilogue(const HeadParams &p, float2 *shares, uint32_t bar_shares, Accumulators<CG> a, uint32_t rank, int warp, int lane,
                                  const Waiter &w)
 {
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    float2 *const slot = halves + 32 * q + lane;
-    const uint32_t bar_ready = bar_halves + 16 * q, bar_free = bar_ready + 8;
+    constexpr int SHARES = kHeadWarps<CG, true> / 4, N = 8 / SHARES;  // warps of a row, their chunks of 32 columns
+    const int q = warp & 3, share = (warp - 2) >> 2;
+    float2 *const slot = shares + 32 * q + lane;  // 128 from one share's to the next
+    const uint32_t bar_ready = bar_shares + 16 * q, bar_free = bar_ready + 8;
     uint32_t phase = 0;
     HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
     const HeadJob &j = p.jobs[0];
@@ -654,22 +678,22 @@ __device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t b
         const int m0 = (h.m_blk * CG + static_cast<int>(rank)) * 128 + 32 * q, row = m0 + lane;
         const int n0 = h.n_blk * j.bn, cols = min(j.bn, j.N - n0);
         const int y = row < p.T ? __ldcg(p.targets + row) - n0 : -1;
-        const bool rows = m0 < p.T;  // the same for both warps
+        const bool rows = m0 < p.T;  // the same for all warps of the row
         // the parts of the sums over K, added up in registers with fp32 rounding
-        float v[4][32];
+        float v[N][32];
         for (int part = 0; part < j.kb_all; part += j.kb_part) {
             if (!a.take(w, rank))
                 return;
             if (part == 0) {
                 // all of them: columns past the tile's lie in TMEM too, and are masked below
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    fetch_acc32(a.columns(q, 32 * half + 64 * i), v[i]);
+                for (int i = 0; i < N; ++i)
+                    fetch_acc32(a.columns(q, 32 * (share + SHARES * i)), v[i]);
                 tmem_ld_wait();
             } else if (rows) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 32 * half + 64 * i;
+                for (int i = 0; i < N; ++i) {
+                    const int c = 32 * (share + SHARES * i);
                     if (c < cols) {
                         add_acc16(a.columns(q, c), v[i]);
                         add_acc16(a.columns(q, c + 16), v[i] + 16);
@@ -681,8 +705,8 @@ __device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t b
         if (!rows)
             continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = 32 * half + 64 * i;
+        for (int i = 0; i < N; ++i) {
+            const int c = 32 * (share + SHARES * i);
             if (c + 32 > cols) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
@@ -693,8 +717,8 @@ __device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t b
         sm.take(v);
         // the target comes last: it has been on its way from memory meanwhile
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = 32 * half + 64 * i;
+        for (int i = 0; i < N; ++i) {
+            const int c = 32 * (share + SHARES * i);
             const bool mine = y >= c && y < min(c + 32, cols);
             if (__any_sync(0xffffffffu, mine)) {
                 const float x = pick32(v[i], y - c);
@@ -702,17 +726,19 @@ __device__ void softmax_epilogue(const HeadParams &p, float2 *halves, uint32_t b
                     p.picked[row] = x;
             }
         }
-        if (half == 1) {
+        if (share > 0) {
             if (!__all_sync(0xffffffffu, w.wait(bar_free, phase ^ 1u, kRoleEpilogue | kWaitPartial)))
                 return;
-            *slot = make_float2(sm.r, sm.s);
+            slot[128 * (share - 1)] = make_float2(sm.r, sm.s);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_ready);
         } else {
             if (!__all_sync(0xffffffffu, w.wait(bar_ready, phase, kRoleEpilogue | kWaitPartial)))
                 return;
-            sm.join(*slot);
+#pragma unroll
+            for (int i = 0; i < SHARES - 1; ++i)
+                sm.join(slot[128 * i]);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_free);
@@ -860,7 +886,7 @@ __device__ void gradient_epilogue(const HeadParams &p, const HeadMaps &maps, uin
 // ---------------------------------------------------------------- kernel
 
 template <int CG, bool FORWARD>
-__global__ void __launch_bounds__(kHeadThreads, 1) head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p)
+__global__ void __launch_bounds__(kHeadThreads<CG, FORWARD>, 1) head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -870,11 +896,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_kernel(const __grid_cons
     const uint32_t rank = CG == 2 ? cluster_ctarank() & 1u : 0u;
     const int stages = p.stages;
     const uint32_t staging = base + static_cast<uint32_t>(stages) * static_cast<uint32_t>(p.a_rows + p.b_rows) * kHeadBK<CG> * 2;
-    const uint32_t bars = staging + (FORWARD ? kHeadHalves : kHeadStageBytes);
+    const uint32_t bars = staging + (FORWARD ? kHeadShares : kHeadStageBytes);
     const uint32_t bar_full = bars, bar_empty = bar_full + 8 * kHeadMaxStages;
     const uint32_t bar_acc_full = bar_empty + 8 * kHeadMaxStages, bar_acc_empty = bar_acc_full + 16;
     const uint32_t bar_drain = bar_acc_empty + 16, bar_inject = bar_drain + 8;
-    const uint32_t bar_halves = bar_inject + 8, misc = bar_halves + 64;
+    const uint32_t bar_shares = bar_inject + 8, misc = bar_shares + 64;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + (misc - base));
     volatile uint32_t *abort_flag = tmem_slot + 1;
     if (threadIdx.x == 0) {
@@ -884,12 +910,14 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_kernel(const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_acc_full + 8 * b, 1);
-            mbar_init(bar_acc_empty + 8 * b, kHeadWarps * CG);
+            mbar_init(bar_acc_empty + 8 * b, kHeadWarps<CG, FORWARD> * CG);
         }
         mbar_init(bar_drain, 1);
         mbar_init(bar_inject, 1);
-        for (int i = 0; i < 8; ++i)
-            mbar_init(bar_halves + 8 * i, 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar_shares + 16 * i, kHeadWarps<CG, FORWARD> / 4 - 1);
+            mbar_init(bar_shares + 16 * i + 8, 1);
+        }
         *abort_flag = 0u;
         fence_mbar_init();
         for (int j = 0; j < p.num_jobs; ++j) {
@@ -932,7 +960,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_kernel(const __grid_cons
     } else {
         const Accumulators<CG> a{bar_acc_full, CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty, tmem};
         if constexpr (FORWARD)
-            softmax_epilogue<CG>(p, reinterpret_cast<float2 *>(smem + (staging - base)), bar_halves, a, rank, warp, lane, w);
+            softmax_epilogue<CG>(p, reinterpret_cast<float2 *>(smem + (staging - base)), bar_shares, a, rank, warp, lane, w);
         else
             gradient_epilogue<CG>(p, maps, staging + static_cast<uint32_t>((warp - 2) * kEpiBufBytes), a, rank, warp, lane, w);
         if (!FORWARD && lane == 0)
@@ -1525,13 +1553,13 @@ gemm_status_t launch_head(HeadParams p, Job *jobs, int n, int sms, cudaStream_t 
     // a role may wait for another to walk all of a unit's K: 10 us a block beside 2 s
     p.timeout_ns = ms > 0 ? static_cast<unsigned long long>(ms) * 1000000ull : 2000000000ull + static_cast<unsigned long long>(longest) * 10000ull;
     const int stage_bytes = (p.a_rows + p.b_rows) * BK * 2;
-    const int rest = (FORWARD ? kHeadHalves : kHeadStageBytes) + kHeadTail;
+    const int rest = (FORWARD ? kHeadShares : kHeadStageBytes) + kHeadTail;
     p.stages = std::min(kHeadMaxStages, (kHeadSmem - rest) / stage_bytes);
     const int smem = p.stages * stage_bytes + rest + 1024;
     auto kern = head_kernel<CG, FORWARD>;
     if (ensure_smem_attribute(kern, kHeadSmem + 1024, head_attribute_set<CG, FORWARD>) != cudaSuccess)
         return GEMM_ERR_CUDA;
-    return host_launch(kern, static_cast<unsigned>(clusters * CG), kHeadThreads, static_cast<size_t>(smem), st, CG == 2 ? 2u : 0u, maps, p);
+    return host_launch(kern, static_cast<unsigned>(clusters * CG), kHeadThreads<CG, FORWARD>, static_cast<size_t>(smem), st, CG == 2 ? 2u : 0u, maps, p);
 }
 
 // Columns of the tiles of the logits: 256, or the width whose rounds of the grid
