@@ -18,12 +18,12 @@
 // two tokens have a kernel of their own below.
 //
 // Many tokens are bound by the tensor cores, whose rate the power limit holds:
-// 8192 x 65536 x 4096 forward took 2554 to 2583 us (1.7 PFLOP/s; of the measured
-// peak 2280 in a burst, 2500 sustained), 4096 x 32768 x 4096 backward 1963 (1710).
-// Few are bound by the weights' bytes: 1 x 131072 x 4096 in 161 us, at the rate of
-// a copy. Small K is bound by the epilogue, one exponential and
-// some additions for each logit, against K products, and backward by dl's bytes:
-// 8192 x 32768 x 256 forward 112 us of 71, backward 352 of 214.
+// 8192 x 65536 x 4096 forward took 2409 to 2472 us (1.8 PFLOP/s; at the measured
+// peaks 2280 in a burst, 2500 sustained), 4096 x 32768 x 4096 backward 1940
+// (1710, 1875). Few are bound by the weights' bytes: 1 x 131072 x 4096 in 161 us,
+// at the rate of a copy. Small K is bound by the epilogue, an exponential and some
+// additions for each logit against K products, and backward by dl's bytes: 8192 x
+// 32768 x 256 forward 112 us of 71, backward 352 of 214.
 //
 // Roles, barriers and waits are those of gemm_kernel.cuh (whose operand
 // geometry, descriptors and bounded waits are used here); the tiles' widths,
@@ -70,8 +70,8 @@ constexpr int kHeadSmem = 232448 - 1024;           // less the slack that rounds
 // added to the others in registers. Their additions truncate (every 16 elements,
 // to the accumulator's 24 bits), which moves a logit towards 0 by up to half a
 // part in 2^24 for each. Relative error of the losses, and time, of 8192 tokens,
-// 65536 words and K = 4096 by parts of 256, 512, 1024 and all of K: 1.2e-7 (3020
-// us), 2.2e-7 (2575), 4.7e-7 (2498), 2.0e-6 (2459); fp32 sums that round 5.2e-7.
+// 65536 words and K = 4096 by parts of 256, 512, 1024 and all of K: 0.9e-7 (2516
+// us), 1.7e-7 (2409), 3.3e-7 (2370), 1.4e-6 (2387).
 constexpr int kSumPart = 512;
 
 // What the epilogue does with the accumulator.
