@@ -998,7 +998,8 @@ __global__ void __launch_bounds__(kHeadThreads<CG, FORWARD>, 1) head_kernel(cons
 // ---------------------------------------------------------------- around the products
 
 // The normaliser and loss of each token from its partial softmaxes: a block has
-// ROWS tokens (32, or 1 where tokens are few), its warps share the partials. r
+// ROWS tokens (8, or 1 where tokens are few), and 16 warps share the partials, a
+// warp 32 / ROWS of them at a time. r
 // is a maximum over the partials, so that the sum is in range; the loss is taken
 // in base 2, where the target's logit cancels against r before anything is
 // rounded.
@@ -1008,10 +1009,11 @@ template <int ROWS>
 __global__ void __launch_bounds__(32 * kCombineWarps)
     head_combine_kernel(const float2 *partials, int parts, long long T, const int *targets, int V, float *losses, float *lse)
 {
-    __shared__ float2 part[kCombineWarps][32];
+    __shared__ float2 part[kCombineWarps][ROWS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = ROWS == 32 ? blockIdx.x * 32ll + lane : static_cast<long long>(blockIdx.x);
-    const int first = ROWS == 32 ? warp : static_cast<int>(threadIdx.x), step = ROWS == 32 ? kCombineWarps : 32 * kCombineWarps;
+    constexpr int SHARES = 32 / ROWS, step = SHARES * kCombineWarps;
+    const long long row = static_cast<long long>(blockIdx.x) * ROWS + lane % ROWS;
+    const int first = warp * SHARES + lane / ROWS;
     grid_start();
     RunningSoftmax sm;
     if (row < T) {
@@ -1025,18 +1027,17 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
                 sm.join(o[u]);
         }
     }
-    if constexpr (ROWS == 1) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            float2 other;
-            other.x = __shfl_xor_sync(0xffffffffu, sm.r, o);
-            other.y = __shfl_xor_sync(0xffffffffu, sm.s, o);
-            sm.join(other);
-        }
+    for (int o = 16; o >= ROWS; o >>= 1) {
+        float2 other;
+        other.x = __shfl_xor_sync(0xffffffffu, sm.r, o);
+        other.y = __shfl_xor_sync(0xffffffffu, sm.s, o);
+        sm.join(other);
     }
-    part[warp][lane] = make_float2(sm.r, sm.s);
+    if (lane < ROWS)
+        part[warp][lane] = make_float2(sm.r, sm.s);
     __syncthreads();
-    if (warp != 0 || (ROWS == 1 && lane != 0) || row >= T)
+    if (warp != 0 || lane >= ROWS || row >= T)
         return;
 #pragma unroll
     for (int i = 1; i < kCombineWarps; ++i)
@@ -1102,26 +1103,49 @@ __global__ void __launch_bounds__(kPrepareThreads)
     }
 }
 
-// dX from the sums over parts of the vocabulary, in the order of the parts.
-template <typename D>
+// dX from the sums over parts of the vocabulary, in a fixed order. GROUPS of a
+// block's 256 threads take every so-manieth part of an item, four columns: many
+// parts of few items would leave each thread with a long chain of loads (383 x
+// 108285 x 178 backward 121 us, 99 by groups of 8).
+constexpr int kSumGroups = 8;
+
+template <typename D, int GROUPS>
 __global__ void __launch_bounds__(256)
     head_sum_kernel(const float *parts, int n, long long stride, long long ld, long long T, int K, const float *scale, D *d, long long ldd)
 {
+    constexpr int ITEMS = 256 / GROUPS;
+    __shared__ float4 sums[GROUPS > 1 ? GROUPS : 1][ITEMS];
+    const int item = static_cast<int>(threadIdx.x) % ITEMS, group = static_cast<int>(threadIdx.x) / ITEMS;
     grid_start();
     const float by = __ldcg(scale + 1);
     const int words = (K + 3) / 4;
-    const long long all = T * words, step = gridDim.x * 256ll;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += step) {
+    const long long all = T * words, step = static_cast<long long>(gridDim.x) * ITEMS;
+    for (long long first = static_cast<long long>(blockIdx.x) * ITEMS; first < all; first += step) {
+        const long long i = min(first + item, all - 1);
         const long long t = i / words;
         const int k = 4 * static_cast<int>(i - t * words);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j < n; ++j) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(parts + j * stride + t * ld + k));
+        auto add = [&](const float4 &v) {
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
             s.w += v.w;
+        };
+#pragma unroll 4
+        for (int j = group; j < n; j += GROUPS)
+            add(__ldcg(reinterpret_cast<const float4 *>(parts + j * stride + t * ld + k)));
+        if constexpr (GROUPS > 1) {
+            __syncthreads();  // the sums of the items before have been read
+            sums[group][item] = s;
+            __syncthreads();
+            if (group > 0)
+                continue;
+#pragma unroll
+            for (int j = 1; j < GROUPS; ++j)
+                add(sums[j][item]);
         }
+        if (first + item >= all)
+            continue;
         D *o = d + t * ldd + k;
         const float v[4] = {s.x * by, s.y * by, s.z * by, s.w * by};
 #pragma unroll
@@ -1855,7 +1879,7 @@ gemm_status_t gemm_cross_entropy(int in_type, int64_t T, int64_t V, int64_t K, c
         return s;
     if (T <= 512)
         return host_launch(head_combine_kernel<1>, static_cast<unsigned>(T), 32 * kCombineWarps, 0, st, 0, p.partials, parts, T, targets, p.V, losses, lse);
-    return host_launch(head_combine_kernel<32>, static_cast<unsigned>((T + 31) / 32), 32 * kCombineWarps, 0, st, 0, p.partials, parts, T, targets, p.V,
+    return host_launch(head_combine_kernel<8>, static_cast<unsigned>((T + 7) / 8), 32 * kCombineWarps, 0, st, 0, p.partials, parts, T, targets, p.V,
                        losses, lse);
 }
 
@@ -1952,15 +1976,16 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
     if (s != GEMM_OK || !dX || splits == 1)
         return s;
     const float *parts = reinterpret_cast<const float *>(ws + b.parts);
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((T * ((K + 3) / 4) + 255) / 256, 8 * sms));
-    const int k = static_cast<int>(K);
+    const int64_t items = T * ((K + 3) / 4);
     const long long stride = T * b.ldk;
-    if (dx_type == GEMM_OUT_F32)
-        return host_launch(head_sum_kernel<float>, grid, 256, 0, st, 0, parts, splits, stride, b.ldk, T, k, scale, static_cast<float *>(dX), lddx);
-    if (dx_type == GEMM_OUT_BF16)
-        return host_launch(head_sum_kernel<__nv_bfloat16>, grid, 256, 0, st, 0, parts, splits, stride, b.ldk, T, k, scale,
-                           static_cast<__nv_bfloat16 *>(dX), lddx);
-    return host_launch(head_sum_kernel<__half>, grid, 256, 0, st, 0, parts, splits, stride, b.ldk, T, k, scale, static_cast<__half *>(dX), lddx);
+    return with_type(dx_type, [&](auto tag) {
+        using D = decltype(tag);
+        if (splits > kSumGroups && items < int64_t(sms) * 1024)
+            return host_launch(head_sum_kernel<D, kSumGroups>, static_cast<unsigned>(std::min<int64_t>((items * kSumGroups + 255) / 256, 8 * sms)), 256, 0,
+                               st, 0, parts, splits, stride, b.ldk, T, static_cast<int>(K), scale, static_cast<D *>(dX), lddx);
+        return host_launch(head_sum_kernel<D, 1>, static_cast<unsigned>(std::min<int64_t>((items + 255) / 256, 8 * sms)), 256, 0, st, 0, parts, splits,
+                           stride, b.ldk, T, static_cast<int>(K), scale, static_cast<D *>(dX), lddx);
+    });
 }
 
 }  // extern "C"
