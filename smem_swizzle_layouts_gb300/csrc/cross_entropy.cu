@@ -104,7 +104,7 @@ struct HeadJob {
     Divisor by_tiles, by_group, by_rows, by_last_rows;  // tiles, tiles of a raster group, its rows, those of the last group
     int kb_all, kb_unit;  // K blocks of the whole product and of a unit
     int kb_part;          // those that the tensor cores sum before the epilogue takes the sum (a unit's, or fewer)
-    int bn;               // columns of a tile
+    int bn, bn_last;      // columns of a tile, and of the last one of a row of tiles
     int a_mn, b_mn;
     int epi;
     // the units are dealt out in turn to all clusters, but for the first
@@ -266,23 +266,22 @@ __device__ ProducerTail head_producer(const HeadParams &p, const HeadMaps &maps,
     HeadUnit h;
     const CUtensorMap *map_a = nullptr, *map_b = nullptr;
     OperandBoxes box_a = {}, box_b = {};
-    int last_job = -1, bn = 0, b_cols = 0, nbox = 0;
-    uint32_t tx = 0;
+    int last_job = -1;
     while (units.next(h)) {
         if (h.job != last_job) {
             const HeadJob &j = p.jobs[h.job];
             last_job = h.job;
             map_a = &maps.a[h.job];
             map_b = &maps.b[h.job];
-            bn = j.bn;
-            b_cols = bn / CG;
             box_a = operand_boxes(j.a_mn, 3, a_rows, BK, 2);
-            box_b = operand_boxes(j.b_mn, 3, b_cols, BK, 2);
-            tx = CG * (a_bytes + static_cast<uint32_t>(b_cols) * BK * 2);
-            nbox = max(box_a.nbox, box_b.nbox);
         }
+        const HeadJob &j = p.jobs[h.job];
+        const int b_cols = (h.n_blk == j.tiles_n - 1 ? j.bn_last : j.bn) / CG;
+        box_b = operand_boxes(j.b_mn, 3, b_cols, BK, 2);
+        const uint32_t tx = CG * (a_bytes + static_cast<uint32_t>(b_cols) * BK * 2);
+        const int nbox = max(box_a.nbox, box_b.nbox);
         const int m0 = (h.m_blk * CG + static_cast<int>(rank)) * 128;
-        const int n0 = h.n_blk * bn + b_cols * static_cast<int>(rank);
+        const int n0 = h.n_blk * j.bn + b_cols * static_cast<int>(rank);
         for (int kb = h.kb0; kb < h.kb1; ++kb) {
             if (!w.wait(bar_empty + 8 * stage, phase ^ 1u, kRoleProducer | kWaitEmpty, rank != 0))
                 return ProducerTail{min(issued, stages), stage, phase};
@@ -322,7 +321,8 @@ __device__ void head_mma(const HeadParams &p, uint32_t smem, uint32_t bar_full, 
     HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
     HeadUnit h;
     int last_job = -1, kb_part = 1;
-    uint32_t idesc = 0, a_off[SLICES], b_off[SLICES];
+    uint32_t idesc_all = 0, idesc_last = 0, a_off[SLICES], b_off[SLICES];
+    int n_last = 0;
     uint64_t a_desc0 = 0, b_desc0 = 0;
     while (units.next(h)) {
         if (h.job != last_job) {
@@ -330,7 +330,9 @@ __device__ void head_mma(const HeadParams &p, uint32_t smem, uint32_t bar_full, 
             const int b_cols = j.bn / CG;
             last_job = h.job;
             kb_part = j.kb_part;
-            idesc = make_idesc_f16(128 * CG, j.bn, p.in_bf16, j.a_mn, j.b_mn);
+            n_last = j.tiles_n - 1;
+            idesc_all = make_idesc_f16(128 * CG, j.bn, p.in_bf16, j.a_mn, j.b_mn);
+            idesc_last = make_idesc_f16(128 * CG, j.bn_last, p.in_bf16, j.a_mn, j.b_mn);
             const OperandPacking pa = operand_packing(j.a_mn, 3, a_rows, BK), pb = operand_packing(j.b_mn, 3, b_cols, BK);
             a_desc0 = make_smem_desc(smem, pa.lbo, pa.sbo, pa.swz);
             b_desc0 = make_smem_desc(smem + a_bytes, pb.lbo, pb.sbo, pb.swz);
@@ -340,6 +342,7 @@ __device__ void head_mma(const HeadParams &p, uint32_t smem, uint32_t bar_full, 
                 b_off[i] = slice_byte_offset(j.b_mn, 3, b_cols, i) >> 4;
             }
         }
+        const uint32_t idesc = h.n_blk == n_last ? idesc_last : idesc_all;
         for (int part = h.kb0; part < h.kb1; part += kb_part) {
             if (!w.wait(bar_acc_empty + 8 * acc, acc_phase ^ 1u, kRoleMma | kWaitAccEmpty, CG == 2))
                 return;
@@ -1515,10 +1518,13 @@ gemm_status_t make_job(Job *job, int bn, int splits, int64_t M, int64_t N, int64
     j.kb_unit = static_cast<int>(unit);
     j.kb_part = static_cast<int>(unit);
     j.bn = bn;
+    // the last tile of a row: as many boxes of 64 columns as it needs (where B's
+    // K is contiguous, the stage's layout goes with the width, which stays)
+    j.bn_last = B.mn_major ? static_cast<int>(round_up(N - (tiles_n - 1) * bn, 64 * CG)) : bn;
     j.a_mn = A.mn_major;
     j.b_mn = B.mn_major;
     // an epilogue that no other unit's products cover costs about four blocks
-    job->cost = (unit + 4) * tile_cost(CG, bn);
+    job->cost = (unit + 4) * ((tiles_n - 1) * tile_cost(CG, bn) + tile_cost(CG, j.bn_last)) / tiles_n;
     gemm_status_t s = encode_16(&job->a, in_bf16, A.ptr, A.mn_major, M, K, A.ld, a_rows, BK);
     if (s == GEMM_OK)
         s = encode_16(&job->b, in_bf16, B.ptr, B.mn_major, N, K, B.ld, bn / CG, BK);

@@ -162,6 +162,12 @@ def test_gradients(g, T, V, K, type):
     check_backward(g, T, V, K, type, seed=T + K, masked=0.3 if T > 4 else 0.0, z=T % 2 == 0, pad=T % 2)
 
 
+@pytest.mark.parametrize("K", [128, 129, 192, 193, 256, 257, 320, 321, 384, 385, 449, 512, 513, 641])
+@pytest.mark.parametrize("T", [20, 300])
+def test_widths_of_the_last_tile(g, T, K):
+    check_backward(g, T, 3500, K, "bf16", seed=K, masked=0.1, x_type="f32" if K % 2 else "same")
+
+
 @pytest.mark.parametrize("x_type", OUT)
 @pytest.mark.parametrize("w_type", OUT)
 @pytest.mark.parametrize("accumulate", [False, True])
