@@ -266,12 +266,27 @@ __global__ void __launch_bounds__(32 * kBalanceWarps<NPL>) balance_kernel(const 
     }
 }
 
+// Parts of the tokens: one for each SM of the GPU this is built for (16384 tokens
+// in 500 sequences 28 us; in a part for each sequence 50). A block takes the
+// sequences that it meets one after another, in 1 to 2 us each, so that few tokens
+// are cut into parts as long as a sequence (51 tokens in 16 sequences took 20.8 us
+// by parts of 32, 7.8 by 4; 2048 in 64 took 12.2 by 32 and 19.9 by 14).
+constexpr int kBalanceBlocks = 152;
+
 constexpr int kJoinThreads = 512;
 constexpr int kJoinGroups = 64;      // at most
 constexpr int kJoinMaxCtas = 8;      // of a cluster, which has a sequence: each has a share of the experts
 
-// CTAs that share a sequence's experts.
-inline int join_ctas(int64_t E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : kJoinMaxCtas; }
+// CTAs that share a sequence's experts: fewer where there are many sequences (2048
+// tokens of 256 experts in 200 sequences 32 us by 8 CTAs each, 19.6 by one; 16384
+// of 64 experts in 500 28 by 2, 23.9 by one), but a thread for each expert.
+inline int join_ctas(int64_t E, int64_t S)
+{
+    int n = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : kJoinMaxCtas;
+    while (n > 1 && S * n > 2 * kBalanceBlocks && (E + 3) / 4 * 4 <= kJoinThreads * (n / 2))
+        n /= 2;
+    return n;
+}
 
 // A sequence's slots, added by groups of threads that take every so-manieth
 // one; then the groups in their order; then the loss over the cluster's CTAs.
@@ -452,11 +467,10 @@ __global__ void __launch_bounds__(32 * kBalanceGradWarps) balance_backward_kerne
 
 // ---------------------------------------------------------------- host
 
-constexpr int kBalanceBlocks = 152;  // parts of the tokens at most: one for each SM of the GPU this is built for
-constexpr int kBalancePart = 32;     // tokens of a part at least
-// Sequences that one block takes alone, one after another (1 us each); more of
-// them are finished side by side by a second launch.
-constexpr int kBalanceAlone = 8;
+constexpr int kBalanceLeastPart = 4, kBalancePart = 32;
+// Sequences that one block takes alone, in one launch: 32 tokens and 64 experts
+// in two sequences 4.9 us (5.9 by two launches), in three 6.9 (5.9 to 7.4).
+constexpr int kBalanceAlone = 2;
 
 struct BalancePlan {
     int blocks;
@@ -468,7 +482,8 @@ struct BalancePlan {
 BalancePlan balance_plan(int64_t T, int64_t E, int64_t S)
 {
     BalancePlan b = {};
-    b.part = std::max<int64_t>(kBalancePart, (T + kBalanceBlocks - 1) / kBalanceBlocks);
+    b.part = S <= kBalanceAlone && T <= kBalancePart ? T : std::clamp<int64_t>(T / std::max<int64_t>(S, 1), kBalanceLeastPart, kBalancePart);
+    b.part = std::max(b.part, (T + kBalanceBlocks - 1) / kBalanceBlocks);
     b.blocks = static_cast<int>((T + b.part - 1) / b.part);
     b.ld = (E + 3) / 4 * 4;
     b.alone = b.blocks <= 1 && S <= kBalanceAlone;
@@ -547,7 +562,12 @@ gemm_status_t gemm_route_balance(int64_t T, int64_t E, const void *logits, gemm_
         return GEMM_ERR_INVALID_ARG;
     if (!aligned_to(counts, 4) || !aligned_to(tokens, 4) || !aligned_to(means, 4) || !aligned_to(losses, 4))
         return GEMM_ERR_ALIGNMENT;
-    const BalancePlan b = balance_plan(std::max<int64_t>(T, 1), E, S);
+    BalancePlan b = balance_plan(std::max<int64_t>(T, 1), E, S);
+    if (T == 0) {  // the second launch alone writes the zeros, from no slots
+        b.bytes = 0;
+        b.alone = false;
+        b.ld = (E + 3) / 4 * 4;
+    }
     if (b.bytes > 0 && (!workspace || workspace_bytes < b.bytes))
         return GEMM_ERR_INVALID_ARG;
     if (b.bytes > 0 && !aligned_to(workspace, 16))
@@ -564,9 +584,9 @@ gemm_status_t gemm_route_balance(int64_t T, int64_t E, const void *logits, gemm_
     p.slot_counts = reinterpret_cast<int *>(ws + b.counts);
     p.slot_tokens = reinterpret_cast<int *>(ws + b.tokens);
     p.ld_slot = b.ld;
-    p.join_ctas = join_ctas(E);
+    p.join_ctas = join_ctas(E, S);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    s = with_type(l_type, [&](auto tag) {
+    s = T == 0 ? GEMM_OK : with_type(l_type, [&](auto tag) {
         using L = decltype(tag);
         return E <= 64    ? launch_balance<L, 2>(logits, p, st)
                : E <= 128 ? launch_balance<L, 4>(logits, p, st)

@@ -144,6 +144,12 @@ def test_many_sequences_most_of_them_empty(g, T, S, score):
     check(g, T, 12, 2, score, cuts.tolist(), seed=S, padded=0.1)
 
 
+@pytest.mark.parametrize("T,E,k,S", [(600, 64, 6, 200), (500, 100, 3, 310), (900, 256, 8, 170), (300, 513, 2, 160), (400, 1024, 8, 45), (400, 1000, 5, 170)])
+def test_many_sequences_of_many_experts(g, T, E, k, S):
+    cuts = torch.randint(0, T + 1, (S + 1,), generator=torch.Generator().manual_seed(S)).sort().values
+    check(g, T, E, k, 0, cuts.tolist(), seed=E, padded=0.1)
+
+
 def test_padded_tokens_may_hold_anything(g):
     logits, ids = make(600, 64, 6, padded=0.3, seed=3)
     dead = (ids < 0).all(-1)
@@ -185,6 +191,14 @@ def test_no_live_token(g):
 def test_no_tokens(g):
     logits, ids = torch.empty(0, 16, device=DEV), torch.empty(0, 2, dtype=torch.int32, device=DEV)
     counts, tokens, means, losses = forward(g, logits, ids, 0, torch.zeros(4, dtype=torch.int32, device=DEV))
+    assert not counts.any() and not tokens.any() and not means.any() and not losses.any()
+
+
+@pytest.mark.parametrize("S,E", [(1, 1), (9, 70), (700, 33)])
+def test_no_tokens_of_many_sequences(g, S, E):
+    logits, ids = torch.empty(0, E, device=DEV), torch.empty(0, 1, dtype=torch.int32, device=DEV)
+    assert g.gemm_route_balance_workspace_size(0, E, S) == 0
+    counts, tokens, means, losses = forward(g, logits, ids, 0, torch.zeros(S + 1, dtype=torch.int32, device=DEV))
     assert not counts.any() and not tokens.any() and not means.any() and not losses.any()
 
 
