@@ -590,8 +590,9 @@ __device__ __forceinline__ void finish_row(W *row, int c, int N, float (&acc)[8]
     store8<W, WIDE>(row, c, kSumThreads, N, acc);
 }
 
-// Sums the runs of one chunk: a block has 1024 columns of it.
-template <typename D, typename W, bool WIDE>
+// Sums the runs of one chunk: a block has 1024 columns of it. ADD: to what the
+// table holds, which is asked for with the last row of each run.
+template <typename D, typename W, bool WIDE, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const D *dd, W *dtable, const SumParams p)
 {
     constexpr int ROWS = WIDE && sizeof(D) == 2 ? 8 : 4;  // in flight: as many as registers hold
@@ -622,27 +623,27 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const D *dd, W *
     int run = ids[1];
     bool before = ids[0] == run;  // the run began in an earlier chunk
     auto part = [&](int which) { store8<float, WIDE>(p.parts + (2 * chunk + which) * p.ld_parts, c, kSumThreads, p.N, acc); };
-    auto flush = [&]() {
-        if (before)
-            part(0);
-        else
-            finish_row<W, WIDE>(dtable + run * p.ldt, c, p.N, acc, p.scale, p.accumulate);
-    };
     for (int j0 = 0; j0 < n; j0 += ROWS) {
         Eight<D> raw[ROWS];
+        Eight<W> old[ADD ? ROWS : 1];
 #pragma unroll
         for (int u = 0; u < ROWS; ++u)
             raw[u].template load<WIDE>(dd + rows[j0 + u], c, kSumThreads, p.N);
+        if constexpr (ADD) {
+#pragma unroll
+            for (int u = 0; u < ROWS; ++u)
+                if (j0 + u < n && ids[1 + j0 + u] != ids[2 + j0 + u])
+                    old[u].template load<WIDE>(dtable + ids[1 + j0 + u] * p.ldt, c, kSumThreads, p.N);
+        }
 #pragma unroll
         for (int u = 0; u < ROWS; ++u) {
-            if (j0 + u >= n)
+            const int j = j0 + u;
+            if (j >= n)
                 break;
             float v[8];
             raw[u].values(v);
-            const int next = ids[1 + j0 + u];
-            if (next != run) {
-                flush();
-                run = next;
+            if (ids[1 + j] != run) {
+                run = ids[1 + j];
                 before = false;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -652,14 +653,24 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const D *dd, W *
                 for (int k = 0; k < 8; ++k)
                     acc[k] += v[k];
             }
+            if (ids[2 + j] != run) {  // the run ends here
+                if (before) {
+                    part(0);
+                } else {
+                    if constexpr (ADD)
+                        old[u].values(v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        acc[k] = ADD ? fmaf(acc[k], p.scale, v[k]) : acc[k] * p.scale;
+                    store8<W, WIDE>(dtable + run * p.ldt, c, kSumThreads, p.N, acc);
+                }
+            }
         }
     }
-    if (n == p.chunk && ids[p.chunk + 1] == run && !before) {
-        part(1);  // the run goes on behind the chunk
-        if (col_block == 0 && tid == 0)
+    if (ids[n + 1] == run) {  // it goes on behind the chunk
+        part(before ? 0 : 1);
+        if (!before && col_block == 0 && tid == 0)
             p.crossing[atomicAdd(p.crossings, 1)] = static_cast<int>(chunk);
-    } else {
-        flush();
     }
 }
 
@@ -991,7 +1002,9 @@ gemm_status_t gemm_embed_backward(int64_t T, int64_t N, int64_t V, const int32_t
             using D = decltype(dtag);
             const D *from = static_cast<const D *>(dD);
             W *to = static_cast<W *>(dtable);
-            gemm_status_t r = host_launch(wide ? embed_sum_kernel<D, W, true> : embed_sum_kernel<D, W, false>, grid, kSumThreads, 0, st, 0, from, to, p);
+            const auto sums = accumulate ? (wide ? embed_sum_kernel<D, W, true, true> : embed_sum_kernel<D, W, false, true>)
+                                         : (wide ? embed_sum_kernel<D, W, true, false> : embed_sum_kernel<D, W, false, false>);
+            gemm_status_t r = host_launch(sums, grid, kSumThreads, 0, st, 0, from, to, p);
             if (r != GEMM_OK || e.chunks == 1)
                 return r;
             return host_launch(wide ? embed_join_kernel<W, true> : embed_join_kernel<W, false>, kJoinBlocks, dim3(kSumThreads, kJoinGroups), 0, st,
