@@ -18,9 +18,9 @@
 // two tokens have a kernel of their own below.
 //
 // Many tokens are bound by the tensor cores, whose rate the power limit holds:
-// 8192 x 65536 x 4096 forward took 2409 to 2472 us (1.8 PFLOP/s; at the measured
-// peaks 2280 in a burst, 2500 sustained), 4096 x 32768 x 4096 backward 1940
-// (1710, 1875). Few are bound by the weights' bytes: 1 x 131072 x 4096 in 161 us,
+// 8192 x 65536 x 4096 forward took 2409 to 2547 us (1.8 PFLOP/s; at the measured
+// peaks 2280 in a burst, 2500 sustained), 4096 x 32768 x 4096 backward
+// 1936 to 1987 (1710, 1875). Few are bound by the weights' bytes: 1 x 131072 x 4096 in 161 us,
 // at the rate of a copy. Small K is bound by the epilogue, an exponential and some
 // additions for each logit against K products, and backward by dl's bytes: 8192 x
 // 32768 x 256 forward 112 us of 71, backward 352 of 214.
