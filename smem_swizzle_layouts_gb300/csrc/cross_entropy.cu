@@ -1558,7 +1558,7 @@ gemm_status_t launch_head(HeadParams p, Job *jobs, int n, int sms, cudaStream_t 
         j.extra = behind > 0 ? static_cast<int>((gap + cost / 2) / cost) : 0;
         const int64_t rest = j.units - j.extra * late;
         if (rest <= 0) {
-            gap -= j.units / late * cost;
+            gap = std::max<int64_t>(0, gap - j.units / late * cost);  // they may have been rounded up past it
         } else if (rest % clusters != 0) {
             behind = rest % clusters;
             gap = cost;

@@ -168,6 +168,12 @@ def test_widths_of_the_last_tile(g, T, K):
     check_backward(g, T, 3500, K, "bf16", seed=K, masked=0.1, x_type="f32" if K % 2 else "same")
 
 
+def test_three_products_whose_rounds_end_together(g):
+    """A launch in which the second product's units are just as many as fill what the first left of its last round: every
+    unit of the third is dealt out all the same."""
+    check_backward(g, 3274, 84699, 424, "bf16", seed=9)
+
+
 @pytest.mark.parametrize("x_type", OUT)
 @pytest.mark.parametrize("w_type", OUT)
 @pytest.mark.parametrize("accumulate", [False, True])
