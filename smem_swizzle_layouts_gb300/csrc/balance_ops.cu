@@ -305,6 +305,8 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
     const int group = words ? tid / words : 0, word = words ? tid - group * words : 0;
     if (tid == 0)
         tokens = 0;
+    if (ctas > 1)
+        cluster_arrive();  // this CTA has started: the others may write its shared memory
     grid_start();
     __syncthreads();
     const Sequence q = sequence(p, s);
@@ -358,6 +360,8 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
     if ((tid & 31) == 0)
         warp_loss[tid >> 5] = loss;
     __syncthreads();
+    if (ctas > 1)
+        cluster_wait();  // the first CTA has started
     if (tid == 0) {
         loss = 0.0f;
         for (int w = 0; w < kJoinThreads / 32; ++w)
