@@ -717,7 +717,8 @@ gemm_status_t gemm_embed(int64_t T, int64_t N, int64_t V, const int32_t *ids, co
  * id names are not touched. dD: T x N of d_type, row stride lddd. Ids outside
  * 0..V-1 carry nothing. scale is finite.
  * workspace: gemm_embed_backward_workspace_size(T, N, V) bytes, 256-byte
- * aligned, in no particular state (may be NULL where that is 0).
+ * aligned, in no particular state (may be NULL where that is 0). More tokens
+ * never ask for less, so that room for the most serves fewer.
  */
 size_t gemm_embed_backward_workspace_size(int64_t T, int64_t N, int64_t V);
 

@@ -789,13 +789,20 @@ struct EmbedPlan {
     int64_t ld_parts;
 };
 
+int64_t column_blocks(int64_t N) { return (N + kSumColumns - 1) / kSumColumns; }
+
+// Entries of a chunk: as many as leave the SMs four blocks each.
+int chunk_of(int64_t T, int64_t N)
+{
+    const int64_t rows = T * column_blocks(N);
+    return rows >= 32 * kSumBlocks ? 32 : rows >= 16 * kSumBlocks ? 16 : 8;
+}
+
 EmbedPlan embed_plan(int64_t T, int64_t N, int64_t V)
 {
     EmbedPlan e = {};
     e.sort = sort_plan(T, V);
-    // as long as they leave the SMs four blocks each
-    const int64_t col_blocks = (N + kSumColumns - 1) / kSumColumns;
-    e.chunk = T * col_blocks >= 32 * kSumBlocks ? 32 : T * col_blocks >= 16 * kSumBlocks ? 16 : 8;
+    e.chunk = chunk_of(T, N);
     e.chunks = (T + e.chunk - 1) / e.chunk;
     e.ld_parts = (N + 7) / 8 * 8;
     size_t at = 0;
@@ -815,6 +822,20 @@ EmbedPlan embed_plan(int64_t T, int64_t N, int64_t V)
     e.parts = take(e.chunks > 1 ? 2 * e.chunks * e.ld_parts * 4 : 0);
     e.bytes = at;
     return e;
+}
+
+// Room for T tokens and for fewer. With chunks of one length more tokens need
+// more; where chunks get longer there are fewer of them, so that the most tokens
+// of each shorter length may need more than T.
+size_t embed_bytes(int64_t T, int64_t N, int64_t V)
+{
+    size_t most = embed_plan(T, N, V).bytes;
+    for (int chunk = 16; chunk <= chunk_of(T, N); chunk *= 2) {
+        const int64_t before = (chunk * static_cast<int64_t>(kSumBlocks) - 1) / column_blocks(N);
+        if (before > 0)
+            most = std::max(most, embed_plan(before, N, V).bytes);
+    }
+    return most;
 }
 
 constexpr int kZeroBlocks = 304;  // beside the sort's
@@ -919,7 +940,7 @@ size_t gemm_embed_backward_workspace_size(int64_t T, int64_t N, int64_t V)
 {
     if (T < 1 || N < 1 || V < 1 || !countable(T) || !countable(N) || !countable(V))
         return 0;
-    return embed_plan(T, N, V).bytes;
+    return embed_bytes(T, N, V);
 }
 
 gemm_status_t gemm_embed_backward(int64_t T, int64_t N, int64_t V, const int32_t *ids, const void *dD, gemm_out_t d_type, int64_t lddd,
@@ -931,13 +952,13 @@ gemm_status_t gemm_embed_backward(int64_t T, int64_t N, int64_t V, const int32_t
         return s;
     if (!dtable)
         return GEMM_ERR_INVALID_ARG;
-    const size_t need = gemm_embed_backward_workspace_size(T, N, V);
+    const EmbedPlan e = embed_plan(std::max<int64_t>(T, 1), N, V);
+    const size_t need = T > 0 ? e.bytes : 0;
     if (need > 0 && (!workspace || workspace_bytes < need))
         return GEMM_ERR_INVALID_ARG;
     if (need > 0 && !aligned_to(workspace, 256))
         return GEMM_ERR_ALIGNMENT;
-    const int64_t col_blocks = (N + kSumColumns - 1) / kSumColumns;
-    const EmbedPlan e = embed_plan(std::max<int64_t>(T, 1), N, V);
+    const int64_t col_blocks = column_blocks(N);
     if (col_blocks * e.chunks > kSizeLimit)
         return GEMM_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

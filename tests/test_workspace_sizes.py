@@ -1,0 +1,41 @@
+"""Workspace sizes of the ends of a training step, on the host: a buffer made for the most tokens serves fewer."""
+import random
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def g():
+    import __graft_entry__
+    __graft_entry__.build()
+    import smem_swizzle_layouts_gb300 as g
+    return g
+
+
+def counts_of_tokens(most, seed):
+    """Every count up to 600, then each limit that a plan may have (powers of two, multiples of 128 and of 608) and its
+    neighbours, and random ones."""
+    rng = random.Random(seed)
+    some = set(range(1, min(most, 600) + 1))
+    for step in (128, 304, 608, 1024):
+        some.update(t + d for t in range(step, min(most, 200 * step) + 1, step) for d in (-1, 0, 1))
+    some.update((1 << i) + d for i in range(1, 32) for d in (-1, 0, 1))
+    some.update(int(most ** rng.random()) for _ in range(2000))
+    return sorted(t for t in some if 1 <= t <= most)
+
+
+def never_falls(sizes):
+    return all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("N,V", [(1024, 32768), (2048, 32768), (8, 100), (1, 5), (1025, 300000), (3001, 131072), (700000, 64), (20000000, 3),
+                                 (96, 1 << 21), (640, 1)])
+def test_table_gradient(g, N, V):
+    sizes = [g.gemm_embed_backward_workspace_size(t, N, V) for t in counts_of_tokens(300000, N)]
+    assert never_falls(sizes) and sizes[0] > 0
+
+
+def test_table_gradient_takes_a_buffer_of_more_tokens(g):
+    """19455 rows of 1024 are summed in chunks half as long as those of 20000."""
+    room = g.gemm_embed_backward_workspace_size(20000, 1024, 32768)
+    assert room >= 2 * 1216 * 1024 * 4 + 16 * 19455
