@@ -651,7 +651,8 @@ gemm_status_t gemm_cross_entropy(int in_type, int64_t T, int64_t V, int64_t K, c
  * pieces that it has room for, of at most 2^27 / T columns (a piece's dl then has
  * 256 MB): gemm_cross_entropy_backward_workspace_size(T, V, K, columns) bytes for
  * pieces of `columns` columns (rounded up to a multiple of 256, the least; 0: the
- * widest), on the current device; 0 for bad arguments or without a device. The
+ * widest), on the current device; 0 for bad arguments or without a device. More
+ * tokens never ask for less, so that room for the most serves fewer. The
  * widths' order of sums differs, so gradients may differ in their last bits.
  */
 size_t gemm_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t K, int64_t columns);
@@ -814,6 +815,17 @@ int gemm_debug_streamk_units(int mode, int64_t tiles, int clusters, int kb_per_t
  * ms. Kind 0 has no tiles and no waits: M tokens, the others 0.
  */
 gemm_status_t gemm_debug_int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, int sms, int32_t *out);
+
+/*
+ * Host-side plan of gemm_cross_entropy_backward on a device with `sms` SMs (no GPU
+ * needed) in a workspace of workspace_bytes. Writes 6 int64: the bytes that
+ * gemm_cross_entropy_backward_workspace_size would return for pieces of `columns`,
+ * those that the call would use of the workspace (more than it has: the call
+ * refuses it), CTAs of a tile, pieces of the vocabulary, columns of a piece and
+ * parts of dX. One or two tokens without tiles have 0 in the last four.
+ */
+gemm_status_t gemm_debug_cross_entropy_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms,
+                                            uint64_t workspace_bytes, int64_t *out);
 
 /* Test hook: the next GEMM launch makes its MMA warp wait on a barrier
  * that nothing arrives at, with a wait bound of `timeout_ms`; every role

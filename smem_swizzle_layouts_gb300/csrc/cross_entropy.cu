@@ -1621,27 +1621,70 @@ struct BackPlan {
     size_t xs, dl[2], parts, bytes;  // offsets
 };
 
+// How the vocabulary is cut into pieces of at most `columns`, and the bytes of dl.
+struct Pieces {
+    int64_t piece, pieces, ldp;
+    size_t dl_bytes;  // one piece's
+};
+
+Pieces cut_vocabulary(int64_t T, int64_t V, int64_t columns)
+{
+    Pieces p;
+    p.pieces = (V + columns - 1) / columns;
+    p.piece = p.pieces == 1 ? V : round_up((V + p.pieces - 1) / p.pieces, 256);
+    p.pieces = (V + p.piece - 1) / p.piece;
+    p.ldp = round_up(p.piece, 64);
+    p.dl_bytes = static_cast<size_t>(round_up(T * p.ldp * 2, 256));
+    return p;
+}
+
+// Rows of a tile and elements of K in a block, and the most parts that dX is cut
+// into: two for each cluster that its tiles leave without one.
+struct DxTiles {
+    int cg, bn, bk;
+    int64_t slots, tiles, most_splits;
+};
+
+DxTiles dx_tiles(int64_t T, int64_t K, int sms)
+{
+    DxTiles d;
+    d.cg = T <= 128 ? 1 : 2;
+    d.bn = K <= 128 ? 128 : 256;
+    d.bk = d.cg == 2 ? kHeadBK<2> : kHeadBK<1>;
+    d.slots = std::max(1, sms / d.cg);
+    d.tiles = (T + 128 * d.cg - 1) / (128 * d.cg) * ((K + d.bn - 1) / d.bn);
+    d.most_splits = std::max<int64_t>(1, 2 * d.slots / d.tiles);
+    return d;
+}
+
+// Room for the most parts of dX that any piece would have: narrower pieces, of
+// which some have more, never need more room than wider ones.
+size_t parts_bytes(int64_t T, int64_t V, int64_t K, int sms)
+{
+    const DxTiles d = dx_tiles(T, K, sms);
+    return static_cast<size_t>(round_up(T * round_up(K, 8) * 4 * std::min(d.most_splits, (V + d.bk - 1) / d.bk), 256));
+}
+
 BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
 {
     BackPlan b = {};
-    b.cg = T <= 128 ? 1 : 2;
-    b.pieces = (V + columns - 1) / columns;
-    b.piece = b.pieces == 1 ? V : round_up((V + b.pieces - 1) / b.pieces, 256);
-    b.pieces = (V + b.piece - 1) / b.piece;
-    b.ldp = round_up(b.piece, 64);
+    const Pieces cut = cut_vocabulary(T, V, columns);
+    const DxTiles d = dx_tiles(T, K, sms);
+    b.cg = d.cg;
+    b.piece = cut.piece;
+    b.pieces = cut.pieces;
+    b.ldp = cut.ldp;
     b.ldk = round_up(K, 8);
-    b.dx_bn = K <= 128 ? 128 : 256;
+    b.dx_bn = d.bn;
     // dX has few tiles with long sums over the piece: in parts, where one would
     // take more than a third of what a cluster has to do in all
-    const int bk = b.cg == 2 ? kHeadBK<2> : kHeadBK<1>, rows = 128 * b.cg;
-    const int64_t slots = std::max(1, sms / b.cg);
-    auto blocks = [&](int64_t n) { return (n + bk - 1) / bk; };
+    const int rows = 128 * b.cg;
+    auto blocks = [&](int64_t n) { return (n + d.bk - 1) / d.bk; };
     auto tiles = [&](int64_t m, int64_t n, int bn) { return (m + rows - 1) / rows * ((n + bn - 1) / bn); };
-    const int64_t x_tiles = tiles(T, K, b.dx_bn), kb = blocks(b.piece);
-    const int64_t work = x_tiles * kb + tiles(b.piece, K, b.dx_bn) * (blocks(T) + 4) + (b.pieces > 1 ? tiles(T, b.piece, 256) * (blocks(K) + 4) : 0);
-    const int64_t most = std::max<int64_t>(8, work / slots / 3);
-    const int64_t most_splits = std::max<int64_t>(1, 2 * slots / x_tiles);
-    const int64_t wanted = std::min<int64_t>((kb + most - 1) / most, most_splits), unit = (kb + wanted - 1) / wanted;
+    const int64_t kb = blocks(b.piece);
+    const int64_t work = d.tiles * kb + tiles(b.piece, K, b.dx_bn) * (blocks(T) + 4) + (b.pieces > 1 ? tiles(T, b.piece, 256) * (blocks(K) + 4) : 0);
+    const int64_t most = std::max<int64_t>(8, work / d.slots / 3);
+    const int64_t wanted = std::min<int64_t>((kb + most - 1) / most, d.most_splits), unit = (kb + wanted - 1) / wanted;
     b.dx_splits = static_cast<int>((kb + unit - 1) / unit);
     size_t at = 256;
     auto take = [&](size_t bytes) {
@@ -1650,11 +1693,9 @@ BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
         return o;
     };
     b.xs = take(static_cast<size_t>(T) * b.ldk * 2);
-    b.dl[0] = take(static_cast<size_t>(T) * b.ldp * 2);
-    b.dl[1] = b.pieces > 1 ? take(static_cast<size_t>(T) * b.ldp * 2) : b.dl[0];
-    // room for the most parts that any piece would have: narrower pieces, of which
-    // some have more, never need more room than wider ones
-    b.parts = take(static_cast<size_t>(T) * b.ldk * 4 * std::min(most_splits, blocks(V)));
+    b.dl[0] = take(cut.dl_bytes);
+    b.dl[1] = b.pieces > 1 ? take(cut.dl_bytes) : b.dl[0];
+    b.parts = take(parts_bytes(T, V, K, sms));
     b.bytes = at;
     return b;
 }
@@ -1664,10 +1705,9 @@ BackPlan back_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
 // to stay in L2 from one launch to the next left most SMs without tiles (1 x
 // 131072 x 4096: 1140 us by tiles in pieces of 8192, 607 in one; 128 x 131072 x
 // 2048: 499 and 338).
-int64_t widest_piece(int64_t T)
-{
-    return std::max<int64_t>(256, (int64_t(1) << 27) / std::max<int64_t>(T, 1) / 256 * 256);
-}
+constexpr int64_t kDlElements = int64_t(1) << 27;
+
+int64_t widest_piece(int64_t T) { return std::max<int64_t>(256, kDlElements / std::max<int64_t>(T, 1) / 256 * 256); }
 
 // What both calls check of their shape.
 gemm_status_t check_head(int in_type, int64_t T, int64_t V, int64_t K, const void *X, int64_t ldx, const void *W, int64_t ldw,
@@ -1711,6 +1751,71 @@ constexpr int kFewTokens = 2;
 bool few_tokens(int64_t T, int64_t K) { return T <= kFewTokens && K <= 8 * kFewThreads; }
 
 size_t few_bytes(int64_t T, int64_t K) { return static_cast<size_t>(kFewBlocks) * T * round_up(K, 8) * 4; }
+
+// Most room for dl that up to T tokens take by pieces of at most `columns` (a
+// multiple of 256). Pieces of one width need more for more tokens, up to as many
+// as may have that width; the next width may then need less.
+size_t most_dl(int64_t T, int64_t V, int64_t columns)
+{
+    auto bytes = [&](int64_t t, int64_t c) {
+        const Pieces p = cut_vocabulary(t, V, c);
+        return p.dl_bytes * (p.pieces > 1 ? 2 : 1);
+    };
+    size_t most = bytes(T, std::min(columns, widest_piece(T)));
+    while (true) {
+        const Pieces p = cut_vocabulary(1, V, columns);
+        const int64_t last = kDlElements / round_up(p.piece, 256);  // tokens that may have pieces so wide
+        if (last >= T)
+            return most;
+        if (p.pieces > 1)  // two of them fill the limit, as all narrower ones may
+            return std::max(most, static_cast<size_t>(2 * 2 * kDlElements));
+        if (last > 0)
+            most = std::max(most, bytes(last, columns));
+        columns = widest_piece(last + 1);
+    }
+}
+
+// The same of dX's parts, whose number falls where a row of tiles begins, and by
+// half where tokens have tiles of CTA pairs.
+size_t most_parts(int64_t T, int64_t V, int64_t K, int sms)
+{
+    size_t most = parts_bytes(T, V, K, sms);
+    for (int64_t rows = 128; rows < T; rows += rows == 128 ? 128 : 256) {
+        most = std::max(most, parts_bytes(rows, V, K, sms));
+        if (rows > 128 && dx_tiles(rows, K, sms).most_splits == 1)
+            break;  // from here on one part, of more and more rows
+    }
+    return most;
+}
+
+// What the backward call asks for, for T tokens and for fewer.
+size_t back_bytes(int64_t T, int64_t V, int64_t K, int64_t columns, int sms)
+{
+    if (few_tokens(T, K))
+        return few_bytes(T, K);
+    const int64_t all = round_up(V, 256), wide = columns ? std::min(all, round_up(columns, 256)) : all;
+    const size_t tiles = 256 + static_cast<size_t>(round_up(T * round_up(K, 8) * 2, 256)) + most_dl(T, V, wide) + most_parts(T, V, K, sms);
+    return few_tokens(1, K) ? std::max(tiles, few_bytes(kFewTokens, K)) : tiles;
+}
+
+// The plan of a call: the widest pieces that its workspace has room for. The
+// only piece has one dl, and may need less than two pieces do.
+BackPlan fit_plan(int64_t T, int64_t V, int64_t K, size_t workspace_bytes, int sms)
+{
+    int64_t low = 1, high = std::min(round_up(V, 256), widest_piece(T)) / 256;
+    if (back_plan(T, V, K, 256 * high, sms).bytes <= workspace_bytes)
+        low = high;
+    else
+        high = std::max<int64_t>(1, high - 1);
+    while (low < high) {
+        const int64_t mid = (low + high + 1) / 2;
+        if (back_plan(T, V, K, 256 * mid, sms).bytes <= workspace_bytes)
+            low = mid;
+        else
+            high = mid - 1;
+    }
+    return back_plan(T, V, K, 256 * low, sms);
+}
 
 // The arguments of a backward call that its launches need.
 struct BackArgs {
@@ -1899,8 +2004,7 @@ size_t gemm_cross_entropy_backward_workspace_size(int64_t T, int64_t V, int64_t 
     unsigned int *status = nullptr;
     if (host_device(&dev, &status, &sms) != GEMM_OK)
         return 0;
-    const int64_t widest = std::min(round_up(V, 256), widest_piece(T));
-    return back_plan(T, V, K, columns ? std::min(widest, round_up(columns, 256)) : widest, sms).bytes;
+    return back_bytes(T, V, K, columns, sms);
 }
 
 gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int64_t K, const void *X, int64_t ldx, const void *W,
@@ -1945,22 +2049,7 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
     HeadParams p = {};
     if ((s = host_device(&dev, &p.status, &sms)) != GEMM_OK)
         return s;
-    // the widest pieces that the workspace has room for; the only piece has one
-    // dl, and may need less than two pieces do
-    BackPlan b = {};
-    int64_t low = 1, high = std::min(round_up(V, 256), widest_piece(T)) / 256;
-    if (back_plan(T, V, K, 256 * high, sms).bytes <= workspace_bytes)
-        low = high;
-    else
-        high = std::max<int64_t>(1, high - 1);
-    while (low < high) {
-        const int64_t mid = (low + high + 1) / 2;
-        if (back_plan(T, V, K, 256 * mid, sms).bytes <= workspace_bytes)
-            low = mid;
-        else
-            high = mid - 1;
-    }
-    b = back_plan(T, V, K, 256 * low, sms);
+    const BackPlan b = fit_plan(T, V, K, workspace_bytes, sms);
     if (b.bytes > workspace_bytes)
         return GEMM_ERR_INVALID_ARG;
     float *scale = reinterpret_cast<float *>(ws);
@@ -1992,6 +2081,25 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
         return host_launch(head_sum_kernel<D, 1>, static_cast<unsigned>(std::min<int64_t>((items + 255) / 256, 8 * sms)), 256, 0, st, 0, parts, splits,
                            stride, b.ldk, T, static_cast<int>(K), scale, static_cast<D *>(dX), lddx);
     });
+}
+
+gemm_status_t gemm_debug_cross_entropy_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms, uint64_t workspace_bytes, int64_t *out)
+{
+    if (!out || T < 1 || V < 1 || K < 1 || columns < 0 || sms < 1 || !countable(T) || !countable(V) || !countable(K))
+        return GEMM_ERR_INVALID_ARG;
+    out[0] = static_cast<int64_t>(back_bytes(T, V, K, columns, sms));
+    if (few_tokens(T, K)) {
+        out[1] = static_cast<int64_t>(few_bytes(T, K));
+        out[2] = out[3] = out[4] = out[5] = 0;
+        return GEMM_OK;
+    }
+    const BackPlan b = fit_plan(T, V, K, static_cast<size_t>(workspace_bytes), sms);
+    out[1] = static_cast<int64_t>(b.bytes);
+    out[2] = b.cg;
+    out[3] = b.pieces;
+    out[4] = b.piece;
+    out[5] = b.dx_splits;
+    return GEMM_OK;
 }
 
 }  // extern "C"

@@ -39,3 +39,37 @@ def test_table_gradient_takes_a_buffer_of_more_tokens(g):
     """19455 rows of 1024 are summed in chunks half as long as those of 20000."""
     room = g.gemm_embed_backward_workspace_size(20000, 1024, 32768)
     assert room >= 2 * 1216 * 1024 * 4 + 16 * 19455
+
+
+HEADS = [(32768, 1024), (131072, 2048), (50001, 1001), (5000, 64), (300, 129), (256, 8200), (1, 1), (1000003, 4096), (1 << 28, 8), (131072, 5000)]
+
+
+@pytest.mark.parametrize("sms", [152, 148, 1])
+@pytest.mark.parametrize("columns", [0, 256, 16384])
+@pytest.mark.parametrize("V,K", HEADS)
+def test_heads_gradients(g, V, K, columns, sms):
+    """More tokens never ask for less, and a call has room in what it asked for."""
+    plans = [(t, g.gemm_debug_cross_entropy_plan(t, V, K, columns, sms)) for t in counts_of_tokens(300000, V + K)]
+    assert never_falls([p["asked"] for _, p in plans])
+    for t, p in plans[::7]:
+        fit = g.gemm_debug_cross_entropy_plan(t, V, K, columns, sms, p["asked"])
+        assert 0 < fit["used"] <= p["asked"]
+        if fit["ctas"]:  # pieces at least as wide as was asked for
+            wide = min(-(-V // 256) * 256, columns or V, max(256, (1 << 27) // t // 256 * 256))
+            assert fit["pieces"] <= -(-V // wide)
+
+
+@pytest.mark.parametrize("most", [3, 129, 257, 600, 5000])
+@pytest.mark.parametrize("V,K", HEADS)
+def test_heads_gradients_take_a_buffer_of_more_tokens(g, V, K, most):
+    for columns in (0, 256, 4096):
+        room = g.gemm_debug_cross_entropy_plan(most, V, K, columns)["asked"]
+        for t in range(1, most + 1, 1 if most < 700 else 13):
+            assert g.gemm_debug_cross_entropy_plan(t, V, K, columns, 152, room)["used"] <= room, t
+
+
+@pytest.mark.parametrize("change", [dict(T=0), dict(V=0), dict(K=-1), dict(columns=-1), dict(sms=0), dict(V=(1 << 31) - 1)])
+def test_no_plan_for_bad_arguments(g, change):
+    with pytest.raises(g.GemmError) as e:
+        g.gemm_debug_cross_entropy_plan(**{**dict(T=100, V=1000, K=64, columns=0, sms=152), **change})
+    assert e.value.status == g.ERR_INVALID_ARG
