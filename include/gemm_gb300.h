@@ -679,7 +679,8 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
  * ids: T x k int32 as gemm_route writes them; logits: T x E of l_type, row
  * stride ldl. counts and means: S x E; all fp32 or int32. E, k as for gemm_route.
  * workspace: gemm_route_balance_workspace_size(T, E, S) bytes, 16-byte aligned,
- * in no particular state (may be NULL where that is 0). Sums have a fixed order.
+ * in no particular state (may be NULL where that is 0). More tokens or sequences
+ * never ask for less, so that room for the most serves fewer. Sums have a fixed order.
  */
 size_t gemm_route_balance_workspace_size(int64_t T, int64_t E, int64_t S);
 

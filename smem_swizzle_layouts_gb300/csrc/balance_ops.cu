@@ -501,6 +501,19 @@ BalancePlan balance_plan(int64_t T, int64_t E, int64_t S)
     return b;
 }
 
+// Room for T tokens and for fewer. Parts of one length are more for more tokens;
+// they get longer by one where the tokens reach another multiple of the sequences
+// or of the blocks. (Fewer sequences never have shorter parts.)
+size_t balance_bytes(int64_t T, int64_t E, int64_t S)
+{
+    size_t most = balance_plan(T, E, S).bytes;
+    for (int64_t part = kBalanceLeastPart; part <= kBalancePart; ++part)
+        for (const int64_t last : {(part + 1) * S - 1, part * kBalanceBlocks})
+            if (last < T)
+                most = std::max(most, balance_plan(last, E, S).bytes);
+    return most;
+}
+
 // What both calls check, and the parameters that they share.
 gemm_status_t check_balance(int64_t T, int64_t E, const void *logits, int l_type, int64_t ldl, int k, const gemm_route_t *route,
                             const int32_t *ids, int64_t S, const int32_t *offsets, BalanceParams *p)
@@ -551,7 +564,7 @@ size_t gemm_route_balance_workspace_size(int64_t T, int64_t E, int64_t S)
 {
     if (T < 1 || T > kSizeLimit || E < 1 || E > GEMM_ROUTE_MAX_EXPERTS || S < 1 || S > kSizeLimit / std::max<int64_t>(E, 8))
         return 0;
-    return balance_plan(T, E, S).bytes;
+    return balance_bytes(T, E, S);
 }
 
 gemm_status_t gemm_route_balance(int64_t T, int64_t E, const void *logits, gemm_out_t l_type, int64_t ldl, int k, const gemm_route_t *route,

@@ -73,3 +73,20 @@ def test_no_plan_for_bad_arguments(g, change):
     with pytest.raises(g.GemmError) as e:
         g.gemm_debug_cross_entropy_plan(**{**dict(T=100, V=1000, K=64, columns=0, sms=152), **change})
     assert e.value.status == g.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("E", [1, 60, 256, 1024])
+@pytest.mark.parametrize("S", [1, 2, 3, 16, 152, 700, 40000])
+def test_balance_loss(g, E, S):
+    sizes = [g.gemm_route_balance_workspace_size(t, E, S) for t in counts_of_tokens(300000, E + S)]
+    assert never_falls(sizes)
+
+
+@pytest.mark.parametrize("T", [1, 5, 32, 33, 600, 4864, 5017, 100000])
+def test_balance_loss_of_fewer_sequences(g, T):
+    assert never_falls([g.gemm_route_balance_workspace_size(T, 64, s) for s in range(1, 3000)])
+
+
+@pytest.mark.parametrize("V", [1, 300, 131072])
+def test_loss(g, V):
+    assert never_falls([g.gemm_cross_entropy_workspace_size(t, V) for t in counts_of_tokens(300000, V)])
