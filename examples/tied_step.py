@@ -26,9 +26,11 @@ def expect(name: str, t: torch.Tensor, dtype: torch.dtype, *shape: int) -> None:
 
 
 class TiedEnds:
-    """Buffers of both ends for up to ``tokens`` tokens of width ``H`` (a multiple of 8) and a table of ``V`` rows.
+    """Buffers of both ends for up to ``tokens`` tokens of width ``H`` (a multiple of 8), in as many sequences at most, and a
+    table of ``V`` rows.
 
-    ``forward`` keeps what ``backward`` needs; the buffers are reused: one step at a time.
+    The calls forward keep what those backward need; the buffers are reused: one step at a time. The workspace has room for
+    the most tokens, and the library's calls never ask for more for fewer.
     """
 
     def __init__(self, V: int, H: int, E: int, k: int, tokens: int, balance: float = 0.01, z: float = 1e-4, device="cuda"):
@@ -43,11 +45,14 @@ class TiedEnds:
                    g.gemm_embed_backward_workspace_size(tokens, H, V), g.gemm_route_balance_workspace_size(tokens, E, tokens))
         self.workspace = torch.empty(room, dtype=torch.uint8, device=device)  # one call uses it at a time
 
+    def fits(self, T: int, S: int = 0) -> None:
+        if T > self.tokens or S > self.tokens:
+            raise ValueError(f"{T} tokens in {S} sequences, with buffers for {self.tokens} of each")
+
     def rows(self, table: torch.Tensor, words: torch.Tensor) -> torch.Tensor:
         """The scaled rows [T, H] of ``words`` [T] int32."""
         T = words.numel()
-        if T > self.tokens:
-            raise ValueError(f"{T} tokens in buffers for {self.tokens}")
+        self.fits(T)
         expect("table", table, torch.bfloat16, self.V, self.H)
         expect("words", words, torch.int32, T)
         out = torch.empty(T, self.H, dtype=torch.bfloat16, device=table.device)
@@ -57,6 +62,7 @@ class TiedEnds:
     def route(self, logits: torch.Tensor, offsets: torch.Tensor):
         """Weights [T, k] and ids of the chosen experts, and the balance loss of each sequence (offsets [S + 1] int32)."""
         T, S = logits.shape[0], offsets.numel() - 1
+        self.fits(T, S)
         expect("logits", logits, torch.float32, T, self.E)
         expect("offsets", offsets, torch.int32, S + 1)
         dev = logits.device
@@ -67,18 +73,25 @@ class TiedEnds:
                              balance, self.workspace, self.workspace.numel())
         return self.weights[:T], self.ids[:T], balance
 
-    def loss(self, table: torch.Tensor, hidden: torch.Tensor, targets: torch.Tensor) -> torch.Tensor:
-        """Each token's loss [T]; targets outside the table (padding) have none."""
+    def head_inputs(self, table, hidden, targets) -> int:
         T = hidden.shape[0]
+        self.fits(T)
+        expect("table", table, torch.bfloat16, self.V, self.H)
         expect("hidden", hidden, torch.bfloat16, T, self.H)
         expect("targets", targets, torch.int32, T)
+        return T
+
+    def loss(self, table: torch.Tensor, hidden: torch.Tensor, targets: torch.Tensor) -> torch.Tensor:
+        """Each token's loss [T]; targets outside the table (padding) have none."""
+        T = self.head_inputs(table, hidden, targets)
         g.gemm_cross_entropy(1, T, self.V, self.H, hidden, self.H, table, self.H, targets, self.losses, self.lse, self.workspace,
                              self.workspace.numel())
         return self.losses[:T]
 
     def loss_backward(self, table, hidden, targets, d_losses):
         """Gradients of hidden [T, H] and of the table [V, H], with that of a penalty z * lse^2 on the normalisers."""
-        T = hidden.shape[0]
+        T = self.head_inputs(table, hidden, targets)
+        expect("d_losses", d_losses, torch.float32, T)
         d_hidden, d_table = torch.empty_like(hidden), torch.empty_like(table)
         d_lse = 2.0 * self.z * self.lse[:T] * d_losses
         g.gemm_cross_entropy_backward(1, T, self.V, self.H, hidden, self.H, table, self.H, targets, self.lse, d_losses, d_lse, d_hidden,
@@ -88,6 +101,9 @@ class TiedEnds:
     def route_backward(self, logits, offsets, d_weights):
         """The logits' gradient: through the weights, and of balance * mean over sequences of their losses."""
         T, S = logits.shape[0], offsets.numel() - 1
+        self.fits(T, S)
+        expect("logits", logits, torch.float32, T, self.E)
+        expect("offsets", offsets, torch.int32, S + 1)
         expect("d_weights", d_weights, torch.float32, T, self.k)
         d_logits = torch.empty_like(logits)
         d_balance = torch.full((S,), self.balance / S, device=logits.device)
@@ -99,6 +115,9 @@ class TiedEnds:
     def rows_backward(self, d_table: torch.Tensor, words: torch.Tensor, d_rows: torch.Tensor) -> None:
         """Adds the rows' gradient to the table's."""
         T = words.numel()
+        self.fits(T)
+        expect("d_table", d_table, torch.bfloat16, self.V, self.H)
+        expect("words", words, torch.int32, T)
         expect("d_rows", d_rows, torch.bfloat16, T, self.H)
         g.gemm_embed_backward(T, self.H, self.V, words, d_rows, g.OUT_BF16, self.H, self.scale, d_table, g.OUT_BF16, self.H, 1,
                               self.workspace, self.workspace.numel())

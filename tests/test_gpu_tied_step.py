@@ -153,3 +153,78 @@ def test_the_calls_together_replayed(example):
     torch.cuda.synchronize()
     for name in got:
         assert torch.equal(got[name], out[name]), name
+
+
+@pytest.mark.parametrize("V,H,most,tokens", [(32768, 1024, 257, 128), (32768, 1024, 129, 100), (700, 96, 600, 128), (700, 96, 600, 129), (700, 96, 600, 1),
+                                             (700, 96, 3, 2), (20000, 1024, 20000, 19455)])
+def test_fewer_tokens_than_the_buffers_hold(example, V, H, most, tokens):
+    """Every call has room for a batch of any size up to the most; the results are those of buffers of that size."""
+    E = 12
+    table, router, directions, words, targets = setup(tokens, V, H, E, seed=most)
+    offsets = torch.tensor([0, tokens // 2, tokens][-min(tokens, 2) - 1:], dtype=torch.int32, device=DEV)
+    outs = [example.step(example.TiedEnds(V, H, E, 3, n), table, router, directions, words, targets, offsets) for n in (most, tokens)]
+    torch.cuda.synchronize()
+    for a, b in zip(*outs):
+        assert bool(torch.isfinite(a.float()).all()) and bool(torch.isfinite(b.float()).all())
+    assert torch.equal(outs[0][1], outs[1][1])
+
+
+def test_each_row_of_the_tables_gradient(example):
+    """Row by row, so that a wrong one does not hide in the others' norm.
+
+    The 64-bit step takes the rows and the hidden rows as the step rounded them. What is rounded after that, u = 2^-8 of it at
+    most: dl (so that dX and the head's part of a table's row are off by u times their terms' absolute sums), dX, the rows'
+    gradient, the head's part and the row at the end. An error of dX comes to the rows' gradient by 1 + |router| |directions|
+    / 2 at most (norms of matrices; a softmax has a derivative of norm 1/2). 1.1 and 2^-16 are for what is done in 32 bits.
+    """
+    T, V, u = 500, 700, 2.0 ** -8
+    table, router, directions, words, targets = setup(T, seed=3, padded=20)
+    offsets = torch.tensor([0, 200, 480], dtype=torch.int32, device=DEV)
+    ends = example.TiedEnds(V, 96, 12, 3, T)
+    seen = {}
+
+    def spy(name, at):
+        call = getattr(ends, name)
+
+        def wrapped(*args):
+            out = call(*args)
+            seen[name] = (out if at is None else args[at]).clone()
+            return out
+
+        setattr(ends, name, wrapped)
+
+    spy("rows", None)
+    spy("loss", 1)
+    spy("rows_backward", 2)
+    got = example.step(ends, table, router, directions, words, targets, offsets)[1]
+    t, r, d = table.double().requires_grad_(), router.double(), directions.double()
+    on = (words >= 0).double()[:, None]
+    rows = t[words.long().clamp(min=0)] * on * ends.scale
+    rows = rows + (seen["rows"].double() - rows).detach()
+    p = torch.softmax(rows @ r, -1)
+    ids = ends.ids[:T].long()  # every token has its experts, padded ones too: those are behind the last sequence
+    hidden = rows + (p.gather(1, ids)[..., None] * d[ids]).sum(1)
+    hidden = hidden + (seen["loss"].double() - hidden).detach()
+    logits = hidden @ t.t()
+    good = ((targets >= 0) & (targets < V)).double()
+    a = good / good.sum()
+    lse = torch.logsumexp(logits, -1)
+    y = targets.long().clamp(0, V - 1)
+    total = (a * (lse - logits.gather(1, y[:, None])[:, 0] + ends.z * lse * lse)).sum()
+    cuts = offsets.tolist()
+    for lo, hi in zip(cuts[:-1], cuts[1:]):
+        f = torch.bincount(ids[lo:hi].flatten(), minlength=12).double() / (3 * (hi - lo))
+        total = total + ends.balance / 2 * 12 * (f * p[lo:hi].mean(0)).sum()
+    total.backward()
+    with torch.no_grad():
+        dl = torch.softmax(logits, -1) * (a * (1 + 2 * ends.z * lse))[:, None]
+        dl.scatter_add_(1, y[:, None], -a[:, None])
+        x, w = hidden.detach(), table.double()
+        d_hidden = u * ((dl.abs() @ w.abs()).norm(dim=1) + (dl @ w).norm(dim=1))
+        gain = 1 + float(torch.linalg.matrix_norm(r, 2) * torch.linalg.matrix_norm(d, 2)) / 2
+        d_rows = (gain * d_hidden + u * seen["rows_backward"].double().norm(dim=1)) * on[:, 0]
+        off = u * ((dl.abs().t() @ x.abs()).norm(dim=1) + (dl.t() @ x).norm(dim=1) + t.grad.norm(dim=1))
+        off.index_add_(0, words.long().clamp(min=0), ends.scale * d_rows)
+        err = (got.double() - t.grad).norm(dim=1)
+        assert bool((err <= 1.1 * off + 2.0 ** -16 * t.grad.norm(dim=1).max()).all()), float((err / off).max())
+        assert float(off.median()) < float(t.grad.norm(dim=1).median()) / 2  # a row of zeros, or another's, would show
