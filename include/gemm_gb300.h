@@ -828,6 +828,19 @@ gemm_status_t gemm_debug_int8_plan(int64_t M, int64_t N, int64_t K, int64_t E, i
 gemm_status_t gemm_debug_cross_entropy_plan(int64_t T, int64_t V, int64_t K, int64_t columns, int sms,
                                             uint64_t workspace_bytes, int64_t *out);
 
+/*
+ * Host-side listing of the units of one launch of the cross entropy calls (no GPU
+ * needed), by the code that deals them out and that the kernel's roles walk: of
+ * the forward call (want 0) or of a backward call for dX (1), dW (2) or both (3)
+ * in pieces of `columns` (0: the widest): `piece`'s gradients and the next piece's
+ * dl (-1: dl alone). Writes 8 int32 for each unit (room for max_units): the
+ * cluster, the product (0 dX, 1 dW, 2 logits), and the first and end of its
+ * rows, columns and K, clipped to the product's. Returns the number of units, or
+ * -1 for bad arguments and for tokens that have no tiles.
+ */
+int64_t gemm_debug_cross_entropy_units(int64_t T, int64_t V, int64_t K, int64_t columns, int sms, int64_t piece,
+                                       int want, int32_t *out, int64_t max_units);
+
 /* Test hook: the next GEMM launch makes its MMA warp wait on a barrier
  * that nothing arrives at, with a wait bound of `timeout_ms`; every role
  * then gives up and the kernel exits with GEMM_ERR_TIMEOUT recorded. */

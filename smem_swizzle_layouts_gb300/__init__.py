@@ -17,7 +17,7 @@ from ._lib import (  # noqa: F401
     gemm_route_balance_workspace_size,
     gemm_cross_entropy, gemm_cross_entropy_backward, gemm_cross_entropy_backward_workspace_size, gemm_cross_entropy_workspace_size,
     GemmCall, GemmError, GemmOptions, GemmProblem, gemm_bf16, gemm_bf16_grouped, gemm_bf16_grouped_noalloc, gemm_debug_descriptors,
-    gemm_debug_inject_timeout, gemm_debug_stage_image, gemm_debug_int8_plan, gemm_debug_cross_entropy_plan, gemm_debug_streamk_units, gemm_ex, gemm_f16, gemm_f16_grouped, gemm_fp4, gemm_fp4_scale_bytes, gemm_fp8, gemm_fp8_ex,
+    gemm_debug_inject_timeout, gemm_debug_stage_image, gemm_debug_int8_plan, gemm_debug_cross_entropy_plan, gemm_debug_cross_entropy_units, gemm_debug_streamk_units, gemm_ex, gemm_f16, gemm_f16_grouped, gemm_fp4, gemm_fp4_scale_bytes, gemm_fp8, gemm_fp8_ex,
     gemm_grouped_ex, gemm_grouped_workspace_size, gemm_mx_scale_bytes, gemm_mxfp8, gemm_streamk_workspace_size, gemm_last_device_status, gemm_launch_count, gemm_status_string,
 )
 

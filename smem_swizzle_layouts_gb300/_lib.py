@@ -93,6 +93,8 @@ _lib.gemm_debug_int8_plan.argtypes = [_i64, _i64, _i64, _i64, _int, ctypes.POINT
 _lib.gemm_debug_int8_plan.restype = _int
 _lib.gemm_debug_cross_entropy_plan.argtypes = [_i64, _i64, _i64, _i64, _int, ctypes.c_uint64, ctypes.POINTER(_i64)]
 _lib.gemm_debug_cross_entropy_plan.restype = _int
+_lib.gemm_debug_cross_entropy_units.argtypes = [_i64, _i64, _i64, _i64, _int, _i64, _int, ctypes.POINTER(ctypes.c_int32), _i64]
+_lib.gemm_debug_cross_entropy_units.restype = _i64
 _lib.gemm_debug_inject_timeout.argtypes = [_int]
 _lib.gemm_debug_inject_timeout.restype = None
 _lib.gemm_debug_inject_timeout_at.argtypes = [_int, _int]
@@ -151,7 +153,7 @@ EXPORTED = ("gemm_bf16", "gemm_f16", "gemm_ex", "gemm_fp8", "gemm_fp8_ex", "gemm
             "gemm_embed", "gemm_embed_backward", "gemm_embed_backward_workspace_size",
             "gemm_f16_grouped", "gemm_bf16_grouped_noalloc", "gemm_last_device_status", "gemm_status_string", "gemm_launch_count",
             "gemm_debug_descriptors", "gemm_debug_stage_image", "gemm_debug_plan", "gemm_debug_streamk_units",
-            "gemm_debug_int8_plan", "gemm_debug_cross_entropy_plan", "gemm_debug_inject_timeout", "gemm_debug_inject_timeout_at")
+            "gemm_debug_int8_plan", "gemm_debug_cross_entropy_plan", "gemm_debug_cross_entropy_units", "gemm_debug_inject_timeout", "gemm_debug_inject_timeout_at")
 
 
 class GemmError(RuntimeError):
@@ -337,6 +339,16 @@ def gemm_debug_cross_entropy_plan(T, V, K, columns=0, sms=152, workspace_bytes=2
     out = (_i64 * 6)()
     _check(_lib.gemm_debug_cross_entropy_plan(T, V, K, columns, sms, workspace_bytes, out), "gemm_debug_cross_entropy_plan")
     return dict(zip(("asked", "used", "ctas", "pieces", "piece", "splits"), out))
+
+
+def gemm_debug_cross_entropy_units(T, V, K, columns=0, sms=152, piece=-1, want=3):
+    """The units of one launch (no GPU needed): eight int32 each, one behind the other; None where there are no tiles."""
+    n = _lib.gemm_debug_cross_entropy_units(T, V, K, columns, sms, piece, want, None, 0)
+    if n < 0:
+        return None
+    out = (ctypes.c_int32 * (8 * n))()
+    _lib.gemm_debug_cross_entropy_units(T, V, K, columns, sms, piece, want, out, n)
+    return out
 
 
 def gemm_debug_streamk_units(mode, tiles, clusters, kb_per_tile, cluster):

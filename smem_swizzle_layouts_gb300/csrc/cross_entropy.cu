@@ -90,9 +90,9 @@ constexpr int kHeadTail = kHeadBars * 8 + 16;
 struct Divisor {
     unsigned d, m;
     int shift;
-    __device__ __forceinline__ int operator()(int n) const
+    __host__ __device__ __forceinline__ int operator()(int n) const
     {
-        return d == 1 ? n : static_cast<int>(__umulhi(static_cast<unsigned>(n), m) >> shift);
+        return d == 1 ? n : static_cast<int>(static_cast<unsigned>(static_cast<unsigned long long>(static_cast<unsigned>(n)) * m >> 32) >> shift);
     }
 };
 
@@ -200,18 +200,20 @@ struct HeadUnit {
     int m_blk, n_blk, split, kb0, kb1;
 };
 
-// A cluster's units, job after job: every role of both CTAs walks the same.
+// A cluster's units, job after job: every role of both CTAs walks the same, and
+// so does the host's listing of them.
 struct HeadUnits {
-    const HeadParams &p;
-    int c, G;
+    const HeadJob *jobs;
+    int num_jobs, c, G;
     int job = 0, round = 0;
 
-    __device__ __forceinline__ HeadUnits(const HeadParams &params, int cluster, int clusters) : p(params), c(cluster), G(clusters) {}
+    __device__ __forceinline__ HeadUnits(const HeadParams &p, int cluster, int clusters) : HeadUnits(p.jobs, p.num_jobs, cluster, clusters) {}
+    __host__ __device__ __forceinline__ HeadUnits(const HeadJob *js, int n, int cluster, int clusters) : jobs(js), num_jobs(n), c(cluster), G(clusters) {}
 
-    __device__ __forceinline__ bool next(HeadUnit &h)
+    __host__ __device__ __forceinline__ bool next(HeadUnit &h)
     {
-        while (job < p.num_jobs) {
-            const HeadJob &j = p.jobs[job];
+        while (job < num_jobs) {
+            const HeadJob &j = jobs[job];
             const int late = G - j.behind;  // clusters that are behind
             int u = -1;
             if (round < j.extra) {
@@ -241,7 +243,7 @@ struct HeadUnits {
             h.n_blk = rows(r);
             h.m_blk = g * j.group_m + r - h.n_blk * static_cast<int>(rows.d);
             h.kb0 = h.split * j.kb_unit;
-            h.kb1 = min(j.kb_all, h.kb0 + j.kb_unit);
+            h.kb1 = j.kb_all < h.kb0 + j.kb_unit ? j.kb_all : h.kb0 + j.kb_unit;
             return true;
         }
         return false;
@@ -1464,7 +1466,6 @@ int64_t whole_words(int64_t cols, int type) { return cols - cols % (16 / type_by
 // One operand of a product.
 struct Operand {
     const void *ptr;
-    int mn_major;
     int64_t ld;
 };
 
@@ -1494,8 +1495,10 @@ struct Job {
 // by three of 112 and 43.8 by two of 176.
 int64_t tile_cost(int cg, int bn) { return cg == 2 ? bn + 160 : bn + 16; }
 
+// The units of a product of A (M x K) and B (N x K), either of which may have its
+// rows or K contiguous (mn).
 template <int CG>
-gemm_status_t make_job(Job *job, int bn, int splits, int64_t M, int64_t N, int64_t K, int in_bf16, const Operand &A, const Operand &B, int a_rows)
+gemm_status_t shape_job(Job *job, int bn, int splits, int64_t M, int64_t N, int64_t K, int a_mn, int b_mn)
 {
     constexpr int BK = kHeadBK<CG>;
     HeadJob &j = job->j;
@@ -1520,36 +1523,36 @@ gemm_status_t make_job(Job *job, int bn, int splits, int64_t M, int64_t N, int64
     j.bn = bn;
     // the last tile of a row: as many boxes of 64 columns as it needs (where B's
     // K is contiguous, the stage's layout goes with the width, which stays)
-    j.bn_last = B.mn_major ? static_cast<int>(round_up(N - (tiles_n - 1) * bn, 64 * CG)) : bn;
-    j.a_mn = A.mn_major;
-    j.b_mn = B.mn_major;
+    j.bn_last = b_mn ? static_cast<int>(round_up(N - (tiles_n - 1) * bn, 64 * CG)) : bn;
+    j.a_mn = a_mn;
+    j.b_mn = b_mn;
     // an epilogue that no other unit's products cover costs about four blocks
     job->cost = (unit + 4) * ((tiles_n - 1) * tile_cost(CG, bn) + tile_cost(CG, j.bn_last)) / tiles_n;
-    gemm_status_t s = encode_16(&job->a, in_bf16, A.ptr, A.mn_major, M, K, A.ld, a_rows, BK);
-    if (s == GEMM_OK)
-        s = encode_16(&job->b, in_bf16, B.ptr, B.mn_major, N, K, B.ld, bn / CG, BK);
-    return s;
+    return GEMM_OK;
+}
+
+// Its operands' maps.
+template <int CG>
+gemm_status_t map_operands(Job *job, int in_bf16, const Operand &A, const Operand &B, int a_rows)
+{
+    constexpr int BK = kHeadBK<CG>;
+    const HeadJob &j = job->j;
+    const gemm_status_t s = encode_16(&job->a, in_bf16, A.ptr, j.a_mn, j.M, j.K, A.ld, a_rows, BK);
+    return s == GEMM_OK ? encode_16(&job->b, in_bf16, B.ptr, j.b_mn, j.N, j.K, B.ld, j.bn / CG, BK) : s;
 }
 
 template <int CG, bool FORWARD>
 std::atomic<uint64_t> head_attribute_set[2] = {{0}, {0}};
 
-// Deals the units of the jobs, the longest first, out to the clusters and
-// launches them together.
-template <int CG, bool FORWARD>
-gemm_status_t launch_head(HeadParams p, Job *jobs, int n, int sms, cudaStream_t st)
+// Deals the units of the jobs, the longest first, out to the clusters: the jobs
+// are put into that order. Returns the clusters.
+int64_t deal_units(Job *jobs, int n, int64_t slots)
 {
-    constexpr int BK = kHeadBK<CG>;
     std::sort(jobs, jobs + n, [](const Job &x, const Job &y) { return x.cost > y.cost; });
-    int64_t units = 0, longest = 0;
-    int bn = 0;
-    for (int i = 0; i < n; ++i) {
+    int64_t units = 0;
+    for (int i = 0; i < n; ++i)
         units += jobs[i].j.units;
-        longest = std::max<int64_t>(longest, jobs[i].j.kb_unit);
-        bn = std::max(bn, jobs[i].j.bn);
-    }
-    const int64_t clusters = std::min<int64_t>(units, std::max(1, sms / CG));
-    HeadMaps maps;
+    const int64_t clusters = std::min<int64_t>(units, slots);
     int64_t behind = 0, gap = 0;  // clusters from `behind` on have `gap` less to do
     for (int i = 0; i < n; ++i) {
         HeadJob &j = jobs[i].j;
@@ -1565,16 +1568,31 @@ gemm_status_t launch_head(HeadParams p, Job *jobs, int n, int sms, cudaStream_t 
         } else {
             behind = gap = 0;
         }
-        p.jobs[i] = j;
-        maps.a[i] = jobs[i].a;
-        maps.b[i] = jobs[i].b;
-        maps.d[i] = jobs[i].d;
     }
-    for (int i = n; i < kMaxJobs; ++i) {
-        p.jobs[i] = p.jobs[0];
-        maps.a[i] = maps.a[0];
-        maps.b[i] = maps.b[0];
-        maps.d[i] = maps.d[0];
+    return clusters;
+}
+
+int64_t cluster_slots(int cg, int sms) { return std::max(1, sms / cg); }
+
+// Deals the units out and launches the jobs together.
+template <int CG, bool FORWARD>
+gemm_status_t launch_head(HeadParams p, Job *jobs, int n, int sms, cudaStream_t st)
+{
+    constexpr int BK = kHeadBK<CG>;
+    const int64_t clusters = deal_units(jobs, n, cluster_slots(CG, sms));
+    int64_t longest = 0;
+    int bn = 0;
+    HeadMaps maps;
+    for (int i = 0; i < n; ++i) {
+        longest = std::max<int64_t>(longest, jobs[i].j.kb_unit);
+        bn = std::max(bn, jobs[i].j.bn);
+    }
+    for (int i = 0; i < kMaxJobs; ++i) {
+        const Job &job = jobs[i < n ? i : 0];
+        p.jobs[i] = job.j;
+        maps.a[i] = job.a;
+        maps.b[i] = job.b;
+        maps.d[i] = job.d;
     }
     p.num_jobs = n;
     p.b_rows = bn / CG;
@@ -1597,7 +1615,7 @@ gemm_status_t launch_head(HeadParams p, Job *jobs, int n, int sms, cudaStream_t 
 // that the 128 rows the tensor cores read of a stage lie inside it.
 int logit_columns(int cg, int64_t T, int64_t V, int a_rows, int step, int sms)
 {
-    const int64_t slots = std::max(1, sms / cg), tiles_m = (T + 128 * cg - 1) / (128 * cg);
+    const int64_t slots = cluster_slots(cg, sms), tiles_m = (T + 128 * cg - 1) / (128 * cg);
     const int least = cg == 2 ? 128 : std::max(64, 128 - a_rows);
     int best = 256;
     int64_t best_cost = 0;
@@ -1651,7 +1669,7 @@ DxTiles dx_tiles(int64_t T, int64_t K, int sms)
     d.cg = T <= 128 ? 1 : 2;
     d.bn = K <= 128 ? 128 : 256;
     d.bk = d.cg == 2 ? kHeadBK<2> : kHeadBK<1>;
-    d.slots = std::max(1, sms / d.cg);
+    d.slots = cluster_slots(d.cg, sms);
     d.tiles = (T + 128 * d.cg - 1) / (128 * d.cg) * ((K + d.bn - 1) / d.bn);
     d.most_splits = std::max<int64_t>(1, 2 * d.slots / d.tiles);
     return d;
@@ -1729,19 +1747,28 @@ gemm_status_t check_head(int in_type, int64_t T, int64_t V, int64_t K, const voi
 // Room for partial softmaxes on any GPU: one for each tile, which has at least 64 columns.
 size_t forward_bytes(int64_t T, int64_t V) { return static_cast<size_t>(T) * static_cast<size_t>((V + 63) / 64) * sizeof(float2); }
 
+// The forward product, and the rows of X's places in a stage.
+template <int CG>
+gemm_status_t forward_job(Job *job, int64_t T, int64_t V, int64_t K, int sms, int *a_rows)
+{
+    *a_rows = CG == 2 ? 128 : static_cast<int>(std::min<int64_t>(128, round_up(T, 8)));
+    const gemm_status_t s = shape_job<CG>(job, logit_columns(CG, T, V, *a_rows, CG == 2 ? 32 : 16, sms), 1, T, V, K, 0, 0);
+    job->j.epi = kEpiSoftmax;
+    job->j.kb_part = kSumPart / kHeadBK<CG>;
+    return s;
+}
+
 template <int CG>
 gemm_status_t run_forward(HeadParams p, int64_t T, int64_t V, int64_t K, int in_type, const Operand &X, const Operand &W, int *tiles, int sms,
                           cudaStream_t st)
 {
-    p.a_rows = CG == 2 ? 128 : static_cast<int>(std::min<int64_t>(128, round_up(T, 8)));
     Job job;
-    const int bn = logit_columns(CG, T, V, p.a_rows, CG == 2 ? 32 : 16, sms);
-    const gemm_status_t s = make_job<CG>(&job, bn, 1, T, V, K, in_type, X, W, p.a_rows);
+    if (forward_job<CG>(&job, T, V, K, sms, &p.a_rows) != GEMM_OK)
+        return GEMM_ERR_UNSUPPORTED;
+    const gemm_status_t s = map_operands<CG>(&job, in_type, X, W, p.a_rows);
     if (s != GEMM_OK)
         return s;
     job.d = job.a;
-    job.j.epi = kEpiSoftmax;
-    job.j.kb_part = kSumPart / kHeadBK<CG>;
     *tiles = job.j.tiles_n;
     return launch_head<CG, true>(p, &job, 1, sms, st);
 }
@@ -1873,6 +1900,51 @@ gemm_status_t run_few(const BackArgs &g, FewParams p, cudaStream_t st)
     });
 }
 
+// The products of one launch, in the order dX, dW, dl (those that it has): piece
+// i's gradients, and the next piece's dl. Piece -1 has dl alone.
+struct PieceJobs {
+    Job jobs[kMaxJobs];
+    int n = 0;
+    Job *dx = nullptr, *dw = nullptr, *dl = nullptr;
+    int a_rows;
+    int64_t v0, cols, w0, next;  // the piece's first column and its columns, the next one's
+};
+
+template <int CG>
+gemm_status_t piece_jobs(PieceJobs *q, const BackPlan &b, int64_t i, int64_t T, int64_t V, int64_t K, bool want_x, bool want_w, int sms)
+{
+    gemm_status_t s;
+    q->v0 = i * b.piece;
+    q->cols = std::min(b.piece, V - q->v0);
+    // dl alone: places of few rows leave the stages to the weights
+    q->a_rows = CG == 1 && i < 0 ? static_cast<int>(std::min<int64_t>(128, round_up(T, 8))) : 128;
+    if (i >= 0 && want_x) {
+        q->dx = &q->jobs[q->n++];
+        if ((s = shape_job<CG>(q->dx, b.dx_bn, b.dx_splits, T, K, q->cols, 0, 1)) != GEMM_OK)
+            return s;
+        q->dx->j.epi = kEpiProduct;
+    }
+    if (i >= 0 && want_w) {
+        q->dw = &q->jobs[q->n++];
+        if ((s = shape_job<CG>(q->dw, b.dx_bn, 1, q->cols, K, T, 1, 1)) != GEMM_OK)
+            return s;
+        q->dw->j.epi = kEpiProduct;
+    }
+    if (i + 1 < b.pieces) {
+        q->dl = &q->jobs[q->n++];
+        q->w0 = (i + 1) * b.piece;
+        q->next = std::min(b.piece, V - q->w0);
+        // by its own rounds of the grid, where it has a launch to itself or too few wide tiles for all clusters
+        const int64_t wide = (T + 128 * CG - 1) / (128 * CG) * ((q->next + 255) / 256);
+        const int bn = q->n == 1 || wide < 2 * sms / CG ? logit_columns(CG, T, q->next, q->a_rows, 64, sms) : 256;
+        if ((s = shape_job<CG>(q->dl, bn, 1, T, q->next, K, 0, 0)) != GEMM_OK)
+            return s;
+        q->dl->j.epi = kEpiLogitGrad;
+        q->dl->j.v0 = static_cast<int>(q->w0);
+    }
+    return GEMM_OK;
+}
+
 // One launch for each piece: its gradients and the next piece's dl, which do not
 // wait for one another, so that the units of one product fill what the rounds of
 // the others leave of the grid.
@@ -1881,21 +1953,19 @@ gemm_status_t run_backward(HeadParams p, const BackArgs &g, const BackPlan &b, i
 {
     const int ew = type_bytes(g.dw_type);
     float *parts = reinterpret_cast<float *>(g.ws + b.parts);
+    auto weights = [&](int64_t v) { return Operand{static_cast<const char *>(g.W.ptr) + v * g.W.ld * 2, g.W.ld}; };
     for (int64_t i = -1; i < b.pieces; ++i) {
-        Job jobs[kMaxJobs];
-        int n = 0;
-        gemm_status_t s;
-        const int64_t v0 = i * b.piece, cols = std::min(b.piece, g.V - v0);
-        // dl alone: places of few rows leave the stages to the weights
-        p.a_rows = CG == 1 && i < 0 ? static_cast<int>(std::min<int64_t>(128, round_up(g.T, 8))) : 128;
-        if (i >= 0 && g.dX) {
-            Job &job = jobs[n++];
-            if ((s = make_job<CG>(&job, b.dx_bn, b.dx_splits, g.T, g.K, cols, g.in_type, {g.ws + b.dl[i & 1], 0, b.ldp},
-                                  {static_cast<const char *>(g.W.ptr) + v0 * g.W.ld * 2, 1, g.W.ld}, 128)) != GEMM_OK)
+        PieceJobs q;
+        gemm_status_t s = piece_jobs<CG>(&q, b, i, g.T, g.V, g.K, g.dX != nullptr, g.dW != nullptr, sms);
+        if (s != GEMM_OK)
+            return s;
+        p.a_rows = q.a_rows;
+        const Operand dl = {i >= 0 ? g.ws + b.dl[i & 1] : nullptr, b.ldp};
+        if (q.dx) {
+            if ((s = map_operands<CG>(q.dx, g.in_type, dl, weights(q.v0), 128)) != GEMM_OK)
                 return s;
             const bool last = i == b.pieces - 1 && b.dx_splits == 1;
-            HeadJob &j = job.j;
-            j.epi = kEpiProduct;
+            HeadJob &j = q.dx->j;
             j.out_type = last ? g.dx_type : GEMM_OUT_F32;
             j.scaled = last;
             j.slot_rows = g.T;
@@ -1906,16 +1976,14 @@ gemm_status_t run_backward(HeadParams p, const BackArgs &g, const BackPlan &b, i
             j.whole = static_cast<int>(last ? whole_words(g.K, g.dx_type) : b.ldk);
             j.d = g.dX;
             j.ldd = g.lddx;
-            if ((s = encode_out(&job.d, j.out_type, last ? g.dX : parts, g.T, j.whole, last ? g.lddx : b.ldk, last ? 1 : b.dx_splits)) != GEMM_OK)
+            if ((s = encode_out(&q.dx->d, j.out_type, last ? g.dX : parts, g.T, j.whole, last ? g.lddx : b.ldk, last ? 1 : b.dx_splits)) != GEMM_OK)
                 return s;
         }
-        if (i >= 0 && g.dW) {
-            Job &job = jobs[n++];
-            if ((s = make_job<CG>(&job, b.dx_bn, 1, cols, g.K, g.T, g.in_type, {g.ws + b.dl[i & 1], 1, b.ldp}, {g.ws + b.xs, 1, b.ldk}, 128)) != GEMM_OK)
+        if (q.dw) {
+            if ((s = map_operands<CG>(q.dw, g.in_type, dl, {g.ws + b.xs, b.ldk}, 128)) != GEMM_OK)
                 return s;
-            char *o = static_cast<char *>(g.dW) + v0 * g.lddw * ew;
-            HeadJob &j = job.j;
-            j.epi = kEpiProduct;
+            char *o = static_cast<char *>(g.dW) + q.v0 * g.lddw * ew;
+            HeadJob &j = q.dw->j;
             j.out_type = g.dw_type;
             j.scaled = 1;
             j.slot_rows = 0;
@@ -1926,28 +1994,78 @@ gemm_status_t run_backward(HeadParams p, const BackArgs &g, const BackPlan &b, i
             j.whole = static_cast<int>(whole_words(g.K, g.dw_type));
             j.d = o;
             j.ldd = g.lddw;
-            if ((s = encode_out(&job.d, g.dw_type, o, cols, j.whole, g.lddw)) != GEMM_OK)
+            if ((s = encode_out(&q.dw->d, g.dw_type, o, q.cols, j.whole, g.lddw)) != GEMM_OK)
                 return s;
         }
-        if (i + 1 < b.pieces) {
-            Job &job = jobs[n++];
-            const int64_t w0 = (i + 1) * b.piece, next = std::min(b.piece, g.V - w0);
-            // by its own rounds of the grid, where it has a launch to itself or too few wide tiles for all clusters
-            const int64_t wide = (g.T + 128 * CG - 1) / (128 * CG) * ((next + 255) / 256);
-            const int bn = n == 1 || wide < 2 * sms / CG ? logit_columns(CG, g.T, next, p.a_rows, 64, sms) : 256;
-            if ((s = make_job<CG>(&job, bn, 1, g.T, next, g.K, g.in_type, g.X, {static_cast<const char *>(g.W.ptr) + w0 * g.W.ld * 2, 0, g.W.ld}, p.a_rows)) !=
-                GEMM_OK)
-                return s;
-            job.j.epi = kEpiLogitGrad;
-            job.j.v0 = static_cast<int>(w0);
-            if ((s = encode_out(&job.d, g.in_type == 1 ? GEMM_OUT_BF16 : GEMM_OUT_F16, g.ws + b.dl[(i + 1) & 1], g.T, round_up(next, 8), b.ldp)) !=
-                GEMM_OK)
+        if (q.dl) {
+            if ((s = map_operands<CG>(q.dl, g.in_type, g.X, weights(q.w0), q.a_rows)) != GEMM_OK ||
+                (s = encode_out(&q.dl->d, g.in_type == 1 ? GEMM_OUT_BF16 : GEMM_OUT_F16, g.ws + b.dl[(i + 1) & 1], g.T, round_up(q.next, 8), b.ldp)) !=
+                    GEMM_OK)
                 return s;
         }
-        if ((s = launch_head<CG, false>(p, jobs, n, sms, st)) != GEMM_OK)
+        if ((s = launch_head<CG, false>(p, q.jobs, q.n, sms, st)) != GEMM_OK)
             return s;
     }
     return GEMM_OK;
+}
+
+// The units of one launch in the order in which its clusters take them: for each
+// the cluster, the product (0 dX, 1 dW, 2 logits), and the first and end of its
+// rows, columns and K.
+template <int CG>
+int64_t list_units(Job *jobs, int n, int sms, const int *product, int32_t *out, int64_t most)
+{
+    for (int i = 0; i < n; ++i)
+        jobs[i].j.out_type = product[i];  // through the sort
+    const int64_t clusters = deal_units(jobs, n, cluster_slots(CG, sms));
+    HeadJob js[kMaxJobs];
+    for (int i = 0; i < n; ++i)
+        js[i] = jobs[i].j;
+    int64_t count = 0;
+    for (int64_t c = 0; c < clusters; ++c) {
+        HeadUnits units(js, n, static_cast<int>(c), static_cast<int>(clusters));
+        HeadUnit h;
+        while (units.next(h)) {
+            if (count < most) {
+                const HeadJob &j = js[h.job];
+                int32_t *o = out + 8 * count;
+                auto range = [&](int first, int step, int end) {
+                    *o++ = first;
+                    *o++ = std::min(first + step, end);
+                };
+                *o++ = static_cast<int32_t>(c);
+                *o++ = j.out_type;
+                range(h.m_blk * 128 * CG, 128 * CG, j.M);
+                range(h.n_blk * j.bn, h.n_blk == j.tiles_n - 1 ? j.bn_last : j.bn, j.N);
+                range(h.kb0 * kHeadBK<CG>, (h.kb1 - h.kb0) * kHeadBK<CG>, j.K);
+            }
+            ++count;
+        }
+    }
+    return count;
+}
+
+template <int CG>
+int64_t launch_units(int64_t T, int64_t V, int64_t K, int64_t columns, int sms, int64_t piece, int want, int32_t *out, int64_t most)
+{
+    if (want == 0) {
+        Job job;
+        int a_rows, product = 2;
+        return forward_job<CG>(&job, T, V, K, sms, &a_rows) == GEMM_OK ? list_units<CG>(&job, 1, sms, &product, out, most) : -1;
+    }
+    const int64_t widest = std::min(round_up(V, 256), widest_piece(T));
+    const BackPlan b = back_plan(T, V, K, columns ? std::min(widest, round_up(columns, 256)) : widest, sms);
+    PieceJobs q;
+    if (piece < -1 || piece >= b.pieces || piece_jobs<CG>(&q, b, piece, T, V, K, want & 1, want & 2, sms) != GEMM_OK)
+        return -1;
+    int products[kMaxJobs], n = 0;
+    if (q.dx)
+        products[n++] = 0;
+    if (q.dw)
+        products[n++] = 1;
+    if (q.dl)
+        products[n++] = 2;
+    return list_units<CG>(q.jobs, n, sms, products, out, most);
 }
 
 }  // namespace
@@ -1984,8 +2102,8 @@ gemm_status_t gemm_cross_entropy(int in_type, int64_t T, int64_t V, int64_t K, c
     p.picked = losses;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     int parts = 0;
-    s = T <= 128 ? run_forward<1>(p, T, V, K, in_type, {X, 0, ldx}, {W, 0, ldw}, &parts, sms, st)
-                 : run_forward<2>(p, T, V, K, in_type, {X, 0, ldx}, {W, 0, ldw}, &parts, sms, st);
+    s = T <= 128 ? run_forward<1>(p, T, V, K, in_type, {X, ldx}, {W, ldw}, &parts, sms, st)
+                 : run_forward<2>(p, T, V, K, in_type, {X, ldx}, {W, ldw}, &parts, sms, st);
     if (s != GEMM_OK)
         return s;
     if (T <= 512)
@@ -2034,7 +2152,7 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
     if (!aligned_to(lse, 4) || !aligned_to(dlosses, 4) || !aligned_to(dlse, 4) || !aligned_to(workspace, 256))
         return GEMM_ERR_ALIGNMENT;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const BackArgs args = {in_type, T, V, K, {X, 0, ldx}, {W, 0, ldw}, dX, dW, dx_type, dw_type, lddx, lddw, accumulate != 0, ws};
+    const BackArgs args = {in_type, T, V, K, {X, ldx}, {W, ldw}, dX, dW, dx_type, dw_type, lddx, lddw, accumulate != 0, ws};
     if (few_tokens(T, K)) {
         if (workspace_bytes < few_bytes(T, K))
             return GEMM_ERR_INVALID_ARG;
@@ -2100,6 +2218,16 @@ gemm_status_t gemm_debug_cross_entropy_plan(int64_t T, int64_t V, int64_t K, int
     out[4] = b.piece;
     out[5] = b.dx_splits;
     return GEMM_OK;
+}
+
+int64_t gemm_debug_cross_entropy_units(int64_t T, int64_t V, int64_t K, int64_t columns, int sms, int64_t piece, int want, int32_t *out,
+                                       int64_t max_units)
+{
+    if (T < 1 || V < 1 || K < 1 || columns < 0 || sms < 1 || !countable(T) || !countable(V) || !countable(K) || want < 0 || want > 3 || max_units < 0 ||
+        (max_units > 0 && !out) || (want > 0 && few_tokens(T, K)))
+        return -1;
+    return T <= 128 ? launch_units<1>(T, V, K, columns, sms, piece, want, out, max_units)
+                    : launch_units<2>(T, V, K, columns, sms, piece, want, out, max_units);
 }
 
 }  // extern "C"
