@@ -620,7 +620,9 @@ gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const voi
  * 16-byte aligned, ldx and ldw multiples of 8, as for gemm_ex). A token whose
  * target is outside 0..V-1 (padding, a prompt that is not trained on) has no
  * loss: losses[t] and lse[t] are 0, whatever its row of X holds. Logits are
- * summed in fp32; sums of exponentials, lse and losses are fp32, the loss
+ * summed in fp32, by tensor cores whose additions truncate in parts of 512
+ * elements of K at most (256 for T <= 128, 128 for T <= 2) and by rounded additions
+ * from part to part; sums of exponentials, lse and losses are fp32, the loss
  * without the rounding of lse. A logit of +inf makes lse +inf, one of NaN NaN.
  * workspace: gemm_cross_entropy_workspace_size(T, V) bytes, 16-byte aligned,
  * in no particular state.
@@ -644,9 +646,12 @@ gemm_status_t gemm_cross_entropy(int in_type, int64_t T, int64_t V, int64_t K, c
  * finite W), and what their rows of X, dlosses and dlse hold has no part in dW.
  * dl is computed for a piece of the vocabulary at a time and rounded to the
  * inputs' type for the tensor cores, after a division by the largest
- * |dlosses| + |dlse| (found on the GPU: any scaling of the loss gives the same
- * gradients, times it); for one or two tokens of K <= 4096 it is not rounded. Products are summed in fp32. T == 0 leaves dX and writes
- * zeros to dW (nothing with accumulate).
+ * |dlosses| + |dlse| (found on the GPU: any scaling of the loss that leaves it
+ * above 1e-30 gives the same gradients, times it); for one or two tokens of
+ * K <= 4096 it is not rounded. The logits are summed as in the forward call, so that
+ * exp(l - lse) of a certain word is 1; dX and dW in fp32 by the tensor cores, whose
+ * additions truncate (every 16 terms, by up to 2^-23 of the sum so far).
+ * T == 0 leaves dX and writes zeros to dW (nothing with accumulate).
  * workspace: 256-byte aligned, in no particular state. The call takes the widest
  * pieces that it has room for, of at most 2^27 / T columns (a piece's dl then has
  * 256 MB): gemm_cross_entropy_backward_workspace_size(T, V, K, columns) bytes for

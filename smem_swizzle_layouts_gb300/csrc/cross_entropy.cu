@@ -53,32 +53,58 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// What a launch of the kernel does: the forward product; gradients; gradients
+// with dl whose sums over K are taken in parts.
+enum : int { kForward = 0, kBackward = 1, kBackwardParts = 2 };
+
 // Epilogue warps: a lane quarter each, and a half or (a pair's softmax) a quarter
 // of the columns. The softmax has no staging buffers, and while some of its 16
 // warps wait for TMEM others have work: 7252 x 118755 x 128 forward 346 us (384
 // by 8), 8192 x 32768 x 256 112 (123); 2048 x 32768 x 1024 78.7 (77.3). A single
 // CTA's few rows leave most warps without any: 1 x 131072 x 4096 167 (157).
-template <int CG, bool FORWARD>
-constexpr int kHeadWarps = CG == 2 && FORWARD ? 16 : 8;
-template <int CG, bool FORWARD>
-constexpr int kHeadThreads = 64 + 32 * kHeadWarps<CG, FORWARD>;
+template <int CG, int MODE>
+constexpr int kHeadWarps = CG == 2 && MODE == kForward ? 16 : 8;
+// Before them the producer and the issuer. Where dl is made of parts, a thread
+// holds 128 sums beside what it packs: two idle warps make the first four a
+// warpgroup that leaves registers to the epilogue's (without that the sums went
+// through memory: 4096 x 32768 x 4096 2070 to 2370 us, now 1918). Such launches
+// have a kernel of their own, as that code in one with the others slowed them down
+// (8192 x 32768 x 256 backward 388 us instead of 365).
+template <int MODE>
+constexpr int kHeadFirstWarp = MODE == kBackwardParts ? 4 : 2;
+template <int CG, int MODE>
+constexpr int kHeadThreads = 32 * (kHeadFirstWarp<MODE> + kHeadWarps<CG, MODE>);
+constexpr int kBackLaunchRegs = 168, kBackIssueRegs = 56, kBackEpiRegs = 224;
+static_assert(128 * kBackIssueRegs + 32 * kHeadWarps<2, kBackwardParts> * kBackEpiRegs <= kHeadThreads<2, kBackwardParts> * kBackLaunchRegs &&
+                  kHeadThreads<2, kBackwardParts> * kBackLaunchRegs <= 65536,
+              "the shares add up to no more than the block is launched with");
 constexpr int kHeadMaxStages = 12;
 constexpr int kAccStride = 256;                    // TMEM columns from one accumulator to the next
 constexpr int kHeadSmem = 232448 - 1024;           // less the slack that rounds the base up to 1024 bytes
 
-// Elements of K that the tensor cores sum for the softmax before the sum is
-// added to the others in registers. Their additions truncate (every 16 elements,
-// to the accumulator's 24 bits), which moves a logit towards 0 by up to half a
-// part in 2^24 for each. Relative error of the losses, and time, of 8192 tokens,
-// 65536 words and K = 4096 by parts of 256, 512, 1024 and all of K: 0.9e-7 (2516
-// us), 1.7e-7 (2409), 3.3e-7 (2370), 1.4e-6 (2387).
-constexpr int kSumPart = 512;
+// Elements of K that the tensor cores sum for a logit before the sum is added to
+// the others in registers. Their additions truncate (every 16 elements, to the
+// accumulator's 24 bits), which moves a logit towards 0 by up to half a part in
+// 2^24 for each. Relative error of the losses, and time, of 8192 tokens, 65536
+// words and K = 4096 by parts of 256, 512, 1024 and all of K: 0.9e-7 (2516 us),
+// 1.7e-7 (2409), 3.3e-7 (2370), 1.4e-6 (2387). A single CTA's tiles wait for the
+// weights: their parts of 256 take as long (77 x 50001 x 2001: 45.1 us by 512,
+// 45.6 by 256, 46.3 by 128). Backward the logits are summed in the same parts, so
+// that exp(l - lse) is 1 where it should be: with all of K in one part a target's
+// dl of 3e-10 came out as 4e-4 (K = 4096, a logit of 30) and 2e-3 (16384); with
+// these parts it is 1e-6, for 2 to 4 % of the time (4096 x 32768 x 4096 1918
+// us instead of 1876, 777 x 50001 x 1001 238 instead of 230, 128 x 131072 x 2048
+// 330 both ways). The gradients of one or two tokens may be without tiles, by
+// sums that round, where the forward pass's error does not cancel: theirs
+// are the smallest parts (1 x 131072 x 4096: 158.1 us by 512, 159.5 by 128; dl 3e-5
+// and 4e-6).
+constexpr int64_t sum_part(int cg, int64_t T) { return cg == 2 ? 512 : T <= 2 ? 128 : 256; }
 
 // What the epilogue does with the accumulator.
 enum : int { kEpiSoftmax = 0, kEpiLogitGrad = 1, kEpiProduct = 2 };
 
 // Offsets behind the stages: staging chunks, then barriers.
-constexpr int kHeadStageBytes = kHeadWarps<2, false> * kEpiBufBytes;
+constexpr int kHeadStageBytes = kHeadWarps<2, kBackward> * kEpiBufBytes;
 constexpr int kHeadBars = 2 * kHeadMaxStages + 4 + 2 + 8;
 constexpr int kHeadShares = 3 * 128 * 8;  // forward: partial softmaxes of up to three quarters of a tile's columns for each of its rows
 constexpr int kHeadTail = kHeadBars * 8 + 16;
@@ -631,7 +657,8 @@ __device__ __forceinline__ void mbar_arrive_read(uint32_t cluster_bar)
 }
 
 // An epilogue warp's view of the accumulators: waits for the next one and hands
-// it back. Warp w has TMEM lanes 32 (w mod 4) .. +31 and half of the columns.
+// it back. Warp w has TMEM lanes 32 (w mod 4) .. +31 and a half or a quarter of the
+// columns.
 template <int CG>
 struct Accumulators {
     uint32_t bar_full, bar_empty, tmem;  // bar_empty: the even CTA's
@@ -671,7 +698,7 @@ template <int CG>
 __device__ void softmax_epilogue(const HeadParams &p, float2 *shares, uint32_t bar_shares, Accumulators<CG> a, uint32_t rank, int warp, int lane,
                                  const Waiter &w)
 {
-    constexpr int SHARES = kHeadWarps<CG, true> / 4, N = 8 / SHARES;  // warps of a row, their chunks of 32 columns
+    constexpr int SHARES = kHeadWarps<CG, kForward> / 4, N = 8 / SHARES;  // warps of a row, their chunks of 32 columns
     const int q = warp & 3, share = (warp - 2) >> 2;
     float2 *const slot = shares + 32 * q + lane;  // 128 from one share's to the next
     const uint32_t bar_ready = bar_shares + 16 * q, bar_free = bar_ready + 8;
@@ -754,41 +781,85 @@ __device__ void softmax_epilogue(const HeadParams &p, float2 *shares, uint32_t b
     }
 }
 
-// One tile of dl.
+// 64 columns of a tile of dl, from column c on.
+__device__ __forceinline__ void logit_grad_chunk(const HeadParams &p, const CUtensorMap *map, const RowGrad &g, float (&lo)[32], float (&hi)[32],
+                                                 int m0, int n0, int c, uint32_t sbuf, int lane)
+{
+    const uint64_t by = pair_of(kLog2e, kLog2e), less = pair_of(-g.lse2, -g.lse2), scale = pair_of(g.a, g.a);
+    uint32_t o[32];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float (&v)[32] = i == 0 ? lo : hi;
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const float2 l = pair_to(fma_pair(pair_of(v[k], v[k + 1]), by, less));
+            const float2 d = pair_to(mul_pair(pair_of(ex2(l.x), ex2(l.y)), scale));
+            v[k] = d.x;
+            v[k + 1] = d.y;
+        }
+        const int at = g.target - (n0 + c + 32 * i);
+        if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                v[k] -= at == k ? g.b : 0.0f;
+        }
+        pack32<64>(v, i, p.in_bf16 ? 1 : 2, o);
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        o[k] = g.live ? o[k] : 0u;  // whatever the row of a token without a loss made of them
+    stage_and_store<64>(o, sbuf, lane, map, n0 + c, m0, 0);
+}
+
+// One tile of dl whose sums over K are one part: each 64 columns as they come.
 template <int CG>
 __device__ __forceinline__ void logit_grad_tile(const HeadParams &p, const CUtensorMap *map, const RowGrad &g, const Accumulators<CG> &a, int q,
                                                 int half, int m0, int n0, int cols, uint32_t sbuf, int lane)
 {
-    const uint64_t by = pair_of(kLog2e, kLog2e), less = pair_of(-g.lse2, -g.lse2), scale = pair_of(g.a, g.a);
     for (int c = 64 * half; c < cols; c += 128) {
-        uint32_t o[32];
         float x[2][32];
         fetch_acc32(a.columns(q, c), x[0]);
         fetch_acc32(a.columns(q, c + 32), x[1]);
         tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float (&v)[32] = x[i];
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-                const float2 l = pair_to(fma_pair(pair_of(v[k], v[k + 1]), by, less));
-                const float2 d = pair_to(mul_pair(pair_of(ex2(l.x), ex2(l.y)), scale));
-                v[k] = d.x;
-                v[k + 1] = d.y;
-            }
-            const int at = g.target - (n0 + c + 32 * i);
-            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    v[k] -= at == k ? g.b : 0.0f;
-            }
-            pack32<64>(v, i, p.in_bf16 ? 1 : 2, o);
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-            o[k] = g.live ? o[k] : 0u;  // whatever the row of a token without a loss made of them
-        stage_and_store<64>(o, sbuf, lane, map, n0 + c, m0, 0);
+        logit_grad_chunk(p, map, g, x[0], x[1], m0, n0, c, sbuf, lane);
     }
+}
+
+// One tile of dl from the parts of its sums over K, added up in registers as the
+// forward pass adds them. False if a wait has run out.
+template <int CG>
+__device__ __forceinline__ bool logit_grad_parts(const HeadParams &p, const HeadJob &j, const CUtensorMap *map, Accumulators<CG> &a, int q,
+                                                 int half, int m0, int n0, int cols, uint32_t sbuf, int lane, uint32_t rank, const Waiter &w)
+{
+    const bool rows = m0 < j.M;  // the same for the whole warp
+    auto column = [&](int i) { return 64 * half + 128 * (i >> 1) + 32 * (i & 1); };
+    float v[4][32] = {};
+    RowValues values = {};
+    for (int part = 0; part < j.kb_all; part += j.kb_part) {
+        if (part + j.kb_part >= j.kb_all)
+            values.load(p, m0 + lane);  // on their way while the last part is waited for
+        if (!a.take(w, rank))
+            return false;
+        if (rows) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = column(i);
+                if (c < cols) {
+                    add_acc16(a.columns(q, c), v[i]);
+                    add_acc16(a.columns(q, c + 16), v[i] + 16);
+                }
+            }
+        }
+        a.release(lane);
+    }
+    if (rows) {
+        const RowGrad g = row_grad(p, values, j.v0);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            if (column(i) < cols)
+                logit_grad_chunk(p, map, g, v[i], v[i + 1], m0, n0, column(i), sbuf, lane);
+    }
+    return true;
 }
 
 // One tile of a gradient, in chunks of 32 (fp32) or 64 columns.
@@ -853,17 +924,18 @@ __device__ __forceinline__ void product_tile(const HeadParams &p, const HeadJob 
 }
 
 // Backward: tiles of dl, dX and dW.
-template <int CG>
+template <int CG, int MODE>
 __device__ void gradient_epilogue(const HeadParams &p, const HeadMaps &maps, uint32_t sbuf, Accumulators<CG> a, uint32_t rank, int warp,
                                   int lane, const Waiter &w)
 {
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    constexpr bool PARTS = MODE == kBackwardParts;
+    const int q = warp & 3, half = (warp - kHeadFirstWarp<MODE>) >> 2;
     HeadUnits units(p, blockIdx.x / CG, gridDim.x / CG);
     auto first_row = [&](const HeadUnit &u) { return (u.m_blk * CG + static_cast<int>(rank)) * 128 + 32 * q; };
     HeadUnit h;
     RowValues values = {}, next_values = {};
     bool more = units.next(h);
-    if (more && p.jobs[h.job].epi == kEpiLogitGrad)
+    if (!PARTS && more && p.jobs[h.job].epi == kEpiLogitGrad)
         next_values.load(p, first_row(h) + lane);
     while (more) {
         const HeadJob &j = p.jobs[h.job];
@@ -872,12 +944,17 @@ __device__ void gradient_epilogue(const HeadParams &p, const HeadMaps &maps, uin
         const int n0 = h.n_blk * j.bn, cols = min(j.bn, j.N - n0);
         values = next_values;
         more = units.next(h);
-        if (more && p.jobs[h.job].epi == kEpiLogitGrad)
+        if (!PARTS && more && p.jobs[h.job].epi == kEpiLogitGrad)
             next_values.load(p, first_row(h) + lane);
+        if (PARTS && j.epi == kEpiLogitGrad) {
+            if (!logit_grad_parts<CG>(p, j, map, a, q, half, m0, n0, cols, sbuf, lane, rank, w))
+                return;
+            continue;
+        }
         if (!a.take(w, rank))
             return;
         if (m0 < j.M) {  // the same for the whole warp
-            if (j.epi == kEpiLogitGrad)
+            if (!PARTS && j.epi == kEpiLogitGrad)
                 logit_grad_tile<CG>(p, map, row_grad(p, values, j.v0), a, q, half, m0, n0, cols, sbuf, lane);
             else if (j.out_type == 0)
                 product_tile<CG, 32>(p, j, map, a, q, half, m0, n0, cols, split, sbuf, lane);
@@ -890,8 +967,8 @@ __device__ void gradient_epilogue(const HeadParams &p, const HeadMaps &maps, uin
 
 // ---------------------------------------------------------------- kernel
 
-template <int CG, bool FORWARD>
-__global__ void __launch_bounds__(kHeadThreads<CG, FORWARD>, 1) head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p)
+template <int CG, int MODE>
+__global__ void __launch_bounds__(kHeadThreads<CG, MODE>, 1) head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -901,7 +978,7 @@ __global__ void __launch_bounds__(kHeadThreads<CG, FORWARD>, 1) head_kernel(cons
     const uint32_t rank = CG == 2 ? cluster_ctarank() & 1u : 0u;
     const int stages = p.stages;
     const uint32_t staging = base + static_cast<uint32_t>(stages) * static_cast<uint32_t>(p.a_rows + p.b_rows) * kHeadBK<CG> * 2;
-    const uint32_t bars = staging + (FORWARD ? kHeadShares : kHeadStageBytes);
+    const uint32_t bars = staging + (MODE == kForward ? kHeadShares : kHeadStageBytes);
     const uint32_t bar_full = bars, bar_empty = bar_full + 8 * kHeadMaxStages;
     const uint32_t bar_acc_full = bar_empty + 8 * kHeadMaxStages, bar_acc_empty = bar_acc_full + 16;
     const uint32_t bar_drain = bar_acc_empty + 16, bar_inject = bar_drain + 8;
@@ -915,12 +992,12 @@ __global__ void __launch_bounds__(kHeadThreads<CG, FORWARD>, 1) head_kernel(cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_acc_full + 8 * b, 1);
-            mbar_init(bar_acc_empty + 8 * b, kHeadWarps<CG, FORWARD> * CG);
+            mbar_init(bar_acc_empty + 8 * b, kHeadWarps<CG, MODE> * CG);
         }
         mbar_init(bar_drain, 1);
         mbar_init(bar_inject, 1);
         for (int i = 0; i < 4; ++i) {
-            mbar_init(bar_shares + 16 * i, kHeadWarps<CG, FORWARD> / 4 - 1);
+            mbar_init(bar_shares + 16 * i, kHeadWarps<CG, MODE> / 4 - 1);
             mbar_init(bar_shares + 16 * i + 8, 1);
         }
         *abort_flag = 0u;
@@ -928,7 +1005,7 @@ __global__ void __launch_bounds__(kHeadThreads<CG, FORWARD>, 1) head_kernel(cons
         for (int j = 0; j < p.num_jobs; ++j) {
             prefetch_tensormap(&maps.a[j]);
             prefetch_tensormap(&maps.b[j]);
-            if constexpr (!FORWARD)
+            if constexpr (MODE != kForward)
                 prefetch_tensormap(&maps.d[j]);
         }
     }
@@ -950,25 +1027,27 @@ __global__ void __launch_bounds__(kHeadThreads<CG, FORWARD>, 1) head_kernel(cons
     w.status = p.status;
     w.all_cluster_scope = false;
     ProducerTail tail{0, 0, 0u};
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < kHeadFirstWarp<MODE>) {
+        if constexpr (MODE == kBackwardParts)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBackIssueRegs));
+        if (warp == 0 && lane == 0) {
             // what kernels before this one wrote by ordinary stores is read by TMA
             asm volatile("fence.proxy.async;" ::: "memory");
             tail = head_producer<CG>(p, maps, base, bar_full, bar_empty, bar_inject, rank, w);
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        } else if (warp == 1 && lane == 0 && rank == 0) {
             head_mma<CG>(p, base, bar_full, bar_empty, bar_acc_full, bar_acc_empty, bar_inject, tmem, w);
             mma_commit<CG>(bar_drain);
             w.drain(bar_drain, 0u, 100000000ull);
         }
     } else {
+        if constexpr (MODE == kBackwardParts)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBackEpiRegs));
         const Accumulators<CG> a{bar_acc_full, CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty, tmem};
-        if constexpr (FORWARD)
+        if constexpr (MODE == kForward)
             softmax_epilogue<CG>(p, reinterpret_cast<float2 *>(smem + (staging - base)), bar_shares, a, rank, warp, lane, w);
         else
-            gradient_epilogue<CG>(p, maps, staging + static_cast<uint32_t>((warp - 2) * kEpiBufBytes), a, rank, warp, lane, w);
-        if (!FORWARD && lane == 0)
+            gradient_epilogue<CG, MODE>(p, maps, staging + static_cast<uint32_t>((warp - kHeadFirstWarp<MODE>) * kEpiBufBytes), a, rank, warp, lane, w);
+        if (MODE != kForward && lane == 0)
             bulk_wait_group<0>();  // stores have finished reading shared memory
     }
     __syncwarp();
@@ -1541,7 +1620,7 @@ gemm_status_t map_operands(Job *job, int in_bf16, const Operand &A, const Operan
     return s == GEMM_OK ? encode_16(&job->b, in_bf16, B.ptr, j.b_mn, j.N, j.K, B.ld, j.bn / CG, BK) : s;
 }
 
-template <int CG, bool FORWARD>
+template <int CG, int MODE>
 std::atomic<uint64_t> head_attribute_set[2] = {{0}, {0}};
 
 // Deals the units of the jobs, the longest first, out to the clusters: the jobs
@@ -1575,7 +1654,7 @@ int64_t deal_units(Job *jobs, int n, int64_t slots)
 int64_t cluster_slots(int cg, int sms) { return std::max(1, sms / cg); }
 
 // Deals the units out and launches the jobs together.
-template <int CG, bool FORWARD>
+template <int CG, int MODE>
 gemm_status_t launch_head(HeadParams p, Job *jobs, int n, int sms, cudaStream_t st)
 {
     constexpr int BK = kHeadBK<CG>;
@@ -1601,13 +1680,22 @@ gemm_status_t launch_head(HeadParams p, Job *jobs, int n, int sms, cudaStream_t 
     // a role may wait for another to walk all of a unit's K: 10 us a block beside 2 s
     p.timeout_ns = ms > 0 ? static_cast<unsigned long long>(ms) * 1000000ull : 2000000000ull + static_cast<unsigned long long>(longest) * 10000ull;
     const int stage_bytes = (p.a_rows + p.b_rows) * BK * 2;
-    const int rest = (FORWARD ? kHeadShares : kHeadStageBytes) + kHeadTail;
+    const int rest = (MODE == kForward ? kHeadShares : kHeadStageBytes) + kHeadTail;
     p.stages = std::min(kHeadMaxStages, (kHeadSmem - rest) / stage_bytes);
     const int smem = p.stages * stage_bytes + rest + 1024;
-    auto kern = head_kernel<CG, FORWARD>;
-    if (ensure_smem_attribute(kern, kHeadSmem + 1024, head_attribute_set<CG, FORWARD>) != cudaSuccess)
+    auto kern = head_kernel<CG, MODE>;
+    if constexpr (MODE == kBackwardParts) {
+        // an inc of more than the launch has would wait for ever
+        static const bool regs_ok = [&] {
+            cudaFuncAttributes at;
+            return cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs == kBackLaunchRegs;
+        }();
+        if (!regs_ok)
+            return GEMM_ERR_UNSUPPORTED;
+    }
+    if (ensure_smem_attribute(kern, kHeadSmem + 1024, head_attribute_set<CG, MODE>) != cudaSuccess)
         return GEMM_ERR_CUDA;
-    return host_launch(kern, static_cast<unsigned>(clusters * CG), kHeadThreads<CG, FORWARD>, static_cast<size_t>(smem), st, CG == 2 ? 2u : 0u, maps, p);
+    return host_launch(kern, static_cast<unsigned>(clusters * CG), kHeadThreads<CG, MODE>, static_cast<size_t>(smem), st, CG == 2 ? 2u : 0u, maps, p);
 }
 
 // Columns of the tiles of the logits: 256, or the width whose rounds of the grid
@@ -1754,7 +1842,7 @@ gemm_status_t forward_job(Job *job, int64_t T, int64_t V, int64_t K, int sms, in
     *a_rows = CG == 2 ? 128 : static_cast<int>(std::min<int64_t>(128, round_up(T, 8)));
     const gemm_status_t s = shape_job<CG>(job, logit_columns(CG, T, V, *a_rows, CG == 2 ? 32 : 16, sms), 1, T, V, K, 0, 0);
     job->j.epi = kEpiSoftmax;
-    job->j.kb_part = kSumPart / kHeadBK<CG>;
+    job->j.kb_part = static_cast<int>(sum_part(CG, T) / kHeadBK<CG>);
     return s;
 }
 
@@ -1770,7 +1858,7 @@ gemm_status_t run_forward(HeadParams p, int64_t T, int64_t V, int64_t K, int in_
         return s;
     job.d = job.a;
     *tiles = job.j.tiles_n;
-    return launch_head<CG, true>(p, &job, 1, sms, st);
+    return launch_head<CG, kForward>(p, &job, 1, sms, st);
 }
 
 constexpr int kFewTokens = 2;
@@ -1940,6 +2028,7 @@ gemm_status_t piece_jobs(PieceJobs *q, const BackPlan &b, int64_t i, int64_t T, 
         if ((s = shape_job<CG>(q->dl, bn, 1, T, q->next, K, 0, 0)) != GEMM_OK)
             return s;
         q->dl->j.epi = kEpiLogitGrad;
+        q->dl->j.kb_part = static_cast<int>(sum_part(CG, T) / kHeadBK<CG>);
         q->dl->j.v0 = static_cast<int>(q->w0);
     }
     return GEMM_OK;
@@ -2003,7 +2092,9 @@ gemm_status_t run_backward(HeadParams p, const BackArgs &g, const BackPlan &b, i
                     GEMM_OK)
                 return s;
         }
-        if ((s = launch_head<CG, false>(p, q.jobs, q.n, sms, st)) != GEMM_OK)
+        const bool by_parts = q.dl && q.dl->j.kb_part < q.dl->j.kb_all;
+        s = by_parts ? launch_head<CG, kBackwardParts>(p, q.jobs, q.n, sms, st) : launch_head<CG, kBackward>(p, q.jobs, q.n, sms, st);
+        if (s != GEMM_OK)
             return s;
     }
     return GEMM_OK;

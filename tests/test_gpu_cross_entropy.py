@@ -468,3 +468,69 @@ def test_more_than_32_bits_of_weights_and_gradients(g):
     sx = sum(p[:, a:a + 16384].abs() @ W[a:a + 16384].double().abs() for a in range(0, V, 16384))
     nx = math.sqrt(sum(float((p[:, a:a + 16384].square() @ W[a:a + 16384].double().square()).sum()) for a in range(0, V, 16384)))
     near(dX, (wx, sx, nx, torch.zeros(K, dtype=torch.float64, device=DEV)), X.dtype)
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("T,K", [(1, 4096), (2, 4096), (1, 5000), (2, 16384), (3, 4096), (64, 1500), (100, 8192), (300, 520), (300, 4096), (600, 16384)])
+def test_confident_tokens(g, T, K, type):
+    """Targets whose logits are 25 to 35 above the rest: dl is p - 1, some 1e-9, the rest of two values that nearly agree.
+
+    Logits that are sums of products of one sign, where truncating additions move a sum the most. The gradients are compared
+    with the true ones (64-bit normalisers). A target's dl may be off by what rounding leaves of lse: five half steps of fp32
+    of about 35 (in the forward pass of the reference, its join with the logarithm of the sum, its return to base e and the
+    constants' product, in the backward pass of lse times log2 e), and 2^-22 for the exponential. Without tiles (one or two tokens
+    of K <= 4096) the logits' sums are others than the forward pass's, whose parts of 128 take eight truncations each of at
+    most a step of 2^-23 of what has been summed, 4.5 parts' in all, and as much for what a step's products lose among
+    themselves.
+    """
+    V = 2000
+    dtype = TYPES[type][0]
+    X, W, y = make(T, V, K, dtype, seed=T + K, spread=1.0)
+    gen = torch.Generator(device=DEV).manual_seed(K)
+    y.copy_(torch.randperm(V, generator=gen, device=DEV)[:T].int())
+    x = X.double()
+    top = 25.0 + 10.0 * torch.rand(T, 1, generator=gen, device=DEV)
+    W[y.long()] = (x * (top / x.square().sum(1, keepdim=True))).to(dtype)
+    losses, lse = forward(g, X, W, y)
+    want, want_lse, logits, _ = forward64(X, W, y)
+    dl = torch.ones(T, device=DEV)
+    dX, dW = backward(g, X, W, y, lse, dl, None, x_type="f32", w_type="f32")
+    status_ok(g)
+    (want_x, size_x, _, values_x), (want_w, size_w, _, values_w) = backward64(X, W, y, want_lse, dl, None)
+    off = 5 * 2.0 ** -24 * 36.0 + 2.0 ** -22
+    if T <= 2 and K <= 4096:
+        off += 2 * 4.5 * 2.0 ** -23 * 36.0
+    at = y.long()
+    slack_x, slack_w = off * W[at].double().abs(), torch.zeros_like(want_w)
+    slack_w[at] = off * x.abs()
+    u = torch.finfo(dtype).eps / 2
+    lost = 2.0 ** -39 if dtype == torch.float16 else 0.0
+    for got, ref, size, values, slack in ((dX, want_x, size_x, values_x, slack_x), (dW, want_w, size_w, values_w, slack_w)):
+        err = (got.double() - ref).abs()
+        bound = 1.01 * slack + (1.01 * u + 2.0 ** -18) * size + lost * values + 1e-36
+        assert bool((err <= bound).all()), (float(err.max()), float((err / bound).max()))
+
+
+@pytest.mark.parametrize("columns", [0, 512])
+@pytest.mark.parametrize("T,V,K", [(20, 1217, 513), (90, 3000, 2001), (129, 2047, 640), (257, 700, 1100), (700, 4001, 1500), (40, 131, 8192)])
+def test_gradients_of_long_rows(g, T, V, K, columns):
+    """Rows whose sums are taken in parts, the last one short; tiles whose columns end anywhere; pieces of the vocabulary."""
+    check_backward(g, T, V, K, "bf16", seed=T, masked=0.2, z=True, columns=columns, pad=1)
+    check_backward(g, T, V, K, "f16", seed=T + 1, columns=columns, x_type="f32", w_type="f32", accumulate=True)
+
+
+@pytest.mark.parametrize("role", [1, 2])
+@pytest.mark.parametrize("T,columns", [(64, 0), (300, 0), (300, 256)])
+def test_waits_of_long_rows_gradients_that_run_out_are_reported(g, T, columns, role):
+    X, W, y = make(T, 2000, 1600, torch.bfloat16, seed=23)
+    lse = forward64(X, W, y)[1].float()
+    dl = torch.ones(T, device=DEV)
+    good = backward(g, X, W, y, lse, dl, None, columns=columns)
+    status_ok(g)
+    g.gemm_debug_inject_timeout(20, role)
+    backward(g, X, W, y, lse, dl, None, columns=columns)
+    status, word = g.gemm_last_device_status()
+    assert status == g.ERR_TIMEOUT and word & 0xFF in (1, 2, 3)
+    again = backward(g, X, W, y, lse, dl, None, columns=columns)
+    assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
+    status_ok(g)
