@@ -625,7 +625,7 @@ gemm_status_t gemm_route_combine_backward(int64_t T, int64_t N, int k, const voi
  * from part to part; sums of exponentials, lse and losses are fp32, the loss
  * without the rounding of lse. A logit of +inf makes lse +inf, one of NaN NaN.
  * workspace: gemm_cross_entropy_workspace_size(T, V) bytes, 16-byte aligned,
- * in no particular state.
+ * in no particular state. More tokens never ask for less.
  */
 size_t gemm_cross_entropy_workspace_size(int64_t T, int64_t V);
 

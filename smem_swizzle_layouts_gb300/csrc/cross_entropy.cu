@@ -1832,8 +1832,13 @@ gemm_status_t check_head(int in_type, int64_t T, int64_t V, int64_t K, const voi
     return GEMM_OK;
 }
 
-// Room for partial softmaxes on any GPU: one for each tile, which has at least 64 columns.
-size_t forward_bytes(int64_t T, int64_t V) { return static_cast<size_t>(T) * static_cast<size_t>((V + 63) / 64) * sizeof(float2); }
+// Room for partial softmaxes on any GPU: one for each tile, which has at least 64
+// columns, or where tokens have CTA pairs 128 (and for the most tokens that have none).
+size_t forward_bytes(int64_t T, int64_t V)
+{
+    const size_t narrow = static_cast<size_t>(std::min<int64_t>(T, 128)) * static_cast<size_t>((V + 63) / 64) * sizeof(float2);
+    return T <= 128 ? narrow : std::max(narrow, static_cast<size_t>(T) * static_cast<size_t>((V + 127) / 128) * sizeof(float2));
+}
 
 // The forward product, and the rows of X's places in a stage.
 template <int CG>

@@ -90,3 +90,17 @@ def test_balance_loss_of_fewer_sequences(g, T):
 @pytest.mark.parametrize("V", [1, 300, 131072])
 def test_loss(g, V):
     assert never_falls([g.gemm_cross_entropy_workspace_size(t, V) for t in counts_of_tokens(300000, V)])
+
+
+def test_loss_asks_for_what_tiles_may_need(g):
+    """A reference and a sum for each token and tile, whatever the tiles' width on any number of SMs; no tile of more than 128
+    tokens is narrower than 128 columns."""
+    assert g.gemm_cross_entropy_workspace_size(8192, 131072) == 8192 * 1024 * 8
+    rng = random.Random(5)
+    for _ in range(400):
+        T, V, K, sms = int(20000 ** rng.random()), int(200000 ** rng.random()), rng.choice([1, 64, 700]), rng.choice([1, 7, 132, 148, 152])
+        if T * V > 1 << 28:
+            continue
+        units = g.gemm_debug_cross_entropy_units(T, V, K, 0, sms, -1, 0)
+        tiles = len(set(units[4::8]))
+        assert tiles * T * 8 <= g.gemm_cross_entropy_workspace_size(T, V)
