@@ -680,7 +680,10 @@ gemm_status_t gemm_cross_entropy_backward(int in_type, int64_t T, int64_t V, int
  *   losses[s]   = E * sum_e counts[s,e] / (k n) * means[s,e]
  * with p the token's softmax over the E experts, or its sigmoid scores over their
  * sum (route->score; its other fields, and a bias, have no part; NULL: softmax).
- * A perfect balance has loss 1; a sequence without live tokens has zeros.
+ * A perfect balance has loss 1; a sequence without live tokens has zeros. Scores
+ * are exponentials and reciprocals of the special-function unit: within 2^-21 of
+ * themselves for logits of up to 10 (below the token's largest one with softmax),
+ * 2^-22 + 1.25 |l| 2^-24 in all; sums are fp32.
  * ids: T x k int32 as gemm_route writes them; logits: T x E of l_type, row
  * stride ldl. counts and means: S x E; all fp32 or int32. E, k as for gemm_route.
  * workspace: gemm_route_balance_workspace_size(T, E, S) bytes, 16-byte aligned,

@@ -61,7 +61,8 @@ enum : int { kForward = 0, kBackward = 1, kBackwardParts = 2 };
 // of the columns. The softmax has no staging buffers, and while some of its 16
 // warps wait for TMEM others have work: 7252 x 118755 x 128 forward 346 us (384
 // by 8), 8192 x 32768 x 256 112 (123); 2048 x 32768 x 1024 78.7 (77.3). A single
-// CTA's few rows leave most warps without any: 1 x 131072 x 4096 167 (157).
+// CTA's few rows leave most warps without any: 1 x 131072 x 4096 167 (157). (By 16
+// a thread has 96 registers, and 32 bytes of it lie in memory.)
 template <int CG, int MODE>
 constexpr int kHeadWarps = CG == 2 && MODE == kForward ? 16 : 8;
 // Before them the producer and the issuer. Where dl is made of parts, a thread
@@ -1258,7 +1259,8 @@ __global__ void __launch_bounds__(256) head_zero_kernel(uint8_t *d, long long ld
 // products read the weights twice): 1 x 131072 x 4096 in 375 us, of 322 at the
 // copy rate, 2 x 131072 x 4096 in 368, 1 x 32000 x 1024 in 33 (by tiles 607, 610
 // and 60). Four tokens, of which registers hold two words at a time, took as
-// long as by tiles.
+// long as by tiles. (One token's eight words leave some 26 registers of a thread in
+// memory, 104 bytes; two tokens' four none.)
 constexpr int kFewThreads = 512;  // K <= 8 * 512
 constexpr int kFewBlocks = 152;   // one for each SM of the GPU this is built for
 
@@ -1751,6 +1753,13 @@ struct DxTiles {
     int64_t slots, tiles, most_splits;
 };
 
+// Up to 128 tokens have tiles of single CTAs: one row of tiles, whose columns twice
+// as many share as there are pairs. More have pairs, since two rows of single
+// tiles would read the weights twice. By the other of the two, at V 131072, K 2048: forward 64 tokens
+// 99.0 us instead of 88.4, 128 99.7 (89.0), 129 116.7 (100.3), 256 127.5 (103.6);
+// backward 64 338.6 (320.2), 128 352.0 (333.1), 129 394 (367), 256 439 (389). At V
+// 32768, K 1024 forward 128 18.9 (14.9), 129 20.4 (18.5), 257 25.8 (27.3), 384 27.2
+// both ways, 512 33.6 (29.4).
 DxTiles dx_tiles(int64_t T, int64_t K, int sms)
 {
     DxTiles d;
