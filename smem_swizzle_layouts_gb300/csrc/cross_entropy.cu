@@ -14,16 +14,17 @@
 // the 6 T V K operations of the backward pass), or the gradients themselves.
 // Backward, one launch has up to three products: a piece's dX and dW, and the
 // next piece's dl, whose units fill what the others' rounds leave of the grid
-// (4096 x 32768 x 4096: 1958 us instead of 2234 by a launch for each). One or
-// two tokens have a kernel of their own below.
+// (4096 x 32768 x 4096: 1958 us instead of 2234 by a launch for each, before
+// the logits were summed in parts of K). One or two tokens have a kernel of
+// their own below.
 //
 // Many tokens are bound by the tensor cores, whose rate the power limit holds:
-// 8192 x 65536 x 4096 forward took 2409 to 2547 us (1.8 PFLOP/s; at the measured
+// 8192 x 65536 x 4096 forward took 2409 to 2551 us (1.8 PFLOP/s; at the measured
 // peaks 2280 in a burst, 2500 sustained), 4096 x 32768 x 4096 backward
-// 1936 to 1987 (1710, 1875). Few are bound by the weights' bytes: 1 x 131072 x 4096 in 161 us,
-// at the rate of a copy. Small K is bound by the epilogue, an exponential and some
+// 1916 to 2003 (1710, 1875). Few are bound by the weights' bytes: 1 x 131072 x
+// 4096 in 159 to 163 us, at the rate of a copy. Small K is bound by the epilogue, an exponential and some
 // additions for each logit against K products, and backward by dl's bytes: 8192 x
-// 32768 x 256 forward 112 us of 71, backward 352 of 214.
+// 32768 x 256 forward 112 to 118 us of 71, backward 352 to 365 of 214.
 //
 // Roles, barriers and waits are those of gemm_kernel.cuh (whose operand
 // geometry, descriptors and bounded waits are used here); the tiles' widths,

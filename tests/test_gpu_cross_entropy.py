@@ -534,3 +534,39 @@ def test_waits_of_long_rows_gradients_that_run_out_are_reported(g, T, columns, r
     again = backward(g, X, W, y, lse, dl, None, columns=columns)
     assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
     status_ok(g)
+
+
+def test_long_rows_on_a_side_stream_and_replayed(g):
+    """Rows whose sums are taken in parts, in pieces of the vocabulary: captured, and replayed on other data."""
+    T, V, K = 200, 3000, 1104
+    X, W, y = make(T, V, K, torch.bfloat16, seed=24, masked=0.1)
+    lse, dl = forward64(X, W, y)[1].float(), torch.full((T,), 1.0 / T, device=DEV)
+    dX, dW = torch.empty(T, K, device=DEV), torch.empty(V, K, device=DEV)
+    n = g.gemm_cross_entropy_backward_workspace_size(T, V, K, 1024)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+
+    def step():
+        g.gemm_cross_entropy_backward(1, T, V, K, X, K, W, K, y, lse, dl, None, dX, 0, K, dW, 0, K, 0, ws, n)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    eager = [dX.clone(), dW.clone()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    other = make(T, V, K, torch.bfloat16, seed=25, masked=0.3)
+    for data in (other, (X.clone(), W.clone(), y.clone())):
+        for t, new in zip((X, W, y), data):
+            t.copy_(new)
+        lse.copy_(forward64(X, W, y)[1].float())
+        dX.fill_(math.nan)
+        dW.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        want_x, want_w = backward64(X, W, y, lse, dl, None)
+        near(dX, want_x, X.dtype)
+        near(dW, want_w, X.dtype)
+    assert torch.equal(dX, eager[0]) and torch.equal(dW, eager[1])
